@@ -33,7 +33,10 @@ EXPORTS = ("conv_out_dim", "conv_status_str", "conv_version",
            "conv_im2col_bf16", "conv_fwd_explicit_bf16",
            "conv_bwd_data_workspace_bytes", "conv_bwd_data_bf16",
            "conv_bwd_weight_workspace_bytes", "conv_bwd_weight_bf16",
-           "conv_fwd_ex_workspace_bytes", "conv_fwd_ex_bf16", "conv_fwd_ex_f32")
+           "conv_fwd_ex_workspace_bytes", "conv_fwd_ex_bf16", "conv_fwd_ex_f32",
+           "conv_causal_fwd", "conv_causal_bwd_workspace_bytes", "conv_causal_bwd", "conv_causal_step",
+           "conv_scan_fwd_workspace_bytes", "conv_scan_fwd", "conv_scan_bwd_workspace_bytes", "conv_scan_bwd",
+           "conv_scan_step", "conv_adamw_step", "conv_adamw_state_values")
 
 LAYOUT = {"nchw": 0, "nhwc": 1}
 OUT_DTYPE = {"f32": 0, "bf16": 1}
@@ -48,6 +51,25 @@ class ConvParams(ctypes.Structure):
 class ConvOptions(ctypes.Structure):
     """conv_options_t: layout of x and y, output dtype, ReLU."""
     _fields_ = [("layout", ctypes.c_int), ("out_dtype", ctypes.c_int), ("relu", ctypes.c_int)]
+
+
+class SeqParams(ctypes.Structure):
+    """conv_seq_t: a batch of sequences of tokens, equal or packed."""
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("tokens", ctypes.c_int64)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """conv_adamw_tensor_t: one tensor's parameters, gradient and moments."""
+    _fields_ = [("n", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale",
+                                                                         "copy")] + [("weight_decay", ctypes.c_float)]
+
+
+class AdamwOptions(ctypes.Structure):
+    """conv_adamw_t: the step's rates and formats."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
+        [("step", ctypes.c_int64), ("bits", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("seed", ctypes.c_uint32),
+         ("grad_scale", ctypes.c_void_p)]
 
 
 class ConvError(RuntimeError):
@@ -126,6 +148,30 @@ def lib():
         L.conv_fwd_ex_bf16.argtypes = [_pp, _po, _vp, _vp, _vp, _vp, _vp, _sz, _i, _vp]
         L.conv_fwd_ex_f32.restype = _i
         L.conv_fwd_ex_f32.argtypes = [_pp, _po, _vp, _vp, _vp, _vp, _i, _vp]
+        _ps = ctypes.POINTER(SeqParams)
+        _f = ctypes.c_float
+        row = [_vp, _i64]                       # a tensor of rows and its row stride
+        L.conv_causal_fwd.restype = _i
+        L.conv_causal_fwd.argtypes = [_ps, _i, _i] + row + [_vp] * 3 + row + [_vp, _vp]
+        L.conv_causal_bwd_workspace_bytes.restype = _sz
+        L.conv_causal_bwd_workspace_bytes.argtypes = [_ps, _i]
+        L.conv_causal_bwd.restype = _i
+        L.conv_causal_bwd.argtypes = [_ps, _i, _i] + row + [_vp] * 3 + row * 2 + [_vp] * 4 + [_sz, _vp]
+        L.conv_causal_step.restype = _i
+        L.conv_causal_step.argtypes = [_ps, _i, _i] + row + [_vp] * 3 + row + [_vp]
+        for name in ("conv_scan_fwd_workspace_bytes", "conv_scan_bwd_workspace_bytes"):
+            getattr(L, name).restype = _sz
+            getattr(L, name).argtypes = [_ps]
+        L.conv_scan_fwd.restype = _i
+        L.conv_scan_fwd.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp] * 3 + [_sz, _vp]
+        L.conv_scan_bwd.restype = _i
+        L.conv_scan_bwd.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp] + row * 3 + [_vp] * 3 + [_sz, _vp]
+        L.conv_scan_step.restype = _i
+        L.conv_scan_step.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp]
+        L.conv_adamw_step.restype = _i
+        L.conv_adamw_step.argtypes = [ctypes.POINTER(AdamwOptions), _vp, _i, _vp]
+        L.conv_adamw_state_values.restype = _i
+        L.conv_adamw_state_values.argtypes = [_vp, _i, _vp, _vp, _vp]
         _lib = L
     return _lib
 
@@ -270,6 +316,57 @@ def conv_fwd_ex_bf16(params, opts, x, w, bias, y, ws, ws_bytes, algo=0, stream=N
 
 def conv_fwd_ex_f32(params, opts, x, w, bias, y, algo=0, stream=None):
     return lib().conv_fwd_ex_f32(_pref(params), _oref(opts), x, w, bias, y, algo, stream)
+
+
+def conv_causal_fwd(seq, K, silu, x, ldx, w, bias, state, y, ldy, state_out, stream=None):
+    return lib().conv_causal_fwd(_pref(seq), K, silu, x, ldx, w, bias, state, y, ldy, state_out, stream)
+
+
+def conv_causal_bwd_workspace_bytes(seq, K):
+    return int(lib().conv_causal_bwd_workspace_bytes(_pref(seq), K))
+
+
+def conv_causal_bwd(seq, K, silu, x, ldx, w, bias, state, dy, lddy, dx, lddx, dw, db, dstate, ws, ws_bytes,
+                    stream=None):
+    return lib().conv_causal_bwd(_pref(seq), K, silu, x, ldx, w, bias, state, dy, lddy, dx, lddx, dw, db, dstate, ws,
+                                 ws_bytes, stream)
+
+
+def conv_causal_step(seq, K, silu, x, ldx, w, bias, state, y, ldy, stream=None):
+    return lib().conv_causal_step(_pref(seq), K, silu, x, ldx, w, bias, state, y, ldy, stream)
+
+
+def conv_scan_fwd_workspace_bytes(seq):
+    return int(lib().conv_scan_fwd_workspace_bytes(_pref(seq)))
+
+
+def conv_scan_fwd(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ws, ws_bytes, stream=None):
+    return lib().conv_scan_fwd(_pref(seq), scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ws,
+                               ws_bytes, stream)
+
+
+def conv_scan_bwd_workspace_bytes(seq):
+    return int(lib().conv_scan_bwd_workspace_bytes(_pref(seq)))
+
+
+def conv_scan_bwd(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp,
+                  lddi, ddecay, dh0, ws, ws_bytes, stream=None):
+    return lib().conv_scan_bwd(_pref(seq), scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx,
+                               dgate, lddg, dinp, lddi, ddecay, dh0, ws, ws_bytes, stream)
+
+
+def conv_scan_step(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream=None):
+    return lib().conv_scan_step(_pref(seq), scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream)
+
+
+def conv_adamw_step(opt, tensors, count, stream=None):
+    """tensors: a ctypes array of AdamwTensor (host memory), or None."""
+    return lib().conv_adamw_step(_pref(opt), tensors, count, stream)
+
+
+def conv_adamw_state_values(tensors, count, m_out, v_out, stream=None):
+    """tensors as in conv_adamw_step; m_out, v_out: ctypes arrays of count device pointers."""
+    return lib().conv_adamw_state_values(tensors, count, m_out, v_out, stream)
 
 
 def make_params(x_shape, w_shape, stride=1, pad=0, dilation=1, groups=1):
@@ -633,3 +730,342 @@ def workspace_ex(x_shape, w_shape, stride=1, pad=0, dilation=1, groups=1, layout
     a = ALGO[algo] if isinstance(algo, str) else int(algo)
     n = conv_fwd_ex_workspace_bytes(prm, opts, a)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+# ---- sequences of tokens ------------------------------------------------------
+
+def _dtype_code(t, name):
+    """CONV_OUT_* of a float32 or bf16 (torch.bfloat16, or int16/uint16 bits) tensor."""
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return 0
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return 1
+    raise TypeError("%s has dtype %s, expected float32 or bf16" % (name, t.dtype))
+
+
+def _ld(t, shape, like, name):
+    """The row stride of a tensor of rows: its last axis is dense, and its leading axes are one
+    evenly strided axis (a column slice of a dense tensor, for instance)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != like.dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
+    if t.is_contiguous():
+        return shape[-1]
+    if t.numel() == 0:
+        return shape[-1]
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError("%s: the channels of a row must be adjacent" % name)
+    if len(shape) == 2:
+        ld = st[0] if shape[0] > 1 else shape[1]
+    elif shape[1] > 1:
+        ld = st[1]
+        if shape[0] > 1 and st[0] != shape[1] * ld:
+            raise ValueError("%s: sequences must follow each other at the row stride" % name)
+    else:
+        ld = st[0] if shape[0] > 1 else shape[2]
+    if ld < shape[-1]:
+        raise ValueError("%s: rows overlap" % name)
+    return ld
+
+
+def _dense(t, shape, dtype, name):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def make_seq(x, offsets=None, max_len=None, name="x"):
+    """SeqParams for x: (B, T, C), or (tokens, C) packed, with offsets (B+1 int32 on the GPU) and
+    max_len, the length of the longest sequence."""
+    torch = _torch()
+    code = _dtype_code(x, name)
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError("%s must be (sequences, tokens, channels), or packed rows with offsets" % name)
+        return SeqParams(code, x.shape[0], x.shape[1], x.shape[2], None, 0)
+    if x.dim() != 2:
+        raise ValueError("packed %s must be (tokens, channels)" % name)
+    if max_len is None:
+        raise ValueError("packed sequences need max_len")
+    if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 vector on the GPU")
+    if offsets.shape[0] < 2:
+        raise ValueError("offsets must hold B + 1 >= 2 values")
+    return SeqParams(code, offsets.shape[0] - 1, max_len, x.shape[1], offsets.data_ptr(), x.shape[0])
+
+
+def _step_seq(x):
+    if x.dim() != 2:
+        raise ValueError("x must be (sequences, channels)")
+    return SeqParams(_dtype_code(x, "x"), x.shape[0], 1, x.shape[1], None, 0)
+
+
+def _run(st, where):
+    if st != CONV_OK:
+        raise ConvError(st, where)
+
+
+def _rows_out(out, x, name):
+    torch = _torch()
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
+    return out, _ld(out, x.shape, x, name)
+
+
+def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=None, with_state=False, out=None):
+    """Causal depthwise convolution over the tokens of x, (B, T, C) or packed (see make_seq), float32 or
+    bf16: conv_causal_fwd.  w: (C, K) of x's dtype, tap K-1 on the token itself; bias: float32 (C);
+    state: the K-1 rows before each sequence, (B, K-1, C) of x's dtype, or None for zeros.  x and out
+    may be column slices of a wider tensor.  Returns y, or (y, state after the last tokens)."""
+    torch = _torch()
+    seq = make_seq(x, offsets, max_len)
+    ldx = _ld(x, x.shape, x, "x")
+    if w.dim() != 2:
+        raise ValueError("w must be (channels, taps)")
+    K = w.shape[1]
+    rows = (seq.B, K - 1, seq.C)
+    y, ldy = _rows_out(out, x, "out")
+    end = torch.empty(rows, dtype=x.dtype, device=x.device) if with_state else None
+    _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
+                         _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
+                         y.data_ptr(), ldy, end.data_ptr() if with_state else None, _stream()), "conv_causal_fwd")
+    return (y, end) if with_state else y
+
+
+def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=None, max_len=None, out=None):
+    """(dx, dw, db, dstate) of y = causal_conv(x, w, bias, silu, state) for upstream gradient dy
+    (conv_causal_bwd): dx and dstate of x's dtype, dw (C, K) and db (C) float32; dstate is None without
+    a state.  `out`: dx to write into, perhaps a column slice."""
+    torch = _torch()
+    seq = make_seq(x, offsets, max_len)
+    ldx, lddy = _ld(x, x.shape, x, "x"), _ld(dy, x.shape, x, "dy")
+    if w.dim() != 2:
+        raise ValueError("w must be (channels, taps)")
+    K = w.shape[1]
+    rows = (seq.B, K - 1, seq.C)
+    dx, lddx = _rows_out(out, x, "out")
+    dw = torch.empty((seq.C, K), dtype=torch.float32, device=x.device)
+    db = torch.empty((seq.C,), dtype=torch.float32, device=x.device)
+    ds = torch.empty(rows, dtype=x.dtype, device=x.device) if state is not None else None
+    n = conv_causal_bwd_workspace_bytes(seq, K)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
+                         _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
+                         dy.data_ptr(), lddy, dx.data_ptr(), lddx, dw.data_ptr(), db.data_ptr(),
+                         None if ds is None else ds.data_ptr(), ws.data_ptr(), n, _stream()), "conv_causal_bwd")
+    return dx, dw, db, ds
+
+
+def causal_conv_step(x, w, state, bias=None, silu=False, out=None):
+    """One new token, x (B, C), of each of B sequences: returns y (B, C) and moves state (B, K-1, C) on
+    by the token in place (conv_causal_step)."""
+    torch = _torch()
+    seq = _step_seq(x)
+    ldx = _ld(x, x.shape, x, "x")
+    if w.dim() != 2:
+        raise ValueError("w must be (channels, taps)")
+    K = w.shape[1]
+    y, ldy = _rows_out(out, x, "out")
+    _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
+                          _dense(bias, (seq.C,), torch.float32, "bias"),
+                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state"), y.data_ptr(), ldy, _stream()),
+         "conv_causal_step")
+    return y
+
+
+SCAN_BLOCK = 64     # CONV_SCAN_BLOCK
+
+
+def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=None, with_states=False, out=None,
+               workspace=None):
+    """The gated linear recurrence over the tokens of x, (B, T, C) or packed (see make_seq), float32 or
+    bf16 (conv_scan_fwd):
+
+        a = exp(-scale * softplus(decay) * sigmoid(gate)),  h = a h + sqrt(1 - a^2) sigmoid(inp) x
+
+    gate and inp: like x; decay: float32 (C); h0: float32 (B, C) or None for zeros.  x, gate, inp and out
+    may be column slices of wider tensors.  Returns (y, h after the last tokens), and with_states also
+    the states gated_scan_backward starts from."""
+    torch = _torch()
+    seq = make_seq(x, offsets, max_len)
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
+    y, ldy = _rows_out(out, x, "out")
+    ends = (seq.B, seq.C)
+    hT = torch.empty(ends, dtype=torch.float32, device=x.device)
+    states = None
+    if with_states:
+        states = torch.empty((seq.B, -(-seq.T // SCAN_BLOCK), seq.C), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        n = conv_scan_fwd_workspace_bytes(seq)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(conv_scan_fwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
+                       _dense(decay, (seq.C,), torch.float32, "decay"), _dense(h0, ends, torch.float32, "h0"),
+                       y.data_ptr(), ldy, hT.data_ptr(), None if states is None else states.data_ptr(),
+                       None if workspace is None else workspace.data_ptr(), wsb, _stream()), "conv_scan_fwd")
+    return (y, hT, states) if with_states else (y, hT)
+
+
+def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, offsets=None, max_len=None, out=None,
+                        workspace=None):
+    """(dx, dgate, dinp, ddecay, dh0) of (y, h) = gated_scan(...) for upstream dy, like x, and dh, float32
+    (B, C) or None for zeros (conv_scan_bwd).  states: as gated_scan(..., with_states=True) returned them
+    for the same inputs.  `out`: (dx, dgate, dinp) to write into, perhaps column slices of one tensor."""
+    torch = _torch()
+    seq = make_seq(x, offsets, max_len)
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
+    lddy = _ld(dy, x.shape, x, "dy")
+    o = (None, None, None) if out is None else out
+    dx, lddx = _rows_out(o[0], x, "dx")
+    dg, lddg = _rows_out(o[1], x, "dgate")
+    di, lddi = _rows_out(o[2], x, "dinp")
+    ends = (seq.B, seq.C)
+    dd = torch.empty((seq.C,), dtype=torch.float32, device=x.device)
+    dh0 = torch.empty(ends, dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(conv_scan_bwd_workspace_bytes(seq), dtype=torch.uint8, device=x.device)
+    nb = -(-seq.T // SCAN_BLOCK)
+    _run(conv_scan_bwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
+                       _dense(decay, (seq.C,), torch.float32, "decay"),
+                       _dense(states, (seq.B, nb, seq.C), torch.float32, "states"), dy.data_ptr(), lddy,
+                       _dense(dh, ends, torch.float32, "dh"), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
+                       lddi, dd.data_ptr(), dh0.data_ptr(), workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), _stream()), "conv_scan_bwd")
+    return dx, dg, di, dd, dh0
+
+
+def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
+    """One new token, x, gate and inp (B, C), of each of B sequences: returns y (B, C) and updates h,
+    float32 (B, C), in place (conv_scan_step)."""
+    torch = _torch()
+    seq = _step_seq(x)
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
+    y, ldy = _rows_out(out, x, "out")
+    _run(conv_scan_step(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
+                        _dense(decay, (seq.C,), torch.float32, "decay"),
+                        _dense(h, (seq.B, seq.C), torch.float32, "h"), y.data_ptr(), ldy, _stream()), "conv_scan_step")
+    return y
+
+
+# ---- the optimiser step --------------------------------------------------------
+
+class AdamW:
+    """AdamW over a list of tensors, one call per step (conv_adamw_step).
+
+    params: float32 master weights, updated in place; grads: float32 or bf16, all alike; m, v: moments,
+    float32, or with bits=8 int8 and uint8 codes, and then m_scale, v_scale, float32 of ceil(n/256).
+    Moments that are not given start at zero.  copies: bf16 tensors that receive the updated weights
+    (what the convolutions read), or None.  weight_decay: a number, or one for each tensor.  steps: how
+    many were taken before.  The tensors are kept and their addresses laid out once; step() may be
+    given other gradients of the same sizes."""
+
+    def __init__(self, params, grads, m=None, v=None, copies=None, bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.0, seed=0, steps=0, m_scale=None, v_scale=None, grad_scale=None):
+        torch = _torch()
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        n = len(params)
+        decays = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
+
+        def fresh(sizes, dtype):
+            return [torch.zeros(k, dtype=dtype, device=p.device) for k, p in zip(sizes, params)]
+
+        sizes, blocks = [p.numel() for p in params], [-(-p.numel() // 256) for p in params]
+        kinds = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+        self.params, self.copies, self.bits = list(params), copies, bits
+        self.m = list(m) if m is not None else fresh(sizes, kinds[0])
+        self.v = list(v) if v is not None else fresh(sizes, kinds[1])
+        self.m_scale = self.v_scale = None
+        if bits == 8:
+            self.m_scale = list(m_scale) if m_scale is not None else fresh(blocks, torch.float32)
+            self.v_scale = list(v_scale) if v_scale is not None else fresh(blocks, torch.float32)
+        self.steps, self.lr, self.betas, self.eps, self.seed = int(steps), lr, betas, eps, seed
+        for name, got in (("m", self.m), ("v", self.v), ("copies", copies), ("weight_decay", decays),
+                          ("m_scale", self.m_scale), ("v_scale", self.v_scale)):
+            if got is not None and len(got) != n:
+                raise ValueError("%s: %d entries for %d tensors" % (name, len(got), n))
+
+        def addr(t, size, dtypes, name):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("%s must be contiguous GPU tensors" % name)
+            if t.dtype not in dtypes:
+                raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+            if t.numel() != size:
+                raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), size))
+            return t.data_ptr()
+
+        half = (torch.bfloat16, torch.int16, torch.uint16)
+        f32 = (torch.float32,)
+        self._addr, self._half = addr, half
+        self._table = (AdamwTensor * max(n, 1))()
+        for i, e in enumerate(self._table[:n]):
+            e.n, e.weight_decay = sizes[i], decays[i]
+            e.p = addr(params[i], sizes[i], f32, "params")
+            e.m = addr(self.m[i], sizes[i], (kinds[0],), "m")
+            e.v = addr(self.v[i], sizes[i], (kinds[1],), "v")
+            if bits == 8:
+                e.m_scale = addr(self.m_scale[i], blocks[i], f32, "m_scale")
+                e.v_scale = addr(self.v_scale[i], blocks[i], f32, "v_scale")
+            if copies is not None and copies[i] is not None:
+                e.copy = addr(copies[i], sizes[i], half, "copies")
+        if grad_scale is not None:
+            addr(grad_scale, 1, f32, "grad_scale")
+        self.grad_scale = grad_scale
+        self._opt = AdamwOptions(bits=bits, grad_scale=None if grad_scale is None else grad_scale.data_ptr())
+        self._set_grads(grads)
+
+    def _set_grads(self, grads):
+        torch = _torch()
+        if len(grads) != len(self.params):
+            raise ValueError("grads: %d entries for %d tensors" % (len(grads), len(self.params)))
+        self.grads = list(grads)
+        kind = self.grads[0].dtype if self.grads else torch.float32
+        self._opt.grad_dtype = 0 if kind == torch.float32 else 1
+        kinds = (torch.float32,) if kind == torch.float32 else self._half
+        for e, g, p in zip(self._table, self.grads, self.params):
+            e.g = self._addr(g, p.numel(), kinds, "grads")
+
+    def step(self, grads=None):
+        """One step; lr and seed may be set between steps."""
+        if grads is not None:
+            self._set_grads(grads)
+        o = self._opt
+        o.lr, (o.beta1, o.beta2), o.eps, o.seed, o.step = self.lr, self.betas, self.eps, self.seed, self.steps + 1
+        _run(conv_adamw_step(o, self._table, len(self.params), _stream()), "conv_adamw_step")
+        self.steps += 1
+
+    def state_values(self, out=None):
+        """The moments as float32, (list of m, list of v): with bits=8 the values their codes stand for
+        (conv_adamw_state_values), written to `out`, two such lists, when given."""
+        torch = _torch()
+        if self.bits == 32:
+            if out is not None:
+                for to, t in zip(list(out[0]) + list(out[1]), self.m + self.v):
+                    to.copy_(t)
+                return out
+            return [t.clone() for t in self.m], [t.clone() for t in self.v]
+        if out is None:
+            out = tuple([torch.empty(p.numel(), dtype=torch.float32, device=p.device) for p in self.params]
+                        for _ in range(2))
+        n = len(self.params)
+        ptrs = []
+        for side in out:
+            if len(side) != n:
+                raise ValueError("out: %d entries for %d tensors" % (len(side), n))
+            ptrs.append((ctypes.c_void_p * max(n, 1))(*[self._addr(t, p.numel(), (torch.float32,), "out")
+                                                        for t, p in zip(side, self.params)]))
+        _run(conv_adamw_state_values(self._table, n, ptrs[0], ptrs[1], _stream()), "conv_adamw_state_values")
+        return out

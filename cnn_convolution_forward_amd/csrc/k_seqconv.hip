@@ -1,0 +1,428 @@
+// k_seqconv.hip -- the causal depthwise convolution over tokens: forward,
+// backward and the single-token step (conv_causal_*).
+//
+// p[t][c] = bias[c] + sum_j w[c][j] X[t-K+1+j][c]: K multiply-adds for two
+// elements moved, so HBM is the bound (each row read once and written once;
+// the backward pass reads x and dy and writes dx).  A thread owns VEC adjacent
+// channels and walks a run of consecutive tokens with the last K rows in
+// registers, so a row is loaded once per run plus K-1 rows in front of it
+// (which the neighbouring run has just read: cache hits).  The row window is
+// indexed by token modulo K with the loop unrolled K times, so that no
+// register is ever moved.
+//
+// Threads of a workgroup lie along the channels first (wide, contiguous
+// loads), then along runs of tokens.
+#include <initializer_list>
+
+#include "seq_common.h"
+namespace convfwd {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Row t of X (t may be negative: the carried rows), VEC channels at c.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void x_row(const T *x, int64_t ldx, const T *state, int64_t first, int b, int C, int c,
+                                      int t, float (&f)[VEC]) {
+    if (t >= 0) {
+        load_f32<T, VEC>(x + (first + t) * ldx + c, f);
+    } else if (K > 1 && state) {
+        load_f32<T, VEC>(state + ((int64_t)b * (K - 1) + (K - 1 + t)) * C + c, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+    }
+}
+
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void load_w(const T *w, int c, float (&wf)[K][VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            float f[1];
+            load_f32<T, 1>(w + (int64_t)(c + i) * K + j, f);
+            wf[j][i] = f[0];
+        }
+}
+
+// The last K-1 rows of X, the state after a sequence of `len` tokens.
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void write_state(const T *x, int64_t ldx, const T *state, T *out, int64_t first, int len,
+                                            int b, int C, int c) {
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        float f[VEC];
+        x_row<T, VEC, K>(x, ldx, state, first, b, C, c, len - (K - 1) + i, f);
+        store_f32(out + ((int64_t)b * (K - 1) + i) * C + c, f);
+    }
+}
+
+// grid (runs of tokens of all sequences, channel blocks); run = by * TL tokens
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__restrict__ x, int64_t ldx,
+                                                              const T *__restrict__ w, const float *__restrict__ bias,
+                                                              const T *__restrict__ state, T *__restrict__ y,
+                                                              int64_t ldy, T *__restrict__ state_out, int nblk,
+                                                              int bx_log2, int tl) {
+    const int b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    const int tx = threadIdx.x & ((1 << bx_log2) - 1), ty = threadIdx.x >> bx_log2;
+    const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
+    if (c >= s.C) return;
+    int64_t first;
+    int len;
+    seq_range(s, b, first, len);
+    if (K > 1 && state_out && blk == 0 && ty == 0) write_state<T, VEC, K>(x, ldx, state, state_out, first, len, b, s.C, c);
+    const int t0 = (blk * (kThreads >> bx_log2) + ty) * tl, t1 = min(t0 + tl, len);
+    if (t0 >= t1) return;
+    float wf[K][VEC], bf[VEC], win[K][VEC];
+    load_w<T, VEC, K>(w, c, wf);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) x_row<T, VEC, K>(x, ldx, state, first, b, s.C, c, t0 - (K - 1) + j, win[j]);
+    const T *xp = x + (first + t0) * ldx + c;
+    T *yp = y + (first + t0) * ldy + c;
+    // at step u (mod K) the new row goes to slot (K-1+u) % K; tap j is slot (u+j) % K
+    for (int t = t0; t < t1; t += K) {
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+            if (t + u < t1) {
+                load_f32<T, VEC>(xp, win[(K - 1 + u) % K]);
+                float p[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    p[i] = bf[i];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) p[i] = fmaf(wf[j][i], win[(u + j) % K][i], p[i]);
+                    if (SILU) p[i] *= sigmoid(p[i]);
+                }
+                store_f32(yp, p);
+                xp += ldx;
+                yp += ldy;
+            }
+        }
+    }
+}
+
+// Backward.  Walking t forward, dp[t] comes from dy[t] and the recomputed p[t];
+// row o = t-(K-1) of dX then has all its K terms dp[o..o+K-1].  A run takes
+// dw and db from its own tokens and computes the dp of K-1 tokens behind it
+// again.  The first run of a sequence also emits rows o < 0, the gradient of
+// the carried rows.  Partial sums of dw and db: one row of (K+1) x C floats per
+// workgroup, reduced over its runs in LDS in a fixed order, then added over
+// workgroups in a fixed order by causal_reduce_kernel.
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__restrict__ x, int64_t ldx,
+                                                              const T *__restrict__ w, const float *__restrict__ bias,
+                                                              const T *__restrict__ state, const T *__restrict__ dy,
+                                                              int64_t lddy, T *__restrict__ dx, int64_t lddx,
+                                                              T *__restrict__ dstate, float *__restrict__ part,
+                                                              int nblk, int bx_log2, int tl) {
+    __shared__ float red[kThreads * VEC];
+    const int b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    const int bx = 1 << bx_log2, by = kThreads >> bx_log2;
+    const int tx = threadIdx.x & (bx - 1), ty = threadIdx.x >> bx_log2;
+    const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
+    int64_t first;
+    int len;
+    seq_range(s, b, first, len);
+    const int t0 = (blk * by + ty) * tl, t1 = min(t0 + tl, len);
+    float dw[K][VEC] = {}, db[VEC] = {};
+    const bool head = t0 == 0 && K > 1 && dstate;
+    if (c < s.C && (t0 < t1 || head)) {
+        float wf[K][VEC], bf[VEC], win[K][VEC], dp[K][VEC];
+        load_w<T, VEC, K>(w, c, wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dp[j][i] = 0.f;
+        if (t0 < t1) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) x_row<T, VEC, K>(x, ldx, state, first, b, s.C, c, t0 - (K - 1) + j, win[j]);
+        }
+        const int end = t1 + K - 1;                    // dX rows up to t1 - 1
+        for (int t = t0; t < end; t += K) {
+#pragma unroll
+            for (int u = 0; u < K; ++u) {
+                const int tt = t + u;
+                if (tt < end) {
+                    float(&d)[VEC] = dp[(K - 1 + u) % K];
+                    if (tt < len) {
+                        load_f32<T, VEC>(x + (first + tt) * ldx + c, win[(K - 1 + u) % K]);
+                        load_f32<T, VEC>(dy + (first + tt) * lddy + c, d);
+                        if (SILU) {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) {
+                                float p = bf[i];
+#pragma unroll
+                                for (int j = 0; j < K; ++j) p = fmaf(wf[j][i], win[(u + j) % K][i], p);
+                                const float sg = sigmoid(p);
+                                d[i] *= sg * fmaf(p, 1.f - sg, 1.f);
+                            }
+                        }
+                        if (tt < t1) {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) {
+                                db[i] += d[i];
+#pragma unroll
+                                for (int j = 0; j < K; ++j) dw[j][i] = fmaf(d[i], win[(u + j) % K][i], dw[j][i]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) d[i] = 0.f;
+                    }
+                    // dX[o] = sum_j w[j] dp[o+K-1-j], o = tt-K+1: dp[tt-j] is in slot (K-1+u-j) % K
+                    const int o = tt - (K - 1);
+                    float g[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        g[i] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
+                    }
+                    if (o >= t0)
+                        store_f32(dx + (first + o) * lddx + c, g);
+                    else if (head)
+                        store_f32(dstate + ((int64_t)b * (K - 1) + tt) * s.C + c, g);
+                }
+            }
+        }
+    }
+    for (int j = 0; j <= K; ++j) {
+        if (j) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            float v = db[i];
+#pragma unroll
+            for (int q = 0; q < K; ++q) v = j == q ? dw[q][i] : v;
+            red[(ty * VEC + i) * bx + tx] = v;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < bx * VEC; e += kThreads) {
+            float v = 0.f;
+            for (int r = 0; r < by; ++r) v += red[(r * VEC + (e & (VEC - 1))) * bx + e / VEC];
+            const int cc = (blockIdx.y << bx_log2) * VEC + e;
+            if (cc < s.C) part[((int64_t)blockIdx.x * (K + 1) + j) * s.C + cc] = v;
+        }
+    }
+}
+
+// dw (C, K) and db from the workgroups' partial sums: 64 channels and one of
+// the K+1 rows per workgroup, four strands of partials added in order.
+__global__ __launch_bounds__(kThreads) void causal_reduce_kernel(const float *__restrict__ part, int64_t n, int C, int K,
+                                                                 float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float red[4][64];
+    const int cl = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + cl, j = blockIdx.y;
+    float v = 0.f;
+    if (c < C)
+        for (int64_t i = q; i < n; i += 4) v += part[(i * (K + 1) + j) * C + c];
+    red[q][cl] = v;
+    __syncthreads();
+    if (q == 0 && c < C) {
+        v = (red[0][cl] + red[1][cl]) + (red[2][cl] + red[3][cl]);
+        if (j < K)
+            dw[(int64_t)c * K + j] = v;
+        else if (db)
+            db[c] = v;
+    }
+}
+
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void causal_step_kernel(int B, int C, const T *__restrict__ x, int64_t ldx,
+                                                               const T *__restrict__ w, const float *__restrict__ bias,
+                                                               T *__restrict__ state, T *__restrict__ y, int64_t ldy) {
+    const int per = C / VEC;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (int64_t)B * per) return;
+    const int b = (int)(i / per), c = (int)(i % per) * VEC;
+    float wf[K][VEC], p[VEC], row[VEC];
+    load_w<T, VEC, K>(w, c, wf);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) p[v] = bias ? bias[c + v] : 0.f;
+    T *sp = state + (int64_t)b * (K - 1) * C + c;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (j < K - 1)
+            load_f32<T, VEC>(sp + (int64_t)j * C, row);
+        else
+            load_f32<T, VEC>(x + b * ldx + c, row);
+        if (j > 0) store_f32(sp + (int64_t)(j - 1) * C, row);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) p[v] = fmaf(wf[j][v], row[v], p[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        if (SILU) p[v] *= sigmoid(p[v]);
+    store_f32(y + b * ldy + c, p);
+}
+
+// Whether VEC channels at a time stay aligned and within a row.
+bool wide(int vec, int esize, int C, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds) {
+    if (C % vec) return false;
+    for (const void *p : ptrs)
+        if ((uintptr_t)p % (vec * esize)) return false;
+    for (int64_t ld : lds)
+        if (ld % vec) return false;
+    return true;
+}
+
+// Channel threads of a workgroup: the power of two that covers the channels,
+// 8 to 64.
+int channel_log2(int groups) {
+    int l = 3;
+    while (l < 6 && (1 << l) < groups) ++l;
+    return l;
+}
+
+struct Tiling {
+    int bx_log2, tl, nblk, cblk;
+};
+
+Tiling tiling(const Seq &s, int vec, int tl) {
+    Tiling t;
+    t.bx_log2 = channel_log2((s.C + vec - 1) / vec);
+    t.tl = tl;
+    const int run = (kThreads >> t.bx_log2) * tl;
+    t.nblk = s.T > 0 ? (int)(((int64_t)s.T + run - 1) / run) : 1;
+    t.cblk = (s.C + (vec << t.bx_log2) - 1) / (vec << t.bx_log2);
+    return t;
+}
+
+constexpr int kFwdTokens = 32, kBwdTokens = 32;
+
+template <typename T, int VEC, int K, bool SILU>
+void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, T *y, int64_t ldy,
+         T *state_out, hipStream_t st) {
+    const Tiling t = tiling(s, VEC, kFwdTokens);
+    causal_fwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)(s.B * (int64_t)t.nblk), t.cblk), kThreads, 0, st>>>(
+        s, x, ldx, w, bias, state, y, ldy, state_out, t.nblk, t.bx_log2, t.tl);
+}
+
+template <typename T, int VEC, int K, bool SILU>
+void bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
+         T *dx, int64_t lddx, float *dw, float *db, T *dstate, float *part, hipStream_t st) {
+    const Tiling t = tiling(s, VEC, kBwdTokens);
+    const int64_t n = s.B * (int64_t)t.nblk;
+    causal_bwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)n, t.cblk), kThreads, 0, st>>>(
+        s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.nblk, t.bx_log2, t.tl);
+    causal_reduce_kernel<<<dim3((s.C + 63) / 64, K + 1), kThreads, 0, st>>>(part, n, s.C, K, dw, db);
+}
+
+template <typename T, int VEC, int K, bool SILU>
+void step(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, T *state, T *y, int64_t ldy,
+          hipStream_t st) {
+    const int64_t n = (int64_t)s.B * (s.C / VEC);
+    causal_step_kernel<T, VEC, K, SILU><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(
+        s.B, s.C, x, ldx, w, bias, state, y, ldy);
+}
+
+// K and silu as template arguments.
+#define SEQCONV_CASES(CALL)                                                                            \
+    switch (K) {                                                                                       \
+        case 1: if (silu) CALL(1, true); else CALL(1, false); break;                                   \
+        case 2: if (silu) CALL(2, true); else CALL(2, false); break;                                   \
+        case 3: if (silu) CALL(3, true); else CALL(3, false); break;                                   \
+        case 4: if (silu) CALL(4, true); else CALL(4, false); break;                                   \
+        case 5: if (silu) CALL(5, true); else CALL(5, false); break;                                   \
+        case 6: if (silu) CALL(6, true); else CALL(6, false); break;                                   \
+        case 7: if (silu) CALL(7, true); else CALL(7, false); break;                                   \
+        default: if (silu) CALL(8, true); else CALL(8, false); break;                                  \
+    }
+
+template <typename T, int VEC>
+void fwd_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, T *y,
+           int64_t ldy, T *so, hipStream_t st) {
+#define CALL(KK, S) fwd<T, VEC, KK, S>(s, x, ldx, w, bias, state, y, ldy, so, st)
+    SEQCONV_CASES(CALL)
+#undef CALL
+}
+
+template <typename T, int VEC>
+void bwd_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, const float *bias, const T *state,
+           const T *dy, int64_t lddy, T *dx, int64_t lddx, float *dw, float *db, T *ds, float *part, hipStream_t st) {
+#define CALL(KK, S) bwd<T, VEC, KK, S>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dw, db, ds, part, st)
+    SEQCONV_CASES(CALL)
+#undef CALL
+}
+
+template <typename T, int VEC>
+void step_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, const float *bias, T *state, T *y,
+            int64_t ldy, hipStream_t st) {
+#define CALL(KK, S) step<T, VEC, KK, S>(s, x, ldx, w, bias, state, y, ldy, st)
+    SEQCONV_CASES(CALL)
+#undef CALL
+}
+
+}  // namespace
+
+int64_t causal_bwd_workspace_floats(const Seq &s, int K) {
+    // the narrowest unit needs the most workgroups along the tokens per channel block
+    int64_t n = 0;
+    for (int vec : {1, 4}) {
+        const Tiling t = tiling(s, vec, kBwdTokens);
+        if (s.B * (int64_t)t.nblk > n) n = s.B * (int64_t)t.nblk;
+    }
+    return n * (K + 1) * s.C;
+}
+
+hipError_t launch_causal_fwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
+                             const float *bias, const void *state, void *y, int64_t ldy, void *so, hipStream_t st) {
+    if (bf16) {
+        typedef uint16_t T;
+        if (wide(8, 2, s.C, {x, state, y, so}, {ldx, ldy}))
+            fwd_k<T, 8>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
+        else
+            fwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
+    } else {
+        typedef float T;
+        if (wide(4, 4, s.C, {x, state, y, so}, {ldx, ldy}))
+            fwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
+        else
+            fwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_causal_bwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
+                             const float *bias, const void *state, const void *dy, int64_t lddy, void *dx, int64_t lddx,
+                             float *dw, float *db, void *ds, float *part, hipStream_t st) {
+    if (bf16) {
+        typedef uint16_t T;
+        if (wide(4, 2, s.C, {x, state, dy, dx, ds}, {ldx, lddy, lddx}))
+            bwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
+                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
+        else
+            bwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
+                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
+    } else {
+        typedef float T;
+        if (wide(4, 4, s.C, {x, state, dy, dx, ds}, {ldx, lddy, lddx}))
+            bwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
+                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
+        else
+            bwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
+                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_causal_step(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
+                              const float *bias, void *state, void *y, int64_t ldy, hipStream_t st) {
+    if (bf16) {
+        typedef uint16_t T;
+        if (wide(2, 2, s.C, {x, state, y}, {ldx, ldy}))
+            step_k<T, 2>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
+        else
+            step_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
+    } else {
+        typedef float T;
+        step_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace convfwd

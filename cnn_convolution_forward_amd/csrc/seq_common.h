@@ -1,0 +1,102 @@
+// seq_common.h -- what the kernels over sequences of tokens share: where a
+// sequence's rows are, and loads and stores of VEC adjacent channels.
+#pragma once
+
+#include "seq_internal.h"
+
+namespace convfwd {
+
+// First row and length of sequence b.  Offsets come from device memory that
+// the host has not seen, so they are clamped here: every row read or written
+// is one of the tensor's.
+__device__ __forceinline__ void seq_range(const Seq &s, int b, int64_t &first, int &len) {
+    if (!s.off) {
+        first = (int64_t)b * s.T;
+        len = s.T;
+        return;
+    }
+    const int64_t o0 = min(max((int64_t)s.off[b], (int64_t)0), s.rows);
+    const int64_t o1 = min(max((int64_t)s.off[b + 1], o0), s.rows);
+    first = o0;
+    len = (int)min(o1 - o0, (int64_t)s.T);
+}
+
+// VEC adjacent channels as fp32.  T is uint16_t (bf16 bits) or float; the
+// address is aligned to VEC elements.
+template <typename T, int VEC> struct Pack;
+template <> struct Pack<uint16_t, 1> { typedef uint16_t type; };
+template <> struct Pack<uint16_t, 2> { typedef uint32_t type; };
+template <> struct Pack<uint16_t, 4> { typedef uint2 type; };
+template <> struct Pack<uint16_t, 8> { typedef uint4 type; };
+template <> struct Pack<float, 1> { typedef float type; };
+template <> struct Pack<float, 2> { typedef float2 type; };
+template <> struct Pack<float, 4> { typedef float4 type; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ typename Pack<T, VEC>::type load_pack(const T *p) {
+    return *reinterpret_cast<const typename Pack<T, VEC>::type *>(p);
+}
+
+// bf16 bits to fp32 is a shift; fp32 to bf16 rounds to nearest even (a NaN
+// stays a NaN) with the conversion instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+template <int VEC> __device__ __forceinline__ void unpack(const uint32_t *u, float *f) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void to_f32(uint16_t v, float (&f)[1]) { f[0] = __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ void to_f32(uint32_t v, float (&f)[2]) { unpack<2>(&v, f); }
+__device__ __forceinline__ void to_f32(uint2 v, float (&f)[4]) {
+    const uint32_t u[2] = {v.x, v.y};
+    unpack<4>(u, f);
+}
+__device__ __forceinline__ void to_f32(uint4 v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    unpack<8>(u, f);
+}
+__device__ __forceinline__ void to_f32(float v, float (&f)[1]) { f[0] = v; }
+__device__ __forceinline__ void to_f32(float2 v, float (&f)[2]) { f[0] = v.x, f[1] = v.y; }
+__device__ __forceinline__ void to_f32(float4 v, float (&f)[4]) { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
+
+template <typename T, int VEC> __device__ __forceinline__ void load_f32(const T *p, float (&f)[VEC]) {
+    to_f32(load_pack<T, VEC>(p), f);
+}
+
+__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[1]) { *p = to_bf16(f[0]); }
+__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[2]) {
+    *reinterpret_cast<uint32_t *>(p) = pack_bf16(f[0], f[1]);
+}
+__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+}
+__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                               pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+__device__ __forceinline__ void store_f32(float *p, const float (&f)[1]) { *p = f[0]; }
+__device__ __forceinline__ void store_f32(float *p, const float (&f)[2]) {
+    *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+}
+__device__ __forceinline__ void store_f32(float *p, const float (&f)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 1/(1 + exp(-v)): 0 where that is no normal number (the reciprocal flushes, exp(-v) = inf
+// gives 0); NaN stays NaN.
+__device__ __forceinline__ float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * v));
+}
+
+}  // namespace convfwd

@@ -404,6 +404,191 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
                                             float *dw, float *db, void *workspace, size_t workspace_bytes,
                                             void *stream);
 
+/* ---- sequences of tokens ---------------------------------------------------
+ *
+ * The operators below run along a sequence: row t holds the C channels of
+ * token t, the channel index fastest (the channels-last order of
+ * CONV_LAYOUT_NHWC with H = 1, so a pointwise convolution over tokens produces
+ * and consumes these rows).  Sequence b of a batch is rows [b*T, (b+1)*T), or,
+ * with `offsets`, rows [offsets[b], offsets[b+1]) of one packed tensor: odd,
+ * single-token and empty sequences in any mixture.  What one sequence computes
+ * never depends on another's rows.
+ *
+ * Strides.  Unlike the tensors above, rows may be strided: `ld*` is the number
+ * of elements from one row to the next, >= C (C when dense), so that a slice
+ * of a fused projection is read, or written, in place.  Channels of a row are
+ * adjacent.  Row offsets are 64-bit: a tensor may hold more than 2^31 elements
+ * (rows stay below 2^30).  All other arrays are dense.
+ *
+ * Types.  x, gates, y, their gradients and the convolution's weights and state
+ * are `dtype` (CONV_OUT_BF16: raw bf16 bits; CONV_OUT_F32); bias, decay, the
+ * recurrent state and the gradients of parameters are fp32.  Arithmetic, sums
+ * and the recurrence are fp32; bf16 results are rounded once, to nearest even.
+ * Infinities and NaN follow IEEE rules within their own sequence and channel.
+ *
+ * Memory, streams and errors are as above: CONV_ERR_NULL for a NULL required
+ * pointer (tensors of zero rows may be NULL), CONV_ERR_PARAM for B < 1, T < 0,
+ * C < 1, an unknown dtype, ld < C, a pointer not aligned to its element or a
+ * bad option, CONV_ERR_OVERFLOW for 2^30 or more rows, more than 2^20 channels,
+ * B*C of 2^31 or more, or B * (T/64 + 1) above 2^23, CONV_ERR_WORKSPACE for a
+ * workspace that is needed and missing, too small or not 16-byte aligned,
+ * CONV_ERR_ALIAS when an output overlaps an input, another output or the
+ * workspace (interleaved column slices of one buffer do not overlap).
+ * `offsets` are read on the device only: values outside [0, tokens], or
+ * decreasing, are clamped, and rows of a sequence past T tokens are ignored.
+ * Results are bitwise reproducible. */
+typedef struct {
+    int dtype;               /* CONV_OUT_F32 or CONV_OUT_BF16                               */
+    int B;                   /* sequences                                                   */
+    int T;                   /* tokens in each; with offsets, in the longest (0 is allowed)  */
+    int C;                   /* channels                                                    */
+    const int32_t *offsets;  /* NULL, or B+1 first rows, ascending, on the device           */
+    int64_t tokens;          /* rows of a packed tensor; ignored when offsets is NULL       */
+} conv_seq_t;
+
+/* Causal depthwise convolution over the tokens of each sequence, 1 <= K <= 8:
+ *
+ *     p[t][c] = bias[c] + sum_{j<K} w[c][j] * X[t-K+1+j][c]
+ *     y = p, or p * sigmoid(p) with silu = 1
+ *
+ * X is x preceded by the carried rows: X[-i] = state[b][K-1-i], i = 1..K-1
+ * (zeros when state is NULL).  w is (C, K), tap K-1 on the token itself; bias
+ * (C) may be NULL; state and state_out are (B, K-1, C), oldest row first.
+ * state_out (NULL: not wanted) receives the last K-1 rows of X, the state
+ * with which the next tokens continue. */
+CONV_API conv_status_t conv_causal_fwd(const conv_seq_t *seq, int K, int silu, const void *x, int64_t ldx,
+                                       const void *w, const float *bias, const void *state, void *y, int64_t ldy,
+                                       void *state_out, void *stream);
+
+/* Device workspace of conv_causal_bwd (partial sums of dw and db over ranges
+ * of tokens); 0 on invalid arguments. */
+CONV_API size_t conv_causal_bwd_workspace_bytes(const conv_seq_t *seq, int K);
+
+/* Gradients for upstream dy (of y): dx, dw (C, K) and db (C) in fp32, and
+ * dstate (B, K-1, C) of the carried rows.  db and dstate may be NULL.  The
+ * pre-activation p is recomputed from x.  With dp = dy * dy/dp:
+ *     dX[t] = sum_j w[j] dp[t+K-1-j],  dw[j] = sum_t dp[t] X[t-K+1+j],  db = sum_t dp[t] */
+CONV_API conv_status_t conv_causal_bwd(const conv_seq_t *seq, int K, int silu, const void *x, int64_t ldx,
+                                       const void *w, const float *bias, const void *state, const void *dy,
+                                       int64_t lddy, void *dx, int64_t lddx, float *dw, float *db, void *dstate,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* One new token for each of B sequences: x and y are (B, C) rows, and state
+ * (B, K-1, C) is read, shifted by one row and extended by x in place.
+ * seq->T, offsets and tokens are not read. */
+CONV_API conv_status_t conv_causal_step(const conv_seq_t *seq, int K, int silu, const void *x, int64_t ldx,
+                                        const void *w, const float *bias, void *state, void *y, int64_t ldy,
+                                        void *stream);
+
+/* Gated linear recurrence.  Per token and channel, with the gates' inputs
+ * gate and inp and the parameter decay (C):
+ *
+ *     r = sigmoid(gate),  s = sigmoid(inp),  k = scale * log(1 + exp(decay))
+ *     a = exp(-k r),      h[t] = a h[t-1] + sqrt(1 - a^2) s x,      y = h
+ *
+ * A sigmoid below 2^-126, the smallest normal fp32 (an argument under about
+ * -87.3), counts as 0: a gate that far down is shut.
+ * h before a sequence's first token is h0 (B, C), or 0 when NULL; hT (B, C),
+ * when not NULL, receives h after its last token (h0 for an empty one).
+ * states, when not NULL, receives what conv_scan_bwd starts from: h before
+ * tokens 0, 64, 128, ... of each sequence, (B, ceil(T/64), C) fp32; entries
+ * past a sequence's end are not written.  scale: finite, >= 0. */
+#define CONV_SCAN_BLOCK 64
+
+/* Device workspace of conv_scan_fwd; 0 when none is needed, or on invalid
+ * arguments.  Overwritten by each call; two calls in flight must not share it. */
+CONV_API size_t conv_scan_fwd_workspace_bytes(const conv_seq_t *seq);
+
+CONV_API conv_status_t conv_scan_fwd(const conv_seq_t *seq, float scale, const void *x, int64_t ldx,
+                                     const void *gate, int64_t ldg, const void *inp, int64_t ldi,
+                                     const float *decay, const float *h0, void *y, int64_t ldy, float *hT,
+                                     float *states, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace of conv_scan_bwd; 0 on invalid arguments. */
+CONV_API size_t conv_scan_bwd_workspace_bytes(const conv_seq_t *seq);
+
+/* Gradients for upstream dy (of y) and dhT (of hT; NULL: zero): dx, dgate,
+ * dinp; ddecay (C) fp32; dh0 (B, C) fp32, or NULL.  h is recomputed in fp32 from
+ * states, as conv_scan_fwd saved them for the same inputs.  With dh the total
+ * gradient of h and la = log a:
+ *     dh[t] = dy[t] + a[t+1] dh[t+1]           (dhT instead of the last term at the end)
+ *     dx = dh sqrt(1-a^2) s,   dinp = dh sqrt(1-a^2) x s (1-s)
+ *     dla = dh (a h[t-1] - s x a^2 / sqrt(1-a^2)),   dgate = -k dla r (1-r)
+ *     ddecay = -scale sigmoid(decay) sum_t r dla,    dh0 = a[0] dh[0] */
+CONV_API conv_status_t conv_scan_bwd(const conv_seq_t *seq, float scale, const void *x, int64_t ldx,
+                                     const void *gate, int64_t ldg, const void *inp, int64_t ldi,
+                                     const float *decay, const float *states, const void *dy, int64_t lddy,
+                                     const float *dhT, void *dx, int64_t lddx, void *dgate, int64_t lddg,
+                                     void *dinp, int64_t lddi, float *ddecay, float *dh0, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* One new token for each of B sequences: x, gate, inp and y are (B, C) rows;
+ * h (B, C) is updated in place.  seq->T, offsets and tokens are not read. */
+CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const void *x, int64_t ldx,
+                                      const void *gate, int64_t ldg, const void *inp, int64_t ldi,
+                                      const float *decay, float *h, void *y, int64_t ldy, void *stream);
+
+/* ---- the optimiser step --------------------------------------------------
+ *
+ * AdamW over `count` tensors at once, from the fp32 (or bf16) gradients that
+ * conv_bwd_weight_bf16, conv_causal_bwd and conv_scan_bwd write to the bf16
+ * weights that the next forward pass reads.  With c1 = 1 - beta1^step and
+ * c2 = 1 - beta2^step (step: this one's number, from 1):
+ *
+ *     g = grad * *grad_scale                   (grad_scale: device scalar, NULL = 1)
+ *     m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - (lr/c1) m / (sqrt(v)/sqrt(c2) + eps)
+ *     copy = bf16(p)                           (copy: NULL = none)
+ *
+ * bits = 32: m and v are fp32.  bits = 8: m is int8 and v uint8 codes q in
+ * blocks of 256 elements (counted from the tensor's first), each block with an
+ * fp32 scale, its largest |m| (largest v):
+ *     m = scale * sign(q) (q/127)^2,   v = scale * (q/255)^4
+ * m_scale and v_scale hold ceil(n/256) floats; all-zero codes and scales are
+ * the zero state.  A new value lies between two codes and takes the upper one
+ * with the probability with which that makes it right on average: rounding to
+ * the nearest would leave v where it is, as one step changes it by less than a
+ * code.  The random bits depend on seed, step, the tensor's place in the list
+ * and the element only, so a step is reproducible.  v > 0 never takes code 0.
+ * A block whose largest value is below 2^-126 is stored as zeros.  A
+ * non-finite gradient makes its element (bits = 8: its block's scales) non-finite.
+ *
+ * `tensors` is a HOST array, read before the call returns (its pointers are
+ * device pointers).  Every tensor: n >= 0; n = 0 is skipped.  Errors:
+ * CONV_ERR_NULL for a NULL array, p, g, m or v (bits = 8: scale), CONV_ERR_PARAM for
+ * count < 0, n < 0, step < 1, betas outside [0, 1), lr, eps or weight_decay
+ * negative or not finite, bits other than 32 or 8, an unknown grad_dtype, or a
+ * pointer not aligned to its element; CONV_ERR_OVERFLOW for n >= 2^31;
+ * CONV_ERR_ALIAS when what is written overlaps anything else of its tensor. */
+typedef struct {
+    int64_t n;            /* elements                                     */
+    float *p;             /* parameters, fp32, updated                    */
+    const void *g;        /* gradient, grad_dtype                         */
+    void *m, *v;          /* moments: fp32, or int8 / uint8 codes, updated */
+    float *m_scale;       /* bits = 8: scales of m and v, updated         */
+    float *v_scale;
+    uint16_t *copy;       /* bf16 copy of p, written, or NULL             */
+    float weight_decay;
+} conv_adamw_tensor_t;
+
+typedef struct {
+    double lr, beta1, beta2, eps;
+    int64_t step;             /* number of this step, from 1             */
+    int bits;                 /* 32 or 8                                 */
+    int grad_dtype;           /* CONV_OUT_F32 or CONV_OUT_BF16            */
+    uint32_t seed;            /* bits = 8: of the random rounding         */
+    const float *grad_scale;  /* device scalar, or NULL                  */
+} conv_adamw_t;
+
+CONV_API conv_status_t conv_adamw_step(const conv_adamw_t *opt, const conv_adamw_tensor_t *tensors, int count,
+                                       void *stream);
+
+/* The values that 8-bit moments stand for, fp32: m_out[i] and v_out[i] (HOST
+ * arrays of device pointers, n of tensors[i] elements each) receive tensor i's.
+ * Reads n, m, v and the scales of `tensors` only. */
+CONV_API conv_status_t conv_adamw_state_values(const conv_adamw_tensor_t *tensors, int count, float *const *m_out,
+                                               float *const *v_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
