@@ -18,7 +18,8 @@ using convfwd::Seq;
 namespace {
 
 constexpr int64_t kMaxRows = INT64_C(1) << 30;
-constexpr int64_t kMaxBlocks = INT64_C(1) << 23;       // 64-token blocks of all sequences: a grid dimension
+constexpr int64_t kMaxBlocks = INT64_C(1) << 23;       // 64-token blocks of all sequences, and these times
+                                                       // 64-channel blocks: grid dimensions
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxStateElems = INT64_C(2147483647);
 
@@ -76,7 +77,8 @@ conv_status_t make_seq(const conv_seq_t *q, bool step, Seq &s) {
     s.off = step ? nullptr : q->offsets;
     s.rows = s.off ? q->tokens : (int64_t)s.B * s.T;
     if (s.rows >= kMaxRows || s.T >= kMaxRows || s.C > kMaxChannels || (int64_t)s.B * s.C > kMaxStateElems ||
-        (int64_t)s.B * ((s.T + CONV_SCAN_BLOCK - 1) / CONV_SCAN_BLOCK + 1) > kMaxBlocks)
+        (int64_t)s.B * ((s.T + CONV_SCAN_BLOCK - 1) / CONV_SCAN_BLOCK + 1) > kMaxBlocks ||
+        (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) > kMaxBlocks)
         return CONV_ERR_OVERFLOW;
     return CONV_OK;
 }

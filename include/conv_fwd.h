@@ -430,12 +430,14 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * pointer (tensors of zero rows may be NULL), CONV_ERR_PARAM for B < 1, T < 0,
  * C < 1, an unknown dtype, ld < C, a pointer not aligned to its element or a
  * bad option, CONV_ERR_OVERFLOW for 2^30 or more rows, more than 2^20 channels,
- * B*C of 2^31 or more, or B * (T/64 + 1) above 2^23, CONV_ERR_WORKSPACE for a
- * workspace that is needed and missing, too small or not 16-byte aligned,
+ * B*C of 2^31 or more, or B * (T/64 + 1) or (rows/64 + B) * (C/64) above 2^23,
+ * CONV_ERR_WORKSPACE for a workspace that is needed and missing, too small or
+ * not 16-byte aligned,
  * CONV_ERR_ALIAS when an output overlaps an input, another output or the
  * workspace (interleaved column slices of one buffer do not overlap).
- * `offsets` are read on the device only: values outside [0, tokens], or
- * decreasing, are clamped, and rows of a sequence past T tokens are ignored.
+ * `offsets` are read on the device only: values outside [0, tokens] are clamped,
+ * rows of a sequence past T tokens are ignored, and where values descend,
+ * which rows are computed is unspecified (never any outside the tensors).
  * Results are bitwise reproducible. */
 typedef struct {
     int dtype;               /* CONV_OUT_F32 or CONV_OUT_BF16                               */
