@@ -36,20 +36,47 @@ __device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t i) {
     return z ^ (z >> 15);
 }
 
+// The tensor that a block belongs to: each lane looks at one entry (kMaxTensors <= 64), so this is
+// one load and not a chain of them.
 __device__ __forceinline__ const AdamwTensor &find(const Table &tb, uint32_t blk) {
-    int lo = 0, hi = tb.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tb.t[mid].first <= blk) lo = mid; else hi = mid - 1;
-    }
-    return tb.t[lo];
+    const int lane = threadIdx.x & 63;
+    const uint32_t first = tb.t[min(lane, tb.count - 1)].first;
+    const uint64_t on = __ballot(lane < tb.count && first <= blk);
+    return tb.t[63 - __builtin_clzll(on)];
 }
 
-template <bool BF16> __device__ __forceinline__ float grad_at(const void *g, int64_t i) {
-    float f[1];
-    if (BF16) to_f32(((const uint16_t *)g)[i], f);
-    else f[0] = ((const float *)g)[i];
-    return f[0];
+// Four adjacent elements at any element-aligned address: tensors may be slices
+// that start anywhere, and a load of 4 to 16 bytes need not be aligned.
+struct __attribute__((packed, aligned(4))) F4 { float f[4]; };
+struct __attribute__((packed, aligned(2))) H4 { uint16_t h[4]; };
+struct __attribute__((packed, aligned(1))) B4 { uint32_t b; };
+
+template <bool BF16> struct Grad { typedef F4 type; typedef float elem; };
+template <> struct Grad<true> { typedef H4 type; typedef uint16_t elem; };
+__device__ __forceinline__ float value(const F4 &g, int e) { return g.f[e]; }
+__device__ __forceinline__ float value(const H4 &g, int e) { return __uint_as_float((uint32_t)g.h[e] << 16); }
+
+// Elements i .. i+3 of p, or what there is of them (n: the tensor's length; FULL: all are there).
+template <bool FULL, typename V, typename E> __device__ __forceinline__ V load4(const E *p, int64_t i, int64_t n) {
+    if (FULL || i + 4 <= n) return *reinterpret_cast<const V *>(p + i);
+    V v = {};
+    E *o = reinterpret_cast<E *>(&v);
+    for (int e = 0; e < 3; ++e)
+        if (i + e < n) o[e] = p[i + e];
+    return v;
+}
+template <bool FULL, typename V, typename E> __device__ __forceinline__ void store4(E *p, int64_t i, int64_t n, const V &v) {
+    if (FULL || i + 4 <= n) {
+        *reinterpret_cast<V *>(p + i) = v;
+        return;
+    }
+    const E *o = reinterpret_cast<const E *>(&v);
+    for (int e = 0; e < 3; ++e)
+        if (i + e < n) p[i + e] = o[e];
+}
+__device__ __forceinline__ H4 to_copy(const F4 &p) {
+    const uint2 u = make_uint2(pack_bf16(p.f[0], p.f[1]), pack_bf16(p.f[2], p.f[3]));
+    return __builtin_bit_cast(H4, u);
 }
 
 // The new moments, each operation rounded by itself: the values that are
@@ -63,25 +90,46 @@ __device__ __forceinline__ void moments(const AdamwHyper &h, float g, float &m, 
     v = v1 + v2;
 }
 
+// The division and the root are the hardware's, good to a unit in the last place: their error is the
+// step's, about 1e-7 of a change that is itself a small part of p.
 __device__ __forceinline__ float update(const AdamwHyper &h, float keep, float p, float m, float v) {
-    return p * keep - h.lr_c1 * m / (sqrtf(v) * h.inv_sqrt_c2 + h.eps);
+    return p * keep - h.lr_c1 * m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v) * h.inv_sqrt_c2 + h.eps);
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void adamw32_kernel(Table tb) {
-    const AdamwTensor &t = find(tb, blockIdx.x);
+constexpr int kUnits = kChunk / (4 * kThreads);     // groups of four elements per thread, all loaded first
+
+template <bool BF16, bool FULL> __device__ __forceinline__ void adamw32_chunk(const Table &tb, const AdamwTensor &t) {
+    typedef typename Grad<BF16>::type G;
     const float gs = tb.h.grad_scale ? *tb.h.grad_scale : 1.f;
-    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk;
-    for (int e = threadIdx.x; e < kChunk; e += kThreads) {
-        const int64_t i = i0 + e;
-        if (i >= t.n) break;
-        float m = ((float *)t.m)[i], v = ((float *)t.v)[i];
-        moments(tb.h, grad_at<BF16>(t.g, i) * gs, m, v);
-        const float p = update(tb.h, t.keep, t.p[i], m, v);
-        ((float *)t.m)[i] = m;
-        ((float *)t.v)[i] = v;
-        t.p[i] = p;
-        if (t.copy) t.copy[i] = to_bf16(p);
+    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk + 4 * threadIdx.x, n = t.n;
+    float *const tp = t.p, *const tm = (float *)t.m, *const tv = (float *)t.v;
+    const auto *const tg = (const typename Grad<BF16>::elem *)t.g;
+    F4 p[kUnits], m[kUnits], v[kUnits];
+    G g[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t i = i0 + u * 4 * kThreads;
+        if (FULL || i < n) {
+            g[u] = load4<FULL, G>(tg, i, n);
+            m[u] = load4<FULL, F4>(tm, i, n);
+            v[u] = load4<FULL, F4>(tv, i, n);
+            p[u] = load4<FULL, F4>(tp, i, n);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t i = i0 + u * 4 * kThreads;
+        if (FULL || i < n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                moments(tb.h, value(g[u], e) * gs, m[u].f[e], v[u].f[e]);
+                p[u].f[e] = update(tb.h, t.keep, p[u].f[e], m[u].f[e], v[u].f[e]);
+            }
+            store4<FULL>(tm, i, n, m[u]);
+            store4<FULL>(tv, i, n, v[u]);
+            store4<FULL>(tp, i, n, p[u]);
+            if (t.copy) store4<FULL>(t.copy, i, n, to_copy(p[u]));
+        }
     }
 }
 
@@ -98,73 +146,102 @@ __device__ __forceinline__ float decode_v(float q, float s) {
 }
 
 // The code of x in [0, s]: the one below or the one above, the upper with
-// probability (x - below)/(above - below).
-template <bool SECOND> __device__ __forceinline__ float encode(float x, float s, float inv, uint32_t bits16) {
+// probability (x - below)/(above - below).  The root only finds the lower code:
+// where its last unit in the last place picks a neighbour, x is one of the two
+// codes and both lead to it.
+template <bool SECOND> __device__ __forceinline__ uint32_t encode(float x, float s, float inv, uint32_t bits16) {
 #pragma clang fp contract(off)
     const float top = SECOND ? 255.f : 127.f;
-    float root = sqrtf(x * inv);
-    if (SECOND) root = sqrtf(root);
+    float root = __builtin_amdgcn_sqrtf(x * inv);
+    if (SECOND) root = __builtin_amdgcn_sqrtf(root);
     const float low = fminf(floorf(root * top), top - 1.f);
     const float v0 = SECOND ? decode_v(low, s) : decode_m(low, s);
     const float v1 = SECOND ? decode_v(low + 1.f, s) : decode_m(low + 1.f, s);
     const float rnd = (float)bits16 * 0x1p-16f, d = v1 - v0, a = rnd * d, e = x - v0;
-    float q = low + (a < e ? 1.f : 0.f);
-    if (SECOND && q == 0.f && x > 0.f && s > 0.f) q = 1.f;
+    uint32_t q = (uint32_t)low + (a < e ? 1u : 0u);
+    if (SECOND && q == 0u && x > 0.f && s > 0.f) q = 1u;
     return q;
 }
 
-// The largest over a wave; NaN wins, so that it reaches the scale.
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-        const float u = __shfl_xor(v, o);
-        v = (u > v || u != u) ? u : v;
-    }
-    return v;
+// The largest of a wave's non-negative values, as their bits (which order alike; a NaN is above all and
+// so reaches the scale): four steps within rows of 16 lanes, then one value of each row.
+template <int CTRL> __device__ __forceinline__ uint32_t max_with(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_max(float f) {
+    uint32_t v = __float_as_uint(f);
+    v = max_with<0xb1>(v);      // lanes 1 0 3 2
+    v = max_with<0x4e>(v);      // lanes 2 3 0 1
+    v = max_with<0x141>(v);     // half rows mirrored
+    v = max_with<0x140>(v);     // rows mirrored
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+    return __uint_as_float(max(a, b));
+}
+__device__ __forceinline__ float larger(float f, float g) {
+    return __uint_as_float(max(__float_as_uint(f), __float_as_uint(g) & 0x7fffffffu));
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(Table tb) {
-    const AdamwTensor &t = find(tb, blockIdx.x);
+__device__ __forceinline__ float signed_code(uint32_t q, int e) { return (float)(int8_t)(q >> (8 * e)); }
+__device__ __forceinline__ float plain_code(uint32_t q, int e) { return (float)(uint8_t)(q >> (8 * e)); }
+
+constexpr int kBlocks = kChunk / kQ / (kThreads / 64);     // 8-bit blocks per wave, all loaded first
+
+template <bool BF16, bool FULL> __device__ __forceinline__ void adamw8_chunk(const Table &tb, const AdamwTensor &t) {
+    typedef typename Grad<BF16>::type G;
     const float gs = tb.h.grad_scale ? *tb.h.grad_scale : 1.f;
-    const int lane = threadIdx.x & 63;
-    for (int q = threadIdx.x >> 6; q < kChunk / kQ; q += kThreads / 64) {
-        const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk + q * kQ;
-        if (i0 >= t.n) break;
-        const int64_t blk = i0 / kQ;
-        const float ms = t.m_scale[blk], vs = t.v_scale[blk];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n = t.n, blk0 = (int64_t)(blockIdx.x - t.first) * (kChunk / kQ) + w * kBlocks;
+    float *const tp = t.p;
+    uint8_t *const tm = (uint8_t *)t.m, *const tv = (uint8_t *)t.v;
+    const auto *const tg = (const typename Grad<BF16>::elem *)t.g;
+    F4 p[kBlocks];
+    B4 qm[kBlocks], qv[kBlocks];
+    G g[kBlocks];
+    float ms[kBlocks], vs[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t i = (blk0 + u) * kQ + 4 * lane;
+        if (FULL || (blk0 + u) * kQ < n) {
+            ms[u] = t.m_scale[blk0 + u];
+            vs[u] = t.v_scale[blk0 + u];
+            g[u] = load4<FULL, G>(tg, i, n);
+            qm[u] = load4<FULL, B4>(tm, i, n);
+            qv[u] = load4<FULL, B4>(tv, i, n);
+            p[u] = load4<FULL, F4>(tp, i, n);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+        const int64_t blk = blk0 + u, i = blk * kQ + 4 * lane;
+        if (!FULL && blk * kQ >= n) break;
         float m[4], v[4], mmax = 0.f, vmax = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t i = i0 + 4 * lane + e;
-            m[e] = v[e] = 0.f;
-            if (i < t.n) {
-                const float qm = (float)((const int8_t *)t.m)[i], qv = (float)((const uint8_t *)t.v)[i];
-                m[e] = copysignf(decode_m(fabsf(qm), ms), qm);
-                v[e] = decode_v(qv, vs);
-                moments(tb.h, grad_at<BF16>(t.g, i) * gs, m[e], v[e]);
-                const float p = update(tb.h, t.keep, t.p[i], m[e], v[e]);
-                t.p[i] = p;
-                if (t.copy) t.copy[i] = to_bf16(p);
-            }
-            const float am = fabsf(m[e]);
-            mmax = (am > mmax || am != am) ? am : mmax;
-            vmax = (v[e] > vmax || v[e] != v[e]) ? v[e] : vmax;
+            const float q = signed_code(qm[u].b, e);
+            m[e] = copysignf(decode_m(fabsf(q), ms[u]), q);
+            v[e] = decode_v(plain_code(qv[u].b, e), vs[u]);
+            moments(tb.h, value(g[u], e) * gs, m[e], v[e]);
+            p[u].f[e] = update(tb.h, t.keep, p[u].f[e], m[e], v[e]);
+            // past the tensor's end there are zeros, which move no maximum (but 0 * NaN must not)
+            if (FULL || i + e < n) mmax = larger(mmax, m[e]), vmax = larger(vmax, v[e]);
         }
+        store4<FULL>(tp, i, n, p[u]);
+        if (t.copy) store4<FULL>(t.copy, i, n, to_copy(p[u]));
         float sm = wave_max(mmax), sv = wave_max(vmax);
         if (sm < 0x1p-126f) sm = 0.f;
         if (sv < 0x1p-126f) sv = 0.f;
         const float im = sm > 0.f ? 1.f / sm : 0.f, iv = sv > 0.f ? 1.f / sv : 0.f;
+        B4 om = {0}, ov = {0};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t i = i0 + 4 * lane + e;
-            if (i < t.n) {
-                const uint32_t z = random_bits(t.key, (uint32_t)i);
-                const float cm = encode<false>(fabsf(m[e]), sm, im, z & 0xffffu), cv = encode<true>(v[e], sv, iv, z >> 16);
-                ((int8_t *)t.m)[i] = (int8_t)(int)copysignf(cm, m[e]);
-                ((uint8_t *)t.v)[i] = (uint8_t)(int)cv;
-            }
+            const uint32_t z = random_bits(t.key, (uint32_t)i + e);
+            const uint32_t cm = encode<false>(fabsf(m[e]), sm, im, z & 0xffffu), cv = encode<true>(v[e], sv, iv, z >> 16);
+            om.b |= ((m[e] < 0.f ? 0u - cm : cm) & 0xffu) << (8 * e);
+            ov.b |= (cv & 0xffu) << (8 * e);
         }
+        store4<FULL>(tm, i, n, om);
+        store4<FULL>(tv, i, n, ov);
         if (lane == 0) {
             t.m_scale[blk] = sm;
             t.v_scale[blk] = sv;
@@ -173,16 +250,55 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(Table tb) {
 }
 
 // p holds the output for m, copy (as float*) the one for v.
+template <bool FULL> __device__ __forceinline__ void values_chunk(const AdamwTensor &t) {
+    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk + 4 * threadIdx.x, n = t.n;
+    B4 qm[kUnits], qv[kUnits];
+    float ms[kUnits], vs[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t i = i0 + u * 4 * kThreads;
+        if (FULL || i < n) {
+            qm[u] = load4<FULL, B4>((const uint8_t *)t.m, i, n);
+            qv[u] = load4<FULL, B4>((const uint8_t *)t.v, i, n);
+            ms[u] = t.m_scale[i / kQ];
+            vs[u] = t.v_scale[i / kQ];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t i = i0 + u * 4 * kThreads;
+        if (FULL || i < n) {
+            F4 m, v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float q = signed_code(qm[u].b, e);
+                m.f[e] = copysignf(decode_m(fabsf(q), ms[u]), q);
+                v.f[e] = decode_v(plain_code(qv[u].b, e), vs[u]);
+            }
+            store4<FULL>(t.p, i, n, m);
+            store4<FULL>((float *)t.copy, i, n, v);
+        }
+    }
+}
+
+// Whether all elements of this workgroup's chunk are there: uniform, so that only a tensor's last chunk
+// pays for the checks.
+__device__ __forceinline__ bool whole(const AdamwTensor &t) { return (int64_t)(blockIdx.x - t.first + 1) * kChunk <= t.n; }
+
+template <bool BF16> __global__ __launch_bounds__(kThreads) void adamw32_kernel(Table tb) {
+    const AdamwTensor &t = find(tb, blockIdx.x);
+    if (whole(t)) adamw32_chunk<BF16, true>(tb, t);
+    else adamw32_chunk<BF16, false>(tb, t);
+}
+template <bool BF16> __global__ __launch_bounds__(kThreads) void adamw8_kernel(Table tb) {
+    const AdamwTensor &t = find(tb, blockIdx.x);
+    if (whole(t)) adamw8_chunk<BF16, true>(tb, t);
+    else adamw8_chunk<BF16, false>(tb, t);
+}
 __global__ __launch_bounds__(kThreads) void values_kernel(Table tb) {
     const AdamwTensor &t = find(tb, blockIdx.x);
-    const int64_t i0 = (int64_t)(blockIdx.x - t.first) * kChunk;
-    for (int e = threadIdx.x; e < kChunk; e += kThreads) {
-        const int64_t i = i0 + e;
-        if (i >= t.n) break;
-        const float qm = (float)((const int8_t *)t.m)[i], qv = (float)((const uint8_t *)t.v)[i];
-        t.p[i] = copysignf(decode_m(fabsf(qm), t.m_scale[i / kQ]), qm);
-        ((float *)t.copy)[i] = decode_v(qv, t.v_scale[i / kQ]);
-    }
+    if (whole(t)) values_chunk<true>(t);
+    else values_chunk<false>(t);
 }
 
 }  // namespace
