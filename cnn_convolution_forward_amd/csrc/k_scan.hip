@@ -1,7 +1,5 @@
 // k_scan.hip -- the gated linear recurrence over tokens: forward, backward and
 // the single-token step (conv_scan_*).
-#include <initializer_list>
-
 #include "conv_fwd.h"
 #include "scan_math.h"
 
@@ -51,10 +49,7 @@ template <typename W> __device__ __forceinline__ W get(const W *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Chunks of `tokens` each, numbered through the batch.  Equal sequences have
-// per = ceil(T/tokens) (at least one) each, and so have packed ones if that is
-// one.  Longer packed ones take the numbers from first/tokens + b on: distinct,
-// and at most rows/tokens + B of them, whatever the lengths; a few stay unused.
+// Chunks are blocks of `tokens` tokens (packed_block numbers them).
 struct Chunks {
     int tokens, per;
     int64_t total;
@@ -80,15 +75,10 @@ template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const
         t.k = REV ? ch.per - 1 - k : k;
         t.slot = (int64_t)t.b * ch.per + t.k;
     } else {
-        // the last sequence whose numbers start at or before this one
         t.slot = REV ? ch.total - 1 - rest : rest;
-        t.b = 0;
-        for (int base = 0; base < s.B; base += 64) {
-            const int i = base + (int)(threadIdx.x & 63);
-            const uint64_t on = __ballot(i < s.B && ch.off[min(i, s.B)] / ch.tokens + i <= t.slot);
-            if (on) t.b = base + 63 - __builtin_clzll(on);
-        }
-        t.k = (int)(t.slot - (ch.off[t.b] / ch.tokens + t.b));
+        const Block k = packed_block(s, ch.tokens, t.slot);
+        t.b = k.b;
+        t.k = k.k;
     }
     return t;
 }
@@ -205,7 +195,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
     if (tile.k < 0 || (t0 >= len && tile.k > 0)) return;
     const int cw = tile.ct * CW + lane * VEC;
     const bool on = cw < C;
-    const int c = on ? cw : C - VEC;
+    const int c = min(cw, C - VEC);                // odd C: the last lane shares a channel, with the same results
     const int tw = t0 + w * L;                     // this wave's tokens: tw .. min(tw + L, len)
     float k[VEC], a[L][VEC], bb[L][VEC], A[VEC], H[VEC];
 #pragma unroll
@@ -330,7 +320,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const int t0 = tile.k * kBwdChunk;
     const int cw = tile.ct * CW + lane * VEC;
     const bool on = cw < C;
-    const int c = on ? cw : C - VEC;
+    const int c = min(cw, C - VEC);                // odd C: the last lane shares a channel, with the same results
     if (tile.k < 0 || t0 >= len) {                // an unused number, or an empty sequence
         if (on && w == 0)
 #pragma unroll
@@ -536,7 +526,7 @@ Chunks chunks(const Seq &s, int tokens) {
     Chunks ch = {};
     ch.tokens = tokens;
     ch.per = s.T > 0 ? (s.T + tokens - 1) / tokens : 1;
-    ch.total = s.off && ch.per > 1 ? s.rows / tokens + s.B : (int64_t)s.B * ch.per;
+    ch.total = block_count(s, tokens, ch.per);
     return ch;
 }
 
@@ -558,16 +548,6 @@ void set_links(Seq &s, Chunks &ch, void *ws, hipStream_t st) {
     const int64_t n = link_units(s, ch);
     scan_fill_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s, ch, n);
     if (s.off) s.off = ch.off;
-}
-
-// Whether two channels at a time stay aligned and within a row.
-bool paired(int C, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds) {
-    if (C % 2) return false;
-    for (const void *p : ptrs)
-        if ((uintptr_t)p % 4) return false;
-    for (int64_t ld : lds)
-        if (ld % 2) return false;
-    return true;
 }
 
 }  // namespace
@@ -598,8 +578,7 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
     set_links(q, ch, ws, st);
-    const auto run = !bf16 ? scan_fwd<float, 1>
-                     : paired(s.C, {x, gate, inp, y}, {ldx, ldg, ldi, ldy}) ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
+    const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, st);
     return hipGetLastError();
 }
@@ -629,9 +608,7 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
     Seq q = s;
     set_links(q, ch, ws, st);
     float *part = (float *)((char *)ws + link_bytes(s, ch));
-    const auto run = !bf16 ? scan_bwd<float, 1>
-                     : paired(s.C, {x, gate, inp, dy, dx, dgate, dinp}, {ldx, ldg, ldi, lddy, lddx, lddg, lddi})
-                         ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
+    const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,
         st);
     scan_reduce_kernel<<<(s.C + 15) / 16, 1024, 0, st>>>(part, ch.total, s.C, scale, decay, ddecay);

@@ -12,13 +12,15 @@
 //
 // Threads of a workgroup lie along the channels first (wide, contiguous
 // loads), then along runs of tokens.
-#include <initializer_list>
-
 #include "seq_common.h"
+
 namespace convfwd {
 namespace {
 
 constexpr int kThreads = 256;
+
+// Rows loaded together: a multiple of K, at least three.
+template <int K> constexpr int kGroup = K >= 3 ? K : 4;
 
 // Row t of X (t may be negative: the carried rows), VEC channels at c.
 template <typename T, int VEC, int K>
@@ -58,50 +60,87 @@ __device__ __forceinline__ void write_state(const T *x, int64_t ldx, const T *st
     }
 }
 
-// grid (runs of tokens of all sequences, channel blocks); run = by * TL tokens
+// Where a thread works: a run of tl tokens of sequence b, VEC channels from c on.
+struct Work {
+    int b, c, t0, t1, len;
+    int64_t first;
+    bool any, head;         // any: channels at all; head: the sequence's first run
+};
+
+template <int VEC> __device__ __forceinline__ Work get_work(const Seq &s, int per, int bx_log2, int tl) {
+    Work k;
+    const int by = kThreads >> bx_log2;
+    const int tx = threadIdx.x & ((1 << bx_log2) - 1), ty = threadIdx.x >> bx_log2;
+    Block at;
+    if (!s.off || per == 1) {
+        at.b = blockIdx.x / per;
+        at.k = blockIdx.x % per;
+    } else {
+        at = packed_block(s, by * tl, blockIdx.x);
+    }
+    const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
+    k.any = c < s.C;
+    k.c = min(c, s.C - VEC);        // the last threads may share channels, with the same results
+    k.b = at.b;
+    seq_range(s, k.b, k.first, k.len);
+    if (at.k < 0) k.len = 0;
+    k.t0 = max(at.k, 0) * by * tl + ty * tl;
+    k.t1 = min(k.t0 + tl, k.len);
+    k.head = at.k == 0 && ty == 0;
+    return k;
+}
+
+// K rows from p on, in bf16 or fp32 as they are; only the first `there` of them are, and the first row
+// stands in for the others, so that loads need no branch.
+template <typename T, int VEC, int K> struct Rows {
+    typename Pack<T, VEC>::type v[K];
+    __device__ __forceinline__ void load(const T *p, int64_t ld, int there) {
+#pragma unroll
+        for (int u = 0; u < K; ++u) v[u] = load_pack<T, VEC>(p + (u < there ? u * ld : 0));
+    }
+};
+
+// grid (blocks of tokens, channel blocks)
 template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__restrict__ x, int64_t ldx,
                                                               const T *__restrict__ w, const float *__restrict__ bias,
                                                               const T *__restrict__ state, T *__restrict__ y,
-                                                              int64_t ldy, T *__restrict__ state_out, int nblk,
+                                                              int64_t ldy, T *__restrict__ state_out, int per,
                                                               int bx_log2, int tl) {
-    const int b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
-    const int tx = threadIdx.x & ((1 << bx_log2) - 1), ty = threadIdx.x >> bx_log2;
-    const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
-    if (c >= s.C) return;
-    int64_t first;
-    int len;
-    seq_range(s, b, first, len);
-    if (K > 1 && state_out && blk == 0 && ty == 0) write_state<T, VEC, K>(x, ldx, state, state_out, first, len, b, s.C, c);
-    const int t0 = (blk * (kThreads >> bx_log2) + ty) * tl, t1 = min(t0 + tl, len);
-    if (t0 >= t1) return;
+    constexpr int U = kGroup<K>;                   // rows loaded together: a multiple of K
+    const Work k = get_work<VEC>(s, per, bx_log2, tl);
+    if (!k.any) return;
+    if (K > 1 && state_out && k.head) write_state<T, VEC, K>(x, ldx, state, state_out, k.first, k.len, k.b, s.C, k.c);
+    if (k.t0 >= k.t1) return;
+    const T *xp = x + (k.first + k.t0) * ldx + k.c;
+    T *yp = y + (k.first + k.t0) * ldy + k.c;
+    Rows<T, VEC, U> next;
+    next.load(xp, ldx, k.t1 - k.t0);
     float wf[K][VEC], bf[VEC], win[K][VEC];
-    load_w<T, VEC, K>(w, c, wf);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[c + i] : 0.f;
+    for (int j = 0; j < K - 1; ++j) x_row<T, VEC, K>(x, ldx, state, k.first, k.b, s.C, k.c, k.t0 - (K - 1) + j, win[j]);
+    load_w<T, VEC, K>(w, k.c, wf);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) x_row<T, VEC, K>(x, ldx, state, first, b, s.C, c, t0 - (K - 1) + j, win[j]);
-    const T *xp = x + (first + t0) * ldx + c;
-    T *yp = y + (first + t0) * ldy + c;
+    for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[k.c + i] : 0.f;
     // at step u (mod K) the new row goes to slot (K-1+u) % K; tap j is slot (u+j) % K
-    for (int t = t0; t < t1; t += K) {
+    for (int t = k.t0; t < k.t1; t += U) {
+        const Rows<T, VEC, U> now = next;
+        xp += U * ldx;
+        if (t + U < k.t1) next.load(xp, ldx, k.t1 - t - U);
 #pragma unroll
-        for (int u = 0; u < K; ++u) {
-            if (t + u < t1) {
-                load_f32<T, VEC>(xp, win[(K - 1 + u) % K]);
-                float p[VEC];
+        for (int u = 0; u < U; ++u) {
+            to_f32(now.v[u], win[(K - 1 + u) % K]);
+            float p[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    p[i] = bf[i];
+            for (int i = 0; i < VEC; ++i) {
+                p[i] = bf[i];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) p[i] = fmaf(wf[j][i], win[(u + j) % K][i], p[i]);
-                    if (SILU) p[i] *= sigmoid(p[i]);
-                }
-                store_f32(yp, p);
-                xp += ldx;
-                yp += ldy;
+                for (int j = 0; j < K; ++j) p[i] = fmaf(wf[j][i], win[(u + j) % K][i], p[i]);
+                if (SILU) p[i] *= sigmoid(p[i]);
             }
+            if (t + u < k.t1) store_f32(yp + u * ldy, p);
         }
+        yp += U * ldy;
     }
 }
 
@@ -118,80 +157,90 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
                                                               const T *__restrict__ state, const T *__restrict__ dy,
                                                               int64_t lddy, T *__restrict__ dx, int64_t lddx,
                                                               T *__restrict__ dstate, float *__restrict__ part,
-                                                              int nblk, int bx_log2, int tl) {
+                                                              int per, int bx_log2, int tl) {
+    constexpr int U = kGroup<K>;
     __shared__ float red[kThreads * VEC];
-    const int b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
     const int bx = 1 << bx_log2, by = kThreads >> bx_log2;
     const int tx = threadIdx.x & (bx - 1), ty = threadIdx.x >> bx_log2;
-    const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
-    int64_t first;
-    int len;
-    seq_range(s, b, first, len);
-    const int t0 = (blk * by + ty) * tl, t1 = min(t0 + tl, len);
+    const Work k = get_work<VEC>(s, per, bx_log2, tl);
     float dw[K][VEC] = {}, db[VEC] = {};
-    const bool head = t0 == 0 && K > 1 && dstate;
-    if (c < s.C && (t0 < t1 || head)) {
+    const bool head = k.head && K > 1 && dstate;
+    if (k.any && (k.t0 < k.t1 || head)) {
+        const int end = max(k.t1, k.t0) + K - 1;       // dX rows up to t1 - 1
+        const T *xp = x + (k.first + k.t0) * ldx + k.c, *dp_ = dy + (k.first + k.t0) * lddy + k.c;
+        Rows<T, VEC, U> nx, nd;
+        if (k.t0 < k.len) {
+            nx.load(xp, ldx, k.len - k.t0);
+            nd.load(dp_, lddy, k.len - k.t0);
+        }
         float wf[K][VEC], bf[VEC], win[K][VEC], dp[K][VEC];
-        load_w<T, VEC, K>(w, c, wf);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[c + i] : 0.f;
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) dp[j][i] = 0.f;
-        if (t0 < t1) {
+            for (int i = 0; i < VEC; ++i) dp[j][i] = win[j][i] = 0.f;
+        if (k.t0 < k.t1) {
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) x_row<T, VEC, K>(x, ldx, state, first, b, s.C, c, t0 - (K - 1) + j, win[j]);
+            for (int j = 0; j < K - 1; ++j)
+                x_row<T, VEC, K>(x, ldx, state, k.first, k.b, s.C, k.c, k.t0 - (K - 1) + j, win[j]);
         }
-        const int end = t1 + K - 1;                    // dX rows up to t1 - 1
-        for (int t = t0; t < end; t += K) {
+        load_w<T, VEC, K>(w, k.c, wf);
 #pragma unroll
-            for (int u = 0; u < K; ++u) {
+        for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[k.c + i] : 0.f;
+        for (int t = k.t0; t < end; t += U) {
+            const Rows<T, VEC, U> x0 = nx, d0 = nd;
+            xp += U * ldx;
+            dp_ += U * lddy;
+            if (t + U < end && t + U < k.len) {
+                nx.load(xp, ldx, k.len - t - U);
+                nd.load(dp_, lddy, k.len - t - U);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
                 const int tt = t + u;
-                if (tt < end) {
-                    float(&d)[VEC] = dp[(K - 1 + u) % K];
-                    if (tt < len) {
-                        load_f32<T, VEC>(x + (first + tt) * ldx + c, win[(K - 1 + u) % K]);
-                        load_f32<T, VEC>(dy + (first + tt) * lddy + c, d);
-                        if (SILU) {
+                float(&d)[VEC] = dp[(K - 1 + u) % K];
+                if (tt < k.len) {
+                    to_f32(x0.v[u], win[(K - 1 + u) % K]);
+                    to_f32(d0.v[u], d);
+                    if (SILU) {
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                float p = bf[i];
+                        for (int i = 0; i < VEC; ++i) {
+                            float p = bf[i];
 #pragma unroll
-                                for (int j = 0; j < K; ++j) p = fmaf(wf[j][i], win[(u + j) % K][i], p);
-                                const float sg = sigmoid(p);
-                                d[i] *= sg * fmaf(p, 1.f - sg, 1.f);
-                            }
+                            for (int j = 0; j < K; ++j) p = fmaf(wf[j][i], win[(u + j) % K][i], p);
+                            const float sg = sigmoid(p);
+                            d[i] *= sg * fmaf(p, 1.f - sg, 1.f);
                         }
-                        if (tt < t1) {
+                    }
+                    if (tt < k.t1) {
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                db[i] += d[i];
+                        for (int i = 0; i < VEC; ++i) {
+                            db[i] += d[i];
 #pragma unroll
-                                for (int j = 0; j < K; ++j) dw[j][i] = fmaf(d[i], win[(u + j) % K][i], dw[j][i]);
-                            }
+                            for (int j = 0; j < K; ++j) dw[j][i] = fmaf(d[i], win[(u + j) % K][i], dw[j][i]);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) d[i] = 0.f;
                     }
-                    // dX[o] = sum_j w[j] dp[o+K-1-j], o = tt-K+1: dp[tt-j] is in slot (K-1+u-j) % K
-                    const int o = tt - (K - 1);
-                    float g[VEC];
+                } else {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        g[i] = 0.f;
+                    for (int i = 0; i < VEC; ++i) d[i] = 0.f;
+                }
+                // dX[o] = sum_j w[j] dp[o+K-1-j], o = tt-K+1: dp[tt-j] is in slot (K-1+u-j) % K
+                const int o = tt - (K - 1);
+                float g[VEC];
 #pragma unroll
-                        for (int j = 0; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
-                    }
-                    if (o >= t0)
-                        store_f32(dx + (first + o) * lddx + c, g);
-                    else if (head)
-                        store_f32(dstate + ((int64_t)b * (K - 1) + tt) * s.C + c, g);
+                for (int i = 0; i < VEC; ++i) {
+                    g[i] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
+                }
+                if (o >= k.t0) {
+                    if (o < k.t1) store_f32(dx + (k.first + o) * lddx + k.c, g);
+                } else if (head && tt < K - 1) {
+                    store_f32(dstate + ((int64_t)k.b * (K - 1) + tt) * s.C + k.c, g);
                 }
             }
         }
     }
+    // the thread of the first run adds its channels over the runs, in order
     for (int j = 0; j <= K; ++j) {
         if (j) __syncthreads();
 #pragma unroll
@@ -203,27 +252,35 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
         }
         __syncthreads();
         for (int e = threadIdx.x; e < bx * VEC; e += kThreads) {
+            const int q = e & (bx - 1), i = e >> bx_log2, c = ((blockIdx.y << bx_log2) + q) * VEC;
             float v = 0.f;
-            for (int r = 0; r < by; ++r) v += red[(r * VEC + (e & (VEC - 1))) * bx + e / VEC];
-            const int cc = (blockIdx.y << bx_log2) * VEC + e;
-            if (cc < s.C) part[((int64_t)blockIdx.x * (K + 1) + j) * s.C + cc] = v;
+            for (int r = 0; r < by; ++r) v += red[(r * VEC + i) * bx + q];
+            if (c < s.C) part[((int64_t)blockIdx.x * (K + 1) + j) * s.C + min(c, s.C - VEC) + i] = v;
         }
     }
 }
 
-// dw (C, K) and db from the workgroups' partial sums: 64 channels and one of
-// the K+1 rows per workgroup, four strands of partials added in order.
-__global__ __launch_bounds__(kThreads) void causal_reduce_kernel(const float *__restrict__ part, int64_t n, int C, int K,
-                                                                 float *__restrict__ dw, float *__restrict__ db) {
-    __shared__ float red[4][64];
-    const int cl = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + cl, j = blockIdx.y;
+// dw (C, K) and db from the workgroups' partial sums: 16 channels of one of the
+// K+1 rows per workgroup, 64 strands of partials, each added in order.
+__global__ __launch_bounds__(1024) void causal_reduce_kernel(const float *__restrict__ part, int64_t n, int C, int K,
+                                                             float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float red[64][17];
+    const int cl = threadIdx.x & 15, q = threadIdx.x >> 4, c = blockIdx.x * 16 + cl, j = blockIdx.y;
     float v = 0.f;
     if (c < C)
-        for (int64_t i = q; i < n; i += 4) v += part[(i * (K + 1) + j) * C + c];
+        for (int64_t i = q; i < n; i += 64) v += part[(i * (K + 1) + j) * C + c];
     red[q][cl] = v;
     __syncthreads();
+    if (q < 8) {
+        v = 0.f;
+        for (int i = 0; i < 8; ++i) v += red[q * 8 + i][cl];
+    }
+    __syncthreads();
+    if (q < 8) red[q][cl] = v;
+    __syncthreads();
     if (q == 0 && c < C) {
-        v = (red[0][cl] + red[1][cl]) + (red[2][cl] + red[3][cl]);
+        v = 0.f;
+        for (int i = 0; i < 8; ++i) v += red[i][cl];
         if (j < K)
             dw[(int64_t)c * K + j] = v;
         else if (db)
@@ -260,16 +317,6 @@ __global__ __launch_bounds__(kThreads) void causal_step_kernel(int B, int C, con
     store_f32(y + b * ldy + c, p);
 }
 
-// Whether VEC channels at a time stay aligned and within a row.
-bool wide(int vec, int esize, int C, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds) {
-    if (C % vec) return false;
-    for (const void *p : ptrs)
-        if ((uintptr_t)p % (vec * esize)) return false;
-    for (int64_t ld : lds)
-        if (ld % vec) return false;
-    return true;
-}
-
 // Channel threads of a workgroup: the power of two that covers the channels,
 // 8 to 64.
 int channel_log2(int groups) {
@@ -279,7 +326,8 @@ int channel_log2(int groups) {
 }
 
 struct Tiling {
-    int bx_log2, tl, nblk, cblk;
+    int bx_log2, tl, per, cblk;
+    int64_t n;              // blocks of tokens
 };
 
 Tiling tiling(const Seq &s, int vec, int tl) {
@@ -287,7 +335,8 @@ Tiling tiling(const Seq &s, int vec, int tl) {
     t.bx_log2 = channel_log2((s.C + vec - 1) / vec);
     t.tl = tl;
     const int run = (kThreads >> t.bx_log2) * tl;
-    t.nblk = s.T > 0 ? (int)(((int64_t)s.T + run - 1) / run) : 1;
+    t.per = s.T > 0 ? (int)(((int64_t)s.T + run - 1) / run) : 1;
+    t.n = block_count(s, run, t.per);
     t.cblk = (s.C + (vec << t.bx_log2) - 1) / (vec << t.bx_log2);
     return t;
 }
@@ -298,18 +347,17 @@ template <typename T, int VEC, int K, bool SILU>
 void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, T *y, int64_t ldy,
          T *state_out, hipStream_t st) {
     const Tiling t = tiling(s, VEC, kFwdTokens);
-    causal_fwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)(s.B * (int64_t)t.nblk), t.cblk), kThreads, 0, st>>>(
-        s, x, ldx, w, bias, state, y, ldy, state_out, t.nblk, t.bx_log2, t.tl);
+    causal_fwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
+        s, x, ldx, w, bias, state, y, ldy, state_out, t.per, t.bx_log2, t.tl);
 }
 
 template <typename T, int VEC, int K, bool SILU>
 void bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
          T *dx, int64_t lddx, float *dw, float *db, T *dstate, float *part, hipStream_t st) {
     const Tiling t = tiling(s, VEC, kBwdTokens);
-    const int64_t n = s.B * (int64_t)t.nblk;
-    causal_bwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)n, t.cblk), kThreads, 0, st>>>(
-        s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.nblk, t.bx_log2, t.tl);
-    causal_reduce_kernel<<<dim3((s.C + 63) / 64, K + 1), kThreads, 0, st>>>(part, n, s.C, K, dw, db);
+    causal_bwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
+        s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per, t.bx_log2, t.tl);
+    causal_reduce_kernel<<<dim3((s.C + 15) / 16, K + 1), 1024, 0, st>>>(part, t.n, s.C, K, dw, db);
 }
 
 template <typename T, int VEC, int K, bool SILU>
@@ -357,71 +405,51 @@ void step_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, 
 #undef CALL
 }
 
+// Channels per thread: 16 bytes of them in the forward pass, four in the backward one, whose window of
+// rows, weights and sums would not fit the registers twice over.
+constexpr int kBwdVec = 4;
+
 }  // namespace
 
 int64_t causal_bwd_workspace_floats(const Seq &s, int K) {
-    // the narrowest unit needs the most workgroups along the tokens per channel block
-    int64_t n = 0;
-    for (int vec : {1, 4}) {
-        const Tiling t = tiling(s, vec, kBwdTokens);
-        if (s.B * (int64_t)t.nblk > n) n = s.B * (int64_t)t.nblk;
-    }
-    return n * (K + 1) * s.C;
+    return tiling(s, s.C >= kBwdVec ? kBwdVec : 1, kBwdTokens).n * (K + 1) * s.C;
 }
 
 hipError_t launch_causal_fwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
                              const float *bias, const void *state, void *y, int64_t ldy, void *so, hipStream_t st) {
-    if (bf16) {
-        typedef uint16_t T;
-        if (wide(8, 2, s.C, {x, state, y, so}, {ldx, ldy}))
-            fwd_k<T, 8>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
-        else
-            fwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
-    } else {
-        typedef float T;
-        if (wide(4, 4, s.C, {x, state, y, so}, {ldx, ldy}))
-            fwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
-        else
-            fwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
-    }
+    const auto run = [&](auto tag, auto f) {
+        typedef decltype(tag) T;
+        f(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (T *)y, ldy, (T *)so, st);
+    };
+    if (bf16)
+        run(uint16_t{}, s.C >= 8 ? fwd_k<uint16_t, 8> : fwd_k<uint16_t, 1>);
+    else
+        run(float{}, s.C >= 4 ? fwd_k<float, 4> : fwd_k<float, 1>);
     return hipGetLastError();
 }
 
 hipError_t launch_causal_bwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
                              const float *bias, const void *state, const void *dy, int64_t lddy, void *dx, int64_t lddx,
                              float *dw, float *db, void *ds, float *part, hipStream_t st) {
-    if (bf16) {
-        typedef uint16_t T;
-        if (wide(4, 2, s.C, {x, state, dy, dx, ds}, {ldx, lddy, lddx}))
-            bwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
-                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
-        else
-            bwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
-                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
-    } else {
-        typedef float T;
-        if (wide(4, 4, s.C, {x, state, dy, dx, ds}, {ldx, lddy, lddx}))
-            bwd_k<T, 4>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
-                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
-        else
-            bwd_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy,
-                        (T *)dx, lddx, dw, db, (T *)ds, part, st);
-    }
+    const auto run = [&](auto tag, auto f) {
+        typedef decltype(tag) T;
+        f(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy, (T *)dx, lddx, dw, db,
+          (T *)ds, part, st);
+    };
+    if (bf16)
+        run(uint16_t{}, s.C >= kBwdVec ? bwd_k<uint16_t, kBwdVec> : bwd_k<uint16_t, 1>);
+    else
+        run(float{}, s.C >= kBwdVec ? bwd_k<float, kBwdVec> : bwd_k<float, 1>);
     return hipGetLastError();
 }
 
 hipError_t launch_causal_step(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
                               const float *bias, void *state, void *y, int64_t ldy, hipStream_t st) {
-    if (bf16) {
-        typedef uint16_t T;
-        if (wide(2, 2, s.C, {x, state, y}, {ldx, ldy}))
-            step_k<T, 2>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
-        else
-            step_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
-    } else {
-        typedef float T;
-        step_k<T, 1>(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (T *)state, (T *)y, ldy, st);
-    }
+    if (bf16)
+        (s.C % 2 ? step_k<uint16_t, 1> : step_k<uint16_t, 2>)(s, K, silu, (const uint16_t *)x, ldx, (const uint16_t *)w, bias,
+                                                              (uint16_t *)state, (uint16_t *)y, ldy, st);
+    else
+        step_k<float, 1>(s, K, silu, (const float *)x, ldx, (const float *)w, bias, (float *)state, (float *)y, ldy, st);
     return hipGetLastError();
 }
 

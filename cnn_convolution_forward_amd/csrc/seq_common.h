@@ -21,8 +21,9 @@ __device__ __forceinline__ void seq_range(const Seq &s, int b, int64_t &first, i
     len = (int)min(o1 - o0, (int64_t)s.T);
 }
 
-// VEC adjacent channels as fp32.  T is uint16_t (bf16 bits) or float; the
-// address is aligned to VEC elements.
+// VEC adjacent channels as fp32.  T is uint16_t (bf16 bits) or float.  The
+// address need only be aligned to an element: rows of odd width and column
+// slices are read and written with the same wide accesses as aligned ones.
 template <typename T, int VEC> struct Pack;
 template <> struct Pack<uint16_t, 1> { typedef uint16_t type; };
 template <> struct Pack<uint16_t, 2> { typedef uint32_t type; };
@@ -34,7 +35,12 @@ template <> struct Pack<float, 4> { typedef float4 type; };
 
 template <typename T, int VEC>
 __device__ __forceinline__ typename Pack<T, VEC>::type load_pack(const T *p) {
-    return *reinterpret_cast<const typename Pack<T, VEC>::type *>(p);
+    typename Pack<T, VEC>::type v;
+    __builtin_memcpy(&v, p, sizeof(v));
+    return v;
+}
+template <typename T, typename V> __device__ __forceinline__ void store_pack(T *p, const V &v) {
+    __builtin_memcpy(p, &v, sizeof(v));
 }
 
 // bf16 bits to fp32 is a shift; fp32 to bf16 rounds to nearest even (a NaN
@@ -73,22 +79,37 @@ template <typename T, int VEC> __device__ __forceinline__ void load_f32(const T 
 }
 
 __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[1]) { *p = to_bf16(f[0]); }
-__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[2]) {
-    *reinterpret_cast<uint32_t *>(p) = pack_bf16(f[0], f[1]);
-}
+__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[2]) { store_pack(p, pack_bf16(f[0], f[1])); }
 __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[4]) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    store_pack(p, make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])));
 }
 __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                               pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    store_pack(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
 }
-__device__ __forceinline__ void store_f32(float *p, const float (&f)[1]) { *p = f[0]; }
-__device__ __forceinline__ void store_f32(float *p, const float (&f)[2]) {
-    *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+template <int VEC> __device__ __forceinline__ void store_f32(float *p, const float (&f)[VEC]) { store_pack(p, f); }
+
+// Blocks of `tokens` tokens, numbered through the batch.  Equal sequences have
+// per = ceil(T/tokens) (at least one) each, and so have packed ones if that is
+// one.  Longer packed ones take the numbers from first/tokens + b on: distinct,
+// and at most rows/tokens + B of them, whatever the lengths; a few stay unused.
+struct Block {
+    int b, k;               // sequence, and block in it: negative or past its end for an unused number
+};
+__host__ __device__ __forceinline__ int64_t block_count(const Seq &s, int tokens, int per) {
+    return s.off && per > 1 ? s.rows / tokens + s.B : (int64_t)s.B * per;
 }
-__device__ __forceinline__ void store_f32(float *p, const float (&f)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+// The block of number n; all lanes of a wave together.
+__device__ __forceinline__ Block packed_block(const Seq &s, int tokens, int64_t n) {
+    const auto start = [&](int b) { return min(max((int64_t)s.off[b], (int64_t)0), s.rows) / tokens + b; };
+    Block t;
+    t.b = 0;
+    for (int base = 0; base < s.B; base += 64) {       // the last sequence that starts at or before n
+        const int i = base + (int)(threadIdx.x & 63);
+        const uint64_t on = __ballot(i < s.B && start(min(i, s.B - 1)) <= n);
+        if (on) t.b = base + 63 - __builtin_clzll(on);
+    }
+    t.k = (int)(n - start(t.b));
+    return t;
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
