@@ -734,12 +734,24 @@ def workspace_ex(x_shape, w_shape, stride=1, pad=0, dilation=1, groups=1, layout
 
 # ---- sequences of tokens ------------------------------------------------------
 
+def _stream_of(t):
+    """The current stream of t's device.  These helpers run once per token of an answer: the direct
+    query takes 0.1 us, torch.cuda.current_stream_of(x) 3 us."""
+    torch = _torch()
+    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if query is not None:
+        return query(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
 def _dtype_code(t, name):
     """CONV_OUT_* of a float32 or bf16 (torch.bfloat16, or int16/uint16 bits) tensor."""
     torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return 1
     if t.dtype == torch.float32:
         return 0
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+    if t.dtype in (torch.int16, torch.uint16):
         return 1
     raise TypeError("%s has dtype %s, expected float32 or bf16" % (name, t.dtype))
 
@@ -821,7 +833,8 @@ def _run(st, where):
 def _rows_out(out, x, name):
     torch = _torch()
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
+        y = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return y, x.shape[-1]
     return out, _ld(out, x.shape, x, name)
 
 
@@ -841,7 +854,7 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
     end = torch.empty(rows, dtype=x.dtype, device=x.device) if with_state else None
     _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
                          _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
-                         y.data_ptr(), ldy, end.data_ptr() if with_state else None, _stream()), "conv_causal_fwd")
+                         y.data_ptr(), ldy, end.data_ptr() if with_state else None, _stream_of(x)), "conv_causal_fwd")
     return (y, end) if with_state else y
 
 
@@ -865,7 +878,7 @@ def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=No
     _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
                          _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
                          dy.data_ptr(), lddy, dx.data_ptr(), lddx, dw.data_ptr(), db.data_ptr(),
-                         None if ds is None else ds.data_ptr(), ws.data_ptr(), n, _stream()), "conv_causal_bwd")
+                         None if ds is None else ds.data_ptr(), ws.data_ptr(), n, _stream_of(x)), "conv_causal_bwd")
     return dx, dw, db, ds
 
 
@@ -881,7 +894,7 @@ def causal_conv_step(x, w, state, bias=None, silu=False, out=None):
     y, ldy = _rows_out(out, x, "out")
     _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
                           _dense(bias, (seq.C,), torch.float32, "bias"),
-                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state"), y.data_ptr(), ldy, _stream()),
+                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state"), y.data_ptr(), ldy, _stream_of(x)),
          "conv_causal_step")
     return y
 
@@ -915,7 +928,7 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
     _run(conv_scan_fwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
                        _dense(decay, (seq.C,), torch.float32, "decay"), _dense(h0, ends, torch.float32, "h0"),
                        y.data_ptr(), ldy, hT.data_ptr(), None if states is None else states.data_ptr(),
-                       None if workspace is None else workspace.data_ptr(), wsb, _stream()), "conv_scan_fwd")
+                       None if workspace is None else workspace.data_ptr(), wsb, _stream_of(x)), "conv_scan_fwd")
     return (y, hT, states) if with_states else (y, hT)
 
 
@@ -943,7 +956,7 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
                        _dense(states, (seq.B, nb, seq.C), torch.float32, "states"), dy.data_ptr(), lddy,
                        _dense(dh, ends, torch.float32, "dh"), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
                        lddi, dd.data_ptr(), dh0.data_ptr(), workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), _stream()), "conv_scan_bwd")
+                       workspace.numel() * workspace.element_size(), _stream_of(x)), "conv_scan_bwd")
     return dx, dg, di, dd, dh0
 
 
@@ -956,7 +969,7 @@ def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
     y, ldy = _rows_out(out, x, "out")
     _run(conv_scan_step(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
                         _dense(decay, (seq.C,), torch.float32, "decay"),
-                        _dense(h, (seq.B, seq.C), torch.float32, "h"), y.data_ptr(), ldy, _stream()), "conv_scan_step")
+                        _dense(h, (seq.B, seq.C), torch.float32, "h"), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
     return y
 
 
@@ -1044,7 +1057,8 @@ class AdamW:
             self._set_grads(grads)
         o = self._opt
         o.lr, (o.beta1, o.beta2), o.eps, o.seed, o.step = self.lr, self.betas, self.eps, self.seed, self.steps + 1
-        _run(conv_adamw_step(o, self._table, len(self.params), _stream()), "conv_adamw_step")
+        if self.params:
+            _run(conv_adamw_step(o, self._table, len(self.params), _stream_of(self.params[0])), "conv_adamw_step")
         self.steps += 1
 
     def state_values(self, out=None):
@@ -1067,5 +1081,7 @@ class AdamW:
                 raise ValueError("out: %d entries for %d tensors" % (len(side), n))
             ptrs.append((ctypes.c_void_p * max(n, 1))(*[self._addr(t, p.numel(), (torch.float32,), "out")
                                                         for t, p in zip(side, self.params)]))
-        _run(conv_adamw_state_values(self._table, n, ptrs[0], ptrs[1], _stream()), "conv_adamw_state_values")
+        if n:
+            _run(conv_adamw_state_values(self._table, n, ptrs[0], ptrs[1], _stream_of(self.params[0])),
+                 "conv_adamw_state_values")
         return out

@@ -12,6 +12,8 @@
 //
 // Threads of a workgroup lie along the channels first (wide, contiguous
 // loads), then along runs of tokens.
+#include <type_traits>
+
 #include "seq_common.h"
 
 namespace convfwd {
@@ -186,19 +188,15 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
         load_w<T, VEC, K>(w, k.c, wf);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[k.c + i] : 0.f;
-        for (int t = k.t0; t < end; t += U) {
-            const Rows<T, VEC, U> x0 = nx, d0 = nd;
-            xp += U * ldx;
-            dp_ += U * lddy;
-            if (t + U < end && t + U < k.len) {
-                nx.load(xp, ldx, k.len - t - U);
-                nd.load(dp_, lddy, k.len - t - U);
-            }
+        // U rows of a run; inner: all are the run's own and so are the rows of dX that they complete
+        const auto group = [&](int t, const Rows<T, VEC, U> &x0, const Rows<T, VEC, U> &d0, auto inner_) {
+            constexpr bool inner = decltype(inner_)::value;
+            T *dxp = dx + (k.first + t - (K - 1)) * lddx + k.c;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int tt = t + u;
                 float(&d)[VEC] = dp[(K - 1 + u) % K];
-                if (tt < k.len) {
+                if (inner || tt < k.len) {
                     to_f32(x0.v[u], win[(K - 1 + u) % K]);
                     to_f32(d0.v[u], d);
                     if (SILU) {
@@ -211,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
                             d[i] *= sg * fmaf(p, 1.f - sg, 1.f);
                         }
                     }
-                    if (tt < k.t1) {
+                    if (inner || tt < k.t1) {
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) {
                             db[i] += d[i];
@@ -228,16 +226,28 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
                 float g[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    g[i] = 0.f;
+                    g[i] = wf[0][i] * dp[(2 * K - 1 + u) % K][i];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
+                    for (int j = 1; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
                 }
-                if (o >= k.t0) {
-                    if (o < k.t1) store_f32(dx + (k.first + o) * lddx + k.c, g);
-                } else if (head && tt < K - 1) {
+                if (inner || (o >= k.t0 && o < k.t1))
+                    store_f32(dxp + u * lddx, g);
+                else if (o < k.t0 && head && tt < K - 1)
                     store_f32(dstate + ((int64_t)k.b * (K - 1) + tt) * s.C + k.c, g);
-                }
             }
+        };
+        for (int t = k.t0; t < end; t += U) {
+            const Rows<T, VEC, U> x0 = nx, d0 = nd;
+            xp += U * ldx;
+            dp_ += U * lddy;
+            if (t + U < end && t + U < k.len) {
+                nx.load(xp, ldx, k.len - t - U);
+                nd.load(dp_, lddy, k.len - t - U);
+            }
+            if (t > k.t0 && t + U <= k.t1)
+                group(t, x0, d0, std::true_type{});
+            else
+                group(t, x0, d0, std::false_type{});
         }
     }
     // the thread of the first run adds its channels over the runs, in order
@@ -330,23 +340,27 @@ struct Tiling {
     int64_t n;              // blocks of tokens
 };
 
-Tiling tiling(const Seq &s, int vec, int tl) {
+// Tokens of a run: long ones read fewer rows twice and leave fewer partial sums, short ones make more
+// workgroups.  The longest of 64, 32 and 16 that still gives `least` workgroups: one for each of 256 CUs
+// forward (at 8 x 2048 x 2048 bf16, runs of 64, 32, 16: 30.5, 31.3, 33.9 us), two backward, which has
+// three waves per SIMD and takes all of them in one round (51, 65, 72 us; 5003 x 999 fp32 packed: 32, 22.6, 21.5).
+constexpr int kFwdLeast = 256, kBwdLeast = 512, kShortest = 16;
+Tiling tiling(const Seq &s, int vec, int least) {
     Tiling t;
     t.bx_log2 = channel_log2((s.C + vec - 1) / vec);
-    t.tl = tl;
-    const int run = (kThreads >> t.bx_log2) * tl;
-    t.per = s.T > 0 ? (int)(((int64_t)s.T + run - 1) / run) : 1;
-    t.n = block_count(s, run, t.per);
     t.cblk = (s.C + (vec << t.bx_log2) - 1) / (vec << t.bx_log2);
-    return t;
+    for (t.tl = 64;; t.tl >>= 1) {
+        const int run = (kThreads >> t.bx_log2) * t.tl;
+        t.per = s.T > 0 ? (int)(((int64_t)s.T + run - 1) / run) : 1;
+        t.n = block_count(s, run, t.per);
+        if (t.tl == kShortest || t.n * t.cblk >= least) return t;
+    }
 }
-
-constexpr int kFwdTokens = 32, kBwdTokens = 32;
 
 template <typename T, int VEC, int K, bool SILU>
 void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, T *y, int64_t ldy,
          T *state_out, hipStream_t st) {
-    const Tiling t = tiling(s, VEC, kFwdTokens);
+    const Tiling t = tiling(s, VEC, kFwdLeast);
     causal_fwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
         s, x, ldx, w, bias, state, y, ldy, state_out, t.per, t.bx_log2, t.tl);
 }
@@ -354,7 +368,7 @@ void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, c
 template <typename T, int VEC, int K, bool SILU>
 void bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
          T *dx, int64_t lddx, float *dw, float *db, T *dstate, float *part, hipStream_t st) {
-    const Tiling t = tiling(s, VEC, kBwdTokens);
+    const Tiling t = tiling(s, VEC, kBwdLeast);
     causal_bwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
         s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per, t.bx_log2, t.tl);
     causal_reduce_kernel<<<dim3((s.C + 15) / 16, K + 1), 1024, 0, st>>>(part, t.n, s.C, K, dw, db);
@@ -412,7 +426,7 @@ constexpr int kBwdVec = 4;
 }  // namespace
 
 int64_t causal_bwd_workspace_floats(const Seq &s, int K) {
-    return tiling(s, s.C >= kBwdVec ? kBwdVec : 1, kBwdTokens).n * (K + 1) * s.C;
+    return tiling(s, s.C >= kBwdVec ? kBwdVec : 1, kBwdLeast).n * (K + 1) * s.C;
 }
 
 hipError_t launch_causal_fwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,
