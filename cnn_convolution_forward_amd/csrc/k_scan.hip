@@ -1,5 +1,7 @@
 // k_scan.hip -- the gated linear recurrence over tokens: forward, backward and
 // the single-token step (conv_scan_*).
+#include <type_traits>
+
 #include "conv_fwd.h"
 #include "scan_math.h"
 
@@ -29,11 +31,14 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 // done, and the lowest unfinished one waits for nobody.  A published word is its
 // own flag: the workspace is filled with ones (a NaN that is never stored)
 // first, and words are written and read whole by relaxed atomics of device
-// scope, so nothing else has to be ordered.  The poll count is bounded all the
-// same; running out gives NaN.
+// scope, so nothing else has to be ordered.  One more word per chunk and block of
+// channels says how far it is; it only tells 64 lanes where to look, at 64
+// chunks in one load.  The poll count is bounded all the same; running out
+// gives NaN.
 
 constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr int kMaxPolls = 1 << 22;
+enum : uint32_t { kNothing = 0, kMap = 1, kState = 2 };
 
 __device__ __forceinline__ uint32_t word(float v) {
     const uint32_t u = __float_as_uint(v);
@@ -51,10 +56,12 @@ template <typename W> __device__ __forceinline__ W get(const W *p) {
 
 // Chunks are blocks of `tokens` tokens (packed_block numbers them).
 struct Chunks {
-    int tokens, per;
+    int tokens, per, nct;   // nct: blocks of channels
     int64_t total;
     uint32_t *counter;
     int32_t *off;           // offsets clamped to [0, rows] and made to ascend
+    float *rate;            // (C): k
+    uint32_t *stage;        // (total, nct): kNothing, kMap, kState
     uint64_t *map;          // (total, C): A, H
     uint32_t *state;        // (total, C): state behind the chunk
 };
@@ -65,10 +72,10 @@ struct Tile {
 };
 
 // REV: later chunks of a sequence first.
-template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const Chunks &ch, int nct, uint32_t ticket) {
+template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const Chunks &ch, uint32_t ticket) {
     Tile t;
-    t.ct = ticket % nct;
-    const int64_t rest = ticket / nct;
+    t.ct = ticket % ch.nct;
+    const int64_t rest = ticket / ch.nct;
     if (!s.off || ch.per == 1) {
         t.b = (int)(rest % s.B);
         const int k = (int)(rest / s.B);
@@ -89,72 +96,92 @@ __device__ __forceinline__ uint32_t take_ticket(uint32_t *counter, uint32_t *sha
     return __builtin_amdgcn_readfirstlane(*shared);
 }
 
-// The state that reaches chunk `slot` from the chunks at slot + dir, slot + 2 dir, ... (nearest first;
-// `n` of them, the last of which publishes its state without waiting).  One wave; lanes beyond the
-// channels hold a valid column.
+// The state that reaches a chunk from those at slot + dir, slot + 2 dir, ... (nearest first; `n` of them,
+// the last of which publishes its state without waiting).  One whole wave.
 template <int VEC>
-__device__ __forceinline__ void carry_in(const Chunks &ch, int C, int c, int64_t slot, int dir, int n, float (&h)[VEC]) {
-    constexpr int kAhead = 4;
-    const uint64_t *maps = ch.map + slot * C + c;
-    const uint32_t *states = ch.state + slot * C + c;
-    const int64_t step = (int64_t)dir * C;
+__device__ __forceinline__ void carry_in(const Chunks &ch, int C, int c, const Tile &tile, int dir, int n, float (&h)[VEC]) {
+    const int lane = threadIdx.x & 63;
     int at = 1, polls = 0, found = 0;
-    uint32_t st[kAhead][VEC];
     while (!found) {
-        uint64_t mp[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t o = (int64_t)min(at + i, n) * step;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) st[i][v] = get(states + o + v);
-            mp[i] = get(maps + o + VEC - 1);
-            if (VEC > 1 && (uint32_t)get(maps + o) == kEmpty) mp[i] = kEmpty;
-        }
-        int moved = 0;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            bool ready = true;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) ready = ready && st[i][v] != kEmpty;
-            if (!found && moved == i && at + i <= n) {
-                if (__all(ready)) {
-                    found = at + i;
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) h[v] = __uint_as_float(st[i][v]);
-                } else if (at + i < n && __all((uint32_t)mp[i] != kEmpty)) {
-                    ++moved;
-                }
-            }
-        }
-        at += moved;
-        if (!found && !moved) {
-            if (++polls > kMaxPolls) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = __uint_as_float(0x7fc00000u);
-                return;
-            }
+        const int i = at + lane;
+        const uint32_t st = i <= n ? get(ch.stage + (tile.slot + (int64_t)dir * i) * ch.nct + tile.ct) : kNothing;
+        const uint64_t states = __ballot(st == kState), some = __ballot(st != kNothing);
+        const int lead = ~some ? __builtin_ctzll(~some) : 64;      // chunks in a row that have published something
+        const int f = states ? __builtin_ctzll(states) : 64;
+        if (f < lead) {
+            found = at + f;
+        } else if (lead == 64) {
+            at += 64;
+        } else {
+            if (++polls > kMaxPolls) break;
             __builtin_amdgcn_s_sleep(1);
         }
     }
-    for (int i = found - 1; i >= 1; i -= kAhead) {
-        uint64_t mp[kAhead][VEC];
+    const int64_t step = (int64_t)dir * C;
+    const uint32_t *sp = ch.state + tile.slot * C + c + found * step;
+    const uint64_t *mp = ch.map + tile.slot * C + c;
+    bool ok = found > 0;
+    for (int v = 0; v < VEC && ok; ++v) {
+        uint32_t u = get(sp + v);
+        while (!__all(u != kEmpty) && (ok = ++polls <= kMaxPolls)) u = get(sp + v);
+        h[v] = __uint_as_float(u);
+    }
+    constexpr int kAhead = 8 / VEC;
+    for (int i = found - 1; i >= 1 && ok;) {
+        uint64_t m[kAhead][VEC];
+        bool ready = true;
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) mp[q][v] = get(maps + (int64_t)max(i - q, 1) * step + v);
+            for (int v = 0; v < VEC; ++v) m[q][v] = get(mp + (int64_t)max(i - q, 1) * step + v);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) ready = ready && (uint32_t)m[q][v] != kEmpty;
+        if (!__all(ready)) {
+            ok = ++polls <= kMaxPolls;
+            continue;
+        }
 #pragma unroll
         for (int q = 0; q < kAhead; ++q)
             if (i - q >= 1) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = fmaf(low(mp[q][v]), h[v], high(mp[q][v]));
+                for (int v = 0; v < VEC; ++v) h[v] = fmaf(low(m[q][v]), h[v], high(m[q][v]));
             }
+        i -= kAhead;
+    }
+    if (!ok) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h[v] = __uint_as_float(0x7fc00000u);
     }
 }
 
-// Empties the links, and (block 0, packed sequences) makes the offsets ascend.
-__global__ __launch_bounds__(256) void scan_fill_kernel(Seq s, Chunks ch, int64_t n) {
+template <int VEC>
+__device__ __forceinline__ void publish_map(const Chunks &ch, int C, int c, const Tile &t, const float (&A)[VEC],
+                                            const float (&H)[VEC], bool on) {
+    if (on) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) put(ch.map + t.slot * C + c + v, pair(A[v], H[v]));
+    }
+    put(ch.stage + t.slot * ch.nct + t.ct, (uint32_t)kMap);
+}
+template <int VEC>
+__device__ __forceinline__ void publish_state(const Chunks &ch, int C, int c, const Tile &t, const float (&h)[VEC], bool on) {
+    if (on) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) put(ch.state + t.slot * C + c + v, word(h[v]));
+    }
+    put(ch.stage + t.slot * ch.nct + t.ct, (uint32_t)kState);
+}
+
+// Empties the links (n units of 16 bytes of ones from ch.map on, zeros before), makes the channels'
+// rates, and (block 0, packed sequences) the ascending offsets.
+__global__ __launch_bounds__(256) void scan_fill_kernel(Seq s, Chunks ch, int64_t n, float scale,
+                                                        const float *__restrict__ decay) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) reinterpret_cast<uint4 *>(ch.map)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+    if (i < ch.total * ch.nct) ch.stage[i] = kNothing;
+    if (i < s.C) ch.rate[i] = scan_rate(scale, decay[i]);
     if (i == 0) *ch.counter = 0;
     if (s.off && blockIdx.x == 0 && threadIdx.x < 64) {
         int most = 0;
@@ -173,6 +200,29 @@ __global__ __launch_bounds__(256) void scan_fill_kernel(Seq s, Chunks ch, int64_
     }
 }
 
+// The channels' rates, from the fill kernel or, where no sequence has a second chunk, made here.
+template <int VEC, bool CHAIN>
+__device__ __forceinline__ void get_rates(const Chunks &ch, float scale, const float *decay, int c, ScanRate (&k)[VEC]) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) k[v].set(CHAIN ? ch.rate[c + v] : scan_rate(scale, decay[c + v]));
+}
+
+// Lane addresses: a uniform row and a 32-bit byte offset, which the memory instructions add themselves.
+template <typename T> __device__ __forceinline__ T *at_byte(T *row, uint32_t bytes) {
+    return reinterpret_cast<T *>(const_cast<char *>(reinterpret_cast<const char *>(row)) + bytes);
+}
+
+// N rows from p on (uniform; off: this lane's channel, in bytes); only the first `there` of them exist, and the last
+// of those stands in for the rest.
+template <typename T, int VEC, int N, bool FULL>
+__device__ __forceinline__ void load_rows(typename Pack<T, VEC>::type (&v)[N], const T *p, int64_t ld, uint32_t off, int there) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = load_pack<T, VEC>(at_byte(p, off));
+        if (FULL || i + 1 < there) p += ld;
+    }
+}
+
 // ---- forward -----------------------------------------------------------------------
 
 constexpr int kFwdRun = 16, kFwdChunk = kWaves * kFwdRun;      // tokens of a wave and of a workgroup
@@ -181,11 +231,11 @@ template <typename T, int VEC, bool CHAIN>
 __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
     Seq s, float scale, const T *__restrict__ x, int64_t ldx, const T *__restrict__ gate, int64_t ldg,
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ h0,
-    T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch, int nct) {
+    T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch) {
     constexpr int L = kFwdRun, CW = 64 * VEC;
     __shared__ float sA[kWaves][CW], sH[kWaves][CW], sC[CW];
     __shared__ uint32_t sTicket;
-    const Tile tile = get_tile<false>(s, ch, nct, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
+    const Tile tile = get_tile<false>(s, ch, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -196,38 +246,39 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
     const int cw = tile.ct * CW + lane * VEC;
     const bool on = cw < C;
     const int c = min(cw, C - VEC);                // odd C: the last lane shares a channel, with the same results
-    const int tw = t0 + w * L;                     // this wave's tokens: tw .. min(tw + L, len)
-    float k[VEC], a[L][VEC], bb[L][VEC], A[VEC], H[VEC];
+    const uint32_t off = (uint32_t)c * sizeof(T);
+    const int tw = t0 + w * L, there = len - tw;   // this wave's tokens: L from tw on, or `there`
+    float a[L][VEC], bb[L][VEC], A[VEC], H[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) A[v] = 1.f, H[v] = 0.f;
-    if (tw < len) {
+    const auto read = [&](auto full_) {
+        constexpr bool full = decltype(full_)::value;
         typename Pack<T, VEC>::type xr[L], gr[L], ir[L];
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int64_t row = first + min(tw + i, len - 1);
-            gr[i] = load_pack<T, VEC>(gate + row * ldg + c);
-            ir[i] = load_pack<T, VEC>(inp + row * ldi + c);
-            xr[i] = load_pack<T, VEC>(x + row * ldx + c);
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) k[v] = scan_rate(scale, decay[c + v]);
+        load_rows<T, VEC, L, full>(gr, gate + (first + tw) * ldg, ldg, off, there);
+        load_rows<T, VEC, L, full>(ir, inp + (first + tw) * ldi, ldi, off, there);
+        load_rows<T, VEC, L, full>(xr, x + (first + tw) * ldx, ldx, off, there);
+        ScanRate k[VEC];
+        get_rates<VEC, CHAIN>(ch, scale, decay, c, k);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             float xv[VEC], gv[VEC], iv[VEC];
             to_f32(xr[i], xv);
             to_f32(gr[i], gv);
             to_f32(ir[i], iv);
-            const bool in = tw + i < len;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const ScanGates g(k[v], gv[v], iv[v]);
-                a[i][v] = in ? g.a : 1.f;
-                bb[i][v] = in ? g.m * g.s * xv[v] : 0.f;
+                a[i][v] = full || i < there ? g.a : 1.f;
+                bb[i][v] = full || i < there ? g.m * g.s * xv[v] : 0.f;
                 A[v] *= a[i][v];
                 H[v] = fmaf(a[i][v], H[v], bb[i][v]);
             }
         }
-    }
+    };
+    if (there >= L)
+        read(std::true_type{});
+    else if (there > 0)
+        read(std::false_type{});
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sA[w][lane * VEC + v] = A[v], sH[w][lane * VEC + v] = H[v];
     __syncthreads();
@@ -242,26 +293,23 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
             PA[v] *= Aq;
         }
     if (w == kWaves - 1) {                       // this wave has the whole chunk's map
-        float c0[VEC];
+        float c0[VEC], out[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             H[v] = fmaf(A[v], PH[v], H[v]);
             A[v] *= PA[v];
         }
-        const bool last = !CHAIN || t0 + kFwdChunk >= len;
-        const int64_t at = tile.slot * C + c;
+        const bool more = CHAIN && t0 + kFwdChunk < len;
         if (tile.k == 0) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) c0[v] = h0 ? h0[(int64_t)b * C + c + v] : 0.f;
         } else if (CHAIN) {
-            if (!last && on)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) put(ch.map + at + v, pair(A[v], H[v]));
-            carry_in<VEC>(ch, C, c, tile.slot, -1, tile.k, c0);
+            if (more) publish_map<VEC>(ch, C, c, tile, A, H, on);
+            carry_in<VEC>(ch, C, c, tile, -1, tile.k, c0);
         }
-        if (!last && on)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) put(ch.state + at + v, word(fmaf(A[v], c0[v], H[v])));
+        for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], H[v]);
+        if (more) publish_state<VEC>(ch, C, c, tile, out, on);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) sC[lane * VEC + v] = c0[v];
     }
@@ -270,25 +318,30 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = fmaf(PA[v], sC[lane * VEC + v], PH[v]);
     if (!on) return;
-    if (tw < len) {
-        if (states && tw % kBlock == 0) {
-            const int64_t nb = (s.T + kBlock - 1) / kBlock;
+    if (states && there > 0 && tw % kBlock == 0) {
+        const int64_t nb = (s.T + kBlock - 1) / kBlock;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) states[(b * nb + tw / kBlock) * C + c + v] = h[v];
-        }
+        for (int v = 0; v < VEC; ++v) states[(b * nb + tw / kBlock) * C + c + v] = h[v];
+    }
+    const auto write = [&](auto full_) {
+        constexpr bool full = decltype(full_)::value;
+        T *yp = y + (first + tw) * ldy;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[i][v], h[v], bb[i][v]);
-            if (tw + i < len) store_f32(y + (first + tw + i) * ldy + c, h);
+            if (full || i < there) store_f32(at_byte(yp, off), h);
+            yp += ldy;
         }
-        if (hT && tw + L >= len)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) hT[(int64_t)b * C + c + v] = h[v];
-    } else if (hT && len == 0 && w == 0) {
+    };
+    if (there >= L)
+        write(std::true_type{});
+    else if (there > 0)
+        write(std::false_type{});
+    // the wave of the last token, or of an empty sequence the first one
+    if (hT && (there > 0 ? there <= L : len == 0 && w == 0))
 #pragma unroll
         for (int v = 0; v < VEC; ++v) hT[(int64_t)b * C + c + v] = h[v];
-    }
 }
 
 // ---- backward ----------------------------------------------------------------------
@@ -307,11 +360,11 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ states,
     const T *__restrict__ dy, int64_t lddy, const float *__restrict__ dhT, T *__restrict__ dx, int64_t lddx,
     T *__restrict__ dgate, int64_t lddg, T *__restrict__ dinp, int64_t lddi, float *__restrict__ part,
-    float *__restrict__ dh0, Chunks ch, int nct) {
+    float *__restrict__ dh0, Chunks ch) {
     constexpr int L = kBwdRun, CW = 64 * VEC;
     __shared__ float sA[kWaves][CW], sH[kWaves][CW], sE[kWaves][CW], sC[CW];
     __shared__ uint32_t sTicket;
-    const Tile tile = get_tile<true>(s, ch, nct, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
+    const Tile tile = get_tile<true>(s, ch, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -321,7 +374,8 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const int cw = tile.ct * CW + lane * VEC;
     const bool on = cw < C;
     const int c = min(cw, C - VEC);                // odd C: the last lane shares a channel, with the same results
-    if (tile.k < 0 || t0 >= len) {                // an unused number, or an empty sequence
+    const uint32_t off = (uint32_t)c * sizeof(T);
+    if (tile.k < 0 || t0 >= len) {                 // an unused number, or an empty sequence
         if (on && w == 0)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
@@ -331,37 +385,41 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
             }
         return;
     }
-    const int tw = t0 + w * L;
-    float k[VEC], A[VEC], H[VEC], E[VEC];
-    float a[L][VEC], r[L][VEC], sg[L][VEC], im[L][VEC], m[L][VEC];
-    typename Pack<T, VEC>::type xr[L], gr[L], ir[L], dr[L];
+    const int tw = t0 + w * L, there = len - tw;
+    float h[VEC], A[VEC], H[VEC], E[VEC];
+    // per token: a, r, s; ms = m s; and q = s x a / m, later a (h[t-1] - q)
+    float a[L][VEC], r[L][VEC], sg[L][VEC], ms[L][VEC], q[L][VEC];
+    typename Pack<T, VEC>::type xr[L], dr[L];
+    ScanRate k[VEC];
+    const int64_t nb = (s.T + kBlock - 1) / kBlock;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) A[v] = 1.f, H[v] = 0.f, E[v] = 0.f;
-    if (tw < len) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int64_t row = first + min(tw + i, len - 1);
-            gr[i] = load_pack<T, VEC>(gate + row * ldg + c);
-            ir[i] = load_pack<T, VEC>(inp + row * ldi + c);
-            xr[i] = load_pack<T, VEC>(x + row * ldx + c);
-            dr[i] = load_pack<T, VEC>(dy + row * lddy + c);
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) k[v] = scan_rate(scale, decay[c + v]);
+    for (int v = 0; v < VEC; ++v) {
+        A[v] = 1.f, H[v] = 0.f, E[v] = 0.f;
+        h[v] = states[(b * nb + tile.k) * C + c + v];
+    }
+    const auto read = [&](auto full_) {
+        constexpr bool full = decltype(full_)::value;
+        typename Pack<T, VEC>::type gr[L], ir[L];
+        load_rows<T, VEC, L, full>(gr, gate + (first + tw) * ldg, ldg, off, there);
+        load_rows<T, VEC, L, full>(ir, inp + (first + tw) * ldi, ldi, off, there);
+        load_rows<T, VEC, L, full>(xr, x + (first + tw) * ldx, ldx, off, there);
+        load_rows<T, VEC, L, full>(dr, dy + (first + tw) * lddy, lddy, off, there);
+        get_rates<VEC, CHAIN>(ch, scale, decay, c, k);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             float xv[VEC], gv[VEC], iv[VEC];
             to_f32(xr[i], xv);
             to_f32(gr[i], gv);
             to_f32(ir[i], iv);
-            const bool in = tw + i < len;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const ScanGates g(k[v], gv[v], iv[v]);
+                const bool in = full || i < there;
                 a[i][v] = in ? g.a : 1.f;
-                r[i][v] = g.r, sg[i][v] = g.s, im[i][v] = g.im, m[i][v] = in ? g.m : 0.f;
+                r[i][v] = g.r, sg[i][v] = g.s, ms[i][v] = in ? g.m * g.s : 0.f;
+                q[i][v] = g.s * xv[v] * g.a * g.im;
                 A[v] *= a[i][v];
-                H[v] = fmaf(a[i][v], H[v], in ? g.m * g.s * xv[v] : 0.f);
+                H[v] = fmaf(a[i][v], H[v], ms[i][v] * xv[v]);
             }
         }
 #pragma unroll
@@ -369,102 +427,110 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
             float dv[VEC];
             to_f32(dr[i], dv);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) E[v] = a[i][v] * (tw + i < len ? dv[v] + E[v] : E[v]);
+            for (int v = 0; v < VEC; ++v) E[v] = a[i][v] * (full || i < there ? dv[v] + E[v] : E[v]);
         }
-    }
+    };
+    if (there >= L)
+        read(std::true_type{});
+    else if (there > 0)
+        read(std::false_type{});
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
         sA[w][lane * VEC + v] = A[v], sH[w][lane * VEC + v] = H[v], sE[w][lane * VEC + v] = E[v];
     __syncthreads();
     // h in front of this wave's tokens; the map from the chunk's e_in to this wave's
-    float h[VEC], PA[VEC], PE[VEC];
-    const int64_t nb = (s.T + kBlock - 1) / kBlock;
+    float PA[VEC], PE[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        h[v] = states[(b * nb + tile.k) * C + c + v];
-        PA[v] = 1.f, PE[v] = 0.f;
-    }
-    for (int q = 0; q < w; ++q)
+    for (int v = 0; v < VEC; ++v) PA[v] = 1.f, PE[v] = 0.f;
+    for (int p = 0; p < w; ++p)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = fmaf(sA[q][lane * VEC + v], h[v], sH[q][lane * VEC + v]);
-    for (int q = kWaves - 1; q > w; --q)
+        for (int v = 0; v < VEC; ++v) h[v] = fmaf(sA[p][lane * VEC + v], h[v], sH[p][lane * VEC + v]);
+    for (int p = kWaves - 1; p > w; --p)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float Aq = sA[q][lane * VEC + v];
-            PE[v] = fmaf(Aq, PE[v], sE[q][lane * VEC + v]);
+            const float Aq = sA[p][lane * VEC + v];
+            PE[v] = fmaf(Aq, PE[v], sE[p][lane * VEC + v]);
             PA[v] *= Aq;
         }
     if (w == 0) {
-        float c0[VEC];
+        float c0[VEC], out[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             E[v] = fmaf(A[v], PE[v], E[v]);
             A[v] *= PA[v];
         }
         const int behind = (len + kBwdChunk - 1) / kBwdChunk - 1 - tile.k;       // chunks after this one
-        const int64_t at = tile.slot * C + c;
+        const bool more = CHAIN && tile.k > 0;
         if (!CHAIN || behind == 0) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) c0[v] = dhT ? dhT[(int64_t)b * C + c + v] : 0.f;
         } else {
-            if (tile.k > 0 && on)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) put(ch.map + at + v, pair(A[v], E[v]));
-            carry_in<VEC>(ch, C, c, tile.slot, 1, behind, c0);
+            if (more) publish_map<VEC>(ch, C, c, tile, A, E, on);
+            carry_in<VEC>(ch, C, c, tile, 1, behind, c0);
         }
-        if (on)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], E[v]);
+        if (more) publish_state<VEC>(ch, C, c, tile, out, on);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            if (on && dh0 && tile.k == 0) dh0[(int64_t)b * C + c + v] = out[v];
+            sC[lane * VEC + v] = c0[v];
+        }
+    }
+    // h forward through this wave's tokens, while the first wave waits
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (i < there) {
+            float xv[VEC];
+            to_f32(xr[i], xv);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float out = fmaf(A[v], c0[v], E[v]);
-                if (CHAIN && tile.k > 0) put(ch.state + at + v, word(out));
-                if (dh0 && tile.k == 0) dh0[(int64_t)b * C + c + v] = out;
+                q[i][v] = a[i][v] * (h[v] - q[i][v]);
+                h[v] = fmaf(a[i][v], h[v], ms[i][v] * xv[v]);
             }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sC[lane * VEC + v] = c0[v];
+        }
     }
     __syncthreads();
     float dk[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) dk[v] = 0.f;
-    if (tw < len) {
-        float e[VEC], before[L][VEC];
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            float xv[VEC];
-            to_f32(xr[i], xv);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                before[i][v] = h[v];
-                h[v] = fmaf(a[i][v], h[v], m[i][v] * sg[i][v] * xv[v]);
-            }
-        }
+    const auto write = [&](auto full_) {
+        constexpr bool full = decltype(full_)::value;
+        float e[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) e[v] = fmaf(PA[v], sC[lane * VEC + v], PE[v]);
+        const int last = full ? L - 1 : there - 1;
+        T *dxp = dx + (first + tw + last) * lddx, *dgp = dgate + (first + tw + last) * lddg,
+          *dip = dinp + (first + tw + last) * lddi;
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
-            if (tw + i >= len) continue;
+            if (!full && i >= there) continue;
             float xv[VEC], dv[VEC], o0[VEC], o1[VEC], o2[VEC];
             to_f32(xr[i], xv);
             to_f32(dr[i], dv);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float dh = dv[v] + e[v], dms = dh * m[i][v] * sg[i][v];
-                const float dla = dh * a[i][v] * (before[i][v] - sg[i][v] * xv[v] * a[i][v] * im[i][v]);
-                const float rdla = r[i][v] * dla;
-                o0[v] = dms;
-                o1[v] = -k[v] * rdla * (1.f - r[i][v]);
-                o2[v] = dms * xv[v] * (1.f - sg[i][v]);
+                const float dh = dv[v] + e[v], rdla = r[i][v] * (dh * q[i][v]);
+                o0[v] = dh * ms[i][v];
+                o1[v] = -k[v].k * rdla * (1.f - r[i][v]);
+                o2[v] = o0[v] * xv[v] * (1.f - sg[i][v]);
                 dk[v] += rdla;
                 e[v] = a[i][v] * dh;
             }
             if (on) {
-                const int64_t row = first + tw + i;
-                store_f32(dx + row * lddx + c, o0);
-                store_f32(dgate + row * lddg + c, o1);
-                store_f32(dinp + row * lddi + c, o2);
+                store_f32(at_byte(dxp, off), o0);
+                store_f32(at_byte(dgp, off), o1);
+                store_f32(at_byte(dip, off), o2);
             }
+            dxp -= lddx;
+            dgp -= lddg;
+            dip -= lddi;
         }
-    }
+    };
+    if (there >= L)
+        write(std::true_type{});
+    else if (there > 0)
+        write(std::false_type{});
     // sA is free: every wave read it before the barrier above
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sA[w][lane * VEC + v] = dk[v];
@@ -473,7 +539,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             float d = 0.f;
-            for (int q = 0; q < kWaves; ++q) d += sA[q][lane * VEC + v];
+            for (int p = 0; p < kWaves; ++p) d += sA[p][lane * VEC + v];
             part[tile.slot * C + c + v] = d;
         }
 }
@@ -516,7 +582,9 @@ __global__ __launch_bounds__(256) void scan_step_kernel(int B, int C, float scal
     load_f32<T, 1>(x + b * ldx + c, xv);
     load_f32<T, 1>(gate + b * ldg + c, gv);
     load_f32<T, 1>(inp + b * ldi + c, iv);
-    const ScanGates g(scan_rate(scale, decay[c]), gv[0], iv[0]);
+    ScanRate k;
+    k.set(scan_rate(scale, decay[c]));
+    const ScanGates g(k, gv[0], iv[0]);
     const float o[1] = {fmaf(g.a, h[i], g.m * g.s * xv[0])};
     h[i] = o[0];
     store_f32(y + b * ldy + c, o);
@@ -526,27 +594,34 @@ Chunks chunks(const Seq &s, int tokens) {
     Chunks ch = {};
     ch.tokens = tokens;
     ch.per = s.T > 0 ? (s.T + tokens - 1) / tokens : 1;
+    ch.nct = (s.C + 63) / 64;          // of the narrowest kernel: the workspace does not depend on the dtype
     ch.total = block_count(s, tokens, ch.per);
     return ch;
 }
 
-// Workspace of the links: the counter (16 bytes), the offsets, then per chunk and channel 8 bytes of
-// map and 4 of state, each part to a multiple of 16; none if no sequence has a second chunk.
-int64_t off_bytes(const Seq &s) { return s.off ? ((int64_t)s.B + 4) / 4 * 16 : 0; }
-int64_t link_units(const Seq &s, const Chunks &ch) { return (ch.total * s.C * 12 + 15) / 16; }
+// Workspace of the links: the counter, the offsets, the rates, the stages, and then per chunk and channel
+// 8 bytes of map and 4 of state, each part to a multiple of 16; none if no sequence has a second chunk.
+int64_t pad16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+int64_t off_bytes(const Seq &s) { return s.off ? pad16(4 * ((int64_t)s.B + 1)) : 0; }
+int64_t stage_bytes(const Chunks &ch) { return pad16(4 * ch.total * ch.nct); }
+int64_t link_units(const Seq &s, const Chunks &ch) { return pad16(ch.total * s.C * 12) / 16; }
 size_t link_bytes(const Seq &s, const Chunks &ch) {
-    return ch.per > 1 ? (size_t)(16 + off_bytes(s) + 16 * link_units(s, ch)) : 0;
+    return ch.per > 1 ? (size_t)(16 + off_bytes(s) + pad16(4 * s.C) + stage_bytes(ch) + 16 * link_units(s, ch)) : 0;
 }
 
 // Lays the links out in ws and empties them; s then has the ascending offsets.
-void set_links(Seq &s, Chunks &ch, void *ws, hipStream_t st) {
+void set_links(Seq &s, Chunks &ch, void *ws, float scale, const float *decay, hipStream_t st) {
     if (ch.per <= 1) return;
-    ch.counter = (uint32_t *)ws;
-    ch.off = (int32_t *)((char *)ws + 16);
-    ch.map = (uint64_t *)((char *)ws + 16 + off_bytes(s));
+    char *p = (char *)ws;
+    ch.counter = (uint32_t *)p;
+    ch.off = (int32_t *)(p += 16);
+    ch.rate = (float *)(p += off_bytes(s));
+    ch.stage = (uint32_t *)(p += pad16(4 * s.C));
+    ch.map = (uint64_t *)(p += stage_bytes(ch));
     ch.state = (uint32_t *)(ch.map + ch.total * s.C);
+    // one thread per unit; there are at least as many units as stages and as channels
     const int64_t n = link_units(s, ch);
-    scan_fill_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s, ch, n);
+    scan_fill_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s, ch, n, scale, decay);
     if (s.off) s.off = ch.off;
 }
 
@@ -562,14 +637,14 @@ template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
                      Chunks ch, hipStream_t st) {
-    const int nct = (s.C + 64 * VEC - 1) / (64 * VEC);
-    const unsigned grid = (unsigned)(ch.total * nct);
+    ch.nct = (s.C + 64 * VEC - 1) / (64 * VEC);
+    const unsigned grid = (unsigned)(ch.total * ch.nct);
     if (ch.per > 1)
         scan_fwd_kernel<T, VEC, true><<<grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
-                                                                 (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch, nct);
+                                                                 (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
     else
         scan_fwd_kernel<T, VEC, false><<<grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
-                                                                  (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch, nct);
+                                                                  (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
 }
 
 hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate,
@@ -577,7 +652,7 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
                            int64_t ldy, float *hT, float *states, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, st);
+    set_links(q, ch, ws, scale, decay, st);
     const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, st);
     return hipGetLastError();
@@ -588,16 +663,16 @@ static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, cons
                      int64_t ldi, const float *decay, const float *states, const void *dy, int64_t lddy, const float *dhT,
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
                      Chunks ch, hipStream_t st) {
-    const int nct = (s.C + 64 * VEC - 1) / (64 * VEC);
-    const unsigned grid = (unsigned)(ch.total * nct);
+    ch.nct = (s.C + 64 * VEC - 1) / (64 * VEC);
+    const unsigned grid = (unsigned)(ch.total * ch.nct);
     if (ch.per > 1)
         scan_bwd_kernel<T, VEC, true><<<grid, kThreads, 0, st>>>(
             s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi, decay, states, (const T *)dy, lddy, dhT,
-            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch, nct);
+            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch);
     else
         scan_bwd_kernel<T, VEC, false><<<grid, kThreads, 0, st>>>(
             s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi, decay, states, (const T *)dy, lddy, dhT,
-            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch, nct);
+            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch);
 }
 
 hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -606,7 +681,7 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
                            float *ddecay, float *dh0, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kBwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, st);
+    set_links(q, ch, ws, scale, decay, st);
     float *part = (float *)((char *)ws + link_bytes(s, ch));
     const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,

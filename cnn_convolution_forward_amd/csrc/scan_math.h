@@ -24,16 +24,25 @@ __device__ __forceinline__ float one_minus_sq(float w, float a) {
     return w < 0.25f ? w * p : fmaf(-a, a, 1.f);
 }
 
+// A channel's constants: -k log2(e), so that a = 2^(kl r), and w = k2 r.
+struct ScanRate {
+    float k, kl, k2;
+    __device__ __forceinline__ void set(float rate) {
+        k = rate;
+        kl = -kLog2e * rate;
+        k2 = rate + rate;
+    }
+};
+
 // v = 0 (k r underflows, or the gate is -inf) leaves h as it is: m is 0 then,
 // and the clamp keeps 1/m finite, as it stands beside factors of k r, or 0.
 struct ScanGates {
     float r, s, a, m, im;     // m = sqrt(1 - a^2), im = 1/m
-    __device__ __forceinline__ ScanGates(float k, float gate, float inp) {
+    __device__ __forceinline__ ScanGates(const ScanRate &c, float gate, float inp) {
         r = sigmoid(gate);
         s = sigmoid(inp);
-        const float z = k * r;
-        a = __builtin_amdgcn_exp2f(-kLog2e * z);
-        const float v = one_minus_sq(z + z, a);
+        a = __builtin_amdgcn_exp2f(c.kl * r);
+        const float v = one_minus_sq(c.k2 * r, a);
         im = __builtin_amdgcn_rsqf(fmaxf(v, 1.17549435e-38f));
         m = v * im;
     }
