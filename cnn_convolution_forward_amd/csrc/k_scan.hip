@@ -1,10 +1,17 @@
 // k_scan.hip -- the gated linear recurrence over tokens: forward, backward and
 // the single-token step (conv_scan_*).
+#include <algorithm>
 #include <type_traits>
 
 #include "conv_fwd.h"
 #include "scan_math.h"
 
+#ifndef BV
+#define BV 2
+#endif
+#ifndef FV
+#define FV 2
+#endif
 namespace convfwd {
 namespace {
 
@@ -28,7 +35,11 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 //
 // Waits end: workgroups take their chunk from a counter, chunks of a sequence
 // in order, so every predecessor is held by a workgroup that is running or
-// done, and the lowest unfinished one waits for nobody.  A published word is its
+// done, and the lowest unfinished one waits for nobody.  One counter for all
+// would be the bound: adds to one address follow each other at about 18 ns, 2048
+// chunks of the training batch 37 us; so there are some 64, each with blocks of
+// channels and sequences of its own, and a workgroup's index says which it uses.
+// A published word is its
 // own flag: the workspace is filled with ones (a NaN that is never stored)
 // first, and words are written and read whole by relaxed atomics of device
 // scope, so nothing else has to be ordered.  One more word per chunk and block of
@@ -57,8 +68,9 @@ template <typename W> __device__ __forceinline__ W get(const W *p) {
 // Chunks are blocks of `tokens` tokens (packed_block numbers them).
 struct Chunks {
     int tokens, per, nct;   // nct: blocks of channels
+    int groups, nb;         // counters (a multiple of nct), sequences of each
     int64_t total;
-    uint32_t *counter;
+    uint32_t *counter;      // kCounter apart
     int32_t *off;           // offsets clamped to [0, rows] and made to ascend
     float *rate;            // (C): k
     uint32_t *stage;        // (total, nct): kNothing, kMap, kState
@@ -66,93 +78,122 @@ struct Chunks {
     uint32_t *state;        // (total, C): state behind the chunk
 };
 
+constexpr int kCounter = 16;        // words: a counter has 64 bytes to itself
+
 struct Tile {
     int b, k, ct;           // sequence, chunk in it (negative: an unused number), block of channels
-    int64_t slot;           // number of the chunk
+    int64_t slot;           // number of the chunk; negative: there is none
 };
 
+// The tile of ticket t of group g (of the whole grid where there is no chain and so no counter).  Groups
+// g = gb * nct + ct share out the blocks of channels and, in equal batches, the sequences gb, gb + gB, ...
 // REV: later chunks of a sequence first.
-template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const Chunks &ch, uint32_t ticket) {
-    Tile t;
-    t.ct = ticket % ch.nct;
-    const int64_t rest = ticket / ch.nct;
+template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const Chunks &ch, uint32_t g, uint32_t t) {
+    Tile o;
+    o.ct = g % ch.nct;
     if (!s.off || ch.per == 1) {
-        t.b = (int)(rest % s.B);
-        const int k = (int)(rest / s.B);
-        t.k = REV ? ch.per - 1 - k : k;
-        t.slot = (int64_t)t.b * ch.per + t.k;
+        const int k = (int)(t / ch.nb);
+        o.b = (int)(g / ch.nct + (t % ch.nb) * (ch.groups / ch.nct));
+        o.k = REV ? ch.per - 1 - k : k;
+        o.slot = (int64_t)o.b * ch.per + o.k;
+        if (o.b >= s.B) o.b = 0, o.k = -1, o.slot = -1;
     } else {
-        t.slot = REV ? ch.total - 1 - rest : rest;
-        const Block k = packed_block(s, ch.tokens, t.slot);
-        t.b = k.b;
-        t.k = k.k;
+        o.slot = REV ? ch.total - 1 - t : t;
+        const Block k = packed_block(s, ch.tokens, o.slot);
+        o.b = k.b;
+        o.k = k.k;
     }
-    return t;
+    return o;
 }
 
-__device__ __forceinline__ uint32_t take_ticket(uint32_t *counter, uint32_t *shared) {
-    if (threadIdx.x == 0) *shared = atomicAdd(counter, 1u);
+template <bool CHAIN> __device__ __forceinline__ uint32_t take_ticket(const Chunks &ch, uint32_t g, uint32_t *shared) {
+    if (!CHAIN) return blockIdx.x / ch.groups;
+    if (threadIdx.x == 0) *shared = atomicAdd(ch.counter + g * kCounter, 1u);
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(*shared);
 }
 
+constexpr int kAhead = 2 * kWaves;      // maps read at once
+template <int VEC> struct Links {
+    float2 map[kAhead][64 * VEC];
+    int found;
+};
+
 // The state that reaches a chunk from those at slot + dir, slot + 2 dir, ... (nearest first; `n` of them,
-// the last of which publishes its state without waiting).  One whole wave.
+// the last of which publishes its state without waiting).  All waves of the workgroup: `leader` looks for
+// the nearest published state; the maps between it and here, which may be as many as there are workgroups
+// on the chip, are read by all waves at once, and folded by the leader, who gets h.
 template <int VEC>
-__device__ __forceinline__ void carry_in(const Chunks &ch, int C, int c, const Tile &tile, int dir, int n, float (&h)[VEC]) {
+__device__ __forceinline__ void carry_in(const Chunks &ch, int C, int c, const Tile &tile, int dir, int n, bool leader,
+                                         int w, Links<VEC> &sh, float (&h)[VEC]) {
     const int lane = threadIdx.x & 63;
-    int at = 1, polls = 0, found = 0;
-    while (!found) {
-        const int i = at + lane;
-        const uint32_t st = i <= n ? get(ch.stage + (tile.slot + (int64_t)dir * i) * ch.nct + tile.ct) : kNothing;
-        const uint64_t states = __ballot(st == kState), some = __ballot(st != kNothing);
-        const int lead = ~some ? __builtin_ctzll(~some) : 64;      // chunks in a row that have published something
-        const int f = states ? __builtin_ctzll(states) : 64;
-        if (f < lead) {
-            found = at + f;
-        } else if (lead == 64) {
-            at += 64;
-        } else {
-            if (++polls > kMaxPolls) break;
-            __builtin_amdgcn_s_sleep(1);
-        }
-    }
     const int64_t step = (int64_t)dir * C;
-    const uint32_t *sp = ch.state + tile.slot * C + c + found * step;
+    const uint32_t *sp = ch.state + tile.slot * C + c;
     const uint64_t *mp = ch.map + tile.slot * C + c;
-    bool ok = found > 0;
-    for (int v = 0; v < VEC && ok; ++v) {
-        uint32_t u = get(sp + v);
-        while (!__all(u != kEmpty) && (ok = ++polls <= kMaxPolls)) u = get(sp + v);
-        h[v] = __uint_as_float(u);
-    }
-    constexpr int kAhead = 8 / VEC;
-    for (int i = found - 1; i >= 1 && ok;) {
-        uint64_t m[kAhead][VEC];
-        bool ready = true;
+    int polls = 0;
+    if (leader) {
+        int at = 1, found = 0;
+        uint32_t u[VEC];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
+        for (int v = 0; v < VEC; ++v) u[v] = get(sp + step + v);      // most often it is the neighbour's
+        while (!found) {
+            const int i = at + lane;
+            const uint32_t st = i <= n ? get(ch.stage + (tile.slot + (int64_t)dir * i) * ch.nct + tile.ct) : kNothing;
+            const uint64_t states = __ballot(st == kState), some = __ballot(st != kNothing);
+            const int lead = ~some ? __builtin_ctzll(~some) : 64;     // chunks in a row that have published something
+            const int f = states ? __builtin_ctzll(states) : 64;
+            if (f < lead) {
+                found = at + f;
+            } else if (lead == 64) {
+                at += 64;
+            } else {
+                if (++polls > kMaxPolls) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
+        }
+        bool ready = found == 1;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) m[q][v] = get(mp + (int64_t)max(i - q, 1) * step + v);
+        for (int v = 0; v < VEC; ++v) ready = ready && u[v] != kEmpty;
+        while (found && !__all(ready)) {
+            ready = true;
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
+            for (int v = 0; v < VEC; ++v) u[v] = get(sp + found * step + v);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) ready = ready && (uint32_t)m[q][v] != kEmpty;
-        if (!__all(ready)) {
-            ok = ++polls <= kMaxPolls;
-            continue;
+            for (int v = 0; v < VEC; ++v) ready = ready && u[v] != kEmpty;
+            if (++polls > kMaxPolls) found = 0;
         }
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-            if (i - q >= 1) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = fmaf(low(m[q][v]), h[v], high(m[q][v]));
-            }
-        i -= kAhead;
+        for (int v = 0; v < VEC; ++v) h[v] = __uint_as_float(found ? u[v] : 0x7fc00000u);
+        if (lane == 0) sh.found = found;
     }
-    if (!ok) {
+    __syncthreads();
+    for (int i = __builtin_amdgcn_readfirstlane(sh.found) - 1; i >= 1; i -= kAhead) {
+        // wave w reads maps i - w, i - w - kWaves, ...
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) h[v] = __uint_as_float(0x7fc00000u);
+        for (int q = 0; q < kAhead / kWaves; ++q) {
+            const int j = i - w - q * kWaves;
+            if (j < 1) continue;
+            uint64_t m[VEC];
+            bool ok;
+            do {
+                ok = true;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) m[v] = get(mp + j * step + v);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) ok = ok && (uint32_t)m[v] != kEmpty;
+            } while (!__all(ok) && ++polls <= kMaxPolls);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sh.map[w + q * kWaves][lane * VEC + v] = make_float2(low(m[v]), high(m[v]));
+        }
+        __syncthreads();
+        if (leader)
+            for (int q = 0; q < min(i, kAhead); ++q)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float2 m = sh.map[q][lane * VEC + v];
+                    h[v] = fmaf(m.x, h[v], m.y);
+                }
+        __syncthreads();
     }
 }
 
@@ -182,7 +223,7 @@ __global__ __launch_bounds__(256) void scan_fill_kernel(Seq s, Chunks ch, int64_
     if (i < n) reinterpret_cast<uint4 *>(ch.map)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
     if (i < ch.total * ch.nct) ch.stage[i] = kNothing;
     if (i < s.C) ch.rate[i] = scan_rate(scale, decay[i]);
-    if (i == 0) *ch.counter = 0;
+    if (i < ch.groups) ch.counter[i * kCounter] = 0;
     if (s.off && blockIdx.x == 0 && threadIdx.x < 64) {
         int most = 0;
         for (int base = 0; base <= s.B; base += 64) {
@@ -225,17 +266,28 @@ __device__ __forceinline__ void load_rows(typename Pack<T, VEC>::type (&v)[N], c
 
 // ---- forward -----------------------------------------------------------------------
 
-constexpr int kFwdRun = 16, kFwdChunk = kWaves * kFwdRun;      // tokens of a wave and of a workgroup
+#ifndef FW
+#define FW 8
+#endif
+#ifndef FL
+#define FL 16
+#endif
+#ifndef FO
+#define FO 4
+#endif
+constexpr int kFwdWaves = FW, kFwdRun = FL, kFwdChunk = kFwdWaves * kFwdRun;      // tokens of a wave and of a workgroup
 
 template <typename T, int VEC, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
+__global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
     Seq s, float scale, const T *__restrict__ x, int64_t ldx, const T *__restrict__ gate, int64_t ldg,
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ h0,
     T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch) {
     constexpr int L = kFwdRun, CW = 64 * VEC;
-    __shared__ float sA[kWaves][CW], sH[kWaves][CW], sC[CW];
+    __shared__ float sA[kFwdWaves][CW], sH[kFwdWaves][CW], sC[CW];
+    __shared__ Links<VEC> sL;
     __shared__ uint32_t sTicket;
-    const Tile tile = get_tile<false>(s, ch, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
+    const uint32_t group = blockIdx.x % ch.groups;
+    const Tile tile = get_tile<false>(s, ch, group, take_ticket<CHAIN>(ch, group, &sTicket));
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -292,21 +344,24 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
             PH[v] = fmaf(Aq, PH[v], Hq);
             PA[v] *= Aq;
         }
-    if (w == kWaves - 1) {                       // this wave has the whole chunk's map
-        float c0[VEC], out[VEC];
+    float c0[VEC];
+    const bool more = CHAIN && t0 + kFwdChunk < len;
+    if (w == kFwdWaves - 1) {                       // this wave has the whole chunk's map
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             H[v] = fmaf(A[v], PH[v], H[v]);
             A[v] *= PA[v];
         }
-        const bool more = CHAIN && t0 + kFwdChunk < len;
         if (tile.k == 0) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) c0[v] = h0 ? h0[(int64_t)b * C + c + v] : 0.f;
         } else if (CHAIN) {
             if (more) publish_map<VEC>(ch, C, c, tile, A, H, on);
-            carry_in<VEC>(ch, C, c, tile, -1, tile.k, c0);
         }
+    }
+    if (CHAIN && tile.k > 0) carry_in<VEC>(ch, C, c, tile, -1, tile.k, w == kFwdWaves - 1, w, sL, c0);
+    if (w == kFwdWaves - 1) {
+        float out[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], H[v]);
         if (more) publish_state<VEC>(ch, C, c, tile, out, on);
@@ -363,8 +418,10 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     float *__restrict__ dh0, Chunks ch) {
     constexpr int L = kBwdRun, CW = 64 * VEC;
     __shared__ float sA[kWaves][CW], sH[kWaves][CW], sE[kWaves][CW], sC[CW];
+    __shared__ Links<VEC> sL;
     __shared__ uint32_t sTicket;
-    const Tile tile = get_tile<true>(s, ch, CHAIN ? take_ticket(ch.counter, &sTicket) : blockIdx.x);
+    const uint32_t group = blockIdx.x % ch.groups;
+    const Tile tile = get_tile<true>(s, ch, group, take_ticket<CHAIN>(ch, group, &sTicket));
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -375,6 +432,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const bool on = cw < C;
     const int c = min(cw, C - VEC);                // odd C: the last lane shares a channel, with the same results
     const uint32_t off = (uint32_t)c * sizeof(T);
+    if (tile.slot < 0) return;                     // no sequence
     if (tile.k < 0 || t0 >= len) {                 // an unused number, or an empty sequence
         if (on && w == 0)
 #pragma unroll
@@ -452,32 +510,23 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
             PE[v] = fmaf(Aq, PE[v], sE[p][lane * VEC + v]);
             PA[v] *= Aq;
         }
+    float c0[VEC];
+    const int behind = (len + kBwdChunk - 1) / kBwdChunk - 1 - tile.k;           // chunks after this one
+    const bool more = CHAIN && tile.k > 0;
     if (w == 0) {
-        float c0[VEC], out[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             E[v] = fmaf(A[v], PE[v], E[v]);
             A[v] *= PA[v];
         }
-        const int behind = (len + kBwdChunk - 1) / kBwdChunk - 1 - tile.k;       // chunks after this one
-        const bool more = CHAIN && tile.k > 0;
         if (!CHAIN || behind == 0) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) c0[v] = dhT ? dhT[(int64_t)b * C + c + v] : 0.f;
         } else {
             if (more) publish_map<VEC>(ch, C, c, tile, A, E, on);
-            carry_in<VEC>(ch, C, c, tile, 1, behind, c0);
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], E[v]);
-        if (more) publish_state<VEC>(ch, C, c, tile, out, on);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            if (on && dh0 && tile.k == 0) dh0[(int64_t)b * C + c + v] = out[v];
-            sC[lane * VEC + v] = c0[v];
         }
     }
-    // h forward through this wave's tokens, while the first wave waits
+    // h forward through this wave's tokens
 #pragma unroll
     for (int i = 0; i < L; ++i) {
         if (i < there) {
@@ -488,6 +537,18 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
                 q[i][v] = a[i][v] * (h[v] - q[i][v]);
                 h[v] = fmaf(a[i][v], h[v], ms[i][v] * xv[v]);
             }
+        }
+    }
+    if (CHAIN && behind > 0) carry_in<VEC>(ch, C, c, tile, 1, behind, w == 0, w, sL, c0);
+    if (w == 0) {
+        float out[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], E[v]);
+        if (more) publish_state<VEC>(ch, C, c, tile, out, on);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            if (on && dh0 && tile.k == 0) dh0[(int64_t)b * C + c + v] = out[v];
+            sC[lane * VEC + v] = c0[v];
         }
     }
     __syncthreads();
@@ -599,29 +660,45 @@ Chunks chunks(const Seq &s, int tokens) {
     return ch;
 }
 
+// Some 64 groups: all blocks of channels, times as many batches of sequences (packed ones, whose chunks
+// are numbered through, stay together).
+void set_groups(const Seq &s, Chunks &ch, int channels) {
+    ch.nct = (s.C + channels - 1) / channels;
+    const bool through = s.off && ch.per > 1;
+    const int gb = through ? 1 : std::min(s.B, std::max(1, 64 / ch.nct));
+    ch.groups = ch.nct * gb;
+    ch.nb = (s.B + gb - 1) / gb;
+}
+int64_t grid_size(const Seq &s, const Chunks &ch) {
+    return ch.groups * (s.off && ch.per > 1 ? ch.total : (int64_t)ch.per * ch.nb);
+}
+
 // Workspace of the links: the counter, the offsets, the rates, the stages, and then per chunk and channel
 // 8 bytes of map and 4 of state, each part to a multiple of 16; none if no sequence has a second chunk.
+int64_t counter_bytes(const Chunks &ch) { return 4 * kCounter * (int64_t)std::max(64, ch.nct); }
 int64_t pad16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 int64_t off_bytes(const Seq &s) { return s.off ? pad16(4 * ((int64_t)s.B + 1)) : 0; }
 int64_t stage_bytes(const Chunks &ch) { return pad16(4 * ch.total * ch.nct); }
 int64_t link_units(const Seq &s, const Chunks &ch) { return pad16(ch.total * s.C * 12) / 16; }
 size_t link_bytes(const Seq &s, const Chunks &ch) {
-    return ch.per > 1 ? (size_t)(16 + off_bytes(s) + pad16(4 * s.C) + stage_bytes(ch) + 16 * link_units(s, ch)) : 0;
+    return ch.per > 1 ? (size_t)(counter_bytes(ch) + off_bytes(s) + pad16(4 * s.C) + stage_bytes(ch) + 16 * link_units(s, ch)) : 0;
 }
 
 // Lays the links out in ws and empties them; s then has the ascending offsets.
-void set_links(Seq &s, Chunks &ch, void *ws, float scale, const float *decay, hipStream_t st) {
-    if (ch.per <= 1) return;
+void set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const float *decay, hipStream_t st) {
     char *p = (char *)ws;
+    const Chunks sizes = ch;
+    set_groups(s, ch, channels);
+    if (ch.per <= 1) return;
     ch.counter = (uint32_t *)p;
-    ch.off = (int32_t *)(p += 16);
+    ch.off = (int32_t *)(p += counter_bytes(sizes));
     ch.rate = (float *)(p += off_bytes(s));
     ch.stage = (uint32_t *)(p += pad16(4 * s.C));
-    ch.map = (uint64_t *)(p += stage_bytes(ch));
+    ch.map = (uint64_t *)(p += stage_bytes(sizes));
     ch.state = (uint32_t *)(ch.map + ch.total * s.C);
-    // one thread per unit; there are at least as many units as stages and as channels
-    const int64_t n = link_units(s, ch);
-    scan_fill_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s, ch, n, scale, decay);
+    // one thread per unit of the links, per stage, per channel and per counter
+    const int64_t n = link_units(s, ch), threads = std::max({n, ch.total * ch.nct, (int64_t)s.C, (int64_t)ch.groups});
+    scan_fill_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(s, ch, n, scale, decay);
     if (s.off) s.off = ch.off;
 }
 
@@ -637,13 +714,12 @@ template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
                      Chunks ch, hipStream_t st) {
-    ch.nct = (s.C + 64 * VEC - 1) / (64 * VEC);
-    const unsigned grid = (unsigned)(ch.total * ch.nct);
+    const unsigned grid = (unsigned)grid_size(s, ch);
     if (ch.per > 1)
-        scan_fwd_kernel<T, VEC, true><<<grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
+        scan_fwd_kernel<T, VEC, true><<<grid, 64 * kFwdWaves, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
                                                                  (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
     else
-        scan_fwd_kernel<T, VEC, false><<<grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
+        scan_fwd_kernel<T, VEC, false><<<grid, 64 * kFwdWaves, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
                                                                   (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
 }
 
@@ -652,8 +728,8 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
                            int64_t ldy, float *hT, float *states, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, scale, decay, st);
-    const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
+    set_links(q, ch, ws, bf16 && s.C > 1 ? 64*FV : 64, scale, decay, st);
+    const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, FV> : scan_fwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, st);
     return hipGetLastError();
 }
@@ -663,8 +739,7 @@ static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, cons
                      int64_t ldi, const float *decay, const float *states, const void *dy, int64_t lddy, const float *dhT,
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
                      Chunks ch, hipStream_t st) {
-    ch.nct = (s.C + 64 * VEC - 1) / (64 * VEC);
-    const unsigned grid = (unsigned)(ch.total * ch.nct);
+    const unsigned grid = (unsigned)grid_size(s, ch);
     if (ch.per > 1)
         scan_bwd_kernel<T, VEC, true><<<grid, kThreads, 0, st>>>(
             s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi, decay, states, (const T *)dy, lddy, dhT,
@@ -681,9 +756,9 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
                            float *ddecay, float *dh0, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kBwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, scale, decay, st);
-    float *part = (float *)((char *)ws + link_bytes(s, ch));
-    const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
+    set_links(q, ch, ws, bf16 && s.C > 1 ? 64*BV : 64, scale, decay, st);
+    float *part = (float *)((char *)ws + link_bytes(s, chunks(s, kBwdChunk)));
+    const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, BV> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,
         st);
     scan_reduce_kernel<<<(s.C + 15) / 16, 1024, 0, st>>>(part, ch.total, s.C, scale, decay, ddecay);
