@@ -56,18 +56,40 @@ template <> struct Grad<true> { typedef H4 type; typedef uint16_t elem; };
 __device__ __forceinline__ float value(const F4 &g, int e) { return g.f[e]; }
 __device__ __forceinline__ float value(const H4 &g, int e) { return __uint_as_float((uint32_t)g.h[e] << 16); }
 
+// Parameters, gradients and moments pass by once a step: non-temporal accesses, as a stream through the
+// caches only displaces (26 M parameters: 152.6 us without the hints, 135.2 us with them).  The bf16 copy
+// goes plainly beside fp32 moments (128 us) and as a stream beside 8-bit ones (60 M parameters with the
+// values: 293 us, 316 us plainly).
+template <typename V, typename E> __device__ __forceinline__ V load_stream(const E *p) {
+    typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) / 4), aligned(sizeof(E))));
+    const W w = __builtin_nontemporal_load(reinterpret_cast<const W *>(p));
+    V v;
+    __builtin_memcpy(&v, &w, sizeof(v));
+    return v;
+}
+template <typename V, typename E> __device__ __forceinline__ void store_stream(E *p, const V &v) {
+    typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) / 4), aligned(sizeof(E))));
+    W w;
+    __builtin_memcpy(&w, &v, sizeof(v));
+    __builtin_nontemporal_store(w, reinterpret_cast<W *>(p));
+}
+
 // Elements i .. i+3 of p, or what there is of them (n: the tensor's length; FULL: all are there).
 template <bool FULL, typename V, typename E> __device__ __forceinline__ V load4(const E *p, int64_t i, int64_t n) {
-    if (FULL || i + 4 <= n) return *reinterpret_cast<const V *>(p + i);
+    if (FULL || i + 4 <= n) return load_stream<V>(p + i);
     V v = {};
     E *o = reinterpret_cast<E *>(&v);
     for (int e = 0; e < 3; ++e)
         if (i + e < n) o[e] = p[i + e];
     return v;
 }
-template <bool FULL, typename V, typename E> __device__ __forceinline__ void store4(E *p, int64_t i, int64_t n, const V &v) {
+template <bool FULL, bool STREAM = true, typename V, typename E>
+__device__ __forceinline__ void store4(E *p, int64_t i, int64_t n, const V &v) {
     if (FULL || i + 4 <= n) {
-        *reinterpret_cast<V *>(p + i) = v;
+        if (STREAM)
+            store_stream(p + i, v);
+        else
+            *reinterpret_cast<V *>(p + i) = v;
         return;
     }
     const E *o = reinterpret_cast<const E *>(&v);
@@ -128,7 +150,7 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw32_chunk(co
             store4<FULL>(tm, i, n, m[u]);
             store4<FULL>(tv, i, n, v[u]);
             store4<FULL>(tp, i, n, p[u]);
-            if (t.copy) store4<FULL>(t.copy, i, n, to_copy(p[u]));
+            if (t.copy) store4<FULL, false>(t.copy, i, n, to_copy(p[u]));
         }
     }
 }

@@ -6,12 +6,6 @@
 #include "conv_fwd.h"
 #include "scan_math.h"
 
-#ifndef BV
-#define BV 2
-#endif
-#ifndef FV
-#define FV 2
-#endif
 namespace convfwd {
 namespace {
 
@@ -255,35 +249,26 @@ template <typename T> __device__ __forceinline__ T *at_byte(T *row, uint32_t byt
 
 // N rows from p on (uniform; off: this lane's channel, in bytes); only the first `there` of them exist, and the last
 // of those stands in for the rest.
-template <typename T, int VEC, int N, bool FULL>
+template <typename T, int VEC, int N, bool FULL, bool ONCE>
 __device__ __forceinline__ void load_rows(typename Pack<T, VEC>::type (&v)[N], const T *p, int64_t ld, uint32_t off, int there) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        v[i] = load_pack<T, VEC>(at_byte(p, off));
+        v[i] = ONCE ? load_once<T, VEC>(at_byte(p, off)) : load_pack<T, VEC>(at_byte(p, off));
         if (FULL || i + 1 < there) p += ld;
     }
 }
 
 // ---- forward -----------------------------------------------------------------------
 
-#ifndef FW
-#define FW 8
-#endif
-#ifndef FL
-#define FL 16
-#endif
-#ifndef FO
-#define FO 4
-#endif
-constexpr int kFwdWaves = FW, kFwdRun = FL, kFwdChunk = kFwdWaves * kFwdRun;      // tokens of a wave and of a workgroup
+constexpr int kFwdRun = 16, kFwdChunk = kWaves * kFwdRun;      // tokens of a wave and of a workgroup
 
-template <typename T, int VEC, bool CHAIN>
-__global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
+template <typename T, int VEC, bool CHAIN, bool ONCE>
+__global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
     Seq s, float scale, const T *__restrict__ x, int64_t ldx, const T *__restrict__ gate, int64_t ldg,
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ h0,
     T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch) {
     constexpr int L = kFwdRun, CW = 64 * VEC;
-    __shared__ float sA[kFwdWaves][CW], sH[kFwdWaves][CW], sC[CW];
+    __shared__ float sA[kWaves][CW], sH[kWaves][CW], sC[CW];
     __shared__ Links<VEC> sL;
     __shared__ uint32_t sTicket;
     const uint32_t group = blockIdx.x % ch.groups;
@@ -306,9 +291,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
     const auto read = [&](auto full_) {
         constexpr bool full = decltype(full_)::value;
         typename Pack<T, VEC>::type xr[L], gr[L], ir[L];
-        load_rows<T, VEC, L, full>(gr, gate + (first + tw) * ldg, ldg, off, there);
-        load_rows<T, VEC, L, full>(ir, inp + (first + tw) * ldi, ldi, off, there);
-        load_rows<T, VEC, L, full>(xr, x + (first + tw) * ldx, ldx, off, there);
+        load_rows<T, VEC, L, full, ONCE>(gr, gate + (first + tw) * ldg, ldg, off, there);
+        load_rows<T, VEC, L, full, ONCE>(ir, inp + (first + tw) * ldi, ldi, off, there);
+        load_rows<T, VEC, L, full, ONCE>(xr, x + (first + tw) * ldx, ldx, off, there);
         ScanRate k[VEC];
         get_rates<VEC, CHAIN>(ch, scale, decay, c, k);
 #pragma unroll
@@ -346,7 +331,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
         }
     float c0[VEC];
     const bool more = CHAIN && t0 + kFwdChunk < len;
-    if (w == kFwdWaves - 1) {                       // this wave has the whole chunk's map
+    if (w == kWaves - 1) {                       // this wave has the whole chunk's map
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             H[v] = fmaf(A[v], PH[v], H[v]);
@@ -359,8 +344,8 @@ __global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
             if (more) publish_map<VEC>(ch, C, c, tile, A, H, on);
         }
     }
-    if (CHAIN && tile.k > 0) carry_in<VEC>(ch, C, c, tile, -1, tile.k, w == kFwdWaves - 1, w, sL, c0);
-    if (w == kFwdWaves - 1) {
+    if (CHAIN && tile.k > 0) carry_in<VEC>(ch, C, c, tile, -1, tile.k, w == kWaves - 1, w, sL, c0);
+    if (w == kWaves - 1) {
         float out[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) out[v] = fmaf(A[v], c0[v], H[v]);
@@ -409,7 +394,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, FO) void scan_fwd_kernel(
 constexpr int kBwdRun = 8, kBwdChunk = kWaves * kBwdRun;
 static_assert(kBwdChunk == kBlock, "a saved state for every chunk");
 
-template <typename T, int VEC, bool CHAIN>
+template <typename T, int VEC, bool CHAIN, bool ONCE>
 __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     Seq s, float scale, const T *__restrict__ x, int64_t ldx, const T *__restrict__ gate, int64_t ldg,
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ states,
@@ -458,10 +443,10 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const auto read = [&](auto full_) {
         constexpr bool full = decltype(full_)::value;
         typename Pack<T, VEC>::type gr[L], ir[L];
-        load_rows<T, VEC, L, full>(gr, gate + (first + tw) * ldg, ldg, off, there);
-        load_rows<T, VEC, L, full>(ir, inp + (first + tw) * ldi, ldi, off, there);
-        load_rows<T, VEC, L, full>(xr, x + (first + tw) * ldx, ldx, off, there);
-        load_rows<T, VEC, L, full>(dr, dy + (first + tw) * lddy, lddy, off, there);
+        load_rows<T, VEC, L, full, ONCE>(gr, gate + (first + tw) * ldg, ldg, off, there);
+        load_rows<T, VEC, L, full, ONCE>(ir, inp + (first + tw) * ldi, ldi, off, there);
+        load_rows<T, VEC, L, full, ONCE>(xr, x + (first + tw) * ldx, ldx, off, there);
+        load_rows<T, VEC, L, full, ONCE>(dr, dy + (first + tw) * lddy, lddy, off, there);
         get_rates<VEC, CHAIN>(ch, scale, decay, c, k);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -714,13 +699,11 @@ template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
                      Chunks ch, hipStream_t st) {
-    const unsigned grid = (unsigned)grid_size(s, ch);
-    if (ch.per > 1)
-        scan_fwd_kernel<T, VEC, true><<<grid, 64 * kFwdWaves, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
-                                                                 (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
-    else
-        scan_fwd_kernel<T, VEC, false><<<grid, 64 * kFwdWaves, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg,
-                                                                  (const T *)inp, ldi, decay, h0, (T *)y, ldy, hT, states, ch);
+    const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T));
+    const auto run = ch.per > 1 ? (once ? scan_fwd_kernel<T, VEC, true, true> : scan_fwd_kernel<T, VEC, true, false>)
+                                : (once ? scan_fwd_kernel<T, VEC, false, true> : scan_fwd_kernel<T, VEC, false, false>);
+    run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
+                                                         decay, h0, (T *)y, ldy, hT, states, ch);
 }
 
 hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate,
@@ -728,8 +711,8 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
                            int64_t ldy, float *hT, float *states, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, bf16 && s.C > 1 ? 64*FV : 64, scale, decay, st);
-    const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, FV> : scan_fwd<uint16_t, 1>;
+    set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, st);
+    const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, st);
     return hipGetLastError();
 }
@@ -739,15 +722,13 @@ static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, cons
                      int64_t ldi, const float *decay, const float *states, const void *dy, int64_t lddy, const float *dhT,
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
                      Chunks ch, hipStream_t st) {
-    const unsigned grid = (unsigned)grid_size(s, ch);
-    if (ch.per > 1)
-        scan_bwd_kernel<T, VEC, true><<<grid, kThreads, 0, st>>>(
-            s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi, decay, states, (const T *)dy, lddy, dhT,
-            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch);
-    else
-        scan_bwd_kernel<T, VEC, false><<<grid, kThreads, 0, st>>>(
-            s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi, decay, states, (const T *)dy, lddy, dhT,
-            (T *)dx, lddx, (T *)dgate, lddg, (T *)dinp, lddi, part, dh0, ch);
+    const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
+                      read_once(dy, lddy, sizeof(T));
+    const auto run = ch.per > 1 ? (once ? scan_bwd_kernel<T, VEC, true, true> : scan_bwd_kernel<T, VEC, true, false>)
+                                : (once ? scan_bwd_kernel<T, VEC, false, true> : scan_bwd_kernel<T, VEC, false, false>);
+    run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
+                                                         decay, states, (const T *)dy, lddy, dhT, (T *)dx, lddx, (T *)dgate,
+                                                         lddg, (T *)dinp, lddi, part, dh0, ch);
 }
 
 hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -756,9 +737,9 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
                            float *ddecay, float *dh0, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kBwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, bf16 && s.C > 1 ? 64*BV : 64, scale, decay, st);
+    set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, st);
     float *part = (float *)((char *)ws + link_bytes(s, chunks(s, kBwdChunk)));
-    const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, BV> : scan_bwd<uint16_t, 1>;
+    const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,
         st);
     scan_reduce_kernel<<<(s.C + 15) / 16, 1024, 0, st>>>(part, ch.total, s.C, scale, decay, ddecay);

@@ -94,16 +94,19 @@ template <int VEC> __device__ __forceinline__ Work get_work(const Seq &s, int pe
 
 // K rows from p on, in bf16 or fp32 as they are; only the first `there` of them are, and the first row
 // stands in for the others, so that loads need no branch.
-template <typename T, int VEC, int K> struct Rows {
+template <typename T, int VEC, int K, bool ONCE> struct Rows {
     typename Pack<T, VEC>::type v[K];
     __device__ __forceinline__ void load(const T *p, int64_t ld, int there) {
 #pragma unroll
-        for (int u = 0; u < K; ++u) v[u] = load_pack<T, VEC>(p + (u < there ? u * ld : 0));
+        for (int u = 0; u < K; ++u) {
+            const T *q = p + (u < there ? u * ld : 0);
+            v[u] = ONCE ? load_once<T, VEC>(q) : load_pack<T, VEC>(q);
+        }
     }
 };
 
 // grid (blocks of tokens, channel blocks)
-template <typename T, int VEC, int K, bool SILU>
+template <typename T, int VEC, int K, bool SILU, bool ONCE>
 __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__restrict__ x, int64_t ldx,
                                                               const T *__restrict__ w, const float *__restrict__ bias,
                                                               const T *__restrict__ state, T *__restrict__ y,
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__
     if (k.t0 >= k.t1) return;
     const T *xp = x + (k.first + k.t0) * ldx + k.c;
     T *yp = y + (k.first + k.t0) * ldy + k.c;
-    Rows<T, VEC, U> next;
+    Rows<T, VEC, U, ONCE> next;
     next.load(xp, ldx, k.t1 - k.t0);
     float wf[K][VEC], bf[VEC], win[K][VEC];
 #pragma unroll
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__
     for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[k.c + i] : 0.f;
     // at step u (mod K) the new row goes to slot (K-1+u) % K; tap j is slot (u+j) % K
     for (int t = k.t0; t < k.t1; t += U) {
-        const Rows<T, VEC, U> now = next;
+        const Rows<T, VEC, U, ONCE> now = next;
         xp += U * ldx;
         if (t + U < k.t1) next.load(xp, ldx, k.t1 - t - U);
 #pragma unroll
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__
 // the carried rows.  Partial sums of dw and db: one row of (K+1) x C floats per
 // workgroup, reduced over its runs in LDS in a fixed order, then added over
 // workgroups in a fixed order by causal_reduce_kernel.
-template <typename T, int VEC, int K, bool SILU>
+template <typename T, int VEC, int K, bool SILU, bool ONCE>
 __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__restrict__ x, int64_t ldx,
                                                               const T *__restrict__ w, const float *__restrict__ bias,
                                                               const T *__restrict__ state, const T *__restrict__ dy,
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
     if (k.any && (k.t0 < k.t1 || head)) {
         const int end = max(k.t1, k.t0) + K - 1;       // dX rows up to t1 - 1
         const T *xp = x + (k.first + k.t0) * ldx + k.c, *dp_ = dy + (k.first + k.t0) * lddy + k.c;
-        Rows<T, VEC, U> nx, nd;
+        Rows<T, VEC, U, ONCE> nx, nd;
         if (k.t0 < k.len) {
             nx.load(xp, ldx, k.len - k.t0);
             nd.load(dp_, lddy, k.len - k.t0);
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
 #pragma unroll
         for (int i = 0; i < VEC; ++i) bf[i] = bias ? bias[k.c + i] : 0.f;
         // U rows of a run; inner: all are the run's own and so are the rows of dX that they complete
-        const auto group = [&](int t, const Rows<T, VEC, U> &x0, const Rows<T, VEC, U> &d0, auto inner_) {
+        const auto group = [&](int t, const Rows<T, VEC, U, ONCE> &x0, const Rows<T, VEC, U, ONCE> &d0, auto inner_) {
             constexpr bool inner = decltype(inner_)::value;
             T *dxp = dx + (k.first + t - (K - 1)) * lddx + k.c;
 #pragma unroll
@@ -237,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
             }
         };
         for (int t = k.t0; t < end; t += U) {
-            const Rows<T, VEC, U> x0 = nx, d0 = nd;
+            const Rows<T, VEC, U, ONCE> x0 = nx, d0 = nd;
             xp += U * ldx;
             dp_ += U * lddy;
             if (t + U < end && t + U < k.len) {
@@ -361,16 +364,19 @@ template <typename T, int VEC, int K, bool SILU>
 void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, T *y, int64_t ldy,
          T *state_out, hipStream_t st) {
     const Tiling t = tiling(s, VEC, kFwdLeast);
-    causal_fwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
-        s, x, ldx, w, bias, state, y, ldy, state_out, t.per, t.bx_log2, t.tl);
+    const auto run = VEC > 1 && read_once(x, ldx, sizeof(T)) ? causal_fwd_kernel<T, VEC, K, SILU, (VEC > 1)>
+                                                             : causal_fwd_kernel<T, VEC, K, SILU, false>;
+    run<<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, y, ldy, state_out, t.per, t.bx_log2, t.tl);
 }
 
 template <typename T, int VEC, int K, bool SILU>
 void bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
          T *dx, int64_t lddx, float *dw, float *db, T *dstate, float *part, hipStream_t st) {
     const Tiling t = tiling(s, VEC, kBwdLeast);
-    causal_bwd_kernel<T, VEC, K, SILU><<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(
-        s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per, t.bx_log2, t.tl);
+    const auto run = VEC > 1 && read_once(x, ldx, sizeof(T)) && read_once(dy, lddy, sizeof(T))
+                         ? causal_bwd_kernel<T, VEC, K, SILU, (VEC > 1)> : causal_bwd_kernel<T, VEC, K, SILU, false>;
+    run<<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per,
+                                                          t.bx_log2, t.tl);
     causal_reduce_kernel<<<dim3((s.C + 15) / 16, K + 1), 1024, 0, st>>>(part, t.n, s.C, K, dw, db);
 }
 

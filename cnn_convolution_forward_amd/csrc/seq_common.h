@@ -39,6 +39,24 @@ __device__ __forceinline__ typename Pack<T, VEC>::type load_pack(const T *p) {
     __builtin_memcpy(&v, p, sizeof(v));
     return v;
 }
+// The same for data that a kernel reads once, with the non-temporal hint: at 8 x 2048 x 2048 bf16 the
+// recurrence's backward pass takes 123 us without and 107 us with it, the causal convolution at 8 x 4096 x
+// 4096 120 and 89 us.  Only for rows that start on a line: where rows share lines, these are fetched
+// twice (5003 x 999 fp32, convolution backward: 21.2 us without, 24.1 us with it).
+template <typename T, int VEC>
+__device__ __forceinline__ typename Pack<T, VEC>::type load_once(const T *p) {
+    typedef typename Pack<T, VEC>::type V;
+    if constexpr (sizeof(V) < 4) {
+        return load_pack<T, VEC>(p);
+    } else {
+        typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) / 4), aligned(sizeof(T))));
+        const W w = __builtin_nontemporal_load(reinterpret_cast<const W *>(p));
+        V v;
+        __builtin_memcpy(&v, &w, sizeof(v));
+        return v;
+    }
+}
+inline bool read_once(const void *p, int64_t ld, size_t esize) { return (uintptr_t)p % 64 == 0 && ld * (int64_t)esize % 64 == 0; }
 template <typename T, typename V> __device__ __forceinline__ void store_pack(T *p, const V &v) {
     __builtin_memcpy(p, &v, sizeof(v));
 }
