@@ -458,3 +458,79 @@ def test_helpers_refuse_wrong_tensors_and_overlap():
     assert B.causal_conv(x[:, :0], w).shape == (2, 0, 24)
     y, hT = B.gated_scan(x[:, :0], x[:, :0], x[:, :0], d, h0=torch.ones(2, 24, device="cuda"))
     assert y.shape == (2, 0, 24) and bool((hT == 1).all())
+
+
+def test_many_packed_sequences():
+    """150 packed sequences of 0 to 300 tokens that do not start at row 0 nor end at the last: rows outside
+    stay untouched, each sequence gives the bits that it gives alone."""
+    rng = np.random.default_rng(31)
+    lens = [int(v) for v in rng.integers(0, 300, 150)]
+    lens[3] = lens[70] = lens[149] = 0
+    C, lead, tail = 24, 77, 300
+    off = lead + np.concatenate([[0], np.cumsum(lens)])
+    n = int(off[-1]) + tail
+    x, g, u, dy = (_cuda(rng.standard_normal((n, C)), torch.bfloat16) for _ in range(4))
+    w, decay, h0 = _cuda(rng.standard_normal((C, 4)), torch.bfloat16), _cuda(rng.uniform(-5, -1, C)), _cuda(rng.standard_normal((150, C)))
+    kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_len=max(lens))
+    out = [torch.full((n, C), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+    B.causal_conv(x, w, silu=True, out=out[0], **kw)
+    _, dw, db, _ = B.causal_conv_backward(x, w, dy, silu=True, out=out[1], **kw)
+    _, hT, st = B.gated_scan(x, g, u, decay, h0=h0, with_states=True, out=out[2], **kw)
+    _, _, _, dd, dh0 = B.gated_scan_backward(x, g, u, decay, dy, st, out=tuple(out[3:]), **kw)
+    for o in out:
+        assert bool(torch.isnan(o[:lead]).all()) and bool(torch.isnan(o[int(off[-1]):]).all())
+    sums = [torch.zeros_like(t, dtype=torch.float64) for t in (dw, db, dd)]
+    for b in range(150):
+        if not lens[b]:
+            assert torch.equal(hT[b], h0[b]) and not bool(dh0[b].any())
+            continue
+        r = slice(int(off[b]), int(off[b + 1]))
+        one = [t[r][None].contiguous() for t in (x, g, u, dy)]
+        cdx, cdw, cdb, _ = B.causal_conv_backward(one[0], w, one[3], silu=True)
+        y1, h1, s1 = B.gated_scan(*one[:3], decay, h0=h0[b:b + 1].contiguous(), with_states=True)
+        g1 = B.gated_scan_backward(*one[:3], decay, one[3], s1)
+        want = [B.causal_conv(one[0], w, silu=True), cdx, y1, *g1[:3]]
+        assert all(torch.equal(o[r], q[0]) for o, q in zip(out, want)), b
+        assert torch.equal(hT[b], h1[0]) and torch.equal(dh0[b], g1[4][0])
+        for t, q in zip(sums, (cdw, cdb, g1[3])):
+            t += q.double()
+    for t, q in zip((dw, db, dd), sums):
+        assert float((t.double() - q).abs().max()) <= 1e-5 * float(q.abs().max())
+
+
+@pytest.mark.parametrize("off", [[0, 700, 300, 1500], [900, 100, 1400, 20], [1500, 0, 0, 0], [-3, 2000, 5, 1 << 30]])
+def test_descending_offsets_end_within_the_rows(off):
+    """Which rows are computed is unspecified; that the calls end, and write no row outside, is not."""
+    rng = np.random.default_rng(2)
+    C, n = 32, 1500
+    buf = torch.full((n + 200, C), 5.0, dtype=torch.bfloat16, device="cuda")
+    x, g, u, dy = (_cuda(rng.standard_normal((n, C)), torch.bfloat16) for _ in range(4))
+    decay, w = _cuda(rng.uniform(-5, -1, C)), _cuda(rng.standard_normal((C, 4)), torch.bfloat16)
+    kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_len=1500)
+    y = buf[100:100 + n]
+    B.causal_conv(x, w, out=y, **kw)
+    B.causal_conv_backward(x, w, dy, out=y, **kw)
+    _, _, st = B.gated_scan(x, g, u, decay, with_states=True, out=y, **kw)
+    B.gated_scan_backward(x, g, u, decay, dy, torch.zeros_like(st), **kw)
+    torch.cuda.synchronize()
+    assert bool((buf[:100] == 5).all()) and bool((buf[100 + n:] == 5).all())
+
+
+def test_nan_of_all_ones():
+    """A float32 NaN whose bits are all ones passes from chunk to chunk like any other."""
+    T, C = 700, 3
+    x = torch.zeros(1, T, C, device="cuda")
+    x.view(torch.int32)[0, 130, 1] = -1
+    g = torch.zeros(1, T, C, device="cuda")
+    y, hT, st = B.gated_scan(x, g, g, torch.zeros(C, device="cuda"), with_states=True)
+    hit = torch.zeros(1, T, C, dtype=torch.bool, device="cuda")
+    hit[0, 130:, 1] = True
+    assert torch.equal(torch.isnan(y), hit)
+    x.view(torch.int32)[0, 130, 1] = 0
+    y, hT, st = B.gated_scan(x, g, g, torch.zeros(C, device="cuda"), with_states=True)
+    dy = torch.zeros(1, T, C, device="cuda")
+    dy.view(torch.int32)[0, 600, 2] = -1
+    dx = B.gated_scan_backward(x, g, g, torch.zeros(C, device="cuda"), dy, st)[0]
+    hit = torch.zeros(1, T, C, dtype=torch.bool, device="cuda")
+    hit[0, :601, 2] = True
+    assert torch.equal(torch.isnan(dx), hit)
