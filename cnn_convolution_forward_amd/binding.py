@@ -761,10 +761,11 @@ def _ld(t, shape, like, name):
     evenly strided axis (a column slice of a dense tensor, for instance)."""
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != like.dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
+    if t is not like:
+        if t.shape != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if t.dtype != like.dtype:
+            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, like.dtype))
     if t.is_contiguous():
         return shape[-1]
     if t.numel() == 0:
@@ -792,7 +793,7 @@ def _dense(t, shape, dtype, name):
         raise ValueError("%s must be a GPU tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)

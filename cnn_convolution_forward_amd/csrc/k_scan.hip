@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
         for (int i = 0; i < L; ++i) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[i][v], h[v], bb[i][v]);
-            if (full || i < there) store_f32(at_byte(yp, off), h);
+            if (full || i < there) store_f32<ONCE>(at_byte(yp, off), h);
             yp += ldy;
         }
     };
@@ -564,9 +564,9 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
                 e[v] = a[i][v] * dh;
             }
             if (on) {
-                store_f32(at_byte(dxp, off), o0);
-                store_f32(at_byte(dgp, off), o1);
-                store_f32(at_byte(dip, off), o2);
+                store_f32<ONCE>(at_byte(dxp, off), o0);
+                store_f32<ONCE>(at_byte(dgp, off), o1);
+                store_f32<ONCE>(at_byte(dip, off), o2);
             }
             dxp -= lddx;
             dgp -= lddg;
@@ -699,7 +699,8 @@ template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
                      Chunks ch, hipStream_t st) {
-    const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T));
+    const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
+                      read_once(y, ldy, sizeof(T));
     const auto run = ch.per > 1 ? (once ? scan_fwd_kernel<T, VEC, true, true> : scan_fwd_kernel<T, VEC, true, false>)
                                 : (once ? scan_fwd_kernel<T, VEC, false, true> : scan_fwd_kernel<T, VEC, false, false>);
     run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
@@ -723,7 +724,8 @@ static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, cons
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
                      Chunks ch, hipStream_t st) {
     const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
-                      read_once(dy, lddy, sizeof(T));
+                      read_once(dy, lddy, sizeof(T)) && read_once(dx, lddx, sizeof(T)) && read_once(dgate, lddg, sizeof(T)) &&
+                      read_once(dinp, lddi, sizeof(T));
     const auto run = ch.per > 1 ? (once ? scan_bwd_kernel<T, VEC, true, true> : scan_bwd_kernel<T, VEC, true, false>)
                                 : (once ? scan_bwd_kernel<T, VEC, false, true> : scan_bwd_kernel<T, VEC, false, false>);
     run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,

@@ -42,7 +42,11 @@ __device__ __forceinline__ typename Pack<T, VEC>::type load_pack(const T *p) {
 // The same for data that a kernel reads once, with the non-temporal hint: at 8 x 2048 x 2048 bf16 the
 // recurrence's backward pass takes 123 us without and 107 us with it, the causal convolution at 8 x 4096 x
 // 4096 120 and 89 us.  Only for rows that start on a line: where rows share lines, these are fetched
-// twice (5003 x 999 fp32, convolution backward: 21.2 us without, 24.1 us with it).
+// twice (5003 x 999 fp32, convolution backward: 21.2 us without, 24.1 us with it).  Stores with the hint are
+// for the recurrence: at the end of a kernel what is dirty in the caches has to leave them before the
+// next one starts (4 x 1024 x 2048 forward 23.4 us without, 21.4 us with it; backward at 8 x 4096 x 4096
+// 409 and 387 us, at 8 x 2048 x 2048 107 and 109 us).  The causal convolution is slower with them (88.7 and
+// 107 us at 8 x 4096 x 4096).
 template <typename T, int VEC>
 __device__ __forceinline__ typename Pack<T, VEC>::type load_once(const T *p) {
     typedef typename Pack<T, VEC>::type V;
@@ -57,8 +61,15 @@ __device__ __forceinline__ typename Pack<T, VEC>::type load_once(const T *p) {
     }
 }
 inline bool read_once(const void *p, int64_t ld, size_t esize) { return (uintptr_t)p % 64 == 0 && ld * (int64_t)esize % 64 == 0; }
-template <typename T, typename V> __device__ __forceinline__ void store_pack(T *p, const V &v) {
-    __builtin_memcpy(p, &v, sizeof(v));
+template <bool ONCE = false, typename T, typename V> __device__ __forceinline__ void store_pack(T *p, const V &v) {
+    if constexpr (ONCE && sizeof(V) >= 4) {
+        typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) / 4), aligned(sizeof(T))));
+        W w;
+        __builtin_memcpy(&w, &v, sizeof(v));
+        __builtin_nontemporal_store(w, reinterpret_cast<W *>(p));
+    } else {
+        __builtin_memcpy(p, &v, sizeof(v));
+    }
 }
 
 // bf16 bits to fp32 is a shift; fp32 to bf16 rounds to nearest even (a NaN
@@ -96,15 +107,19 @@ template <typename T, int VEC> __device__ __forceinline__ void load_f32(const T 
     to_f32(load_pack<T, VEC>(p), f);
 }
 
-__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[1]) { *p = to_bf16(f[0]); }
-__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[2]) { store_pack(p, pack_bf16(f[0], f[1])); }
-__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[4]) {
-    store_pack(p, make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])));
+template <bool ONCE = false> __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[1]) { *p = to_bf16(f[0]); }
+template <bool ONCE = false> __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[2]) {
+    store_pack<ONCE>(p, pack_bf16(f[0], f[1]));
 }
-__device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[8]) {
-    store_pack(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+template <bool ONCE = false> __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[4]) {
+    store_pack<ONCE>(p, make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])));
 }
-template <int VEC> __device__ __forceinline__ void store_f32(float *p, const float (&f)[VEC]) { store_pack(p, f); }
+template <bool ONCE = false> __device__ __forceinline__ void store_f32(uint16_t *p, const float (&f)[8]) {
+    store_pack<ONCE>(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+}
+template <bool ONCE = false, int VEC> __device__ __forceinline__ void store_f32(float *p, const float (&f)[VEC]) {
+    store_pack<ONCE>(p, f);
+}
 
 // Blocks of `tokens` tokens, numbered through the batch.  Equal sequences have
 // per = ceil(T/tokens) (at least one) each, and so have packed ones if that is
