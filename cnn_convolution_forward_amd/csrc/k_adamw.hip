@@ -8,8 +8,12 @@
 // One launch takes up to kMaxTensors tensors, whose pointers travel in the
 // kernel's arguments: nothing is copied to the device and nothing has to be
 // kept between calls.  Blocks of kChunk elements are numbered through all of
-// its tensors; a workgroup finds its tensor by bisection over their first
-// numbers (uniform: scalar loads).
+// its tensors; a workgroup finds its tensor by looking at all first numbers.
+//
+// Measured: 26 M parameters in 60 tensors with fp32 moments 128.9 us, 6.05 TB/s (a
+// large copy reaches 5.2); 60 M in 120 with 8-bit moments, their values read back
+// too, 306 us, 4.7 TB/s; 20 000 in 14 6.4 us, mostly the launch.  One element per
+// load took 163.5, 661.9 and 8.0 us.
 #include "optim_internal.h"
 #include "seq_common.h"
 
@@ -27,7 +31,7 @@ struct Table {
 };
 static_assert(sizeof(Table) <= 4096, "kernel arguments");
 
-// z = step and seed for the tensor; 32 bits per element, by two rounds of
+// 32 bits per element from the tensor's key (seed, step and its place in the list), by two rounds of
 // xor-shift and odd multiplication.
 __device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t i) {
     uint32_t z = key + i * 0x9e3779b1u;
