@@ -10,9 +10,9 @@
 // kept between calls.  Blocks of kChunk elements are numbered through all of
 // its tensors; a workgroup finds its tensor by looking at all first numbers.
 //
-// Measured: 26 M parameters in 60 tensors with fp32 moments 128.9 us, 6.05 TB/s (a
+// Measured: 26 M parameters in 60 tensors with fp32 moments 129.4 us, 6.0 TB/s (a
 // large copy reaches 5.2); 60 M in 120 with 8-bit moments, their values read back
-// too, 306 us, 4.7 TB/s; 20 000 in 14 6.4 us, mostly the launch.  One element per
+// too, 307 us, 4.7 TB/s; 20 000 in 14 6.4 us, mostly the launch.  One element per
 // load took 163.5, 661.9 and 8.0 us.
 #include "optim_internal.h"
 #include "seq_common.h"
