@@ -77,7 +77,7 @@ conv_status_t make_seq(const conv_seq_t *q, bool step, Seq &s) {
     s.off = step ? nullptr : q->offsets;
     s.rows = s.off ? q->tokens : (int64_t)s.B * s.T;
     if (s.rows >= kMaxRows || s.T >= kMaxRows || s.C > kMaxChannels || (int64_t)s.B * s.C > kMaxStateElems ||
-        (int64_t)s.B * ((s.T + CONV_SCAN_BLOCK - 1) / CONV_SCAN_BLOCK + 1) > kMaxBlocks ||
+        s.rows / CONV_SCAN_BLOCK + 2 * (int64_t)s.B > kMaxBlocks ||
         (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) > kMaxBlocks)
         return CONV_ERR_OVERFLOW;
     return CONV_OK;

@@ -131,17 +131,22 @@ struct Block {
 __host__ __device__ __forceinline__ int64_t block_count(const Seq &s, int tokens, int per) {
     return s.off && per > 1 ? s.rows / tokens + s.B : (int64_t)s.B * per;
 }
-// The block of number n; all lanes of a wave together.
+// The block of number n; all lanes of a wave together.  64 starts are looked at in one load, so that 64
+// sequences take one round and 4096 two.  Offsets that descend lead to some sequence, and to a block that
+// the tensor could have, or to an unused number.
 __device__ __forceinline__ Block packed_block(const Seq &s, int tokens, int64_t n) {
     const auto start = [&](int b) { return min(max((int64_t)s.off[b], (int64_t)0), s.rows) / tokens + b; };
     Block t;
     t.b = 0;
-    for (int base = 0; base < s.B; base += 64) {       // the last sequence that starts at or before n
-        const int i = base + (int)(threadIdx.x & 63);
-        const uint64_t on = __ballot(i < s.B && start(min(i, s.B - 1)) <= n);
-        if (on) t.b = base + 63 - __builtin_clzll(on);
+    for (int left = s.B; left > 1;) {                   // the last of `left` sequences from t.b on that starts at or before n
+        const int step = (left + 63) / 64, i = t.b + (int)(threadIdx.x & 63) * step;
+        const uint64_t on = __ballot(i < t.b + left && start(min(i, s.B - 1)) <= n);
+        const int j = on ? 63 - __builtin_clzll(on) : 0;
+        t.b += j * step;
+        left = min(step, left - j * step);
     }
-    t.k = (int)(n - start(t.b));
+    const int64_t k = n - start(t.b);
+    t.k = k >= 0 && k <= s.rows / tokens ? (int)k : -1;
     return t;
 }
 

@@ -411,8 +411,8 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * CONV_LAYOUT_NHWC with H = 1, so a pointwise convolution over tokens produces
  * and consumes these rows).  Sequence b of a batch is rows [b*T, (b+1)*T), or,
  * with `offsets`, rows [offsets[b], offsets[b+1]) of one packed tensor: odd,
- * single-token and empty sequences in any mixture.  What one sequence computes
- * never depends on another's rows.
+ * single-token and empty sequences in any mixture.  A sequence's results (not
+ * the sums over all of them) have the same bits in any batch.
  *
  * Strides.  Unlike the tensors above, rows may be strided: `ld*` is the number
  * of elements from one row to the next, >= C (C when dense), so that a slice
@@ -430,7 +430,7 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * pointer (tensors of zero rows may be NULL), CONV_ERR_PARAM for B < 1, T < 0,
  * C < 1, an unknown dtype, ld < C, a pointer not aligned to its element or a
  * bad option, CONV_ERR_OVERFLOW for 2^30 or more rows, more than 2^20 channels,
- * B*C of 2^31 or more, or B * (T/64 + 1) or (rows/64 + B) * (C/64) above 2^23,
+ * B*C of 2^31 or more, or rows/64 + 2 B or (rows/64 + B) * (C/64) above 2^23,
  * CONV_ERR_WORKSPACE for a workspace that is needed and missing, too small or
  * not 16-byte aligned,
  * CONV_ERR_ALIAS when an output overlaps an input, another output or the
@@ -457,7 +457,8 @@ typedef struct {
  * (zeros when state is NULL).  w is (C, K), tap K-1 on the token itself; bias
  * (C) may be NULL; state and state_out are (B, K-1, C), oldest row first.
  * state_out (NULL: not wanted) receives the last K-1 rows of X, the state
- * with which the next tokens continue. */
+ * with which the next tokens continue.  (It is a copy: a gradient of state_out
+ * is to be added to the gradients of the rows it holds.) */
 CONV_API conv_status_t conv_causal_fwd(const conv_seq_t *seq, int K, int silu, const void *x, int64_t ldx,
                                        const void *w, const float *bias, const void *state, void *y, int64_t ldy,
                                        void *state_out, void *stream);

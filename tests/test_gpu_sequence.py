@@ -534,3 +534,30 @@ def test_nan_of_all_ones():
     hit = torch.zeros(1, T, C, dtype=torch.bool, device="cuda")
     hit[0, :601, 2] = True
     assert torch.equal(torch.isnan(dx), hit)
+
+
+@pytest.mark.parametrize("B_", [65, 4097, 5000])
+def test_thousands_of_packed_sequences(B_):
+    """Packed sequences, many of them empty, give the rows of the same sequences in an equal batch with
+    arbitrary rows behind their ends: bit for bit, forward and backward."""
+    rng = np.random.default_rng(B_)
+    lens = rng.integers(0, 200, B_) * (rng.random(B_) < 0.7)
+    lens[-1] = 199
+    T, C = int(lens.max()), 8
+    x, g, u, dy = (_cuda(rng.standard_normal((B_, T, C)), torch.bfloat16) for _ in range(4))
+    w, decay = _cuda(rng.standard_normal((C, 4)), torch.bfloat16), _cuda(rng.uniform(-5, -1, C))
+    live = torch.arange(T, device="cuda")[None] < torch.tensor(lens, device="cuda")[:, None]
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    kw = dict(offsets=off, max_len=T)
+    px, pg, pu, pd = (t[live] for t in (x, g, u, dy))
+    assert torch.equal(B.causal_conv(px, w, silu=True, **kw), B.causal_conv(x, w, silu=True)[live])
+    y, hT, st = B.gated_scan(px, pg, pu, decay, with_states=True, **kw)
+    want, _, st2 = B.gated_scan(x, g, u, decay, with_states=True)
+    assert torch.equal(y, want[live])
+    # a gradient of zero behind the ends is no gradient
+    grads = B.gated_scan_backward(px, pg, pu, decay, pd, st, **kw)
+    ref = B.gated_scan_backward(x, g, u, decay, dy * live[..., None], st2)
+    for a, b in zip(grads[:3], ref[:3]):
+        assert torch.equal(a, b[live])
+    dx = B.causal_conv_backward(px, w, pd, silu=True, **kw)[0]
+    assert torch.equal(dx, B.causal_conv_backward(x, w, dy * live[..., None], silu=True)[0][live])
