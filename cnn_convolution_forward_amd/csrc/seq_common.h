@@ -4,6 +4,10 @@
 
 #include "seq_internal.h"
 
+// A product and a sum are one operation only where the code says fmaf: whole and ragged runs, compiled
+// apart, then give the same bits.
+#pragma clang fp contract(off)
+
 namespace convfwd {
 
 // First row and length of sequence b.  Offsets come from device memory that
