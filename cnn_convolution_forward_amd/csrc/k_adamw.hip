@@ -33,8 +33,8 @@ static_assert(sizeof(Table) <= 4096, "kernel arguments");
 
 // 32 bits per element from the tensor's key (seed, step and its place in the list), by two rounds of
 // xor-shift and odd multiplication.
-__device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t i) {
-    uint32_t z = key + i * 0x9e3779b1u;
+constexpr uint32_t kPlace = 0x9e3779b1u;       // z = key + place in the tensor * kPlace
+__device__ __forceinline__ uint32_t random_bits(uint32_t z) {
     z = (z ^ (z >> 15)) * 0x2c1b3c6du;
     z = (z ^ (z >> 12)) * 0x297a2d39u;
     return z ^ (z >> 15);
@@ -105,10 +105,9 @@ __device__ __forceinline__ H4 to_copy(const F4 &p) {
     return __builtin_bit_cast(H4, u);
 }
 
-// The new moments, each operation rounded by itself: the values that are
-// encoded in 8 bits do not depend on how the compiler contracts them.
+// The new moments, each operation rounded by itself (seq_common.h switches
+// contraction off): what is encoded in 8 bits does not depend on the compiler.
 __device__ __forceinline__ void moments(const AdamwHyper &h, float g, float &m, float &v) {
-#pragma clang fp contract(off)
     const float m1 = m * h.b1, m2 = g * h.ob1;
     m = m1 + m2;
     const float g2 = g * g;
@@ -161,26 +160,37 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw32_chunk(co
 
 // Values of the codes: m = s (q/127)^2 with q's sign, v = s (q/255)^4.
 __device__ __forceinline__ float decode_m(float q, float s) {
-#pragma clang fp contract(off)
     const float u = q * (1.f / 127.f), w = u * u;
     return w * s;
 }
 __device__ __forceinline__ float decode_v(float q, float s) {
-#pragma clang fp contract(off)
     const float u = q * (1.f / 255.f), w = u * u, z = w * w;
     return z * s;
 }
 
-// The code of x in [0, s]: the one below or the one above, the upper with
-// probability (x - below)/(above - below).  The root only finds the lower code:
-// where its last unit in the last place picks a neighbour, x is one of the two
-// codes and both lead to it.
-template <bool SECOND> __device__ __forceinline__ uint32_t encode(float x, float s, float inv, uint32_t bits16) {
-#pragma clang fp contract(off)
+// The correctly rounded square root of y in [0, 1], from the hardware's s, which is a unit in the last
+// place off at most.  The midpoint to the neighbour below, s', squares to s s' and a quarter of a unit's
+// square: y <= s s' puts the root nearer to s' (and the like above).  Below 2^-100 it may miss: the code is 0
+// there anyway.  Without the correction one element in some ten million takes another code than the same
+// operations give elsewhere.
+__device__ __forceinline__ float exact_root(float y) {
+    const float s = __builtin_amdgcn_sqrtf(y);
+    const float below = __int_as_float(__float_as_int(s) - 1), above = __int_as_float(__float_as_int(s) + 1);
+    const float r = fmaf(-below, s, y) <= 0.f ? below : s;
+    return fmaf(-above, s, y) > 0.f ? above : r;
+}
+
+// The lower one of the two codes around x in [0, s], inv = 1/s.
+template <bool SECOND> __device__ __forceinline__ float lower_code(float x, float inv) {
     const float top = SECOND ? 255.f : 127.f;
-    float root = __builtin_amdgcn_sqrtf(x * inv);
-    if (SECOND) root = __builtin_amdgcn_sqrtf(root);
-    const float low = fminf(floorf(root * top), top - 1.f);
+    float root = exact_root(x * inv);
+    if (SECOND) root = exact_root(root);
+    return fminf(floorf(root * top), top - 1.f);
+}
+
+// The code of x: the lower one or the one above, that with probability
+// (x - below)/(above - below).
+template <bool SECOND> __device__ __forceinline__ uint32_t encode(float x, float s, float low, uint32_t bits16) {
     const float v0 = SECOND ? decode_v(low, s) : decode_m(low, s);
     const float v1 = SECOND ? decode_v(low + 1.f, s) : decode_m(low + 1.f, s);
     const float rnd = (float)bits16 * 0x1p-16f, d = v1 - v0, a = rnd * d, e = x - v0;
@@ -259,10 +269,13 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw8_chunk(con
         if (sv < 0x1p-126f) sv = 0.f;
         const float im = sm > 0.f ? 1.f / sm : 0.f, iv = sv > 0.f ? 1.f / sv : 0.f;
         B4 om = {0}, ov = {0};
+        const uint32_t place = t.key + ((uint32_t)i) * kPlace;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t z = random_bits(t.key, (uint32_t)i + e);
-            const uint32_t cm = encode<false>(fabsf(m[e]), sm, im, z & 0xffffu), cv = encode<true>(v[e], sv, iv, z >> 16);
+            const uint32_t z = random_bits(place + e * kPlace);
+            const float am = fabsf(m[e]);
+            const uint32_t cm = encode<false>(am, sm, lower_code<false>(am, im), z & 0xffffu);
+            const uint32_t cv = encode<true>(v[e], sv, lower_code<true>(v[e], iv), z >> 16);
             om.b |= ((m[e] < 0.f ? 0u - cm : cm) & 0xffu) << (8 * e);
             ov.b |= (cv & 0xffu) << (8 * e);
         }
