@@ -12,7 +12,8 @@
 //
 // Measured: 26 M parameters in 60 tensors with fp32 moments 129.4 us, 6.0 TB/s (a
 // large copy reaches 5.2); 60 M in 120 with 8-bit moments, their values read back
-// too, 307 us, 4.7 TB/s; 20 000 in 14 6.4 us, mostly the launch.  One element per
+// too, 314 us, 4.6 TB/s, the step's vector instructions taking about as long as its
+// bytes; 20 000 in 14 6.4 us, mostly the launch.  One element per
 // load took 163.5, 661.9 and 8.0 us.
 #include "optim_internal.h"
 #include "seq_common.h"
@@ -63,7 +64,7 @@ __device__ __forceinline__ float value(const H4 &g, int e) { return __uint_as_fl
 // Parameters, gradients and moments pass by once a step: non-temporal accesses, as a stream through the
 // caches only displaces (26 M parameters: 152.6 us without the hints, 135.2 us with them).  The bf16 copy
 // goes plainly beside fp32 moments (128 us) and as a stream beside 8-bit ones (60 M parameters with the
-// values: 293 us, 316 us plainly).
+// values, before the roots were corrected: 293 us, 316 us plainly).
 template <typename V, typename E> __device__ __forceinline__ V load_stream(const E *p) {
     typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) / 4), aligned(sizeof(E))));
     const W w = __builtin_nontemporal_load(reinterpret_cast<const W *>(p));
@@ -160,7 +161,7 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw32_chunk(co
 
 // Values of the codes: m = s (q/127)^2 with q's sign, v = s (q/255)^4.
 __device__ __forceinline__ float decode_m(float q, float s) {
-    const float u = q * (1.f / 127.f), w = u * u;
+    const float u = q * (1.f / 127.f), w = u * fabsf(u);
     return w * s;
 }
 __device__ __forceinline__ float decode_v(float q, float s) {
@@ -172,7 +173,7 @@ __device__ __forceinline__ float decode_v(float q, float s) {
 // place off at most.  The midpoint to the neighbour below, s', squares to s s' and a quarter of a unit's
 // square: y <= s s' puts the root nearer to s' (and the like above).  Below 2^-100 it may miss: the code is 0
 // there anyway.  Without the correction one element in some ten million takes another code than the same
-// operations give elsewhere.
+// operations give elsewhere; it costs 5 us of 314, the library's own root would cost 35.
 __device__ __forceinline__ float exact_root(float y) {
     const float s = __builtin_amdgcn_sqrtf(y);
     const float below = __int_as_float(__float_as_int(s) - 1), above = __int_as_float(__float_as_int(s) + 1);
@@ -190,13 +191,11 @@ template <bool SECOND> __device__ __forceinline__ float lower_code(float x, floa
 
 // The code of x: the lower one or the one above, that with probability
 // (x - below)/(above - below).
-template <bool SECOND> __device__ __forceinline__ uint32_t encode(float x, float s, float low, uint32_t bits16) {
+template <bool SECOND> __device__ __forceinline__ float encode(float x, float s, float low, uint32_t bits16) {
     const float v0 = SECOND ? decode_v(low, s) : decode_m(low, s);
     const float v1 = SECOND ? decode_v(low + 1.f, s) : decode_m(low + 1.f, s);
     const float rnd = (float)bits16 * 0x1p-16f, d = v1 - v0, a = rnd * d, e = x - v0;
-    uint32_t q = (uint32_t)low + (a < e ? 1u : 0u);
-    if (SECOND && q == 0u && x > 0.f && s > 0.f) q = 1u;
-    return q;
+    return a < e ? low + 1.f : low;
 }
 
 // The largest of a wave's non-negative values, as their bits (which order alike; a NaN is above all and
@@ -213,6 +212,11 @@ __device__ __forceinline__ float wave_max(float f) {
     const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
     const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
     return __uint_as_float(max(a, b));
+}
+// 1/s, one Newton step after the hardware's; 0 for s = 0.
+__device__ __forceinline__ float inverse(float s) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    return s > 0.f ? fmaf(r, fmaf(-s, r, 1.f), r) : 0.f;
 }
 __device__ __forceinline__ float larger(float f, float g) {
     return __uint_as_float(max(__float_as_uint(f), __float_as_uint(g) & 0x7fffffffu));
@@ -255,7 +259,7 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw8_chunk(con
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float q = signed_code(qm[u].b, e);
-            m[e] = copysignf(decode_m(fabsf(q), ms[u]), q);
+            m[e] = decode_m(q, ms[u]);
             v[e] = decode_v(plain_code(qv[u].b, e), vs[u]);
             moments(tb.h, value(g[u], e) * gs, m[e], v[e]);
             p[u].f[e] = update(tb.h, t.keep, p[u].f[e], m[e], v[e]);
@@ -267,17 +271,18 @@ template <bool BF16, bool FULL> __device__ __forceinline__ void adamw8_chunk(con
         float sm = wave_max(mmax), sv = wave_max(vmax);
         if (sm < 0x1p-126f) sm = 0.f;
         if (sv < 0x1p-126f) sv = 0.f;
-        const float im = sm > 0.f ? 1.f / sm : 0.f, iv = sv > 0.f ? 1.f / sv : 0.f;
+        const float im = inverse(sm), iv = inverse(sv), tiny = sv > 0.f ? 0.f : INFINITY;    // what a code 0 is for
         B4 om = {0}, ov = {0};
         const uint32_t place = t.key + ((uint32_t)i) * kPlace;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t z = random_bits(place + e * kPlace);
             const float am = fabsf(m[e]);
-            const uint32_t cm = encode<false>(am, sm, lower_code<false>(am, im), z & 0xffffu);
-            const uint32_t cv = encode<true>(v[e], sv, lower_code<true>(v[e], iv), z >> 16);
-            om.b |= ((m[e] < 0.f ? 0u - cm : cm) & 0xffu) << (8 * e);
-            ov.b |= (cv & 0xffu) << (8 * e);
+            const float cm = encode<false>(am, sm, lower_code<false>(am, im), z & 0xffffu);
+            float cv = encode<true>(v[e], sv, lower_code<true>(v[e], iv), z >> 16);
+            cv = v[e] > tiny ? fmaxf(cv, 1.f) : cv;
+            om.b = __builtin_amdgcn_cvt_pk_u8_f32(m[e] < 0.f && cm > 0.f ? 256.f - cm : cm, e, om.b);      // two's complement
+            ov.b = __builtin_amdgcn_cvt_pk_u8_f32(cv, e, ov.b);
         }
         store4<FULL>(tm, i, n, om);
         store4<FULL>(tv, i, n, ov);
@@ -311,7 +316,7 @@ template <bool FULL> __device__ __forceinline__ void values_chunk(const AdamwTen
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float q = signed_code(qm[u].b, e);
-                m.f[e] = copysignf(decode_m(fabsf(q), ms[u]), q);
+                m.f[e] = decode_m(q, ms[u]);
                 v.f[e] = decode_v(plain_code(qv[u].b, e), vs[u]);
             }
             store4<FULL>(t.p, i, n, m);
