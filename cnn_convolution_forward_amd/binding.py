@@ -911,8 +911,9 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
         a = exp(-scale * softplus(decay) * sigmoid(gate)),  h = a h + sqrt(1 - a^2) sigmoid(inp) x
 
     gate and inp: like x; decay: float32 (C); h0: float32 (B, C) or None for zeros.  x, gate, inp and out
-    may be column slices of wider tensors.  Returns (y, h after the last tokens), and with_states also
-    the states gated_scan_backward starts from."""
+    may be column slices of wider tensors.  workspace: a uint8 tensor of
+    conv_scan_fwd_workspace_bytes(make_seq(x, ...)) bytes to use, or None to allocate one.  Returns
+    (y, h after the last tokens), and with_states also the states gated_scan_backward starts from."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
     ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
@@ -937,7 +938,8 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
                         workspace=None):
     """(dx, dgate, dinp, ddecay, dh0) of (y, h) = gated_scan(...) for upstream dy, like x, and dh, float32
     (B, C) or None for zeros (conv_scan_bwd).  states: as gated_scan(..., with_states=True) returned them
-    for the same inputs.  `out`: (dx, dgate, dinp) to write into, perhaps column slices of one tensor."""
+    for the same inputs.  `out`: (dx, dgate, dinp) to write into, perhaps column slices of one tensor;
+    workspace: as in gated_scan, of conv_scan_bwd_workspace_bytes."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
     ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
@@ -983,8 +985,10 @@ class AdamW:
     float32, or with bits=8 int8 and uint8 codes, and then m_scale, v_scale, float32 of ceil(n/256).
     Moments that are not given start at zero.  copies: bf16 tensors that receive the updated weights
     (what the convolutions read), or None.  weight_decay: a number, or one for each tensor.  steps: how
-    many were taken before.  The tensors are kept and their addresses laid out once; step() may be
-    given other gradients of the same sizes."""
+    many were taken before.  grad_scale: a float32 scalar on the GPU that multiplies every gradient (a clipping
+    factor, for instance), or None.  The tensors are kept and their addresses laid out once; step() may be
+    given other gradients of the same sizes.  8-bit moments round at random, by seed and step; lr and seed may
+    be changed between steps."""
 
     def __init__(self, params, grads, m=None, v=None, copies=None, bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.0, seed=0, steps=0, m_scale=None, v_scale=None, grad_scale=None):
