@@ -1046,24 +1046,33 @@ class AdamW:
         self._set_grads(grads)
 
     def _set_grads(self, grads):
+        """All of the list, or, where an entry is refused, nothing of it."""
         torch = _torch()
+        grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("grads: %d entries for %d tensors" % (len(grads), len(self.params)))
-        self.grads = list(grads)
-        kind = self.grads[0].dtype if self.grads else torch.float32
-        self._opt.grad_dtype = 0 if kind == torch.float32 else 1
-        kinds = (torch.float32,) if kind == torch.float32 else self._half
-        for e, g, p in zip(self._table, self.grads, self.params):
-            e.g = self._addr(g, p.numel(), kinds, "grads")
+        f32 = not grads or grads[0].dtype == torch.float32
+        kinds = (torch.float32,) if f32 else self._half
+        addrs = [self._addr(g, p.numel(), kinds, "grads") for g, p in zip(grads, self.params)]
+        self.grads = grads
+        self._opt.grad_dtype = 0 if f32 else 1
+        for e, a in zip(self._table, addrs):
+            e.g = a
 
     def step(self, grads=None):
-        """One step; lr and seed may be set between steps."""
-        if grads is not None:
-            self._set_grads(grads)
+        """One step; lr and seed may be set between steps.  A step that raises leaves the gradients as they were."""
         o = self._opt
         o.lr, (o.beta1, o.beta2), o.eps, o.seed, o.step = self.lr, self.betas, self.eps, self.seed, self.steps + 1
+        before = self.grads
+        if grads is not None:
+            self._set_grads(grads)
         if self.params:
-            _run(conv_adamw_step(o, self._table, len(self.params), _stream_of(self.params[0])), "conv_adamw_step")
+            try:
+                _run(conv_adamw_step(o, self._table, len(self.params), _stream_of(self.params[0])), "conv_adamw_step")
+            except ConvError:
+                if grads is not None:
+                    self._set_grads(before)
+                raise
         self.steps += 1
 
     def state_values(self, out=None):

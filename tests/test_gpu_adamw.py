@@ -247,3 +247,17 @@ def test_helper_refuses():
         B.AdamW(p, g, betas=(1.0, 0.9)).step()
     empty = B.AdamW([], [])
     empty.step()
+
+
+def test_refused_step_changes_nothing():
+    """After a list that is refused, the next step equals that of an optimiser that never saw it."""
+    n = 300
+    start, grad = torch.linspace(-1, 1, n, device="cuda"), torch.linspace(1, 2, n, device="cuda")
+    a, b = (B.AdamW([start.clone(), start.clone()], [grad.clone(), grad.clone()]) for _ in range(2))
+    for bad in ([grad.bfloat16(), grad], [grad * 3, grad[1:]], [grad * 3, a.params[1]]):     # a type, a size, an overlap
+        with pytest.raises((TypeError, ValueError, B.ConvError)):
+            a.step(bad)
+        a.step()
+        b.step()
+        for x, y in zip(a.params + a.m + a.v, b.params + b.m + b.v):
+            assert torch.equal(x, y)
