@@ -738,10 +738,20 @@ def _stream_of(t):
     """The current stream of t's device.  These helpers run once per token of an answer: the direct
     query takes 0.1 us, torch.cuda.current_stream_of(x) 3 us."""
     torch = _torch()
+    _on_current_device(t)
     query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if query is not None:
         return query(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _on_current_device(t):
+    """The default stream of every device is the same null handle, which a launch takes as the current
+    device's: a tensor of another one must not get there."""
+    torch = _torch()
+    now = torch._C._cuda_getDevice() if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device()
+    if t.get_device() != now:
+        raise ValueError("the tensors are on GPU %d, the current device is %d" % (t.get_device(), now))
 
 
 def _dtype_code(t, name):
@@ -759,9 +769,12 @@ def _dtype_code(t, name):
 def _ld(t, shape, like, name):
     """The row stride of a tensor of rows: its last axis is dense, and its leading axes are one
     evenly strided axis (a column slice of a dense tensor, for instance)."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    if t is not like:
+    if t is like:
+        if not t.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % name)
+    else:
+        if t.get_device() != like.get_device():
+            raise ValueError("%s must be on x's GPU" % name)
         if t.shape != shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
         if t.dtype != like.dtype:
@@ -786,11 +799,12 @@ def _ld(t, shape, like, name):
     return ld
 
 
-def _dense(t, shape, dtype, name):
+def _dense(t, shape, dtype, name, x):
+    """The address of a dense tensor on x's GPU."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
+    if t.get_device() != x.get_device():
+        raise ValueError("%s must be on x's GPU" % name)
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
@@ -815,6 +829,8 @@ def make_seq(x, offsets=None, max_len=None, name="x"):
         raise ValueError("packed sequences need max_len")
     if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 vector on the GPU")
+    if offsets.get_device() != x.get_device():
+        raise ValueError("offsets must be on the GPU of %s" % name)
     if offsets.shape[0] < 2:
         raise ValueError("offsets must hold B + 1 >= 2 values")
     return SeqParams(code, offsets.shape[0] - 1, max_len, x.shape[1], offsets.data_ptr(), x.shape[0])
@@ -829,6 +845,19 @@ def _step_seq(x):
 def _run(st, where):
     if st != CONV_OK:
         raise ConvError(st, where)
+
+
+def _workspace(ws, need, x):
+    """(address, bytes) of the workspace: the caller's, which the library holds to the size it needs, or a
+    new one (returned too, to be kept for the call)."""
+    torch = _torch()
+    if ws is None:
+        if not need:
+            return None, 0, None
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif ws.get_device() != x.get_device() or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on x's GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def _rows_out(out, x, name):
@@ -853,8 +882,8 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
     rows = (seq.B, K - 1, seq.C)
     y, ldy = _rows_out(out, x, "out")
     end = torch.empty(rows, dtype=x.dtype, device=x.device) if with_state else None
-    _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
-                         _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
+    _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
+                         _dense(bias, (seq.C,), torch.float32, "bias", x), _dense(state, rows, x.dtype, "state", x),
                          y.data_ptr(), ldy, end.data_ptr() if with_state else None, _stream_of(x)), "conv_causal_fwd")
     return (y, end) if with_state else y
 
@@ -876,8 +905,8 @@ def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=No
     ds = torch.empty(rows, dtype=x.dtype, device=x.device) if state is not None else None
     n = conv_causal_bwd_workspace_bytes(seq, K)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
-                         _dense(bias, (seq.C,), torch.float32, "bias"), _dense(state, rows, x.dtype, "state"),
+    _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
+                         _dense(bias, (seq.C,), torch.float32, "bias", x), _dense(state, rows, x.dtype, "state", x),
                          dy.data_ptr(), lddy, dx.data_ptr(), lddx, dw.data_ptr(), db.data_ptr(),
                          None if ds is None else ds.data_ptr(), ws.data_ptr(), n, _stream_of(x)), "conv_causal_bwd")
     return dx, dw, db, ds
@@ -893,9 +922,9 @@ def causal_conv_step(x, w, state, bias=None, silu=False, out=None):
         raise ValueError("w must be (channels, taps)")
     K = w.shape[1]
     y, ldy = _rows_out(out, x, "out")
-    _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w"),
-                          _dense(bias, (seq.C,), torch.float32, "bias"),
-                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state"), y.data_ptr(), ldy, _stream_of(x)),
+    _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
+                          _dense(bias, (seq.C,), torch.float32, "bias", x),
+                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state", x), y.data_ptr(), ldy, _stream_of(x)),
          "conv_causal_step")
     return y
 
@@ -923,14 +952,11 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
     states = None
     if with_states:
         states = torch.empty((seq.B, -(-seq.T // SCAN_BLOCK), seq.C), dtype=torch.float32, device=x.device)
-    if workspace is None:
-        n = conv_scan_fwd_workspace_bytes(seq)
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws, wsb, held = _workspace(workspace, conv_scan_fwd_workspace_bytes(seq) if workspace is None else 0, x)
     _run(conv_scan_fwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                       _dense(decay, (seq.C,), torch.float32, "decay"), _dense(h0, ends, torch.float32, "h0"),
+                       _dense(decay, (seq.C,), torch.float32, "decay", x), _dense(h0, ends, torch.float32, "h0", x),
                        y.data_ptr(), ldy, hT.data_ptr(), None if states is None else states.data_ptr(),
-                       None if workspace is None else workspace.data_ptr(), wsb, _stream_of(x)), "conv_scan_fwd")
+                       ws, wsb, _stream_of(x)), "conv_scan_fwd")
     return (y, hT, states) if with_states else (y, hT)
 
 
@@ -951,15 +977,13 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
     ends = (seq.B, seq.C)
     dd = torch.empty((seq.C,), dtype=torch.float32, device=x.device)
     dh0 = torch.empty(ends, dtype=torch.float32, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(conv_scan_bwd_workspace_bytes(seq), dtype=torch.uint8, device=x.device)
+    ws, wsb, held = _workspace(workspace, conv_scan_bwd_workspace_bytes(seq) if workspace is None else 0, x)
     nb = -(-seq.T // SCAN_BLOCK)
     _run(conv_scan_bwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                       _dense(decay, (seq.C,), torch.float32, "decay"),
-                       _dense(states, (seq.B, nb, seq.C), torch.float32, "states"), dy.data_ptr(), lddy,
-                       _dense(dh, ends, torch.float32, "dh"), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
-                       lddi, dd.data_ptr(), dh0.data_ptr(), workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), _stream_of(x)), "conv_scan_bwd")
+                       _dense(decay, (seq.C,), torch.float32, "decay", x),
+                       _dense(states, (seq.B, nb, seq.C), torch.float32, "states", x), dy.data_ptr(), lddy,
+                       _dense(dh, ends, torch.float32, "dh", x), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
+                       lddi, dd.data_ptr(), dh0.data_ptr(), ws, wsb, _stream_of(x)), "conv_scan_bwd")
     return dx, dg, di, dd, dh0
 
 
@@ -971,8 +995,8 @@ def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
     ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
     y, ldy = _rows_out(out, x, "out")
     _run(conv_scan_step(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                        _dense(decay, (seq.C,), torch.float32, "decay"),
-                        _dense(h, (seq.B, seq.C), torch.float32, "h"), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
+                        _dense(decay, (seq.C,), torch.float32, "decay", x),
+                        _dense(h, (seq.B, seq.C), torch.float32, "h", x), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
     return y
 
 
@@ -1016,9 +1040,13 @@ class AdamW:
             if got is not None and len(got) != n:
                 raise ValueError("%s: %d entries for %d tensors" % (name, len(got), n))
 
+        device = params[0].get_device() if n else -1
+
         def addr(t, size, dtypes, name):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("%s must be contiguous GPU tensors" % name)
+            if t.get_device() != device:
+                raise ValueError("%s must be on the first parameter's GPU" % name)
             if t.dtype not in dtypes:
                 raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
             if t.numel() != size:
@@ -1039,7 +1067,7 @@ class AdamW:
                 e.v_scale = addr(self.v_scale[i], blocks[i], f32, "v_scale")
             if copies is not None and copies[i] is not None:
                 e.copy = addr(copies[i], sizes[i], half, "copies")
-        if grad_scale is not None:
+        if grad_scale is not None and n:
             addr(grad_scale, 1, f32, "grad_scale")
         self.grad_scale = grad_scale
         self._opt = AdamwOptions(bits=bits, grad_scale=None if grad_scale is None else grad_scale.data_ptr())

@@ -561,3 +561,27 @@ def test_thousands_of_packed_sequences(B_):
         assert torch.equal(a, b[live])
     dx = B.causal_conv_backward(px, w, pd, silu=True, **kw)[0]
     assert torch.equal(dx, B.causal_conv_backward(x, w, dy * live[..., None], silu=True)[0][live])
+
+
+def test_workspaces_of_other_memory_are_refused():
+    """A workspace has to be the GPU's, dense and large enough; one that is gives the same bits as none."""
+    rng = np.random.default_rng(1)
+    x, g, u, dy = (_cuda(rng.standard_normal((2, 300, 32)), torch.bfloat16) for _ in range(4))
+    decay = _cuda(rng.uniform(-5, -1, 32))
+    y, hT, st = B.gated_scan(x, g, u, decay, with_states=True)
+    want = B.gated_scan_backward(x, g, u, decay, dy, st)
+    seq = B.make_seq(x)
+    for n, call in ((B.conv_scan_fwd_workspace_bytes(seq), lambda w: B.gated_scan(x, g, u, decay, with_states=True, workspace=w)),
+                    (B.conv_scan_bwd_workspace_bytes(seq), lambda w: B.gated_scan_backward(x, g, u, decay, dy, st, workspace=w))):
+        for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)):
+            with pytest.raises(ValueError):
+                call(bad)
+        with pytest.raises(B.ConvError):
+            call(torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+        got = call(torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert all(torch.equal(a, b) for a, b in zip(got, (y, hT, st) if len(got) == 3 else want))
+    # checked on the host only: no call is made with it
+    with pytest.raises(ValueError):
+        B.gated_scan(x, g, u, decay.cpu())
+    with pytest.raises(ValueError):
+        B.gated_scan(x, g.cpu(), u, decay)
