@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "conv_fwd.h"
+#include "scan_grid.h"
 #include "scan_math.h"
 
 namespace convfwd {
@@ -20,6 +21,7 @@ namespace {
 
 constexpr int kBlock = CONV_SCAN_BLOCK;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+static_assert(kThreads == kScanThreads, "the grid is limited by its threads");
 
 // ---- chunks and the carries between them -----------------------------------------
 //
@@ -665,17 +667,13 @@ Chunks chunks(const Seq &s, int tokens) {
     return ch;
 }
 
-// Some 64 groups: all blocks of channels, times as many batches of sequences (packed ones, whose chunks
-// are numbered through, stay together).
-void set_groups(const Seq &s, Chunks &ch, int channels) {
+// Groups for `channels` channels a workgroup; returns the workgroups there are.
+int64_t set_groups(const Seq &s, Chunks &ch, int channels) {
     ch.nct = (s.C + channels - 1) / channels;
-    const bool through = s.off && ch.per > 1;
-    const int gb = through ? 1 : std::min(s.B, std::max(1, 64 / ch.nct));
-    ch.groups = ch.nct * gb;
-    ch.nb = (s.B + gb - 1) / gb;
-}
-int64_t grid_size(const Seq &s, const Chunks &ch) {
-    return ch.groups * (s.off && ch.per > 1 ? ch.total : (int64_t)ch.per * ch.nb);
+    const ScanGrid g = scan_grid(s.B, ch.nct, ch.per, s.off && ch.per > 1 ? ch.total : 0);
+    ch.groups = g.groups;
+    ch.nb = g.nb;
+    return g.size;
 }
 
 // Workspace of the links: the counter, the offsets, the rates, the stages, and then per chunk and channel
@@ -689,12 +687,12 @@ size_t link_bytes(const Seq &s, const Chunks &ch) {
     return ch.per > 1 ? (size_t)(counter_bytes(ch) + off_bytes(s) + pad16(4 * s.C) + stage_bytes(ch) + 16 * link_units(s, ch)) : 0;
 }
 
-// Lays the links out in ws and empties them; s then has the ascending offsets.
-void set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const float *decay, hipStream_t st) {
+// Lays the links out in ws and empties them; s then has the ascending offsets.  grid: workgroups.
+hipError_t set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const float *decay, int64_t &grid, hipStream_t st) {
     char *p = (char *)ws;
     const Chunks sizes = ch;
-    set_groups(s, ch, channels);
-    if (ch.per <= 1) return;
+    grid = set_groups(s, ch, channels);
+    if (ch.per <= 1) return hipSuccess;
     ch.counter = (uint32_t *)p;
     ch.off = (int32_t *)(p += counter_bytes(sizes));
     ch.rate = (float *)(p += off_bytes(s));
@@ -705,6 +703,7 @@ void set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const fl
     const int64_t n = link_units(s, ch), threads = std::max({n, ch.total * ch.nct, (int64_t)s.C, (int64_t)ch.groups});
     scan_fill_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(s, ch, n, scale, decay);
     if (s.off) s.off = ch.off;
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -718,12 +717,12 @@ size_t scan_bwd_workspace(const Seq &s) {
 template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
-                     Chunks ch, hipStream_t st) {
+                     Chunks ch, int64_t grid, hipStream_t st) {
     const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
                       read_once(y, ldy, sizeof(T));
     const auto run = ch.per > 1 ? (once ? scan_fwd_kernel<T, VEC, true, true> : scan_fwd_kernel<T, VEC, true, false>)
                                 : (once ? scan_fwd_kernel<T, VEC, false, true> : scan_fwd_kernel<T, VEC, false, false>);
-    run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
+    run<<<(unsigned)grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
                                                          decay, h0, (T *)y, ldy, hT, states, ch);
 }
 
@@ -732,9 +731,11 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
                            int64_t ldy, float *hT, float *states, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, st);
+    int64_t grid;
+    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, st);
+    if (e != hipSuccess) return e;              // no chunk may be taken from counters that are not set
     const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
-    run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, st);
+    run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, grid, st);
     return hipGetLastError();
 }
 
@@ -742,13 +743,13 @@ template <typename T, int VEC>
 static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *states, const void *dy, int64_t lddy, const float *dhT,
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
-                     Chunks ch, hipStream_t st) {
+                     Chunks ch, int64_t grid, hipStream_t st) {
     const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
                       read_once(dy, lddy, sizeof(T)) && read_once(dx, lddx, sizeof(T)) && read_once(dgate, lddg, sizeof(T)) &&
                       read_once(dinp, lddi, sizeof(T));
     const auto run = ch.per > 1 ? (once ? scan_bwd_kernel<T, VEC, true, true> : scan_bwd_kernel<T, VEC, true, false>)
                                 : (once ? scan_bwd_kernel<T, VEC, false, true> : scan_bwd_kernel<T, VEC, false, false>);
-    run<<<(unsigned)grid_size(s, ch), kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
+    run<<<(unsigned)grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
                                                          decay, states, (const T *)dy, lddy, dhT, (T *)dx, lddx, (T *)dgate,
                                                          lddg, (T *)dinp, lddi, part, dh0, ch);
 }
@@ -759,11 +760,15 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
                            float *ddecay, float *dh0, void *ws, hipStream_t st) {
     Chunks ch = chunks(s, kBwdChunk);
     Seq q = s;
-    set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, st);
+    int64_t grid;
+    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, st);
+    if (e != hipSuccess) return e;              // no chunk may be taken from counters that are not set
     float *part = (float *)((char *)ws + link_bytes(s, chunks(s, kBwdChunk)));
     const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,
-        st);
+        grid, st);
+    const hipError_t e2 = hipGetLastError();
+    if (e2 != hipSuccess) return e2;            // there are no partial sums
     scan_reduce_kernel<<<(s.C + 15) / 16, 1024, 0, st>>>(part, ch.total, s.C, scale, decay, ddecay);
     return hipGetLastError();
 }

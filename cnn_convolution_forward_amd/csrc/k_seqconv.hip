@@ -375,14 +375,17 @@ void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, c
 }
 
 template <typename T, int VEC, int K, bool SILU>
-void bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
+hipError_t bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, const T *state, const T *dy, int64_t lddy,
          T *dx, int64_t lddx, float *dw, float *db, T *dstate, float *part, hipStream_t st) {
     const Tiling t = tiling(s, VEC, kBwdLeast);
     const auto run = VEC > 1 && read_once(x, ldx, sizeof(T)) && read_once(dy, lddy, sizeof(T))
                          ? causal_bwd_kernel<T, VEC, K, SILU, (VEC > 1)> : causal_bwd_kernel<T, VEC, K, SILU, false>;
     run<<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per,
                                                           t.bx_log2, t.tl);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;              // there are no partial sums
     causal_reduce_kernel<<<dim3((s.C + 15) / 16, K + 1), 1024, 0, st>>>(part, t.n, s.C, K, dw, db);
+    return hipGetLastError();
 }
 
 template <typename T, int VEC, int K, bool SILU>
@@ -415,9 +418,9 @@ void fwd_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, c
 }
 
 template <typename T, int VEC>
-void bwd_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, const float *bias, const T *state,
+hipError_t bwd_k(const Seq &s, int K, int silu, const T *x, int64_t ldx, const T *w, const float *bias, const T *state,
            const T *dy, int64_t lddy, T *dx, int64_t lddx, float *dw, float *db, T *ds, float *part, hipStream_t st) {
-#define CALL(KK, S) bwd<T, VEC, KK, S>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dw, db, ds, part, st)
+#define CALL(KK, S) return bwd<T, VEC, KK, S>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dw, db, ds, part, st)
     SEQCONV_CASES(CALL)
 #undef CALL
 }
@@ -458,14 +461,11 @@ hipError_t launch_causal_bwd(const Seq &s, bool bf16, int K, int silu, const voi
                              float *dw, float *db, void *ds, float *part, hipStream_t st) {
     const auto run = [&](auto tag, auto f) {
         typedef decltype(tag) T;
-        f(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy, (T *)dx, lddx, dw, db,
+        return f(s, K, silu, (const T *)x, ldx, (const T *)w, bias, (const T *)state, (const T *)dy, lddy, (T *)dx, lddx, dw, db,
           (T *)ds, part, st);
     };
-    if (bf16)
-        run(uint16_t{}, s.C >= kBwdVec ? bwd_k<uint16_t, kBwdVec> : bwd_k<uint16_t, 1>);
-    else
-        run(float{}, s.C >= kBwdVec ? bwd_k<float, kBwdVec> : bwd_k<float, 1>);
-    return hipGetLastError();
+    return bf16 ? run(uint16_t{}, s.C >= kBwdVec ? bwd_k<uint16_t, kBwdVec> : bwd_k<uint16_t, 1>)
+                : run(float{}, s.C >= kBwdVec ? bwd_k<float, kBwdVec> : bwd_k<float, 1>);
 }
 
 hipError_t launch_causal_step(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,

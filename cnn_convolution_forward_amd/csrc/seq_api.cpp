@@ -83,6 +83,14 @@ conv_status_t make_seq(const conv_seq_t *q, bool step, Seq &s) {
     return CONV_OK;
 }
 
+// The recurrence has 512 threads to a workgroup and a launch fewer than 2^32: the last of the sizes above is
+// one too many.
+conv_status_t make_scan(const conv_seq_t *q, Seq &s) {
+    const conv_status_t st = make_seq(q, false, s);
+    if (st != CONV_OK) return st;
+    return (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) >= kMaxBlocks ? CONV_ERR_OVERFLOW : CONV_OK;
+}
+
 int esize(const conv_seq_t *q) { return q->dtype == CONV_OUT_BF16 ? 2 : 4; }
 
 conv_status_t check_workspace(const void *ws, size_t bytes, size_t need) {
@@ -164,14 +172,14 @@ conv_status_t conv_causal_step(const conv_seq_t *seq, int K, int silu, const voi
 
 size_t conv_scan_fwd_workspace_bytes(const conv_seq_t *seq) {
     Seq s;
-    return make_seq(seq, false, s) == CONV_OK ? convfwd::scan_fwd_workspace(s) : 0;
+    return make_scan(seq, s) == CONV_OK ? convfwd::scan_fwd_workspace(s) : 0;
 }
 
 conv_status_t conv_scan_fwd(const conv_seq_t *seq, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg,
                             const void *inp, int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy,
                             float *hT, float *states, void *workspace, size_t workspace_bytes, void *stream) {
     Seq s;
-    TRY(make_seq(seq, false, s));
+    TRY(make_scan(seq, s));
     if (!decay || (s.rows > 0 && (!x || !gate || !inp || !y))) return CONV_ERR_NULL;
     if (!(scale >= 0.f) || isinf(scale)) return CONV_ERR_PARAM;
     const size_t need = convfwd::scan_fwd_workspace(s);
@@ -189,7 +197,7 @@ conv_status_t conv_scan_fwd(const conv_seq_t *seq, float scale, const void *x, i
 
 size_t conv_scan_bwd_workspace_bytes(const conv_seq_t *seq) {
     Seq s;
-    return make_seq(seq, false, s) == CONV_OK ? convfwd::scan_bwd_workspace(s) : 0;
+    return make_scan(seq, s) == CONV_OK ? convfwd::scan_bwd_workspace(s) : 0;
 }
 
 conv_status_t conv_scan_bwd(const conv_seq_t *seq, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -197,7 +205,7 @@ conv_status_t conv_scan_bwd(const conv_seq_t *seq, float scale, const void *x, i
                             int64_t lddy, const float *dhT, void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp,
                             int64_t lddi, float *ddecay, float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
     Seq s;
-    TRY(make_seq(seq, false, s));
+    TRY(make_scan(seq, s));
     if (!decay || !ddecay || (s.rows > 0 && (!x || !gate || !inp || !states || !dy || !dx || !dgate || !dinp)))
         return CONV_ERR_NULL;
     if (!(scale >= 0.f) || isinf(scale)) return CONV_ERR_PARAM;

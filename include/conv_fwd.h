@@ -430,7 +430,8 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * pointer (tensors of zero rows may be NULL), CONV_ERR_PARAM for B < 1, T < 0,
  * C < 1, an unknown dtype, ld < C, a pointer not aligned to its element or a
  * bad option, CONV_ERR_OVERFLOW for 2^30 or more rows, more than 2^20 channels,
- * B*C of 2^31 or more, or rows/64 + 2 B or (rows/64 + B) * (C/64) above 2^23,
+ * B*C of 2^31 or more, or rows/64 + 2 B or (rows/64 + B) * (C/64) above 2^23
+ * (for the recurrence the latter of 2^23 or more),
  * CONV_ERR_WORKSPACE for a workspace that is needed and missing, too small or
  * not 16-byte aligned,
  * CONV_ERR_ALIAS when an output overlaps an input, another output or the

@@ -585,3 +585,21 @@ def test_workspaces_of_other_memory_are_refused():
         B.gated_scan(x, g, u, decay.cpu())
     with pytest.raises(ValueError):
         B.gated_scan(x, g.cpu(), u, decay)
+
+
+def test_long_sequences_of_one_channel():
+    """65 sequences of 2^22 tokens: 65 x 65536 chunks, near what a launch can hold.  Each gives the bits
+    that it gives alone."""
+    n, T = 65, 1 << 22
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x, g, u, dy = (torch.empty(n, T, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(4))
+    decay = torch.tensor([-4.0], device="cuda")
+    y, hT, st = B.gated_scan(x, g, u, decay, with_states=True)
+    grads = B.gated_scan_backward(x, g, u, decay, dy, st)
+    for b in (0, 31, 64):
+        one = [t[b:b + 1] for t in (x, g, u, dy)]
+        y1, h1, s1 = B.gated_scan(*one[:3], decay, with_states=True)
+        assert torch.equal(y1[0], y[b]) and torch.equal(h1[0], hT[b]) and torch.equal(s1[0], st[b])
+        alone = B.gated_scan_backward(*one[:3], decay, one[3], s1)
+        for p, q in zip(alone[:3], grads[:3]):
+            assert torch.equal(p[0], q[b])
