@@ -274,6 +274,29 @@ __device__ __forceinline__ void load_rows(typename Pack<T, VEC>::type (&v)[N], c
     }
 }
 
+// Composed factors.  A product of many factors above 0 may underflow, and 0 * inf would then make NaN of an
+// infinite state that each factor by itself passes on; so it stays at the smallest number there is, and is
+// 0 only with a factor 0.  What that adds to a finite result is below 2^-149 of the state.
+constexpr float kLeast = 0x1p-149f;
+__device__ __forceinline__ float compose(float p, float q) {
+    const float v = p * q;
+    return v == 0.f && p != 0.f && q != 0.f ? kLeast : v;
+}
+// The same for the product A of a run's factors, which are looked at only where it is 0.
+template <int VEC, int L> __device__ __forceinline__ void keep_positive(float (&A)[VEC], const float (&a)[L][VEC]) {
+    bool under = false;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) under = under || A[v] == 0.f;
+    if (!__any(under)) return;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        bool all = A[v] == 0.f;
+#pragma unroll
+        for (int i = 0; i < L; ++i) all = all && a[i][v] != 0.f;
+        A[v] = all ? kLeast : A[v];
+    }
+}
+
 // ---- forward -----------------------------------------------------------------------
 
 // Tokens of a wave and of a workgroup.  Per lane 16 tokens of two channels: 48 loads under way, a and b in
@@ -330,6 +353,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
                 H[v] = fmaf(a[i][v], H[v], bb[i][v]);
             }
         }
+        keep_positive(A, a);
     };
     if (there >= L)
         read(std::true_type{});
@@ -346,7 +370,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
         for (int v = 0; v < VEC; ++v) {
             const float Aq = sA[q][lane * VEC + v], Hq = sH[q][lane * VEC + v];
             PH[v] = fmaf(Aq, PH[v], Hq);
-            PA[v] *= Aq;
+            PA[v] = compose(PA[v], Aq);
         }
     float c0[VEC];
     const bool more = CHAIN && t0 + kFwdChunk < len;
@@ -354,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             H[v] = fmaf(A[v], PH[v], H[v]);
-            A[v] *= PA[v];
+            A[v] = compose(A[v], PA[v]);
         }
         if (tile.k == 0) {
 #pragma unroll
@@ -487,6 +511,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
                 H[v] = fmaf(a[i][v], H[v], ms[i][v] * xv[v]);
             }
         }
+        keep_positive(A, a);
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
             float dv[VEC];
@@ -515,7 +540,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
         for (int v = 0; v < VEC; ++v) {
             const float Aq = sA[p][lane * VEC + v];
             PE[v] = fmaf(Aq, PE[v], sE[p][lane * VEC + v]);
-            PA[v] *= Aq;
+            PA[v] = compose(PA[v], Aq);
         }
     float c0[VEC];
     const int behind = (len + kBwdChunk - 1) / kBwdChunk - 1 - tile.k;           // chunks after this one
@@ -524,7 +549,7 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             E[v] = fmaf(A[v], PE[v], E[v]);
-            A[v] *= PA[v];
+            A[v] = compose(A[v], PA[v]);
         }
         if (!CHAIN || behind == 0) {
 #pragma unroll
