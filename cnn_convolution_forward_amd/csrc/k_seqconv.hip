@@ -229,14 +229,19 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) d[i] = 0.f;
                 }
-                // dX[o] = sum_j w[j] dp[o+K-1-j], o = tt-K+1: dp[tt-j] is in slot (K-1+u-j) % K
+                // dX[o] = sum_j w[j] dp[o+K-1-j], o = tt-K+1: dp[tt-j] is in slot (K-1+u-j) % K.  Tokens in front of
+                // the sequence and behind it have no term: an infinite weight must not meet a zero there.
                 const int o = tt - (K - 1);
                 float g[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    g[i] = wf[0][i] * dp[(2 * K - 1 + u) % K][i];
+                for (int j = 0; j < K; ++j) {
+                    const bool there = inner || (tt - j >= 0 && tt - j < k.len);
 #pragma unroll
-                    for (int j = 1; j < K; ++j) g[i] = fmaf(wf[j][i], dp[(2 * K - 1 + u - j) % K][i], g[i]);
+                    for (int i = 0; i < VEC; ++i) {
+                        const float dj = dp[(2 * K - 1 + u - j) % K][i], before = j ? g[i] : 0.f;
+                        const float sum = j ? fmaf(wf[j][i], dj, before) : wf[j][i] * dj;
+                        g[i] = there ? sum : before;
+                    }
                 }
                 if (inner || (o >= k.t0 && o < k.t1))
                     store_f32(dxp + u * lddx, g);

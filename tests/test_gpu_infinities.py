@@ -1,6 +1,6 @@
 """Infinities in sequences go where the definition, taken token by token, sends
 them: an infinite value or gradient passes every factor above 0, however small
-the product of many is."""
+the product of many is, and terms that a sum does not have are not there."""
 import numpy as np
 import pytest
 import torch
@@ -93,3 +93,29 @@ def test_zero_factor_stops_infinities_as_nan():
     h0[0, 2] = 1.0
     y, _ = B.gated_scan(x, g, u, decay, h0=h0)
     assert bool(torch.isnan(y[0, :, 0]).all()) and bool((y[0, :, 1] == float("inf")).all()) and bool(torch.isfinite(y[0, :, 2]).all())
+
+
+# ---- causal convolution: a term that the sum does not have ------------------------
+
+@pytest.mark.parametrize("dtype,C", [("f32", 3), ("f32", 8), ("bf16", 24)])
+@pytest.mark.parametrize("weight", [float("inf"), float("nan")])
+def test_weights_touch_only_the_terms_there_are(dtype, C, weight):
+    """dX[t] sums w[j] dp[t+K-1-j] over the tokens there are: near a sequence's end, and in front of its start
+    for the carried rows, a weight whose token is missing does not enter."""
+    dt, K = DT[dtype], 4
+    for lens in ([1], [2], [7], [64], [65], [130]):
+        L = lens[0]
+        rng = np.random.default_rng(L)
+        x, dy = (_cuda(rng.standard_normal((1, L, C)), dt) for _ in range(2))
+        for j in range(K):
+            w = _cuda(rng.standard_normal((C, K)), dt)
+            w[:, j] = weight
+            dx, dw, db, ds = B.causal_conv_backward(x, w, dy, state=_cuda(rng.standard_normal((1, K - 1, C)), dt))
+            whole = np.zeros((L + K - 1, C))                   # rows -3 .. L-1 of dX
+            wv, dp, err = _np(w), _np(dy)[0], np.zeros((L + K - 1, C))
+            with np.errstate(invalid="ignore"):
+                for i in range(K):
+                    whole[i:i + L] += wv[:, i] * dp
+                    err[i:i + L] += (K + 1) * R.U * np.abs(wv[:, i] * dp)
+            _same(dx[0], whole[K - 1:], err[K - 1:], dtype == "bf16", "dx, %d tokens, tap %d" % (L, j))
+            _same(ds[0], whole[:K - 1], err[:K - 1], dtype == "bf16", "dstate, %d tokens, tap %d" % (L, j))
