@@ -741,26 +741,22 @@ def workspace_ex(x_shape, w_shape, stride=1, pad=0, dilation=1, groups=1, layout
 
 # ---- sequences of tokens ------------------------------------------------------
 
+_queries = None     # the current device, and the stream of a device, as integers
+
+
 def _stream_of(t):
-    """The current stream of t's device.  These helpers run once per token of an answer: the direct
-    query takes 0.1 us, torch.cuda.current_stream_of(x) 3 us."""
-    torch = _torch()
-    device = _on_current_device(t)
-    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if query is not None:
-        return query(device)
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _on_current_device(t):
-    """t's device, which has to be the current one: the default stream of every device is the same null
-    handle, which a launch takes as the current device's."""
-    torch = _torch()
-    query = getattr(torch._C, "_cuda_getDevice", None)
-    device, now = t.get_device(), torch.cuda.current_device() if query is None else query()
+    """The current stream of t's device, which has to be the current one: the default stream of every device is
+    the same null handle, which a launch takes as the current device's.  These helpers run once per token of
+    an answer: the direct queries take 0.1 us, torch.cuda.current_stream_of(x) 3 us."""
+    global _queries
+    if _queries is None:
+        torch = _torch()
+        _queries = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream))
+    device, now = t.get_device(), _queries[0]()
     if device != now:
         raise ValueError("the tensors are on GPU %d, the current device is %d" % (device, now))
-    return device
+    return _queries[1](device)
 
 
 def _dtype_code(t, name):
@@ -775,14 +771,14 @@ def _dtype_code(t, name):
     raise TypeError("%s has dtype %s, expected float32 or bf16" % (name, t.dtype))
 
 
-def _ld(t, shape, like, name):
+def _ld(t, shape, like, name, device=None):
     """The row stride of a tensor of rows: its last axis is dense, and its leading axes are one
     evenly strided axis (a column slice of a dense tensor, for instance)."""
     if t is like:
         if not t.is_cuda:
             raise ValueError("%s must be a GPU tensor" % name)
     else:
-        if t.get_device() != like.get_device():
+        if t.get_device() != (like.get_device() if device is None else device):
             raise ValueError("%s must be on x's GPU" % name)
         if t.shape != shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
@@ -808,11 +804,11 @@ def _ld(t, shape, like, name):
     return ld
 
 
-def _dense(t, shape, dtype, name, x):
-    """The address of a dense tensor on x's GPU."""
+def _dense(t, shape, dtype, name, device):
+    """The address of a dense tensor on x's GPU, `device`."""
     if t is None:
         return None
-    if t.get_device() != x.get_device():
+    if t.get_device() != device:
         raise ValueError("%s must be on x's GPU" % name)
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
@@ -884,6 +880,7 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
     may be column slices of a wider tensor.  Returns y, or (y, state after the last tokens)."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
+    dev = x.get_device()
     ldx = _ld(x, x.shape, x, "x")
     if w.dim() != 2:
         raise ValueError("w must be (channels, taps)")
@@ -891,8 +888,8 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
     rows = (seq.B, K - 1, seq.C)
     y, ldy = _rows_out(out, x, "out")
     end = torch.empty(rows, dtype=x.dtype, device=x.device) if with_state else None
-    _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
-                         _dense(bias, (seq.C,), torch.float32, "bias", x), _dense(state, rows, x.dtype, "state", x),
+    _run(conv_causal_fwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", dev),
+                         _dense(bias, (seq.C,), torch.float32, "bias", dev), _dense(state, rows, x.dtype, "state", dev),
                          y.data_ptr(), ldy, end.data_ptr() if with_state else None, _stream_of(x)), "conv_causal_fwd")
     return (y, end) if with_state else y
 
@@ -903,7 +900,8 @@ def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=No
     a state.  `out`: dx to write into, perhaps a column slice."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
-    ldx, lddy = _ld(x, x.shape, x, "x"), _ld(dy, x.shape, x, "dy")
+    dev = x.get_device()
+    ldx, lddy = _ld(x, x.shape, x, "x"), _ld(dy, x.shape, x, "dy", dev)
     if w.dim() != 2:
         raise ValueError("w must be (channels, taps)")
     K = w.shape[1]
@@ -914,8 +912,8 @@ def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=No
     ds = torch.empty(rows, dtype=x.dtype, device=x.device) if state is not None else None
     n = conv_causal_bwd_workspace_bytes(seq, K)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
-                         _dense(bias, (seq.C,), torch.float32, "bias", x), _dense(state, rows, x.dtype, "state", x),
+    _run(conv_causal_bwd(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", dev),
+                         _dense(bias, (seq.C,), torch.float32, "bias", dev), _dense(state, rows, x.dtype, "state", dev),
                          dy.data_ptr(), lddy, dx.data_ptr(), lddx, dw.data_ptr(), db.data_ptr(),
                          None if ds is None else ds.data_ptr(), ws.data_ptr(), n, _stream_of(x)), "conv_causal_bwd")
     return dx, dw, db, ds
@@ -926,14 +924,15 @@ def causal_conv_step(x, w, state, bias=None, silu=False, out=None):
     by the token in place (conv_causal_step)."""
     torch = _torch()
     seq = _step_seq(x)
+    dev = x.get_device()
     ldx = _ld(x, x.shape, x, "x")
     if w.dim() != 2:
         raise ValueError("w must be (channels, taps)")
     K = w.shape[1]
     y, ldy = _rows_out(out, x, "out")
-    _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", x),
-                          _dense(bias, (seq.C,), torch.float32, "bias", x),
-                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state", x), y.data_ptr(), ldy, _stream_of(x)),
+    _run(conv_causal_step(seq, K, int(bool(silu)), x.data_ptr(), ldx, _dense(w, (seq.C, K), x.dtype, "w", dev),
+                          _dense(bias, (seq.C,), torch.float32, "bias", dev),
+                          _dense(state, (seq.B, K - 1, seq.C), x.dtype, "state", dev), y.data_ptr(), ldy, _stream_of(x)),
          "conv_causal_step")
     return y
 
@@ -954,7 +953,8 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
     (y, h after the last tokens), and with_states also the states gated_scan_backward starts from."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
-    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
+    dev = x.get_device()
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate", dev), _ld(inp, x.shape, x, "inp", dev)
     y, ldy = _rows_out(out, x, "out")
     ends = (seq.B, seq.C)
     hT = torch.empty(ends, dtype=torch.float32, device=x.device)
@@ -963,7 +963,7 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
         states = torch.empty((seq.B, -(-seq.T // SCAN_BLOCK), seq.C), dtype=torch.float32, device=x.device)
     ws, wsb, held = _workspace(workspace, conv_scan_fwd_workspace_bytes(seq) if workspace is None else 0, x)
     _run(conv_scan_fwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                       _dense(decay, (seq.C,), torch.float32, "decay", x), _dense(h0, ends, torch.float32, "h0", x),
+                       _dense(decay, (seq.C,), torch.float32, "decay", dev), _dense(h0, ends, torch.float32, "h0", dev),
                        y.data_ptr(), ldy, hT.data_ptr(), None if states is None else states.data_ptr(),
                        ws, wsb, _stream_of(x)), "conv_scan_fwd")
     return (y, hT, states) if with_states else (y, hT)
@@ -977,8 +977,9 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
     workspace: as in gated_scan, of conv_scan_bwd_workspace_bytes."""
     torch = _torch()
     seq = make_seq(x, offsets, max_len)
-    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
-    lddy = _ld(dy, x.shape, x, "dy")
+    dev = x.get_device()
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate", dev), _ld(inp, x.shape, x, "inp", dev)
+    lddy = _ld(dy, x.shape, x, "dy", dev)
     o = (None, None, None) if out is None else out
     dx, lddx = _rows_out(o[0], x, "dx")
     dg, lddg = _rows_out(o[1], x, "dgate")
@@ -989,9 +990,9 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
     ws, wsb, held = _workspace(workspace, conv_scan_bwd_workspace_bytes(seq) if workspace is None else 0, x)
     nb = -(-seq.T // SCAN_BLOCK)
     _run(conv_scan_bwd(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                       _dense(decay, (seq.C,), torch.float32, "decay", x),
-                       _dense(states, (seq.B, nb, seq.C), torch.float32, "states", x), dy.data_ptr(), lddy,
-                       _dense(dh, ends, torch.float32, "dh", x), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
+                       _dense(decay, (seq.C,), torch.float32, "decay", dev),
+                       _dense(states, (seq.B, nb, seq.C), torch.float32, "states", dev), dy.data_ptr(), lddy,
+                       _dense(dh, ends, torch.float32, "dh", dev), dx.data_ptr(), lddx, dg.data_ptr(), lddg, di.data_ptr(),
                        lddi, dd.data_ptr(), dh0.data_ptr(), ws, wsb, _stream_of(x)), "conv_scan_bwd")
     return dx, dg, di, dd, dh0
 
@@ -1001,11 +1002,12 @@ def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
     float32 (B, C), in place (conv_scan_step)."""
     torch = _torch()
     seq = _step_seq(x)
-    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate"), _ld(inp, x.shape, x, "inp")
+    dev = x.get_device()
+    ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate", dev), _ld(inp, x.shape, x, "inp", dev)
     y, ldy = _rows_out(out, x, "out")
     _run(conv_scan_step(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
-                        _dense(decay, (seq.C,), torch.float32, "decay", x),
-                        _dense(h, (seq.B, seq.C), torch.float32, "h", x), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
+                        _dense(decay, (seq.C,), torch.float32, "decay", dev),
+                        _dense(h, (seq.B, seq.C), torch.float32, "h", dev), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
     return y
 
 

@@ -40,7 +40,7 @@ def test_tensors_of_another_device_are_refused(index, monkeypatch):
     with pytest.raises(ValueError, match="gate"):
         B._ld(Fake((2, 5, 8), index=index), x.shape, x, "gate")
     with pytest.raises(ValueError, match="decay"):
-        B._dense(Fake((8,), index=index), (8,), torch.float32, "decay", x)
+        B._dense(Fake((8,), index=index), (8,), torch.float32, "decay", 0)
     with pytest.raises(ValueError, match="offsets"):
         B.make_seq(Fake((5, 8)), Fake((3,), torch.int32, index), 5)
     with pytest.raises(ValueError, match="workspace"):
@@ -52,10 +52,10 @@ def test_tensors_of_another_device_are_refused(index, monkeypatch):
         B.AdamW(row(), row(), row(index), row())
     with pytest.raises(ValueError, match="grad_scale"):
         B.AdamW(row(), row(), row(), row(), grad_scale=Fake((1,), index=index))
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    B._on_current_device(x)
+    monkeypatch.setattr(B, "_queries", (lambda: 0, lambda d: 0x5000 + d))
+    assert B._stream_of(x) == 0x5000
     with pytest.raises(ValueError, match="current device"):
-        B._on_current_device(Fake((1,), index=index))
+        B._stream_of(Fake((1,), index=index))
 
 
 def test_workspace_is_memory_of_its_size():
