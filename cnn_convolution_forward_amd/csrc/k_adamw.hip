@@ -213,10 +213,12 @@ __device__ __forceinline__ float wave_max(float f) {
     const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
     return __uint_as_float(max(a, b));
 }
-// 1/s, one Newton step after the hardware's; 0 for s = 0.
+// 1/s, one Newton step after the hardware's; 0 for s = 0.  The hardware's is 0 where 1/s is below the normal
+// numbers (s > 2^126): there it is taken of s/16, and the result, two to three bits shorter, is still a place
+// within 2^-20 of x/s.
 __device__ __forceinline__ float inverse(float s) {
-    const float r = __builtin_amdgcn_rcpf(s);
-    return s > 0.f ? fmaf(r, fmaf(-s, r, 1.f), r) : 0.f;
+    const float f = s > 0x1p125f ? 0x1p-4f : 1.f, t = s * f, r = __builtin_amdgcn_rcpf(t);
+    return s > 0.f ? fmaf(r, fmaf(-t, r, 1.f), r) * f : 0.f;
 }
 __device__ __forceinline__ float larger(float f, float g) {
     return __uint_as_float(max(__float_as_uint(f), __float_as_uint(g) & 0x7fffffffu));
