@@ -1,6 +1,7 @@
 // seq_api.cpp -- the extern "C" entry points of the operators over sequences of
 // tokens and of the optimiser step.  As in conv_api.cpp, every argument is
 // checked on the host before any HIP call.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -277,7 +278,9 @@ conv_status_t conv_adamw_step(const conv_adamw_t *o, const conv_adamw_tensor_t *
     h.b2 = (float)o->beta2, h.ob2 = (float)(1.0 - o->beta2);
     h.lr_c1 = (float)(o->lr / (1.0 - pow(o->beta1, (double)o->step)));
     h.inv_sqrt_c2 = (float)(1.0 / sqrt(1.0 - pow(o->beta2, (double)o->step)));
-    h.eps = (float)o->eps;
+    // An eps below the normal numbers counts as the smallest of these: the hardware's reciprocal would make 0 * inf
+    // of 0 / eps.  A v above 0 has a root of 2^-75 or more, which does not notice either.
+    h.eps = o->eps > 0 && o->eps < FLT_MIN ? FLT_MIN : (float)o->eps;
     h.pad = 0.f;
     h.grad_scale = o->grad_scale;
     return to_status(convfwd::launch_adamw(h, list.data(), (int)list.size(), me == 1 ? convfwd::kAdamw8 : convfwd::kAdamw32,

@@ -1,5 +1,6 @@
 """The AdamW step at the ends of float32's range: 8-bit blocks whose scale has no
-normal reciprocal, or is at the cut below which a block is stored as zeros."""
+normal reciprocal, or is at the cut below which a block is stored as zeros, and
+an epsilon below the smallest normal number."""
 import numpy as np
 import pytest
 import torch
@@ -58,3 +59,19 @@ def test_scales_without_a_normal_reciprocal(largest):
         got = new[0].double().cpu().numpy()
         assert np.all(_between_neighbours(np.abs(now), scale, np.abs(got), top, power)), (top, largest)
         assert np.all(np.abs(got[::256]) == scale) and np.all(np.sign(got[got != 0]) == np.sign(now[got != 0]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-40, 1e-45, 1e-60])
+def test_zero_moments_with_a_tiny_epsilon(bits, eps):
+    """0 / eps is 0 for every eps above 0; the update of other elements does not notice it."""
+    n = 300
+    g = torch.zeros(n, device="cuda")
+    g[::3] = 0.5
+    opt = B.AdamW([torch.ones(n, device="cuda")], [g], bits=bits, eps=eps, lr=0.25)
+    opt.step()
+    p = opt.params[0]
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[::3] = False
+    assert bool((p[rest] == 1).all())
+    assert float((p[::3] - 0.75).abs().max()) <= 16 * 2.0 ** -23
