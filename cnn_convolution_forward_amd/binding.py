@@ -1118,6 +1118,9 @@ class AdamW:
         """The moments as float32, (list of m, list of v): with bits=8 the values their codes stand for
         (conv_adamw_state_values), written to `out`, two such lists, when given."""
         torch = _torch()
+        n = len(self.params)
+        if out is not None and [len(side) for side in out] != [n, n]:
+            raise ValueError("out: lists of %s tensors for the m and v of %d" % ([len(side) for side in out], n))
         if self.bits == 32:
             if out is not None:
                 for to, t in zip(list(out[0]) + list(out[1]), self.m + self.v):
@@ -1127,11 +1130,8 @@ class AdamW:
         if out is None:
             out = tuple([torch.empty(p.numel(), dtype=torch.float32, device=p.device) for p in self.params]
                         for _ in range(2))
-        n = len(self.params)
         ptrs = []
         for side in out:
-            if len(side) != n:
-                raise ValueError("out: %d entries for %d tensors" % (len(side), n))
             ptrs.append((ctypes.c_void_p * max(n, 1))(*[self._addr(t, p.numel(), (torch.float32,), "out")
                                                         for t, p in zip(side, self.params)]))
         if n:

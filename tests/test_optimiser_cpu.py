@@ -91,3 +91,21 @@ def test_gradients_of_another_type_are_taken_whole(calls):
     opt.step(iter(new))
     opt.step()
     assert seen == [(1, [g.address for g in new], 1), (1, [g.address for g in new], 2)]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lengths", [(2, 4), (3, 2), (3,), (3, 3, 3), (0, 6)])
+def test_state_values_needs_two_lists_of_all_tensors(bits, lengths, monkeypatch):
+    """Six tensors in another split would take m for v."""
+    row = lambda k, dtype=torch.float32: [Fake(0x10000 * k + 0x1000 * i, 10, dtype) for i in range(3)]
+    one = lambda k: [Fake(0x10000 * k + 0x1000 * i, 1) for i in range(3)]
+    kinds = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+    scales = {} if bits == 32 else {"m_scale": one(5), "v_scale": one(6)}
+    opt = B.AdamW(row(1), row(2), row(3, kinds[0]), row(4, kinds[1]), bits=bits, **scales)
+    monkeypatch.setattr(Fake, "copy_", lambda self, t: None, raising=False)
+    monkeypatch.setattr(B, "conv_adamw_state_values", lambda *a: 0)
+    monkeypatch.setattr(B, "_stream_of", lambda t: None)
+    with pytest.raises(ValueError):
+        opt.state_values(out=tuple([Fake(0x90000 + 0x1000 * i, 10) for i in range(n)] for n in lengths))
+    good = (row(7), row(8))
+    assert opt.state_values(out=good) is good
