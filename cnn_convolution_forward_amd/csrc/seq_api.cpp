@@ -207,7 +207,8 @@ conv_status_t conv_scan_bwd(const conv_seq_t *seq, float scale, const void *x, i
                             int64_t lddi, float *ddecay, float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
     Seq s;
     TRY(make_scan(seq, s));
-    if (!decay || !ddecay || (s.rows > 0 && (!x || !gate || !inp || !states || !dy || !dx || !dgate || !dinp)))
+    if (!decay || !ddecay || (s.rows > 0 && (!x || !gate || !inp || !dy || !dx || !dgate || !dinp)) ||
+        (s.rows > 0 && s.T > 0 && !states))                 // no tokens, no states
         return CONV_ERR_NULL;
     if (!(scale >= 0.f) || isinf(scale)) return CONV_ERR_PARAM;
     TRY(check_workspace(workspace, workspace_bytes, convfwd::scan_bwd_workspace(s)));

@@ -603,3 +603,14 @@ def test_long_sequences_of_one_channel():
         alone = B.gated_scan_backward(*one[:3], decay, one[3], s1)
         for p, q in zip(alone[:3], grads[:3]):
             assert torch.equal(p[0], q[b])
+
+
+def test_packed_rows_of_no_tokens():
+    """max_len = 0: every sequence is empty, whatever rows there are; all gradients are there."""
+    x = torch.ones(50, 8, dtype=torch.bfloat16, device="cuda")
+    kw = dict(offsets=torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda"), max_len=0)
+    decay, h0 = torch.zeros(8, device="cuda"), torch.full((2, 8), 3.0, device="cuda")
+    _, hT, st = B.gated_scan(x, x, x, decay, h0=h0, with_states=True, **kw)
+    assert torch.equal(hT, h0) and st.shape == (2, 0, 8)
+    grads = B.gated_scan_backward(x, x, x, decay, x, st, dh=h0, **kw)
+    assert not bool(grads[3].any()) and torch.equal(grads[4], h0)

@@ -189,3 +189,10 @@ def test_helpers_refuse_cpu_tensors_and_wrong_shapes():
         B.AdamW([x], [x])
     with pytest.raises(ValueError):
         B.AdamW([x], [x], bits=4)
+
+
+def test_scan_backward_of_no_tokens_needs_no_states():
+    """Packed rows with T = 0: the (B, 0, C) states have no address.  Refused for its workspace here, not for them."""
+    seq = _seq(T=0, offsets=0x100, tokens=50)
+    call = lambda seq: B.conv_scan_bwd(seq, 8.0, X, 24, G, 24, I, 24, D, None, Y, 24, None, S, 24, H, 24, WS, 24, W, None, None, 0)
+    assert call(seq) == 6 and call(_seq(offsets=0x100, tokens=50)) == 1
