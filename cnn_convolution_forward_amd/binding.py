@@ -819,9 +819,13 @@ def _dense(t, shape, dtype, name, device):
     return t.data_ptr()
 
 
-def make_seq(x, offsets=None, max_len=None, name="x"):
+SEQ_FILL = 256      # CONV_SEQ_FILL
+
+
+def make_seq(x, offsets=None, max_len=None, name="x", fill=False):
     """SeqParams for x: (B, T, C), or (tokens, C) packed, with offsets (B+1 int32 on the GPU) and
-    max_len, the length of the longest sequence."""
+    max_len, the length of the longest sequence: a sequence's rows past it belong to none.  fill: rows of
+    outputs that no sequence holds are set to zero (packed rows only; otherwise they are left)."""
     torch = _torch()
     code = _dtype_code(x, name)
     if offsets is None:
@@ -838,7 +842,7 @@ def make_seq(x, offsets=None, max_len=None, name="x"):
         raise ValueError("offsets must be on the GPU of %s" % name)
     if offsets.shape[0] < 2:
         raise ValueError("offsets must hold B + 1 >= 2 values")
-    return SeqParams(code, offsets.shape[0] - 1, max_len, x.shape[1], offsets.data_ptr(), x.shape[0])
+    return SeqParams(code + SEQ_FILL if fill else code, offsets.shape[0] - 1, max_len, x.shape[1], offsets.data_ptr(), x.shape[0])
 
 
 def _step_seq(x):
@@ -865,8 +869,11 @@ def _workspace(ws, need, x):
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
-def _rows_out(out, x, name):
+def _rows_out(out, x, name, fill=True):
+    """An output of rows and its row stride.  fill: rows that no sequence holds are set by the call."""
     torch = _torch()
+    if out is None and not fill:
+        return torch.zeros(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
     if out is None:
         y = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         return y, x.shape[-1]
@@ -877,9 +884,11 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
     """Causal depthwise convolution over the tokens of x, (B, T, C) or packed (see make_seq), float32 or
     bf16: conv_causal_fwd.  w: (C, K) of x's dtype, tap K-1 on the token itself; bias: float32 (C);
     state: the K-1 rows before each sequence, (B, K-1, C) of x's dtype, or None for zeros.  x and out
-    may be column slices of a wider tensor.  Returns y, or (y, state after the last tokens)."""
+    may be column slices of a wider tensor.  Packed rows that no sequence holds (in front of offsets[0],
+    behind offsets[-1], past max_len) come back as zeros; in a given out they stay as they are.
+    Returns y, or (y, state after the last tokens)."""
     torch = _torch()
-    seq = make_seq(x, offsets, max_len)
+    seq = make_seq(x, offsets, max_len, fill=out is None)
     dev = x.get_device()
     ldx = _ld(x, x.shape, x, "x")
     if w.dim() != 2:
@@ -897,9 +906,9 @@ def causal_conv(x, w, bias=None, silu=False, state=None, offsets=None, max_len=N
 def causal_conv_backward(x, w, dy, bias=None, silu=False, state=None, offsets=None, max_len=None, out=None):
     """(dx, dw, db, dstate) of y = causal_conv(x, w, bias, silu, state) for upstream gradient dy
     (conv_causal_bwd): dx and dstate of x's dtype, dw (C, K) and db (C) float32; dstate is None without
-    a state.  `out`: dx to write into, perhaps a column slice."""
+    a state.  `out`: dx to write into, perhaps a column slice.  Rows that no sequence holds: as in causal_conv."""
     torch = _torch()
-    seq = make_seq(x, offsets, max_len)
+    seq = make_seq(x, offsets, max_len, fill=out is None)
     dev = x.get_device()
     ldx, lddy = _ld(x, x.shape, x, "x"), _ld(dy, x.shape, x, "dy", dev)
     if w.dim() != 2:
@@ -949,10 +958,12 @@ def gated_scan(x, gate, inp, decay, scale=8.0, h0=None, offsets=None, max_len=No
 
     gate and inp: like x; decay: float32 (C); h0: float32 (B, C) or None for zeros.  x, gate, inp and out
     may be column slices of wider tensors.  workspace: a uint8 tensor of
-    conv_scan_fwd_workspace_bytes(make_seq(x, ...)) bytes to use, or None to allocate one.  Returns
-    (y, h after the last tokens), and with_states also the states gated_scan_backward starts from."""
+    conv_scan_fwd_workspace_bytes(make_seq(x, ...)) bytes to use, or None to allocate one.  Packed rows that
+    no sequence holds (in front of offsets[0], behind offsets[-1], past max_len) come back as zeros; in a given out they
+    stay as they are.  Returns (y, h after the last tokens), and with_states also the states that gated_scan_backward
+    starts from: float32 (B, ceil(T / 64), C), T being max_len for packed rows, not written past a sequence's end."""
     torch = _torch()
-    seq = make_seq(x, offsets, max_len)
+    seq = make_seq(x, offsets, max_len, fill=out is None)
     dev = x.get_device()
     ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate", dev), _ld(inp, x.shape, x, "inp", dev)
     y, ldy = _rows_out(out, x, "out")
@@ -973,17 +984,18 @@ def gated_scan_backward(x, gate, inp, decay, dy, states, scale=8.0, dh=None, off
                         workspace=None):
     """(dx, dgate, dinp, ddecay, dh0) of (y, h) = gated_scan(...) for upstream dy, like x, and dh, float32
     (B, C) or None for zeros (conv_scan_bwd).  states: as gated_scan(..., with_states=True) returned them
-    for the same inputs.  `out`: (dx, dgate, dinp) to write into, perhaps column slices of one tensor;
-    workspace: as in gated_scan, of conv_scan_bwd_workspace_bytes."""
+    for the same inputs.  `out`: (dx, dgate, dinp) to write into, perhaps column slices of one tensor, None for one to be
+    allocated; rows that no sequence holds, and workspace (of conv_scan_bwd_workspace_bytes): as in gated_scan."""
     torch = _torch()
-    seq = make_seq(x, offsets, max_len)
+    seq = make_seq(x, offsets, max_len, fill=out is None)
     dev = x.get_device()
     ldx, ldg, ldi = _ld(x, x.shape, x, "x"), _ld(gate, x.shape, x, "gate", dev), _ld(inp, x.shape, x, "inp", dev)
     lddy = _ld(dy, x.shape, x, "dy", dev)
     o = (None, None, None) if out is None else out
-    dx, lddx = _rows_out(o[0], x, "dx")
-    dg, lddg = _rows_out(o[1], x, "dgate")
-    di, lddi = _rows_out(o[2], x, "dinp")
+    fill = out is None or offsets is None
+    dx, lddx = _rows_out(o[0], x, "dx", fill)
+    dg, lddg = _rows_out(o[1], x, "dgate", fill)
+    di, lddi = _rows_out(o[2], x, "dinp", fill)
     ends = (seq.B, seq.C)
     dd = torch.empty((seq.C,), dtype=torch.float32, device=x.device)
     dh0 = torch.empty(ends, dtype=torch.float32, device=x.device)

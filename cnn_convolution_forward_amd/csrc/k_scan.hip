@@ -116,8 +116,8 @@ template <bool REV> __device__ __forceinline__ Tile get_tile(const Seq &s, const
     return o;
 }
 
-template <bool CHAIN> __device__ __forceinline__ uint32_t take_ticket(const Chunks &ch, uint32_t g, uint32_t *shared) {
-    if (!CHAIN) return blockIdx.x / ch.groups;
+template <bool CHAIN> __device__ __forceinline__ uint32_t take_ticket(const Chunks &ch, unsigned block, uint32_t g, uint32_t *shared) {
+    if (!CHAIN) return block / ch.groups;
     if (threadIdx.x == 0) *shared = atomicAdd(ch.counter + g * kCounter, 1u);
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(*shared);
@@ -226,9 +226,14 @@ __device__ __forceinline__ void publish_state(const Chunks &ch, int C, int c, co
 }
 
 // Empties the links (n units of 16 bytes of ones from ch.map on, zeros before), makes the channels'
-// rates, and (block 0, packed sequences) the ascending offsets.
+// rates, and (block 0, packed sequences) the ascending offsets; the last workgroups fill rows of outputs.
 __global__ __launch_bounds__(256) void scan_fill_kernel(Seq s, Chunks ch, int64_t n, float scale,
-                                                        const float *__restrict__ decay) {
+                                                        const float *__restrict__ decay, Fill f) {
+    const unsigned links = gridDim.x - f.blocks;
+    if (blockIdx.x >= links) {
+        fill_rows(s, f, blockIdx.x - links, f.blocks);
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) reinterpret_cast<uint4 *>(ch.map)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
     if (i < ch.total * ch.nct) ch.stage[i] = kNothing;
@@ -308,13 +313,21 @@ template <typename T, int VEC, bool CHAIN, bool ONCE>
 __global__ __launch_bounds__(kThreads, 4) void scan_fwd_kernel(
     Seq s, float scale, const T *__restrict__ x, int64_t ldx, const T *__restrict__ gate, int64_t ldg,
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ h0,
-    T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch) {
+    T *__restrict__ y, int64_t ldy, float *__restrict__ hT, float *__restrict__ states, Chunks ch, Fill f) {
     constexpr int L = kFwdRun, CW = 64 * VEC;
     __shared__ float sA[kWaves][CW], sH[kWaves][CW], sC[CW];
     __shared__ Links<VEC> sL;
     __shared__ uint32_t sTicket;
-    const uint32_t group = blockIdx.x % ch.groups;
-    const Tile tile = get_tile<false>(s, ch, group, take_ticket<CHAIN>(ch, group, &sTicket));
+    unsigned block = blockIdx.x;
+    if (!CHAIN) {                                  // the first workgroups fill; with chains the kernel in front of this one does
+        if (block < (unsigned)f.blocks) {
+            fill_rows(s, f, block, f.blocks);
+            return;
+        }
+        block -= f.blocks;
+    }
+    const uint32_t group = block % ch.groups;
+    const Tile tile = get_tile<false>(s, ch, group, take_ticket<CHAIN>(ch, block, group, &sTicket));
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -446,13 +459,21 @@ __global__ __launch_bounds__(kThreads, 4) void scan_bwd_kernel(
     const T *__restrict__ inp, int64_t ldi, const float *__restrict__ decay, const float *__restrict__ states,
     const T *__restrict__ dy, int64_t lddy, const float *__restrict__ dhT, T *__restrict__ dx, int64_t lddx,
     T *__restrict__ dgate, int64_t lddg, T *__restrict__ dinp, int64_t lddi, float *__restrict__ part,
-    float *__restrict__ dh0, Chunks ch) {
+    float *__restrict__ dh0, Chunks ch, Fill f) {
     constexpr int L = kBwdRun, CW = 64 * VEC;
     __shared__ float sA[kWaves][CW], sH[kWaves][CW], sE[kWaves][CW], sC[CW];
     __shared__ Links<VEC> sL;
     __shared__ uint32_t sTicket;
-    const uint32_t group = blockIdx.x % ch.groups;
-    const Tile tile = get_tile<true>(s, ch, group, take_ticket<CHAIN>(ch, group, &sTicket));
+    unsigned block = blockIdx.x;
+    if (!CHAIN) {                                  // the first workgroups fill; with chains the kernel in front of this one does
+        if (block < (unsigned)f.blocks) {
+            fill_rows(s, f, block, f.blocks);
+            return;
+        }
+        block -= f.blocks;
+    }
+    const uint32_t group = block % ch.groups;
+    const Tile tile = get_tile<true>(s, ch, group, take_ticket<CHAIN>(ch, block, group, &sTicket));
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int b = tile.b, C = s.C;
     int64_t first;
@@ -713,11 +734,18 @@ size_t link_bytes(const Seq &s, const Chunks &ch) {
 }
 
 // Lays the links out in ws and empties them; s then has the ascending offsets.  grid: workgroups.
-hipError_t set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const float *decay, int64_t &grid, hipStream_t st) {
+// f: the rows to fill; where there is no second chunk, and so no kernel for the links, the main one fills them
+// with workgroups of its own, if its grid has room for them.
+hipError_t set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, const float *decay, int64_t &grid, Fill &f,
+                     hipStream_t st) {
     char *p = (char *)ws;
     const Chunks sizes = ch;
     grid = set_groups(s, ch, channels);
-    if (ch.per <= 1) return hipSuccess;
+    if (ch.per <= 1) {
+        if (f.blocks) f.blocks = (int)std::min<int64_t>(f.blocks, kScanMaxGrid - grid);
+        grid += f.blocks;
+        return hipSuccess;
+    }
     ch.counter = (uint32_t *)p;
     ch.off = (int32_t *)(p += counter_bytes(sizes));
     ch.rate = (float *)(p += off_bytes(s));
@@ -726,7 +754,7 @@ hipError_t set_links(Seq &s, Chunks &ch, void *ws, int channels, float scale, co
     ch.state = (uint32_t *)(ch.map + ch.total * s.C);
     // one thread per unit of the links, per stage, per channel and per counter
     const int64_t n = link_units(s, ch), threads = std::max({n, ch.total * ch.nct, (int64_t)s.C, (int64_t)ch.groups});
-    scan_fill_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(s, ch, n, scale, decay);
+    scan_fill_kernel<<<(unsigned)((threads + 255) / 256) + f.blocks, 256, 0, st>>>(s, ch, n, scale, decay, f);
     if (s.off) s.off = ch.off;
     return hipGetLastError();
 }
@@ -742,13 +770,13 @@ size_t scan_bwd_workspace(const Seq &s) {
 template <typename T, int VEC>
 static void scan_fwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *h0, void *y, int64_t ldy, float *hT, float *states,
-                     Chunks ch, int64_t grid, hipStream_t st) {
+                     Chunks ch, int64_t grid, const Fill &f, hipStream_t st) {
     const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
                       read_once(y, ldy, sizeof(T));
     const auto run = ch.per > 1 ? (once ? scan_fwd_kernel<T, VEC, true, true> : scan_fwd_kernel<T, VEC, true, false>)
                                 : (once ? scan_fwd_kernel<T, VEC, false, true> : scan_fwd_kernel<T, VEC, false, false>);
     run<<<(unsigned)grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
-                                                         decay, h0, (T *)y, ldy, hT, states, ch);
+                                                         decay, h0, (T *)y, ldy, hT, states, ch, f);
 }
 
 hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate,
@@ -757,10 +785,12 @@ hipError_t launch_scan_fwd(const Seq &s, bool bf16, float scale, const void *x, 
     Chunks ch = chunks(s, kFwdChunk);
     Seq q = s;
     int64_t grid;
-    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, st);
+    const int waves = ch.per > 1 ? 4 : kWaves;
+    Fill f = bf16 ? fill_of<uint16_t>(s, waves, {(uint16_t *)y}, {ldy}) : fill_of<float>(s, waves, {(float *)y}, {ldy});
+    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, f, st);
     if (e != hipSuccess) return e;              // no chunk may be taken from counters that are not set
     const auto run = !bf16 ? scan_fwd<float, 1> : s.C > 1 ? scan_fwd<uint16_t, 2> : scan_fwd<uint16_t, 1>;
-    run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, grid, st);
+    run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, h0, y, ldy, hT, states, ch, grid, f, st);
     return hipGetLastError();
 }
 
@@ -768,7 +798,7 @@ template <typename T, int VEC>
 static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg, const void *inp,
                      int64_t ldi, const float *decay, const float *states, const void *dy, int64_t lddy, const float *dhT,
                      void *dx, int64_t lddx, void *dgate, int64_t lddg, void *dinp, int64_t lddi, float *part, float *dh0,
-                     Chunks ch, int64_t grid, hipStream_t st) {
+                     Chunks ch, int64_t grid, const Fill &f, hipStream_t st) {
     const bool once = read_once(x, ldx, sizeof(T)) && read_once(gate, ldg, sizeof(T)) && read_once(inp, ldi, sizeof(T)) &&
                       read_once(dy, lddy, sizeof(T)) && read_once(dx, lddx, sizeof(T)) && read_once(dgate, lddg, sizeof(T)) &&
                       read_once(dinp, lddi, sizeof(T));
@@ -776,7 +806,7 @@ static void scan_bwd(const Seq &s, float scale, const void *x, int64_t ldx, cons
                                 : (once ? scan_bwd_kernel<T, VEC, false, true> : scan_bwd_kernel<T, VEC, false, false>);
     run<<<(unsigned)grid, kThreads, 0, st>>>(s, scale, (const T *)x, ldx, (const T *)gate, ldg, (const T *)inp, ldi,
                                                          decay, states, (const T *)dy, lddy, dhT, (T *)dx, lddx, (T *)dgate,
-                                                         lddg, (T *)dinp, lddi, part, dh0, ch);
+                                                         lddg, (T *)dinp, lddi, part, dh0, ch, f);
 }
 
 hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -786,12 +816,16 @@ hipError_t launch_scan_bwd(const Seq &s, bool bf16, float scale, const void *x, 
     Chunks ch = chunks(s, kBwdChunk);
     Seq q = s;
     int64_t grid;
-    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, st);
+    const int waves = ch.per > 1 ? 4 : kWaves;
+    const std::initializer_list<int64_t> lds = {lddx, lddg, lddi};
+    Fill f = bf16 ? fill_of<uint16_t>(s, waves, {(uint16_t *)dx, (uint16_t *)dgate, (uint16_t *)dinp}, lds)
+                  : fill_of<float>(s, waves, {(float *)dx, (float *)dgate, (float *)dinp}, lds);
+    const hipError_t e = set_links(q, ch, ws, bf16 && s.C > 1 ? 128 : 64, scale, decay, grid, f, st);
     if (e != hipSuccess) return e;              // no chunk may be taken from counters that are not set
     float *part = (float *)((char *)ws + link_bytes(s, chunks(s, kBwdChunk)));
     const auto run = !bf16 ? scan_bwd<float, 1> : s.C > 1 ? scan_bwd<uint16_t, 2> : scan_bwd<uint16_t, 1>;
     run(q, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, lddy, dhT, dx, lddx, dgate, lddg, dinp, lddi, part, dh0, ch,
-        grid, st);
+        grid, f, st);
     const hipError_t e2 = hipGetLastError();
     if (e2 != hipSuccess) return e2;            // there are no partial sums
     scan_reduce_kernel<<<(s.C + 15) / 16, 1024, 0, st>>>(part, ch.total, s.C, scale, decay, ddecay);

@@ -74,16 +74,16 @@ struct Work {
     bool any, head;         // any: channels at all; head: the sequence's first run
 };
 
-template <int VEC> __device__ __forceinline__ Work get_work(const Seq &s, int per, int bx_log2, int tl) {
+template <int VEC> __device__ __forceinline__ Work get_work(const Seq &s, int64_t block, int per, int bx_log2, int tl) {
     Work k;
     const int by = kThreads >> bx_log2;
     const int tx = threadIdx.x & ((1 << bx_log2) - 1), ty = threadIdx.x >> bx_log2;
     Block at;
     if (!s.off || per == 1) {
-        at.b = blockIdx.x / per;
-        at.k = blockIdx.x % per;
+        at.b = (int)((unsigned)block / per);
+        at.k = (int)((unsigned)block % per);
     } else {
-        at = packed_block(s, by * tl, blockIdx.x);
+        at = packed_block(s, by * tl, block);
     }
     const int c = ((blockIdx.y << bx_log2) + tx) * VEC;
     k.any = c < s.C;
@@ -116,9 +116,14 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(Seq s, const T *__
                                                               const T *__restrict__ w, const float *__restrict__ bias,
                                                               const T *__restrict__ state, T *__restrict__ y,
                                                               int64_t ldy, T *__restrict__ state_out, int per,
-                                                              int bx_log2, int tl) {
+                                                              int bx_log2, int tl, Fill f) {
     constexpr int U = kGroup<K>;                   // rows loaded together: a multiple of K
-    const Work k = get_work<VEC>(s, per, bx_log2, tl);
+    const int block = (int)blockIdx.x - f.blocks;  // the first workgroups fill
+    if (block < 0) {
+        fill_rows(s, f, (int64_t)blockIdx.x * gridDim.y + blockIdx.y, (int64_t)f.blocks * gridDim.y);
+        return;
+    }
+    const Work k = get_work<VEC>(s, block, per, bx_log2, tl);
     if (!k.any) return;
     if (K > 1 && state_out && k.head) write_state<T, VEC, K>(x, ldx, state, state_out, k.first, k.len, k.b, s.C, k.c);
     if (k.t0 >= k.t1) return;
@@ -167,12 +172,17 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
                                                               const T *__restrict__ state, const T *__restrict__ dy,
                                                               int64_t lddy, T *__restrict__ dx, int64_t lddx,
                                                               T *__restrict__ dstate, float *__restrict__ part,
-                                                              int per, int bx_log2, int tl) {
+                                                              int per, int bx_log2, int tl, Fill f) {
     constexpr int U = kGroup<K>;
     __shared__ float red[kThreads * VEC];
+    const int block = (int)blockIdx.x - f.blocks;
+    if (block < 0) {
+        fill_rows(s, f, (int64_t)blockIdx.x * gridDim.y + blockIdx.y, (int64_t)f.blocks * gridDim.y);
+        return;
+    }
     const int bx = 1 << bx_log2, by = kThreads >> bx_log2;
     const int tx = threadIdx.x & (bx - 1), ty = threadIdx.x >> bx_log2;
-    const Work k = get_work<VEC>(s, per, bx_log2, tl);
+    const Work k = get_work<VEC>(s, block, per, bx_log2, tl);
     float dw[K][VEC] = {}, db[VEC] = {};
     const bool head = k.head && K > 1 && dstate;
     if (k.any && (k.t0 < k.t1 || head)) {
@@ -278,7 +288,7 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(Seq s, const T *__
             const int q = e & (bx - 1), i = e >> bx_log2, c = ((blockIdx.y << bx_log2) + q) * VEC;
             float v = 0.f;
             for (int r = 0; r < by; ++r) v += red[(r * VEC + i) * bx + q];
-            if (c < s.C) part[((int64_t)blockIdx.x * (K + 1) + j) * s.C + min(c, s.C - VEC) + i] = v;
+            if (c < s.C) part[((int64_t)block * (K + 1) + j) * s.C + min(c, s.C - VEC) + i] = v;
         }
     }
 }
@@ -376,7 +386,9 @@ void fwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *bias, c
     const Tiling t = tiling(s, VEC, kFwdLeast);
     const auto run = VEC > 1 && read_once(x, ldx, sizeof(T)) ? causal_fwd_kernel<T, VEC, K, SILU, (VEC > 1)>
                                                              : causal_fwd_kernel<T, VEC, K, SILU, false>;
-    run<<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, y, ldy, state_out, t.per, t.bx_log2, t.tl);
+    const Fill f = fill_of(s, kThreads / 64 * t.cblk, {y}, {ldy});
+    run<<<dim3((unsigned)t.n + f.blocks, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, y, ldy, state_out, t.per,
+                                                                     t.bx_log2, t.tl, f);
 }
 
 template <typename T, int VEC, int K, bool SILU>
@@ -385,8 +397,9 @@ hipError_t bwd(const Seq &s, const T *x, int64_t ldx, const T *w, const float *b
     const Tiling t = tiling(s, VEC, kBwdLeast);
     const auto run = VEC > 1 && read_once(x, ldx, sizeof(T)) && read_once(dy, lddy, sizeof(T))
                          ? causal_bwd_kernel<T, VEC, K, SILU, (VEC > 1)> : causal_bwd_kernel<T, VEC, K, SILU, false>;
-    run<<<dim3((unsigned)t.n, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part, t.per,
-                                                          t.bx_log2, t.tl);
+    const Fill f = fill_of(s, kThreads / 64 * t.cblk, {dx}, {lddx});
+    run<<<dim3((unsigned)t.n + f.blocks, t.cblk), kThreads, 0, st>>>(s, x, ldx, w, bias, state, dy, lddy, dx, lddx, dstate, part,
+                                                                     t.per, t.bx_log2, t.tl, f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;              // there are no partial sums
     causal_reduce_kernel<<<dim3((s.C + 15) / 16, K + 1), 1024, 0, st>>>(part, t.n, s.C, K, dw, db);

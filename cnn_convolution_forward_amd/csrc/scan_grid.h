@@ -20,14 +20,18 @@ struct ScanGrid {
 // B sequences of `per` chunks each; through > 0: chunks are numbered through, `through` of them, and stay together.
 inline ScanGrid scan_grid(int B, int nct, int per, int64_t through) {
     if (through > 0) return ScanGrid{nct, B, nct * through};
-    ScanGrid g;
+    const int64_t tiles = (int64_t)nct * per;
     int gB = nct >= 64 ? 1 : 64 / nct;
     if (gB > B) gB = B;
+    ScanGrid g;
     g.nb = (B + gB - 1) / gB;
-    gB = (B + g.nb - 1) / g.nb;              // no more batches than nb sequences each need: 65 make 33 batches of two, not 64
-    if ((int64_t)nct * per * gB * g.nb > kScanMaxGrid) gB = 1, g.nb = B;      // no empty places at all
+    // Where the empty places of the last batches are too many for a launch: no more batches than nb sequences each
+    // need (65 sequences make 33 of two, not 64), or one batch, which has none.  Otherwise more counters are better
+    // (65 x 512 x 512 forward: 40.1 us with 16 batches of five, 41.3 with 13).
+    if (tiles * gB * g.nb >= kScanMaxGrid) gB = (B + g.nb - 1) / g.nb;
+    if (tiles * gB * g.nb >= kScanMaxGrid) gB = 1, g.nb = B;
     g.groups = nct * gB;
-    g.size = (int64_t)g.groups * per * g.nb;
+    g.size = tiles * gB * g.nb;
     return g;
 }
 

@@ -70,13 +70,15 @@ conv_status_t check_align(std::initializer_list<Span> all) {
 // step: one row for each sequence.
 conv_status_t make_seq(const conv_seq_t *q, bool step, Seq &s) {
     if (!q) return CONV_ERR_NULL;
-    if ((q->dtype != CONV_OUT_F32 && q->dtype != CONV_OUT_BF16) || q->B < 1 || q->C < 1) return CONV_ERR_PARAM;
+    const int dtype = q->dtype & ~CONV_SEQ_FILL;
+    if ((dtype != CONV_OUT_F32 && dtype != CONV_OUT_BF16) || q->B < 1 || q->C < 1) return CONV_ERR_PARAM;
     if (!step && (q->T < 0 || (q->offsets && q->tokens < 0) || (uintptr_t)q->offsets % 4)) return CONV_ERR_PARAM;
     s.B = q->B;
     s.C = q->C;
     s.T = step ? 1 : q->T;
     s.off = step ? nullptr : q->offsets;
     s.rows = s.off ? q->tokens : (int64_t)s.B * s.T;
+    s.fill = s.off && (q->dtype & CONV_SEQ_FILL);
     if (s.rows >= kMaxRows || s.T >= kMaxRows || s.C > kMaxChannels || (int64_t)s.B * s.C > kMaxStateElems ||
         s.rows / CONV_SCAN_BLOCK + 2 * (int64_t)s.B > kMaxBlocks ||
         (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) > kMaxBlocks)
@@ -85,14 +87,14 @@ conv_status_t make_seq(const conv_seq_t *q, bool step, Seq &s) {
 }
 
 // The recurrence has 512 threads to a workgroup and a launch fewer than 2^32: the last of the sizes above is
-// one too many.
+// one too many, and so is the one before it where a workgroup more fills rows.
 conv_status_t make_scan(const conv_seq_t *q, Seq &s) {
     const conv_status_t st = make_seq(q, false, s);
     if (st != CONV_OK) return st;
-    return (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) >= kMaxBlocks ? CONV_ERR_OVERFLOW : CONV_OK;
+    return (s.rows / CONV_SCAN_BLOCK + s.B) * ((s.C + 63) / 64) + s.fill >= kMaxBlocks ? CONV_ERR_OVERFLOW : CONV_OK;
 }
 
-int esize(const conv_seq_t *q) { return q->dtype == CONV_OUT_BF16 ? 2 : 4; }
+int esize(const conv_seq_t *q) { return (q->dtype & ~CONV_SEQ_FILL) == CONV_OUT_BF16 ? 2 : 4; }
 
 conv_status_t check_workspace(const void *ws, size_t bytes, size_t need) {
     return need && (!ws || bytes < need || (uintptr_t)ws % 16) ? CONV_ERR_WORKSPACE : CONV_OK;

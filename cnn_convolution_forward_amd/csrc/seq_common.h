@@ -2,6 +2,9 @@
 // sequence's rows are, and loads and stores of VEC adjacent channels.
 #pragma once
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "seq_internal.h"
 
 // A product and a sum are one operation only where the code says fmaf: whole and ragged runs, compiled
@@ -152,6 +155,58 @@ __device__ __forceinline__ Block packed_block(const Seq &s, int tokens, int64_t 
     const int64_t k = n - start(t.b);
     t.k = k >= 0 && k <= s.rows / tokens ? (int)k : -1;
     return t;
+}
+
+// Rows of up to three outputs that no sequence holds, to be set to zero: 64 rows to a wave, `blocks`
+// workgroups for all of them (0: nothing is filled).  Rows are counted in units of two bytes.
+struct Fill {
+    uint16_t *p[3];
+    int64_t ld[3];
+    int n, units, blocks;
+};
+template <typename T> Fill fill_of(const Seq &s, int waves, std::initializer_list<T *> out, std::initializer_list<int64_t> ld) {
+    constexpr int e = sizeof(T) / 2;
+    Fill f = {};
+    if (!s.fill || s.rows == 0) return f;
+    for (T *o : out) f.p[f.n++] = (uint16_t *)o;
+    int i = 0;
+    for (int64_t l : ld) f.ld[i++] = l * e;
+    f.units = s.C * e;
+    f.blocks = (int)std::min<int64_t>((s.rows + 64 * waves - 1) / (64 * waves), 1024);
+    return f;
+}
+// Worker `k` of n workgroups.  Each lane finds out about one row, by bisection of the offsets.
+__device__ __forceinline__ void fill_rows(const Seq &s, const Fill &f, int64_t k, int64_t n) {
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    for (int64_t r0 = (k * waves + (threadIdx.x >> 6)) * 64; r0 < s.rows; r0 += n * waves * 64) {
+        const int64_t r = r0 + lane;
+        int lo = 0, hi = s.B;                           // sequences from lo on start behind row r
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (min(max((int64_t)s.off[mid], (int64_t)0), s.rows) <= r) lo = mid + 1;
+            else hi = mid;
+        }
+        bool held = false;
+        if (lo > 0) {
+            int64_t first;
+            int len;
+            seq_range(s, lo - 1, first, len);
+            held = r < first + len;
+        }
+        for (uint64_t open = __ballot(!held && r < s.rows); open; open &= open - 1) {
+            const int64_t row = r0 + __builtin_ctzll(open);
+            for (int o = 0; o < f.n; ++o) {
+                uint16_t *p = f.p[o] + row * f.ld[o];
+                for (int c = 8 * lane; c < f.units; c += 8 * 64) {
+                    if (c + 8 <= f.units) {
+                        store_pack(p + c, make_uint4(0, 0, 0, 0));
+                    } else {
+                        for (int q = c; q < f.units; ++q) p[q] = 0;
+                    }
+                }
+            }
+        }
+    }
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;

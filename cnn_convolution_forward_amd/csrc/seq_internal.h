@@ -13,8 +13,8 @@ struct Seq {
     int B, T, C;
     const int32_t *off;      // NULL: sequence b is rows [b*T, (b+1)*T)
     int64_t rows;            // rows of x: B*T, or the packed tensor's
+    bool fill;               // packed: rows of outputs that no sequence holds become zero
 };
-
 
 int64_t causal_bwd_workspace_floats(const Seq &s, int K);
 hipError_t launch_causal_fwd(const Seq &s, bool bf16, int K, int silu, const void *x, int64_t ldx, const void *w,

@@ -431,7 +431,7 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * C < 1, an unknown dtype, ld < C, a pointer not aligned to its element or a
  * bad option, CONV_ERR_OVERFLOW for 2^30 or more rows, more than 2^20 channels,
  * B*C of 2^31 or more, or rows/64 + 2 B or (rows/64 + B) * (C/64) above 2^23
- * (for the recurrence the latter of 2^23 or more),
+ * (for the recurrence the latter of 2^23 or more, or 2^23 - 1 with CONV_SEQ_FILL),
  * CONV_ERR_WORKSPACE for a workspace that is needed and missing, too small or
  * not 16-byte aligned,
  * CONV_ERR_ALIAS when an output overlaps an input, another output or the
@@ -439,9 +439,13 @@ CONV_API conv_status_t conv_bwd_weight_bf16(const conv_params_t *params, const u
  * `offsets` are read on the device only: values outside [0, tokens] are clamped,
  * rows of a sequence past T tokens are ignored, and where values descend,
  * which rows are computed is unspecified (never any outside the tensors).
+ * Rows that no sequence holds (in front of offsets[0], behind offsets[B], past T
+ * tokens) are left as they are in every output of rows, or, with CONV_SEQ_FILL, set to zero.
  * Results are bitwise reproducible. */
+#define CONV_SEQ_FILL 256    /* added to dtype: rows of outputs that no sequence holds are set to zero */
+
 typedef struct {
-    int dtype;               /* CONV_OUT_F32 or CONV_OUT_BF16                               */
+    int dtype;               /* CONV_OUT_F32 or CONV_OUT_BF16, and CONV_SEQ_FILL or not     */
     int B;                   /* sequences                                                   */
     int T;                   /* tokens in each; with offsets, in the longest (0 is allowed)  */
     int C;                   /* channels                                                    */

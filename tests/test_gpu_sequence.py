@@ -614,3 +614,90 @@ def test_packed_rows_of_no_tokens():
     assert torch.equal(hT, h0) and st.shape == (2, 0, 8)
     grads = B.gated_scan_backward(x, x, x, decay, x, st, dh=h0, **kw)
     assert not bool(grads[3].any()) and torch.equal(grads[4], h0)
+
+
+# ---- rows that no sequence holds ---------------------------------------------------
+
+GAPS = [
+    # offsets, rows, max_len
+    ([0, 40, 40, 100], 100, 60),                    # none
+    ([7, 40, 40, 100], 131, 60),                    # in front and behind
+    ([0, 300, 300, 1000], 2300, 200),               # and past max_len
+    ([0, 0, 0], 70, 1),                             # all rows
+    ([0, 0], 500, 0),
+    ([64, 64 + 900], 64 * 40, 900),
+    ([3] + [3 + 5 * i for i in range(1, 200)], 1500, 5),
+    ([3] + [3 + 5 * i for i in range(1, 200)], 1500, 2),
+]
+
+
+def _held(off, rows, max_len):
+    on = np.zeros(rows, dtype=bool)
+    for a, b in zip(off, off[1:]):
+        on[a:min(b, a + max_len)] = True
+    return torch.from_numpy(on).cuda()
+
+
+def _dirty(n):
+    """Memory that the next allocations may get: all NaN."""
+    t = [torch.full((n,), float("nan"), device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del t
+
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 1), ("bf16", 13), ("bf16", 600), ("f32", 3), ("f32", 132)])
+@pytest.mark.parametrize("case", range(len(GAPS)))
+def test_rows_of_no_sequence_are_zero(case, dtype, C):
+    """Without an out, rows that no sequence holds are zeros, in results and in gradients; in a given out
+    they stay as they are, and rows that a sequence holds are the same either way."""
+    off, rows, max_len = GAPS[case]
+    dt, rng = DT[dtype], np.random.default_rng(case)
+    on = _held(off, rows, max_len)
+    kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_len=max_len)
+    x, g, u, dy = (_cuda(rng.standard_normal((rows, C)), dt) for _ in range(4))
+    for t in (x, g, u, dy):
+        t[~on] = float("nan")
+    w, decay = _cuda(rng.standard_normal((C, 4)), dt), _cuda(rng.uniform(-5, -1, C))
+
+    def both(call, n):
+        given = [torch.full((rows, 3 * C + 2), 5.0, dtype=dt, device="cuda")[:, 1 + C:1 + 2 * C] for _ in range(n)]
+        _dirty(rows * C)
+        new = call(None)
+        call(tuple(given) if n > 1 else given[0])
+        for a, b in zip(new if n > 1 else [new], given):
+            assert bool((a[~on] == 0).all()) and bool((b[~on] == 5).all())
+            assert torch.equal(a[on], b[on]) and not bool(torch.isnan(a).any())
+
+    both(lambda o: B.causal_conv(x, w, silu=True, out=o, **kw), 1)
+    both(lambda o: B.causal_conv_backward(x, w, dy, silu=True, out=o, **kw)[0], 1)
+    both(lambda o: B.gated_scan(x, g, u, decay, out=o, **kw)[0], 1)
+    _, _, st = B.gated_scan(x, g, u, decay, with_states=True, **kw)
+    both(lambda o: B.gated_scan_backward(x, g, u, decay, dy, st, out=o, **kw)[:3], 3)
+    one = torch.full((rows, C), 5.0, dtype=dt, device="cuda")
+    _dirty(rows * C)
+    mixed = B.gated_scan_backward(x, g, u, decay, dy, st, out=(None, one, None), **kw)
+    assert bool((mixed[0][~on] == 0).all()) and bool((one[~on] == 5).all()) and bool((mixed[2][~on] == 0).all())
+
+
+def test_rows_of_no_sequence_in_a_graph():
+    """A captured call fills them at every replay."""
+    rng = np.random.default_rng(1)
+    off, rows = [5, 300, 420], 700
+    on = _held(off, rows, 250)
+    kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_len=250)
+    x, g, u = (_cuda(rng.standard_normal((rows, 72)), torch.bfloat16) for _ in range(3))
+    w, decay = _cuda(rng.standard_normal((72, 4)), torch.bfloat16), _cuda(rng.uniform(-5, -1, 72))
+    run = lambda: (B.causal_conv(x, w, **kw), B.gated_scan(x, g, u, decay, **kw)[0])
+    want = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for _ in range(3):
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b) and bool((a[~on] == 0).all())
+        run()

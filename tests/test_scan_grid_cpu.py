@@ -96,3 +96,15 @@ def test_one_workgroup_too_many_is_refused():
     assert B.conv_scan_bwd(seq, 8.0, X, 64, G, 64, I, 64, D, H, Y, 64, None, WS, 64, WS * 2, 64, WS * 3, 64, D * 5, None, WS * 4, 1) == 4
     less = B.SeqParams(0, 1, ((1 << 23) - 2) * 64, 64, None, 0)
     assert B.conv_scan_fwd_workspace_bytes(less) > 0 and call(less) == 6         # only its workspace is too small
+
+
+def test_batches_with_rows_to_fill_leave_room_for_a_workgroup(grid):
+    """CONV_SEQ_FILL takes at least one workgroup more: the batch that leaves no room is refused."""
+    full, off = (1 << 23) - 1, 0x100000000000                  # = 47 * 178481
+    seq = lambda fill, B_: B.SeqParams(fill, B_, 1, 47 * 64, off, 0)
+    assert B.conv_scan_fwd_workspace_bytes(seq(0, 178481)) == 0        # no workspace: one chunk each
+    call = lambda s: B.conv_scan_fwd(s, -1.0, None, 64, None, 64, None, 64, off * 2, None, None, 64, None, None, None, 0)
+    assert call(seq(0, 178481)) == 2 and call(seq(B.SEQ_FILL, 178481)) == 4 and call(seq(B.SEQ_FILL, 178480)) == 2      # 2: the scale
+    for B_ in (178480, 178479, 89240, 59493):
+        nct, per, total, (groups, nb, size) = grid(B_, 1, 47 * 64, 64, 128, 0)
+        assert size < full or B_ * nct == full
