@@ -13,7 +13,7 @@ __device__ __forceinline__ float scan_rate(float scale, float decay) {
 }
 
 // v = 1 - a^2 = 1 - exp(-w), w = 2 k r.  Near w = 0, where the difference
-// cancels, the series w - w^2/2 + ... (its first dropped term is below 5e-8 of
+// cancels, the series w - w^2/2 + ... (its first dropped term is below 5.5e-8 of
 // the sum for w < 1/4); beyond, the difference itself loses at most two bits.
 __device__ __forceinline__ float one_minus_sq(float w, float a) {
     float p = fmaf(w, -1.f / 720.f, 1.f / 120.f);

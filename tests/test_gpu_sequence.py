@@ -701,3 +701,32 @@ def test_rows_of_no_sequence_in_a_graph():
         for a, b in zip(out, want):
             assert torch.equal(a, b) and bool((a[~on] == 0).all())
         run()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_scan_extreme_gradients(dtype):
+    """All gradients at gates of +-inf and +-100 and decays from -40 to 40, within the bounds of scan_grad.  Where
+    v = 1 - a^2 is below 2^-126, 1/m is clamped to 2^63: what it stands beside there, k r (or scale sigmoid(decay) r,
+    which is no more), is at most v/2 of the exact m = sqrt(v) and at most 2^-127 of the clamped one, so that both
+    terms are below 2^-63 |dh s x|.  dh0 has none."""
+    dt, half, rng = DT[dtype], dtype == "bf16", np.random.default_rng(15)
+    L, C = 150, 80
+    g, u = (rng.standard_normal((1, L, C)) * 30 for _ in range(2))
+    g[0, ::7], g[0, 3::11] = np.inf, -np.inf
+    u[0, ::5], u[0, 4::13] = -np.inf, np.inf
+    x, dy = rng.standard_normal((1, L, C)), rng.standard_normal((1, L, C))
+    X, G, I, DY, D = _cuda(x, dt), _cuda(g, dt), _cuda(u, dt), _cuda(dy, dt), _cuda(np.linspace(-40, 40, C))
+    h0, dh = _cuda(rng.standard_normal((1, C))), _cuda(rng.standard_normal((1, C)))
+    _, _, st = B.gated_scan(X, G, I, D, h0=h0, with_states=True)
+    got = B.gated_scan_backward(X, G, I, D, DY, st, dh=dh)
+    args = (_np(X)[0], _np(G)[0], _np(I)[0], _np(D), 8.0, _np(h0)[0])
+    ref, err = R.scan_grad(*args, _np(DY)[0], _np(dh)[0])
+    # |dh| <= |dhT| + the sum of |dy| behind, as a <= 1; s <= 1
+    most = np.abs(_np(dh)[0]) + np.abs(_np(DY)[0])[::-1].cumsum(0)[::-1]
+    clamp = 2.0 ** -63 * most * np.abs(_np(X)[0])
+    _check(got[1][0], ref[1], err[1] + clamp, half, "dgate")
+    _check(got[3], ref[3], (err[3] + clamp.sum(0)) * (2 + L / 512), False, "ddecay")
+    _check(got[4][0], ref[4], err[4], False, "dh0")
+    # dx and dinp: m itself is below 2^-63 there
+    _check(got[0][0], ref[0], err[0] + 2.0 ** -63 * most, half, "dx")
+    _check(got[2][0], ref[2], err[2] + clamp, half, "dinp")
