@@ -1035,7 +1035,8 @@ class AdamW:
     many were taken before.  grad_scale: a float32 scalar on the GPU that multiplies every gradient (a clipping
     factor, for instance), or None.  The tensors are kept and their addresses laid out once; step() may be
     given other gradients of the same sizes.  8-bit moments round at random, by seed and step; lr and seed may
-    be changed between steps."""
+    be changed between steps.  No two tensors may share memory.  A step captured in a graph repeats its own number,
+    rates and random bits at every replay (conv_adamw_step): call step() beside the graph."""
 
     def __init__(self, params, grads, m=None, v=None, copies=None, bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.0, seed=0, steps=0, m_scale=None, v_scale=None, grad_scale=None):

@@ -559,10 +559,18 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * code.  The random bits depend on seed, step, the tensor's place in the list
  * and the element only, so a step is reproducible.  v > 0 never takes code 0.
  * A block whose largest value is below 2^-126 is stored as zeros.  A
- * non-finite gradient makes its element (bits = 8: its block's scales) non-finite.
+ * non-finite gradient, or a square beyond fp32, makes its element (bits = 8: its
+ * block's scales) non-finite.
+ *
+ * The numbers in `opt` are taken when the call is made.  A call captured in a
+ * graph therefore takes the same step again at every replay: the step's number in
+ * c1 and c2, the rates, and with bits = 8 the same random bits for every element,
+ * whose rounding is then no longer right on average.  Only the gradients' scale is read
+ * on the device.  Capture the passes, and call the step beside the graph.
  *
  * `tensors` is a HOST array, read before the call returns (its pointers are
- * device pointers).  Every tensor: n >= 0; n = 0 is skipped.  Errors:
+ * device pointers).  No two of them may share memory that is written (not
+ * checked).  Every tensor: n >= 0; n = 0 is skipped.  Errors:
  * CONV_ERR_NULL for a NULL array, p, g, m or v (bits = 8: scale), CONV_ERR_PARAM for
  * count < 0, n < 0, step < 1, betas outside [0, 1), lr, eps or weight_decay
  * negative or not finite, bits other than 32 or 8, an unknown grad_dtype, or a
