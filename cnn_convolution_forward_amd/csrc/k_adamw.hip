@@ -33,7 +33,8 @@ struct Table {
 static_assert(sizeof(Table) <= 4096, "kernel arguments");
 
 // 32 bits per element from the tensor's key (seed, step and its place in the list), by two rounds of
-// xor-shift and odd multiplication.
+// xor-shift and odd multiplication; shifts and multipliers are published ones (C. Wellons, "Prospecting for
+// Hash Functions", 2018), found there by search for the least bias.
 constexpr uint32_t kPlace = 0x9e3779b1u;       // z = key + place in the tensor * kPlace
 __device__ __forceinline__ uint32_t random_bits(uint32_t z) {
     z = (z ^ (z >> 15)) * 0x2c1b3c6du;
@@ -171,7 +172,8 @@ __device__ __forceinline__ float decode_v(float q, float s) {
 
 // The correctly rounded square root of y in [0, 1], from the hardware's s, which is a unit in the last
 // place off at most.  The midpoint to the neighbour below, s', squares to s s' and a quarter of a unit's
-// square: y <= s s' puts the root nearer to s' (and the like above).  Below 2^-100 it may miss: the code is 0
+// square: y <= s s' puts the root nearer to s' (and the like above): Tuckerman's rounding test
+// (R. Agarwal et al., IBM J. Res. Dev. 30, 1986), with the products' exact residuals.  Below 2^-100 it may miss: the code is 0
 // there anyway.  Without the correction one element in some ten million takes another code than the same
 // operations give elsewhere; it costs 5 us of 314, the library's own root would cost 35.
 __device__ __forceinline__ float exact_root(float y) {
