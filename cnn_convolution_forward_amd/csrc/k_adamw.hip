@@ -10,11 +10,11 @@
 // kept between calls.  Blocks of kChunk elements are numbered through all of
 // its tensors; a workgroup finds its tensor by looking at all first numbers.
 //
-// Measured: 26 M parameters in 60 tensors with fp32 moments 129.4 us, 6.0 TB/s (a
+// Measured: 26 M parameters in 60 tensors with fp32 moments 129.1 us, 6.0 TB/s (a
 // large copy reaches 5.2); 60 M in 120 with 8-bit moments, their values read back
-// too, 314 us, 4.6 TB/s, the step's vector instructions taking about as long as its
-// bytes; 20 000 in 14 6.4 us, mostly the launch.  One element per
-// load took 163.5, 661.9 and 8.0 us.
+// too, 319 us, 4.5 TB/s (219 us for the step alone, its vector instructions taking
+// about as long as its bytes); 20 000 in 14 6.6 us, mostly the launch.  One element
+// per load took 163.5, 661.9 and 8.0 us.
 #include "optim_internal.h"
 #include "seq_common.h"
 
@@ -173,9 +173,10 @@ __device__ __forceinline__ float decode_v(float q, float s) {
 // The correctly rounded square root of y in [0, 1], from the hardware's s, which is a unit in the last
 // place off at most.  The midpoint to the neighbour below, s', squares to s s' and a quarter of a unit's
 // square: y <= s s' puts the root nearer to s' (and the like above): Tuckerman's rounding test
-// (R. Agarwal et al., IBM J. Res. Dev. 30, 1986), with the products' exact residuals.  Below 2^-100 it may miss: the code is 0
-// there anyway.  Without the correction one element in some ten million takes another code than the same
-// operations give elsewhere; it costs 5 us of 314, the library's own root would cost 35.
+// (R. Agarwal et al., IBM J. Res. Dev. 30, 1986), with the products' exact residuals.  Below 2^-100 it may
+// miss: the code is 0 there anyway.  Without the correction one element in some ten million takes another code
+// than the same operations give elsewhere.  It costs 13 us of 321; before codes were packed as they are now it
+// cost 17 of 326, and the library's own root 35.
 __device__ __forceinline__ float exact_root(float y) {
     const float s = __builtin_amdgcn_sqrtf(y);
     const float below = __int_as_float(__float_as_int(s) - 1), above = __int_as_float(__float_as_int(s) + 1);

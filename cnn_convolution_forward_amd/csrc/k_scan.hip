@@ -5,8 +5,8 @@
 // those and dy and writes three gradients, each once; the arithmetic of the gates
 // (six transcendental and about 28 other instructions an element forward) takes
 // half of that time, counted by SQ_ACTIVE_INST_VALU.  Measured at 8 x 2048 x 2048
-// bf16: forward 62.9 us, 4.3 TB/s (52 us at the rate of a large copy, 5.2 TB/s);
-// backward 108.8 us, 4.3 TB/s, with 4 to 5 us each in the kernel before it and the
+// bf16: forward 62.7 us, 4.3 TB/s (52 us at the rate of a large copy, 5.2 TB/s);
+// backward 108.3 us, 4.4 TB/s, with 4 to 5 us each in the kernel before it and the
 // one behind; one sequence of 32768 x 1024 forward 78 us, 3.4 TB/s.  A thread per
 // sequence and channel, walking its tokens, took 1064, 2044 and 16454 us.
 #include <algorithm>

@@ -13,9 +13,9 @@
 // Threads of a workgroup lie along the channels first (wide, contiguous
 // loads), then along runs of tokens; K or more rows are loaded ahead of their use.
 //
-// Measured at 8 x 2048 x 2048 bf16, K = 4 with SiLU: forward 27.3 us, 4.9 TB/s, the rate
-// of a copy of that size; backward 49.1 us, 4.1 TB/s, of which the vector
-// instructions take 30 us (SQ_ACTIVE_INST_VALU) and the reduction 4 us.  8 x 4096 x 4096:
+// Measured at 8 x 2048 x 2048 bf16, K = 4 with SiLU: forward 27.6 us, 4.9 TB/s, the rate
+// of a copy of that size; backward 49.6 us, 4.1 TB/s, of which the vector
+// instructions take 31 us (SQ_ACTIVE_INST_VALU) and the reduction 4 us.  8 x 4096 x 4096:
 // 88.7 us, 6.05 TB/s, and 163 us, 4.9 TB/s.
 #include <type_traits>
 
