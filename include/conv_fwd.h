@@ -495,7 +495,9 @@ CONV_API conv_status_t conv_causal_step(const conv_seq_t *seq, int K, int silu, 
  *     a = exp(-k r),      h[t] = a h[t-1] + sqrt(1 - a^2) s x,      y = h
  *
  * A sigmoid below 2^-126, the smallest normal fp32 (an argument under about
- * -87.3), counts as 0: a gate that far down is shut.
+ * -87.3), counts as 0: a gate that far down is shut.  So does a factor a below 2^-126
+ * (k r above about 87.3): nothing of the state before it is left, and an infinite one
+ * becomes NaN there.
  * h before a sequence's first token is h0 (B, C), or 0 when NULL; hT (B, C),
  * when not NULL, receives h after its last token (h0 for an empty one).
  * states, when not NULL, receives what conv_scan_bwd starts from: h before
