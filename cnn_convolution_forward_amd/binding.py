@@ -36,7 +36,7 @@ EXPORTS = ("conv_out_dim", "conv_status_str", "conv_version",
            "conv_fwd_ex_workspace_bytes", "conv_fwd_ex_bf16", "conv_fwd_ex_f32",
            "conv_causal_fwd", "conv_causal_bwd_workspace_bytes", "conv_causal_bwd", "conv_causal_step",
            "conv_scan_fwd_workspace_bytes", "conv_scan_fwd", "conv_scan_bwd_workspace_bytes", "conv_scan_bwd",
-           "conv_scan_step", "conv_adamw_step", "conv_adamw_state_values")
+           "conv_scan_step", "conv_norm_fwd", "conv_norm_bwd_workspace_bytes", "conv_norm_bwd", "conv_adamw_step", "conv_adamw_state_values")
 
 LAYOUT = {"nchw": 0, "nhwc": 1}
 OUT_DTYPE = {"f32": 0, "bf16": 1}
@@ -168,6 +168,12 @@ def lib():
         L.conv_scan_bwd.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp] + row * 3 + [_vp] * 3 + [_sz, _vp]
         L.conv_scan_step.restype = _i
         L.conv_scan_step.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp]
+        L.conv_norm_fwd.restype = _i
+        L.conv_norm_fwd.argtypes = [_i, _i64, _i, _f] + row + [_vp] * 2 + row + [_vp] * 3
+        L.conv_norm_bwd_workspace_bytes.restype = _sz
+        L.conv_norm_bwd_workspace_bytes.argtypes = [_i, _i64, _i]
+        L.conv_norm_bwd.restype = _i
+        L.conv_norm_bwd.argtypes = [_i, _i64, _i] + row + [_vp] * 3 + row * 2 + [_vp] * 3 + [_sz, _vp]
         L.conv_adamw_step.restype = _i
         L.conv_adamw_step.argtypes = [ctypes.POINTER(AdamwOptions), _vp, _i, _vp]
         L.conv_adamw_state_values.restype = _i
@@ -357,6 +363,19 @@ def conv_scan_bwd(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, ld
 
 def conv_scan_step(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream=None):
     return lib().conv_scan_step(_pref(seq), scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream)
+
+
+def conv_norm_fwd(dtype, rows, C, eps, x, ldx, weight, bias, y, ldy, mean, rstd, stream=None):
+    return lib().conv_norm_fwd(dtype, rows, C, eps, x, ldx, weight, bias, y, ldy, mean, rstd, stream)
+
+
+def conv_norm_bwd_workspace_bytes(dtype, rows, C):
+    return lib().conv_norm_bwd_workspace_bytes(dtype, rows, C)
+
+
+def conv_norm_bwd(dtype, rows, C, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, dweight, dbias, ws, ws_bytes, stream=None):
+    return lib().conv_norm_bwd(dtype, rows, C, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, dweight, dbias, ws, ws_bytes,
+                               stream)
 
 
 def conv_adamw_step(opt, tensors, count, stream=None):
@@ -1021,6 +1040,51 @@ def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
                         _dense(decay, (seq.C,), torch.float32, "decay", dev),
                         _dense(h, (seq.B, seq.C), torch.float32, "h", dev), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
     return y
+
+
+# ---- layer norm ----------------------------------------------------------------
+
+def _rows(x, name):
+    """(rows, channels) of a tensor of rows, (rows, C) or (B, T, C)."""
+    if x.dim() not in (2, 3):
+        raise ValueError("%s must be (rows, channels) or (sequences, tokens, channels)" % name)
+    return x.numel() // x.shape[-1] if x.shape[-1] else 0, x.shape[-1]
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, with_stats=False, out=None):
+    """Layer norm over the channels of each row of x, (rows, C) or (B, T, C), float32 or bf16 (conv_norm_fwd):
+    (x - mean) / sqrt(variance + eps) * weight + bias.  weight, bias: float32 (C), None for ones and zeros.  x and out may
+    be column slices of a wider tensor.  Returns y, or (y, mean, rstd), the latter float32 of one value for each row, for
+    layer_norm_backward."""
+    torch = _torch()
+    code, (rows, C), dev = _dtype_code(x, "x"), _rows(x, "x"), x.get_device()
+    ldx = _ld(x, x.shape, x, "x")
+    y, ldy = _rows_out(out, x, "out")
+    mean = rstd = None
+    if with_stats:
+        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device).unbind(0)
+    _run(conv_norm_fwd(code, rows, C, eps, x.data_ptr(), ldx, _dense(weight, (C,), torch.float32, "weight", dev),
+                       _dense(bias, (C,), torch.float32, "bias", dev), y.data_ptr(), ldy,
+                       mean.data_ptr() if with_stats else None, rstd.data_ptr() if with_stats else None, _stream_of(x)),
+         "conv_norm_fwd")
+    return (y, mean, rstd) if with_stats else y
+
+
+def layer_norm_backward(x, weight, dy, mean, rstd, out=None, workspace=None):
+    """(dx, dweight, dbias) of layer_norm for upstream dy, like x, and the mean and rstd that it returned
+    (conv_norm_bwd): dx of x's dtype, dweight and dbias float32 (C).  weight: as it was given, None for ones.  `out`: dx to
+    write into, perhaps a column slice; workspace: a uint8 tensor of conv_norm_bwd_workspace_bytes bytes, or None."""
+    torch = _torch()
+    code, (rows, C), dev = _dtype_code(x, "x"), _rows(x, "x"), x.get_device()
+    ldx, lddy = _ld(x, x.shape, x, "x"), _ld(dy, x.shape, x, "dy", dev)
+    dx, lddx = _rows_out(out, x, "out")
+    dw, db = torch.empty((2, C), dtype=torch.float32, device=x.device).unbind(0)
+    ws, wsb, held = _workspace(workspace, conv_norm_bwd_workspace_bytes(code, rows, C) if workspace is None else 0, x)
+    _run(conv_norm_bwd(code, rows, C, x.data_ptr(), ldx, _dense(weight, (C,), torch.float32, "weight", dev),
+                       _dense(mean, x.shape[:-1], torch.float32, "mean", dev),
+                       _dense(rstd, x.shape[:-1], torch.float32, "rstd", dev), dy.data_ptr(), lddy, dx.data_ptr(), lddx,
+                       dw.data_ptr(), db.data_ptr(), ws, wsb, _stream_of(x)), "conv_norm_bwd")
+    return dx, dw, db
 
 
 # ---- the optimiser step --------------------------------------------------------

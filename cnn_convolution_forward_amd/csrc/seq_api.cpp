@@ -1,5 +1,5 @@
 // seq_api.cpp -- the extern "C" entry points of the operators over sequences of
-// tokens and of the optimiser step.  As in conv_api.cpp, every argument is
+// tokens, of the layer norm and of the optimiser step.  As in conv_api.cpp, every argument is
 // checked on the host before any HIP call.
 #include <float.h>
 #include <math.h>
@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "conv_fwd.h"
+#include "norm_internal.h"
 #include "optim_internal.h"
 #include "seq_internal.h"
 
@@ -239,6 +240,48 @@ conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const void *x, 
     TRY(check_alias({sy, sh}, {sx, sg, si, sd}));
     return to_status(convfwd::launch_scan_step(s, e == 2, scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy,
                                                (hipStream_t)stream));
+}
+
+// ---- layer norm ----
+
+static conv_status_t check_norm(int dtype, int64_t rows, int C) {
+    if ((dtype != CONV_OUT_F32 && dtype != CONV_OUT_BF16) || rows < 0 || C < 1) return CONV_ERR_PARAM;
+    return rows >= kMaxRows || C > kMaxChannels ? CONV_ERR_OVERFLOW : CONV_OK;
+}
+
+conv_status_t conv_norm_fwd(int dtype, int64_t rows, int C, float eps, const void *x, int64_t ldx, const float *weight,
+                            const float *bias, void *y, int64_t ldy, float *mean, float *rstd, void *stream) {
+    TRY(check_norm(dtype, rows, C));
+    if (rows > 0 && (!x || !y)) return CONV_ERR_NULL;
+    if (!(eps >= 0.f) || isinf(eps)) return CONV_ERR_PARAM;
+    const int e = dtype == CONV_OUT_BF16 ? 2 : 4;
+    const Span sx{x, rows, C, ldx, e}, sy{y, rows, C, ldy, e}, sw = dense(weight, C, 4), sb = dense(bias, C, 4),
+        sm = dense(mean, rows, 4), sr = dense(rstd, rows, 4);
+    TRY(check_align({sx, sy, sw, sb, sm, sr}));
+    TRY(check_alias({sy, sm, sr}, {sx, sw, sb}));
+    return to_status(convfwd::launch_norm_fwd(rows, C, e == 2, eps, x, ldx, weight, bias, y, ldy, mean, rstd, (hipStream_t)stream));
+}
+
+size_t conv_norm_bwd_workspace_bytes(int dtype, int64_t rows, int C) {
+    if (check_norm(dtype, rows, C) != CONV_OK) return 0;
+    return (size_t)convfwd::norm_bwd_workspace_floats(rows, C, dtype == CONV_OUT_BF16) * 4;
+}
+
+conv_status_t conv_norm_bwd(int dtype, int64_t rows, int C, const void *x, int64_t ldx, const float *weight, const float *mean,
+                            const float *rstd, const void *dy, int64_t lddy, void *dx, int64_t lddx, float *dweight,
+                            float *dbias, void *workspace, size_t workspace_bytes, void *stream) {
+    TRY(check_norm(dtype, rows, C));
+    if (rows > 0 && (!x || !mean || !rstd || !dy || !dx)) return CONV_ERR_NULL;
+    const int e = dtype == CONV_OUT_BF16 ? 2 : 4;
+    const size_t need = dweight || dbias ? (size_t)convfwd::norm_bwd_workspace_floats(rows, C, e == 2) * 4 : 0;
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    const Span sx{x, rows, C, ldx, e}, sdy{dy, rows, C, lddy, e}, sdx{dx, rows, C, lddx, e}, sw = dense(weight, C, 4),
+        sm = dense(mean, rows, 4), sr = dense(rstd, rows, 4), sdw = dense(dweight, C, 4), sdb = dense(dbias, C, 4),
+        sws = dense(need ? workspace : nullptr, (int64_t)workspace_bytes, 1);
+    TRY(check_align({sx, sdy, sdx, sw, sm, sr, sdw, sdb}));
+    TRY(check_alias({sdx, sdw, sdb, sws}, {sx, sdy, sw, sm, sr}));
+    return to_status(convfwd::launch_norm_bwd(rows, C, e == 2, x, ldx, weight, mean, rstd, dy, lddy, dx, lddx, dweight, dbias,
+                                              (float *)workspace, (hipStream_t)stream));
 }
 
 // ---- optimiser ----

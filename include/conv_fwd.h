@@ -538,6 +538,39 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
                                       const void *gate, int64_t ldg, const void *inp, int64_t ldi,
                                       const float *decay, float *h, void *y, int64_t ldy, void *stream);
 
+/* ---- layer norm ------------------------------------------------------------
+ *
+ * Over the C channels of each of `rows` rows (those of any sequences, packed or
+ * not, or one row for each head), in the layouts, types and strides of the
+ * operators over sequences; dtype is CONV_OUT_F32 or CONV_OUT_BF16, for x, y, dy
+ * and dx.  weight, bias (C; NULL: ones, zeros), mean, rstd (rows) and the gradients of
+ * parameters are fp32:
+ *
+ *     mean = sum x / C,   rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),   y = (x - mean) rstd weight + bias
+ *
+ * Arithmetic is fp32, y is rounded once.  mean and rstd, where not NULL, receive
+ * what conv_norm_bwd starts from.  eps: finite, >= 0.  A row's results have the
+ * same bits among any other rows (dweight and dbias are sums over all).  Errors
+ * are those of the operators over sequences: rows < 0, C < 1, ld < C and
+ * alignment CONV_ERR_PARAM, 2^30 or more rows or more than 2^20 channels
+ * CONV_ERR_OVERFLOW.  No rows: nothing is done, and sums are zeros. */
+CONV_API conv_status_t conv_norm_fwd(int dtype, int64_t rows, int C, float eps, const void *x, int64_t ldx,
+                                     const float *weight, const float *bias, void *y, int64_t ldy, float *mean,
+                                     float *rstd, void *stream);
+
+/* Device workspace of conv_norm_bwd: sums of dweight and dbias over ranges of
+ * rows; 0 on invalid arguments, and where there are no rows. */
+CONV_API size_t conv_norm_bwd_workspace_bytes(int dtype, int64_t rows, int C);
+
+/* Gradients for upstream dy, with mean and rstd as the forward pass gave them and xh = (x - mean) rstd:
+ *     dx = rstd (weight dy - sum(weight dy) / C - xh sum(weight dy xh) / C)
+ *     dweight = sum over rows of dy xh,   dbias = sum over rows of dy
+ * dweight and dbias (C) may be NULL; with both NULL no workspace is needed. */
+CONV_API conv_status_t conv_norm_bwd(int dtype, int64_t rows, int C, const void *x, int64_t ldx, const float *weight,
+                                     const float *mean, const float *rstd, const void *dy, int64_t lddy, void *dx,
+                                     int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* ---- the optimiser step --------------------------------------------------
  *
  * AdamW over `count` tensors at once, from the fp32 (or bf16) gradients that
