@@ -36,7 +36,7 @@ EXPORTS = ("conv_out_dim", "conv_status_str", "conv_version",
            "conv_fwd_ex_workspace_bytes", "conv_fwd_ex_bf16", "conv_fwd_ex_f32",
            "conv_causal_fwd", "conv_causal_bwd_workspace_bytes", "conv_causal_bwd", "conv_causal_step",
            "conv_scan_fwd_workspace_bytes", "conv_scan_fwd", "conv_scan_bwd_workspace_bytes", "conv_scan_bwd",
-           "conv_scan_step", "conv_norm_fwd", "conv_norm_bwd_workspace_bytes", "conv_norm_bwd", "conv_adamw_step", "conv_adamw_state_values")
+           "conv_scan_step", "conv_delta_fwd_workspace_bytes", "conv_delta_fwd", "conv_delta_step", "conv_norm_fwd", "conv_norm_bwd_workspace_bytes", "conv_norm_bwd", "conv_adamw_step", "conv_adamw_state_values")
 
 LAYOUT = {"nchw": 0, "nhwc": 1}
 OUT_DTYPE = {"f32": 0, "bf16": 1}
@@ -57,6 +57,12 @@ class SeqParams(ctypes.Structure):
     """conv_seq_t: a batch of sequences of tokens, equal or packed."""
     _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
                 ("offsets", ctypes.c_void_p), ("tokens", ctypes.c_int64)]
+
+
+class DeltaParams(ctypes.Structure):
+    """conv_delta_t: the heads of a gated delta rule."""
+    _fields_ = [("heads", ctypes.c_int), ("heads_v", ctypes.c_int), ("dim_k", ctypes.c_int), ("dim_v", ctypes.c_int),
+                ("unit", ctypes.c_int), ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class AdamwTensor(ctypes.Structure):
@@ -168,6 +174,13 @@ def lib():
         L.conv_scan_bwd.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp] + row * 3 + [_vp] * 3 + [_sz, _vp]
         L.conv_scan_step.restype = _i
         L.conv_scan_step.argtypes = [_ps, _f] + row * 3 + [_vp] * 2 + row + [_vp]
+        _pd = ctypes.POINTER(DeltaParams)
+        L.conv_delta_fwd_workspace_bytes.restype = _sz
+        L.conv_delta_fwd_workspace_bytes.argtypes = [_ps, _pd]
+        L.conv_delta_fwd.restype = _i
+        L.conv_delta_fwd.argtypes = [_ps, _pd] + row * 5 + [_vp] + row + [_vp] * 3 + [_sz, _vp]
+        L.conv_delta_step.restype = _i
+        L.conv_delta_step.argtypes = [_ps, _pd] + row * 5 + [_vp] + row + [_vp]
         L.conv_norm_fwd.restype = _i
         L.conv_norm_fwd.argtypes = [_i, _i64, _i, _f] + row + [_vp] * 2 + row + [_vp] * 3
         L.conv_norm_bwd_workspace_bytes.restype = _sz
@@ -363,6 +376,19 @@ def conv_scan_bwd(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, states, dy, ld
 
 def conv_scan_step(seq, scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream=None):
     return lib().conv_scan_step(_pref(seq), scale, x, ldx, gate, ldg, inp, ldi, decay, h, y, ldy, stream)
+
+
+def conv_delta_fwd_workspace_bytes(seq, par):
+    return lib().conv_delta_fwd_workspace_bytes(seq, par)
+
+
+def conv_delta_fwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, s0, y, ldy, sT, states, ws, ws_bytes, stream=None):
+    return lib().conv_delta_fwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, s0, y, ldy, sT, states, ws, ws_bytes,
+                                stream)
+
+
+def conv_delta_step(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, S, y, ldy, stream=None):
+    return lib().conv_delta_step(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, S, y, ldy, stream)
 
 
 def conv_norm_fwd(dtype, rows, C, eps, x, ldx, weight, bias, y, ldy, mean, rstd, stream=None):
@@ -1039,6 +1065,137 @@ def gated_scan_step(x, gate, inp, decay, h, scale=8.0, out=None):
     _run(conv_scan_step(seq, scale, x.data_ptr(), ldx, gate.data_ptr(), ldg, inp.data_ptr(), ldi,
                         _dense(decay, (seq.C,), torch.float32, "decay", dev),
                         _dense(h, (seq.B, seq.C), torch.float32, "h", dev), y.data_ptr(), ldy, _stream_of(x)), "conv_scan_step")
+    return y
+
+
+# ---- gated delta rule ----------------------------------------------------------
+
+def _heads_ld(t, shape, dtype, name, device):
+    """The row stride of a tensor of heads, (..., heads, dim): the heads of a row are adjacent, rows may be strided."""
+    if t.get_device() != device:
+        raise ValueError("%s must be on v's GPU" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.is_contiguous() or t.numel() == 0:
+        return shape[-2] * shape[-1]
+    if (shape[-1] > 1 and t.stride(-1) != 1) or (shape[-2] > 1 and t.stride(-2) != shape[-1]):
+        raise ValueError("%s: the heads of a row must be adjacent" % name)
+    return _row_step(t, shape[:-2], shape[-2] * shape[-1], name)
+
+
+def _row_step(t, rows, width, name):
+    """Elements between rows of `width` adjacent ones, whose leading axes `rows` are one evenly strided axis."""
+    st, ld = t.stride(), width
+    if len(rows) == 1:
+        ld = st[0] if rows[0] > 1 else width
+    elif rows[1] > 1:
+        ld = st[1]
+        if rows[0] > 1 and st[0] != rows[1] * ld:
+            raise ValueError("%s: sequences must follow each other at the row stride" % name)
+    elif rows[0] > 1:
+        ld = st[0]
+    if ld < width:
+        raise ValueError("%s: rows overlap" % name)
+    return ld
+
+
+def _gate_ld(t, shape, name, device):
+    """The row stride of float32 rows of one value for each head."""
+    torch = _torch()
+    if t.get_device() != device:
+        raise ValueError("%s must be on v's GPU" % name)
+    if t.dtype != torch.float32:
+        raise TypeError("%s has dtype %s, expected float32" % (name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.is_contiguous() or t.numel() == 0:
+        return shape[-1]
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the heads of a row must be adjacent" % name)
+    return _row_step(t, shape[:-1], shape[-1], name)
+
+
+def make_delta(q, v, offsets=None, max_len=None, scale=None, unit=False, eps=1e-6, fill=False, step=False):
+    """(SeqParams, DeltaParams) of a gated delta rule: q (B, T, heads, dim_k) and v (B, T, value heads, dim_v), or
+    (tokens, heads, dim) packed (see make_seq), or, for a step, (B, heads, dim)."""
+    if q.dim() != v.dim() or v.dim() != (3 if step or offsets is not None else 4):
+        raise ValueError("q and v must be (sequences, %sheads, dim)%s" % ("" if step else "tokens, ",
+                                                                      "" if step else ", or (tokens, heads, dim) packed with offsets"))
+    rows = v.shape[:-2]
+    heads, dim = v.shape[-2:]
+    par = DeltaParams(q.shape[-2], heads, q.shape[-1], dim, int(bool(unit)), q.shape[-1] ** -0.5 if scale is None else scale, eps)
+    code = _dtype_code(v, "v")
+    if step:
+        return SeqParams(code, rows[0], 1, heads * dim, None, 0), par
+    if offsets is None:
+        return SeqParams(code, rows[0], rows[1], heads * dim, None, 0), par
+    seq = make_seq(v[:, 0], offsets, max_len, name="v", fill=fill)
+    seq.C = heads * dim
+    return seq, par
+
+
+def _delta_inputs(q, k, v, g, beta):
+    """Addresses and row strides, q, k, v, g, beta in turn."""
+    dev = v.get_device()
+    if not v.is_cuda:
+        raise ValueError("v must be a GPU tensor")
+    rows, dt = v.shape[:-2], v.dtype
+    qs = rows + q.shape[-2:]
+    gs = v.shape[:-1]
+    return (q.data_ptr(), _heads_ld(q, qs, dt, "q", dev), k.data_ptr(), _heads_ld(k, qs, dt, "k", dev),
+            v.data_ptr(), _heads_ld(v, v.shape, dt, "v", dev), g.data_ptr(), _gate_ld(g, gs, "g", dev),
+            beta.data_ptr(), _gate_ld(beta, gs, "beta", dev))
+
+
+def _heads_out(out, like, name):
+    torch = _torch()
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device), like.shape[-2] * like.shape[-1]
+    return out, _heads_ld(out, like.shape, like.dtype, name, like.get_device())
+
+
+def delta_rule(q, k, v, g, beta, scale=None, unit=False, eps=1e-6, s0=None, offsets=None, max_len=None, with_states=False,
+               out=None, workspace=None):
+    """The gated delta rule over the tokens of (B, T, heads, dim), or packed (tokens, heads, dim) with offsets and max_len
+    (see make_seq), float32 or bf16 (conv_delta_fwd): per token and value head, with its state S (dim_k, dim_v),
+
+        S = exp(g) S,  S = S + beta k (v - S^T k)^T,  y = scale S^T q
+
+    q, k: (..., heads, dim_k); v: (..., value heads, dim_v), a multiple of heads: value head h uses query and key head
+    h // (value heads // heads).  g and beta: float32 (..., value heads), g <= 0 the log decay.  scale: 1/sqrt(dim_k) if
+    None.  unit: q and k of each head are brought to unit length first (eps is added to their sum of squares).  s0: float32
+    (B, value heads, dim_k, dim_v), or None for zeros.  Rows of all tensors may be strided (slices of a fused projection).
+    workspace: a uint8 tensor of conv_delta_fwd_workspace_bytes(*make_delta(q, v, ...)) bytes to use, or None to allocate one.
+    Packed rows that no sequence holds come back as zeros; in a given out they stay as they are.  Returns (y like v, S after the last tokens), and
+    with_states also the states that delta_rule_backward starts from: float32 (B, ceil(T / 64), value heads, dim_k, dim_v), not
+    written past a sequence's end."""
+    torch = _torch()
+    seq, par = make_delta(q, v, offsets, max_len, scale, unit, eps, fill=out is None)
+    data = _delta_inputs(q, k, v, g, beta)
+    dev = v.get_device()
+    y, ldy = _heads_out(out, v, "out")
+    ends = (seq.B, par.heads_v, par.dim_k, par.dim_v)
+    sT = torch.empty(ends, dtype=torch.float32, device=v.device)
+    states = None
+    if with_states:
+        states = torch.empty((seq.B, -(-seq.T // SCAN_BLOCK)) + ends[1:], dtype=torch.float32, device=v.device)
+    ws, wsb, held = _workspace(workspace, conv_delta_fwd_workspace_bytes(seq, par) if workspace is None else 0, v)
+    _run(conv_delta_fwd(seq, par, *data, _dense(s0, ends, torch.float32, "s0", dev), y.data_ptr(), ldy, sT.data_ptr(),
+                        None if states is None else states.data_ptr(), ws, wsb, _stream_of(v)), "conv_delta_fwd")
+    return (y, sT, states) if with_states else (y, sT)
+
+
+def delta_rule_step(q, k, v, g, beta, s, scale=None, unit=False, eps=1e-6, out=None):
+    """One new token of each of B sequences: q, k (B, heads, dim_k), v (B, value heads, dim_v), g and beta float32 (B, value
+    heads).  Returns y like v and updates s, float32 (B, value heads, dim_k, dim_v), in place (conv_delta_step)."""
+    torch = _torch()
+    seq, par = make_delta(q, v, None, None, scale, unit, eps, step=True)
+    data = _delta_inputs(q, k, v, g, beta)
+    y, ldy = _heads_out(out, v, "out")
+    _run(conv_delta_step(seq, par, *data, _dense(s, (seq.B, par.heads_v, par.dim_k, par.dim_v), torch.float32, "s", v.get_device()),
+                         y.data_ptr(), ldy, _stream_of(v)), "conv_delta_step")
     return y
 
 

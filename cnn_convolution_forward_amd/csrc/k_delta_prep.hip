@@ -1,0 +1,345 @@
+// k_delta_prep.hip -- what a block of 64 tokens of the gated delta rule needs
+// before any state is known, for all blocks at once:
+//
+//   G = cumulative log decays,  D[i][j] = exp(G[i] - G[j]),  A = beta_i D[i][j] k_i.k_j (j < i)
+//   T = (I + A)^-1,  P = scale D[i][j] q_i.k_j (j <= i)
+//
+// and queries and keys as pages of fp16 operands, in both orientations.  Strides,
+// packing, odd widths and the sequence's end are dealt with here; the kernels
+// behind it see whole tiles, with zeros for tokens that are not there.
+//
+// A workgroup has one block and one key head, and walks through the value heads
+// that share it.  q.k and k.k are matrix products (exact for bf16).  Differences of
+// G are taken in fp64: their error is relative to the difference, whatever decays came
+// before.  T: the four 16x16 blocks on the diagonal by substitution, a lane to a
+// column, then the blocks below from the products T_ii A_ij T_jj on the fp32 matrix
+// instructions: three levels instead of 64 steps.
+#include "delta_common.h"
+
+namespace convfwd {
+namespace {
+
+constexpr int kThreads = 256;
+
+// N = 8 DKB elements of a row from p + c on, of which those below `n` are there.
+template <typename T, int N> __device__ __forceinline__ void load_part(const T *p, int c, int n, float (&f)[N]) {
+    constexpr int VEC = sizeof(T) == 2 ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += VEC) {
+        if (c + i + VEC <= n) {
+            float t[VEC];
+            load_f32<T, VEC>(p + c + i, t);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[i + j] = t[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                float t[1] = {0.f};
+                if (c + i + j < n) load_f32<T, 1>(p + c + i + j, t);
+                f[i + j] = t[0];
+            }
+        }
+    }
+}
+
+template <typename T, int DKB, bool BWD>
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
+                                                              const T *__restrict__ k, int64_t ldk,
+                                                              const float *__restrict__ g, int64_t ldg,
+                                                              const float *__restrict__ beta, int64_t ldb) {
+    constexpr int DKP = 32 * DKB, PARTS = sizeof(T) == 2 ? 1 : 2, LD = DKP + 8, N = 8 * DKB;
+    typedef float Square[kBlock][65];
+    typedef _Float16 Tiles[PARTS][kBlock][LD];
+    // keys and queries; once their products are taken, A and T lie in their place
+    constexpr int kTiles = 2 * sizeof(Tiles) > 2 * sizeof(Square) ? 2 * sizeof(Tiles) : 2 * sizeof(Square);
+    __shared__ __align__(16) char shared[kTiles];
+    Tiles *xs = reinterpret_cast<Tiles *>(shared);
+    Square &A = *reinterpret_cast<Square *>(shared), &Ti = *reinterpret_cast<Square *>(shared + sizeof(Square));
+    __shared__ Square kk, qk;
+    __shared__ double G[kBlock];
+    __shared__ float kap[2][kBlock], size[2][kBlock], bt[kBlock], red[8];
+    const int64_t slot = blockIdx.x / d.H;
+    const int hk = (int)(blockIdx.x % d.H);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
+    const Block at = find_block(s, ws.per, slot);
+    int64_t first;
+    int len;
+    seq_range(s, at.b, first, len);
+    if (at.k < 0 || (int64_t)at.k * kBlock >= len) return;
+    const int64_t r0 = first + (int64_t)at.k * kBlock;
+    const int n = min(len - at.k * kBlock, kBlock);
+
+    // rows as fp16 under their own power of two, and the factor that makes the row of it
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const int row = tid >> 2, c = (tid & 3) * N;
+        float f[N];
+        if (row < n) {
+            load_part<T, N>((which ? q + (r0 + row) * ldq : k + (r0 + row) * ldk) + hk * d.Dk, c, d.Dk, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = 0.f;
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[i]));
+        m = fmaxf(m, __shfl_xor(m, 1));
+        m = fmaxf(m, __shfl_xor(m, 2));
+        const float sc = pow2_scale(m, 60);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            h4_t hi, lo;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = f[i + j] * sc;
+                ss = fmaf(x, x, ss);
+                hi[j] = (_Float16)x;
+                lo[j] = (_Float16)(x - (float)hi[j]);
+            }
+            *reinterpret_cast<h4_t *>(&xs[which][0][row][c + i]) = hi;
+            if constexpr (PARTS == 2) *reinterpret_cast<h4_t *>(&xs[which][PARTS - 1][row][c + i]) = lo;
+        }
+        ss += __shfl_xor(ss, 1);
+        ss += __shfl_xor(ss, 2);
+        if ((tid & 3) == 0) {
+            // unit length: x / sqrt(sum x^2 + eps) with sum x^2 = ss / sc^2; a row of zeros stays
+            const float f0 = !d.unit ? pow2_inv(sc) : ss == 0.f ? 0.f : 1.f / sqrtf(ss + d.eps * sc * sc);
+            kap[which][row] = f0;
+            size[which][row] = f0 * sc;
+        }
+    }
+    __syncthreads();
+
+    const auto row_page = [&](int which, int part, int rb, int m) {       // lane = token
+        const _Float16 *p = &xs[which][part][32 * rb + col][16 * m + 4 * half];
+        const h4_t a = *reinterpret_cast<const h4_t *>(p), b = *reinterpret_cast<const h4_t *>(p + 8);
+        h8_t v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+        return v;
+    };
+    {   // pages of keys and queries
+        uint4 *out = ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage + lane;
+        constexpr int F = 4 * DKB;
+        for (int i = wave; i < (BWD ? 4 : 3) * PARTS * F; i += 4) {
+            const int kind = i / (PARTS * F), part = i / F % PARTS, f = i % F;      // K, KT, Q, QT
+            const int which = kind >> 1;
+            h8_t v;
+            if (!(kind & 1)) {
+                v = row_page(which, part, f / (2 * DKB), f % (2 * DKB));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = xs[which][part][page_at(f % 4, half, j)][32 * (f / 4) + col];
+            }
+            out[i * kPage] = __builtin_bit_cast(uint4, v);
+        }
+    }
+    // k.k and q.k, the three blocks of 32x32 on and below the diagonal
+    for (int i = wave; i < 6; i += 4) {
+        const int which = i / 3, ib = i % 3 ? 1 : 0, jb = i % 3 == 2 ? 1 : 0;
+        acc_t c = zeros();
+#pragma unroll
+        for (int m = 0; m < 2 * DKB; ++m) {
+            const h8_t a = row_page(which, 0, ib, m), b = row_page(0, 0, jb, m);
+            c = mfma(a, b, c);
+            if constexpr (PARTS == 2) {
+                c = mfma(a, row_page(0, 1, jb, m), c);
+                c = mfma(row_page(which, 1, ib, m), b, c);
+            }
+        }
+        float(*out)[65] = which ? qk : kk;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = 32 * ib + acc_row(r, half), cl = 32 * jb + col;
+            out[row][cl] = c[r] * kap[which][row] * kap[0][cl];
+        }
+    }
+
+    for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
+        __syncthreads();                                                // the last head's arrays are free
+        const int64_t rec = slot * d.Hv + hv;
+        float *rows = ws.rows + rec * kRowsFloats;
+        if (wave == 0) {
+            const float gv = lane < n ? g[(r0 + lane) * ldg + hv] : 0.f, b = lane < n ? beta[(r0 + lane) * ldb + hv] : 0.f;
+            double v = gv < -1e4f ? -1e4 : (double)gv;                  // a NaN stays
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double t = __shfl_up(v, m);
+                if (lane >= m) v += t;
+            }
+            const float E = (float)exp(v), F = (float)exp(__shfl(v, 63) - v);
+            G[lane] = v;
+            bt[lane] = b;
+            rows[64 * kRowBEK + lane] = b * E * kap[0][lane];
+            rows[64 * kRowBeta + lane] = b;
+            rows[64 * kRowFK + lane] = F * kap[0][lane];
+            rows[64 * kRowEQ + lane] = d.scale * E * kap[1][lane];
+            if constexpr (BWD) {
+                rows[64 * kRowE + lane] = E;
+                rows[64 * kRowF + lane] = F;
+                rows[64 * kRowKK + lane] = kap[0][lane];
+                rows[64 * kRowKQ + lane] = kap[1][lane];
+                rows[64 * kRowSizeK + lane] = size[0][lane];
+                rows[64 * kRowSizeQ + lane] = size[1][lane];
+                reinterpret_cast<double *>(rows + 64 * kRowG)[lane] = v;
+            }
+            if (lane == 63) rows[kGamma] = E;
+        }
+        __syncthreads();
+        const auto decay = [&](int i, int j) { return expf((float)(G[i] - G[j])); };
+        // P where it is wanted, and A into LDS
+        Pair pp[2];
+        float pv[2][8], pm = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int m = wave, ib = 1 - u;                             // block 1 has pages 0..3, block 0 pages 0 and 1
+            if (u && wave > 1) break;
+            const int i = 32 * ib + col;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = page_at(m, half, e);
+                const float D = j <= i ? decay(i, j) : 0.f;
+                pv[u][e] = j <= i ? d.scale * qk[i][j] * D : 0.f;
+                pm = fmaxf(pm, fabsf(pv[u][e]));
+                A[i][j] = j < i ? bt[i] * kk[i][j] * D : 0.f;
+            }
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) pm = fmaxf(pm, __shfl_xor(pm, m));
+        if (lane == 0) red[wave] = pm;
+        __syncthreads();
+        const float sp = pow2_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+
+        // T: the blocks on the diagonal
+        {
+            const int o = 16 * wave, c = lane & 15;
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float v = i == c ? 1.f : 0.f;
+#pragma unroll
+                for (int j = 0; j < i; ++j) v = fmaf(-A[o + i][o + j], t[j], v);
+                t[i] = v;
+            }
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) Ti[o + i][o + c] = t[i];
+            }
+        }
+        __syncthreads();
+        // and those below it: T_ij = -T_ii sum_k A_ik T_kj.  The contraction of step u takes elements 4 (lane/16) + u, the
+        // rows in which a result lies in registers
+#pragma unroll
+        for (int lev = 1; lev < 4; ++lev) {
+            if (wave < 4 - lev) {
+                const int bi = wave + lev, bj = wave, c = lane & 15, o = 4 * (lane >> 4);
+                f4_t sum = {0.f, 0.f, 0.f, 0.f}, out = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < lev; ++kb)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x4f32(A[16 * bi + c][16 * (bj + kb) + o + u],
+                                                                   Ti[16 * (bj + kb) + o + u][16 * bj + c], sum, 0, 0, 0);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    out = __builtin_amdgcn_mfma_f32_16x16x4f32(Ti[16 * bi + c][16 * bi + o + u], sum[u], out, 0, 0, 0);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) Ti[16 * bi + o + u][16 * bj + c] = -out[u];
+            }
+            __syncthreads();
+        }
+        float tm = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int i = tid >> 2, j = (tid & 3) * 16 + e;
+            if (j <= i) tm = fmaxf(tm, fabsf(Ti[i][j]));
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) tm = fmaxf(tm, __shfl_xor(tm, m));
+        if (lane == 0) red[4 + wave] = tm;
+        __syncthreads();
+        const float st = pow2_scale(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
+        if (tid == 0) rows[kInvT] = pow2_inv(st), rows[kInvP] = pow2_inv(sp);
+        uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
+        const auto put = [&](int kind, int page, const Pair &p) {
+            out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
+            out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
+        };
+        for (int f = wave; f < kTriPages; f += 4) {
+            const int ib = f < 2 ? 0 : 1, m = ib ? f - 2 : f, i = 32 * ib + col;
+            put(0, f, split8([&](int e) {
+                    const int j = page_at(m, half, e);
+                    return j <= i ? Ti[i][j] * st : 0.f;
+                }));
+        }
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u && wave > 1) break;
+                put(1, low_page(1 - u, wave), split8([&](int e) { return pv[u][e] * sp; }));
+            }
+        } else {
+            for (int f = wave; f < kTriPages; f += 4) {
+                const int jb = f < 4 ? 0 : 1, m = jb ? f - 2 : f, j = 32 * jb + col;
+                put(1, f, split8([&](int e) {
+                        const int i = page_at(m, half, e);
+                        return j <= i ? Ti[i][j] * st : 0.f;
+                    }));
+                put(2, f, split8([&](int e) {
+                        const int i = page_at(m, half, e);
+                        return j <= i ? d.scale * qk[i][j] * decay(i, j) * sp : 0.f;
+                    }));
+            }
+        }
+    }
+}
+
+template <typename T, bool BWD>
+void prep(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, hipStream_t st) {
+    const dim3 grid((unsigned)(ws.blocks * d.H));
+#define CASE(n)                                                                                                               \
+    case n:                                                                                                                   \
+        delta_prep_kernel<T, n, BWD><<<grid, kThreads, 0, st>>>(s, d, ws, (const T *)in.q.p, in.q.ld, (const T *)in.k.p,       \
+                                                                in.k.ld, (const float *)in.g.p, in.g.ld, (const float *)in.beta.p, \
+                                                                in.beta.ld);                                                  \
+        break
+    switch ((d.Dk + 31) / 32) {
+        CASE(1);
+        CASE(2);
+        CASE(3);
+        CASE(4);
+    }
+#undef CASE
+}
+
+int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+
+}  // namespace
+
+int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *base, DeltaWs &ws) {
+    const int dkb = (d.Dk + 31) / 32, dvb = (d.Dv + 31) / 32;
+    ws.per = (s.T + kBlock - 1) / kBlock;
+    ws.blocks = s.off ? s.rows / kBlock + s.B : (int64_t)s.B * ws.per;
+    ws.qk_pages = (bwd ? 4 : 3) * (bf16 ? 1 : 2) * 4 * dkb;
+    ws.tri_pages = (bwd ? 6 : 4) * kTriPages;
+    char *p = (char *)base;
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        char *r = p + at;
+        at += round16(bytes);
+        return r;
+    };
+    ws.qk = (uint4 *)take(ws.blocks * d.H * ws.qk_pages * 1024);
+    ws.tri = (uint4 *)take(ws.blocks * d.Hv * ws.tri_pages * 1024);
+    ws.rows = (float *)take(ws.blocks * d.Hv * kRowsFloats * 4);
+    ws.ends = bwd ? (float *)take(ws.blocks * d.Hv * dkb * dvb * 4096) : nullptr;
+    return at;
+}
+
+void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, hipStream_t st) {
+    if (bf16) bwd ? prep<uint16_t, true>(s, d, ws, in, st) : prep<uint16_t, false>(s, d, ws, in, st);
+    else bwd ? prep<float, true>(s, d, ws, in, st) : prep<float, false>(s, d, ws, in, st);
+}
+
+}  // namespace convfwd

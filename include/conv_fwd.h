@@ -538,6 +538,67 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
                                       const void *gate, int64_t ldg, const void *inp, int64_t ldi,
                                       const float *decay, float *h, void *y, int64_t ldy, void *stream);
 
+/* ---- gated delta rule -------------------------------------------------------
+ *
+ * A recurrence whose state is a matrix: a memory that is read at a key, corrected
+ * towards a value there, and read at a query.  Each of heads_v value heads has a
+ * state S (dim_k x dim_v).  Per token, with the head's query and key q, k (dim_k),
+ * value v (dim_v), log decay g and strength beta:
+ *
+ *     e = v - exp(g) S^T k,    S = exp(g) S + beta k e^T,    y = scale S^T q
+ *
+ * heads query and key heads; heads divides heads_v, and value head h uses query
+ * and key head h / (heads_v/heads).  unit = 1: q and k of each head are brought to unit
+ * length first, q / sqrt(sum q^2 + eps); with unit = 0 they are used as they are
+ * (k with beta |k|^2 < 2, or the state grows without bound).
+ *
+ * Sequences, rows, strides, packing and errors are those of the operators over
+ * sequences; seq->C is heads_v*dim_v, the channels of v, y, dy and dv, head after
+ * head.  Rows of q, k, dq and dk hold heads*dim_k channels.  gate (the log decays g)
+ * and beta, and their gradients, are fp32 rows of heads_v.  States are fp32,
+ * (B, heads_v, dim_k, dim_v) with dim_v fastest.
+ *
+ * 1 <= dim_k, dim_v <= 128, heads, heads_v >= 1.  CONV_ERR_PARAM otherwise, and where
+ * heads does not divide heads_v, seq->C is not heads_v*dim_v, scale is not finite, or
+ * eps is negative or not finite; CONV_ERR_OVERFLOW where B*heads_v*dim_k*dim_v is 2^31 or
+ * more, or the sequences' 64-token blocks (rows/64 + B of them) times heads_v 2^21 or more.
+ *
+ * Whole sequences are computed in blocks of 64 tokens by matrix products whose
+ * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
+ * fp32; decays are added up in fp64.  A log decay below -10000 counts as -10000: nothing of the state
+ * is left.  Infinities and NaN: a state, or a token's values, that are not finite
+ * make results of their head non-finite from the start of their 64-token
+ * block on, in their own sequence only. */
+typedef struct {
+    int heads, heads_v;      /* of queries and keys; of values                  */
+    int dim_k, dim_v;        /* of each head                                    */
+    int unit;                /* 0 or 1                                          */
+    float scale, eps;        /* of the output; of the unit length               */
+} conv_delta_t;
+
+/* Device workspace of conv_delta_fwd: what each block needs before its state is
+ * known; 0 where none is needed, or on invalid arguments.  Overwritten by each
+ * call; two calls in flight must not share it. */
+CONV_API size_t conv_delta_fwd_workspace_bytes(const conv_seq_t *seq, const conv_delta_t *par);
+
+/* S before a sequence's first token is s0, or 0 when NULL; sT, when not NULL,
+ * receives S after its last token (s0 for an empty one).  states, when not NULL,
+ * receives what conv_delta_bwd starts from: S before tokens 0, 64, 128, ... of
+ * each sequence, (B, ceil(T/64), heads_v, dim_k, dim_v) fp32; entries past a
+ * sequence's end are not written. */
+CONV_API conv_status_t conv_delta_fwd(const conv_seq_t *seq, const conv_delta_t *par, const void *q, int64_t ldq,
+                                      const void *k, int64_t ldk, const void *v, int64_t ldv, const float *gate,
+                                      int64_t ldg, const float *beta, int64_t ldb, const float *s0, void *y, int64_t ldy,
+                                      float *sT, float *states, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One new token for each of B sequences: q, k, v, gate, beta and y are one row
+ * for each; S (B, heads_v, dim_k, dim_v) is updated in place.  seq->T, offsets and
+ * tokens are not read. */
+CONV_API conv_status_t conv_delta_step(const conv_seq_t *seq, const conv_delta_t *par, const void *q, int64_t ldq,
+                                       const void *k, int64_t ldk, const void *v, int64_t ldv, const float *gate,
+                                       int64_t ldg, const float *beta, int64_t ldb, float *S, void *y, int64_t ldy,
+                                       void *stream);
+
 /* ---- layer norm ------------------------------------------------------------
  *
  * Over the C channels of each of `rows` rows (those of any sequences, packed or
