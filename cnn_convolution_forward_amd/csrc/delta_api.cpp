@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kMaxDim = 128;
 constexpr int64_t kMaxHeadBlocks = INT64_C(1) << 21;
+constexpr int64_t kMaxStep = INT64_C(1) << 22;         // elements between rows: a block's rows stay below 2^30 bytes
 
 conv_status_t make_delta(const conv_seq_t *q, const conv_delta_t *p, bool step, Seq &s, Delta &d) {
     if (!p) return CONV_ERR_NULL;
@@ -35,6 +36,12 @@ Inputs inputs(const DeltaIn &in, const Delta &d, int64_t n, int e) {
     const auto rows = [n](const Rows &r, int64_t cols, int esize) { return Span{r.p, n, cols, r.ld, esize}; };
     return {rows(in.q, (int64_t)d.H * d.Dk, e), rows(in.k, (int64_t)d.H * d.Dk, e), rows(in.v, (int64_t)d.Hv * d.Dv, e),
             rows(in.g, d.Hv, 4), rows(in.beta, d.Hv, 4)};
+}
+
+conv_status_t check_steps(std::initializer_list<Span> all) {
+    for (const Span &s : all)
+        if (s.ld >= kMaxStep) return CONV_ERR_OVERFLOW;
+    return CONV_OK;
 }
 
 }  // namespace
@@ -64,6 +71,7 @@ conv_status_t conv_delta_fwd(const conv_seq_t *seq, const conv_delta_t *par, con
     const Span sy{y, s.rows, s.C, ldy, e}, ss0 = dense(s0, ends, 4), ssT = dense(sT, ends, 4), ss = dense(states, ends * nb, 4),
         sws = dense(need ? workspace : nullptr, (int64_t)workspace_bytes, 1);
     TRY(check_align({i.q, i.k, i.v, i.g, i.b, sy, ss0, ssT, ss}));
+    TRY(check_steps({i.q, i.k, i.v, i.g, i.b, sy}));
     TRY(check_alias({sy, ssT, ss, sws}, {i.q, i.k, i.v, i.g, i.b, ss0}));
     return to_status(launch_delta_fwd(s, d, e == 2, in, s0, RowsOut{y, ldy}, sT, states, workspace, (hipStream_t)stream));
 }
@@ -80,6 +88,7 @@ conv_status_t conv_delta_step(const conv_seq_t *seq, const conv_delta_t *par, co
     const Inputs i = inputs(in, d, s.B, e);
     const Span sS = dense(S, (int64_t)s.B * d.Hv * d.Dk * d.Dv, 4), sy{y, s.B, s.C, ldy, e};
     TRY(check_align({i.q, i.k, i.v, i.g, i.b, sS, sy}));
+    TRY(check_steps({i.q, i.k, i.v, i.g, i.b, sy}));
     TRY(check_alias({sS, sy}, {i.q, i.k, i.v, i.g, i.b}));
     return to_status(launch_delta_step(s, d, e == 2, in, S, RowsOut{y, ldy}, (hipStream_t)stream));
 }

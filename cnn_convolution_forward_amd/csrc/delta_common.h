@@ -18,6 +18,7 @@
 #pragma once
 
 #include "delta_internal.h"
+#include "mfma_common.h"
 #include "seq_common.h"
 
 namespace convfwd {
@@ -51,17 +52,27 @@ __device__ __forceinline__ float pow2_scale(float a, int most = 113) {
 // 1/s of a power of two.
 __device__ __forceinline__ float pow2_inv(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-// Eight values as hi + lo.
+// Eight values times a power of two as hi + lo, or as hi alone.  hi is hidden from the optimiser, which would
+// make it a second time from the values where lo needs it.
 struct Pair {
     h8_t hi, lo;
 };
-template <typename F> __device__ __forceinline__ Pair split8(F value) {
+template <typename F> __device__ __forceinline__ h8_t half8(float scale, F value) {
+    h8_t v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (_Float16)(value(j) * scale);
+    return v;
+}
+template <typename F> __device__ __forceinline__ Pair split8(float scale, F value) {
+    typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
     Pair p;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = value(j);
-        p.hi[j] = (_Float16)x;
-        p.lo[j] = (_Float16)(x - (float)p.hi[j]);
+    for (int j = 0; j < 8; j += 2) {
+        h2_t h = {(_Float16)(value(j) * scale), (_Float16)(value(j + 1) * scale)};
+        asm("" : "+v"(h));
+        p.hi[j] = h[0], p.hi[j + 1] = h[1];
+        p.lo[j] = (_Float16)fmaf(value(j), scale, -(float)h[0]);
+        p.lo[j + 1] = (_Float16)fmaf(value(j + 1), scale, -(float)h[1]);
     }
     return p;
 }
@@ -75,7 +86,7 @@ __device__ __forceinline__ float max_abs(const acc_t &v, float m = 0.f) {
 __device__ __forceinline__ float max_halves(float m) { return fmaxf(m, __shfl_xor(m, 32)); }
 
 // Rows record of a block and value head: 64 floats each, then scalars.  The first four fill a page.
-enum { kRowBEK, kRowBeta, kRowFK, kRowEQ, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ, kRowG /* doubles */, kRowG2, kRowCount };
+enum { kRowEK, kRowBeta, kRowFK, kRowEQ, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ, kRowG /* doubles */, kRowG2, kRowCount };
 enum { kGamma = 64 * kRowCount, kInvT, kInvP };
 constexpr int kRowsFloats = 64 * kRowCount + 64;
 
@@ -110,6 +121,101 @@ __device__ __forceinline__ Block find_block(const Seq &s, int per, int64_t n) {
     t.b = (int)(n / per);
     t.k = (int)(n % per);
     return t;
+}
+
+// ---- memory ----
+
+// Pages from global memory to LDS, asynchronously: four to a workgroup's wave in turn.  The instruction takes the
+// LDS address from M0 (one wait state after it is written) and adds its offset on both sides.  In assembly because the
+// compiler, which cannot tell one buffer from the other, waits for all such loads before any
+// read of LDS.  They have no output registers; wait_copies is their wait.  Nothing else here uses M0.
+__device__ __forceinline__ void copy4(const uint4 *src, uint32_t dst, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:2048\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072"
+                 :
+                 : "s"(dst), "v"(at), "s"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy1(const uint4 *src, uint32_t dst, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(at), "s"(src) : "memory");
+}
+template <int PAGES> __device__ __forceinline__ void copy_pages(const void *from, uint32_t dst, int wave, int waves, int lane) {
+    const uint4 *src = (const uint4 *)from;
+    for (int i = 4 * wave; i < PAGES; i += 4 * waves) {
+        if (PAGES % 4 == 0 || i + 4 <= PAGES) {
+            copy4(src + i * kPage, dst + i * 1024, 16 * lane);
+        } else {
+            for (int j = i; j < PAGES; ++j) copy1(src + j * kPage, dst + j * 1024, 16 * lane);
+        }
+    }
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+}
+
+// Buffers of one block's rows, and of one head's state: offsets at or past `bytes` load zeros and store nothing, so rows
+// past the sequence's end, columns past the head and the padding of a state need no branch.  Sizes stay below 2^30 (delta_api.cpp).
+template <typename T> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const T *p, int n, int64_t ld, int cols) {
+    return make_rsrc(p, (uint32_t)(((n - 1) * ld + cols) * sizeof(T)));
+}
+__device__ __forceinline__ float load_at(__amdgpu_buffer_rsrc_t r, uint32_t off) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0)); }
+__device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t r, uint32_t off, float v) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)off, 0, 0); }
+
+// A column of a block's rows, in the order of a result's registers: token 32 (i / 16) + acc_row(i % 16, half).  at: the
+// column's bytes, or kOob for none.
+// As loaded: 16 bits are not packed, which would wait for the load.
+template <typename T> struct Column {
+    uint32_t v[32];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t ld, int half) {
+        const uint32_t base = at + 4 * half * ld;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int off = (int)(base + (32 * (i >> 4) + acc_row(i & 15, 0)) * ld);
+            if constexpr (sizeof(T) == 2) v[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+            else v[i] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(sizeof(T) == 2 ? v[i] << 16 : v[i]); }
+};
+
+// A state's columns (dim_k x dim_v, dim_v apart) to and from a result's registers.
+template <int DKB> __device__ __forceinline__ void load_state(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t ld, int half, acc_t (&S)[DKB]) {
+    const uint32_t base = at + 4 * half * ld;
+#pragma unroll
+    for (int i = 0; i < 16 * DKB; ++i) {
+        S[i >> 4][i & 15] = load_at(r, base + (32 * (i >> 4) + acc_row(i & 15, 0)) * ld);
+    }
+}
+template <int DKB> __device__ __forceinline__ void store_state(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t ld, int half, const acc_t (&S)[DKB]) {
+    const uint32_t base = at + 4 * half * ld;
+#pragma unroll
+    for (int i = 0; i < 16 * DKB; ++i) store_at(r, base + (32 * (i >> 4) + acc_row(i & 15, 0)) * ld, S[i >> 4][i & 15]);
+}
+
+// Four neighbouring columns of a row, of which `left` are the head's.  WIDE: rows and columns are aligned to four.
+template <bool WIDE> __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left, const float (&f)[4], uint16_t *) {
+    if constexpr (WIDE) {
+        typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+        const u2_t v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(v, r, left > 0 ? (int)off : (int)kOob, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(f[j]), r, left > j ? (int)off + 2 * j : (int)kOob, 0, 0);
+    }
+}
+template <bool WIDE> __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left, const float (&f)[4], float *) {
+    if constexpr (WIDE) {
+        const u32x4_t v = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, left > 0 ? (int)off : (int)kOob, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) store_at(r, left > j ? off + 4 * j : kOob, f[j]);
+    }
+}
+// Rows of heads of `dim` whose groups of four columns are aligned.
+template <typename T> bool wide_rows(const void *p, int64_t ld, int dim) {
+    return dim % 4 == 0 && ld % 4 == 0 && (uintptr_t)p % (4 * sizeof(T)) == 0;
 }
 
 }  // namespace convfwd

@@ -13,19 +13,12 @@
 // The pages of K, K^T, Q, T and P (66 KB for bf16 heads of 128) are brought to LDS
 // asynchronously, a block ahead where two buffers fit.  Values are
 // loaded a block ahead into registers.
+#include <type_traits>
+
 #include "delta_common.h"
 
 namespace convfwd {
 namespace {
-
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
-
-// Copies `pages` pages from global memory to LDS, the workgroup's waves in turn.
-__device__ __forceinline__ void copy_pages(const uint4 *src, char *dst, int pages, int wave, int waves, int lane) {
-    for (int i = wave; i < pages; i += waves)
-        __builtin_amdgcn_global_load_lds((global_void *)(src + i * kPage + lane), (lds_void *)(dst + i * 1024), 16, 0, 0);
-}
 
 template <int DKB, int PARTS> struct FwdPages {
     static constexpr int F = 4 * DKB;                   // pages of one part of K, KT or Q
@@ -38,131 +31,143 @@ template <int DKB, int PARTS> struct FwdPages {
 template <typename T, int DKB>
 __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ v,
                                                         int64_t ldv, const float *__restrict__ s0, T *__restrict__ y,
-                                                        int64_t ldy, float *__restrict__ sT, float *__restrict__ states) {
+                                                        int64_t ldy, bool wide, float *__restrict__ sT,
+                                                        float *__restrict__ states) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
     typedef FwdPages<DKB, PARTS> P;
     extern __shared__ __align__(1024) char lds[];
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     float *table = reinterpret_cast<float *>(lds + P::kBuffers * P::kAll * 1024) + wave * 64;      // two factors for each column
-    const int64_t bh = blockIdx.x % ((int64_t)s.B * d.Hv);
-    const int slice = (int)(blockIdx.x / ((int64_t)s.B * d.Hv)) * waves + wave;
-    const int b = (int)(bh / d.Hv), hv = (int)(bh % d.Hv), hk = hv / d.group;
-    const int c = slice * 32 + col, cc = min(c, d.Dv - 1);             // columns past the last are computed and not stored
-    const bool on = slice < slices && c < d.Dv;
+    const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads);
+    const int slice = (int)(blockIdx.x / heads) * waves + wave;
+    const int b = bh / d.Hv, hv = bh % d.Hv, hk = hv / d.group;
+    const int c = slice * 32 + col;                                    // columns past the last are zeros and not stored
+    const uint32_t at_s = c < d.Dv ? 4 * c : kOob, at_v = c < d.Dv ? (uint32_t)sizeof(T) * c : kOob;
+    const uint32_t ld_s = 4 * d.Dv, ld_v = (uint32_t)(ldv * sizeof(T)), ld_y = (uint32_t)(ldy * sizeof(T));
     int64_t first;
     int len;
     seq_range(s, b, first, len);
     const int blocks = (len + kBlock - 1) / kBlock;
     const int64_t slot0 = first_block(s, ws.per, b, first);
-    const int64_t state_at = bh * d.Dk * d.Dv;
+    const int state = d.Dk * d.Dv;
+    const uint32_t lds0 = lds_address(lds);
 
     acc_t S[DKB];
 #pragma unroll
-    for (int i = 0; i < DKB; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = 32 * i + acc_row(r, half);
-            S[i][r] = s0 && row < d.Dk ? s0[state_at + (int64_t)row * d.Dv + cc] : 0.f;
-        }
+    for (int i = 0; i < DKB; ++i) S[i] = zeros();
+    if (s0) load_state<DKB>(make_rsrc(s0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
 
-    T next[32];
-    float ngamma = 0.f, ninvT = 0.f, ninvP = 0.f;
     const auto fetch = [&](int k) {
-        char *buf = lds + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
+        const uint32_t buf = lds0 + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
         const int64_t slot = slot0 + k, rec = slot * d.Hv + hv;
-        const float *rows = ws.rows + rec * kRowsFloats;
-        copy_pages(ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage, buf, P::kQK, wave, waves, lane);
-        copy_pages(ws.tri + rec * ws.tri_pages * kPage, buf + P::kQK * 1024, P::kTri, wave, waves, lane);
-        copy_pages(reinterpret_cast<const uint4 *>(rows), buf + (P::kAll - 1) * 1024, 1, wave, waves, lane);
-        ngamma = rows[kGamma], ninvT = rows[kInvT], ninvP = rows[kInvP];
-        const int n = min(len - k * kBlock, kBlock);
-        const T *p = v + (first + (int64_t)k * kBlock) * ldv + hv * d.Dv + cc;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) next[i] = p[min(32 * (i >> 4) + acc_row(i & 15, half), n - 1) * ldv];
+        copy_pages<P::kQK>(ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage, buf, wave, waves, lane);
+        copy_pages<P::kTri>(ws.tri + rec * ws.tri_pages * kPage, buf + P::kQK * 1024, wave, waves, lane);
+        if (wave == waves - 1) copy1((const uint4 *)(ws.rows + rec * kRowsFloats), buf + (P::kAll - 1) * 1024, 16 * lane);
     };
-    if (P::kBuffers == 2 && blocks > 0) fetch(0);
+    if (blocks > 0) fetch(0);
+    wait_copies();
 
     for (int k = 0; k < blocks; ++k) {
-        if (P::kBuffers == 1) {
-            __syncthreads();                                           // every wave is done with the last block's pages
-            fetch(k);
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // Every wave's part of the pages is there; every wave is done with the other buffer.
         __syncthreads();
         const char *buf = lds + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
-        const float gamma = ngamma, invT = ninvT, invP = ninvP;
         const int n = min(len - k * kBlock, kBlock);
-        float vf[2][16];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            float f[1];
-            to_f32(next[i], f);
-            vf[i >> 4][i & 15] = 32 * (i >> 4) + acc_row(i & 15, half) < n ? f[0] : 0.f;
-        }
-        if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);
+        const float *rec = ws.rows + ((slot0 + k) * d.Hv + hv) * kRowsFloats;
+        const float gamma = rec[kGamma], invT = rec[kInvT], invP = rec[kInvP];
+        Column<T> V;
+        V.load(rows_buffer(v + (first + (int64_t)k * kBlock) * ldv + hv * d.Dv, n, ldv, d.Dv), at_v, ld_v, half);
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
         const float *fac = reinterpret_cast<const float *>(buf + (P::kAll - 1) * 1024);
-        if (states && on) {
-            float *p = states + (((int64_t)b * ((s.T + kBlock - 1) / kBlock) + k) * d.Hv + hv) * d.Dk * d.Dv + c;
-#pragma unroll
-            for (int i = 0; i < DKB; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (32 * i + acc_row(r, half) < d.Dk) p[(32 * i + acc_row(r, half)) * d.Dv] = S[i][r];
-        }
+        const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(fac + 64 * row + 32 * t + 8 * a + 4 * half); };
+        if (states)
+            store_state<DKB>(make_rsrc(states + (((int64_t)b * ((s.T + kBlock - 1) / kBlock) + k) * d.Hv + hv) * state, 4 * state), at_s,
+                             ld_s, half, S);
 
-        // products with S: K S for U, and (Q S)^T for y
+        // products with S: K S for U, and (Q S)^T for y.  Pages are read a step ahead, or in front of the phase that needs them:
+        // there is one wave to a SIMD, so nothing else would hide LDS's latency
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < DKB; ++i) m = max_abs(S[i], m);
         const float sc = pow2_scale(max_halves(m)), isc = pow2_inv(sc);
         acc_t X[2] = {zeros(), zeros()}, Y[2] = {zeros(), zeros()};
+        constexpr int kT = P::kQK, kP = kT + 2 * kTriPages, kQ = 2 * PARTS * P::F;
+        h8_t kp[2][2 * PARTS], qp[2][2 * PARTS];
+        const auto read_kq = [&](int i) {
+#pragma unroll
+            for (int u = 0; u < 2 * PARTS; ++u) {
+                kp[i & 1][u] = page((u >> 1) * P::F + (u & 1) * 2 * DKB + i);
+                qp[i & 1][u] = page(kQ + (u >> 1) * P::F + (u & 1) * 2 * DKB + i);
+            }
+        };
+        read_kq(0);
+        h8_t tri[2 * kTriPages];
+        f4_t ek[2][4];
 #pragma unroll
         for (int i = 0; i < 2 * DKB; ++i) {
-            const Pair f = split8([&](int j) { return S[i >> 1][8 * (i & 1) + j] * sc; });
+            if (i + 1 < 2 * DKB) {
+                read_kq(i + 1);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2 * kTriPages; ++u) tri[u] = page(kT + u);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) ek[u >> 2][u & 3] = factors(kRowEK, u >> 2, u & 3);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const Pair f = split8(sc, [&](int j) { return S[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const h8_t kp = page(t * 2 * DKB + i), qp = page(2 * PARTS * P::F + t * 2 * DKB + i);
-                X[t] = mfma(kp, f.hi, X[t]);
-                X[t] = mfma(kp, f.lo, X[t]);
-                Y[t] = mfma(f.hi, qp, Y[t]);
+                X[t] = mfma(kp[i & 1][t], f.hi, X[t]);
+                Y[t] = mfma(f.hi, qp[i & 1][t], Y[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                X[t] = mfma(kp[i & 1][t], f.lo, X[t]);
                 if constexpr (PARTS == 2) {
-                    X[t] = mfma(page(P::F + t * 2 * DKB + i), f.hi, X[t]);
-                    Y[t] = mfma(f.lo, qp, Y[t]);
-                    Y[t] = mfma(f.hi, page((2 * PARTS + 1) * P::F + t * 2 * DKB + i), Y[t]);
+                    X[t] = mfma(kp[i & 1][2 + t], f.hi, X[t]);
+                    Y[t] = mfma(f.lo, qp[i & 1][t], Y[t]);
+                    Y[t] = mfma(f.hi, qp[i & 1][2 + t], Y[t]);
                 }
             }
         }
-        // R = beta (V - E K S)
-        acc_t R[2];
+        // R = V - E K S
+        acc_t Rr[2];
         m = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                const f4_t bek = *reinterpret_cast<const f4_t *>(fac + 64 * kRowBEK + 32 * t + 8 * a + 4 * half);
-                const f4_t bt = *reinterpret_cast<const f4_t *>(fac + 64 * kRowBeta + 32 * t + 8 * a + 4 * half);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    R[t][4 * a + j] = bt[j] * vf[t][4 * a + j] - bek[j] * (X[t][4 * a + j] * isc);
+                    Rr[t][4 * a + j] = fmaf(-(ek[t][a][j] * isc), X[t][4 * a + j], V.get(16 * t + 4 * a + j));
             }
-            m = max_abs(R[t], m);
+            m = max_abs(Rr[t], m);
         }
         const float sr = pow2_scale(max_halves(m));
-        // U = T R
-        constexpr int kT = P::kQK, kP = kT + 2 * kTriPages;
+        if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);           // behind V's loads, which would wait for it
+        h8_t kt[4 * PARTS], kt2[4 * PARTS], low[PARTS * kTriPages];
+        const auto read_kt = [&](int i, h8_t(&to)[4 * PARTS]) {
+#pragma unroll
+            for (int u = 0; u < 4 * PARTS; ++u) to[u] = page((PARTS + (u >> 2)) * P::F + 4 * i + (u & 3));
+        };
+        f4_t fk[2][4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
+#pragma unroll
+        for (int u = 0; u < PARTS * kTriPages; ++u) low[u] = page(kP + u);
+        read_kt(0, kt);
+        __builtin_amdgcn_sched_barrier(0);
+        // U = T beta R
         acc_t U[2] = {zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Pair f = split8([&](int j) { return R[i >> 1][8 * (i & 1) + j] * sr; });
+            const Pair f = split8(sr, [&](int j) { return Rr[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
-            for (int t = i >> 1; t < 2; ++t) {
-                const h8_t hi = page(kT + low_page(t, i)), lo = page(kT + kTriPages + low_page(t, i));
-                U[t] = mfma(hi, f.hi, U[t]);
-                U[t] = mfma(hi, f.lo, U[t]);
-                U[t] = mfma(lo, f.hi, U[t]);
-            }
+            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[low_page(t, i)], f.hi, U[t]);
+#pragma unroll
+            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[low_page(t, i)], f.lo, U[t]);
+#pragma unroll
+            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[kTriPages + low_page(t, i)], f.hi, U[t]);
         }
         const float iu = pow2_inv(sr) * invT;
         acc_t W[2];
@@ -172,87 +177,80 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                const f4_t fk = *reinterpret_cast<const f4_t *>(fac + 64 * kRowFK + 32 * t + 8 * a + 4 * half);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= iu, W[t][4 * a + j] = U[t][4 * a + j] * fk[j];
+                for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= iu, W[t][4 * a + j] = U[t][4 * a + j] * fk[t][a][j];
             }
             m = max_abs(U[t], m);
             mw = max_abs(W[t], mw);
         }
-        // (P U)^T for y
         const float su = pow2_scale(max_halves(m)), sw = pow2_scale(max_halves(mw)), isw = pow2_inv(sw);
-        acc_t Z[2] = {zeros(), zeros()};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Pair f = split8([&](int j) { return U[i >> 1][8 * (i & 1) + j] * su; });
-#pragma unroll
-            for (int t = i >> 1; t < 2; ++t) {
-                const h8_t hi = page(kP + low_page(t, i));
-                Z[t] = mfma(f.hi, hi, Z[t]);
-                if constexpr (PARTS == 2) {
-                    Z[t] = mfma(f.lo, hi, Z[t]);
-                    Z[t] = mfma(f.hi, page(kP + kTriPages + low_page(t, i)), Z[t]);
-                }
-            }
-        }
-        // S = E_last S + (F K)^T U
+        // S = E_last S + (F K)^T U, and between its products (P U)^T for y
         Pair wf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wf[i] = split8([&](int j) { return W[i >> 1][8 * (i & 1) + j] * sw; });
+        for (int i = 0; i < 4; ++i) wf[i] = split8(sw, [&](int j) { return W[i >> 1][8 * (i & 1) + j]; });
+        acc_t Z[2] = {zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < DKB; ++i) {
+            h8_t(&now)[4 * PARTS] = i & 1 ? kt2 : kt;
+            if (i + 1 < DKB) read_kt(i + 1, i & 1 ? kt : kt2);
+            __builtin_amdgcn_sched_barrier(0);
             acc_t a = zeros();
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const h8_t kt = page(PARTS * P::F + 4 * i + u);
-                a = mfma(kt, wf[u].hi, a);
-                a = mfma(kt, wf[u].lo, a);
-                if constexpr (PARTS == 2) a = mfma(page((PARTS + 1) * P::F + 4 * i + u), wf[u].hi, a);
+                a = mfma(now[u], wf[u].hi, a);
+                a = mfma(now[u], wf[u].lo, a);
+                if constexpr (PARTS == 2) a = mfma(now[4 + u], wf[u].hi, a);
+            }
+            // every page of U in one of the DKB steps
+#pragma unroll
+            for (int q = i; q < 4; q += DKB) {
+                Pair f;
+                if constexpr (PARTS == 2) f = split8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
+                else f.hi = half8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
+#pragma unroll
+                for (int t = q >> 1; t < 2; ++t) {
+                    Z[t] = mfma(f.hi, low[low_page(t, q)], Z[t]);
+                    if constexpr (PARTS == 2) {
+                        Z[t] = mfma(f.lo, low[low_page(t, q)], Z[t]);
+                        Z[t] = mfma(f.hi, low[kTriPages + low_page(t, q)], Z[t]);
+                    }
+                }
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) S[i][r] = fmaf(a[r], isw, gamma * S[i][r]);
         }
+        const float eq[2] = {fac[64 * kRowEQ + col], fac[64 * kRowEQ + 32 + col]};
+        if (P::kBuffers == 1 && k + 1 < blocks) {
+            __syncthreads();                                           // every wave is done with the pages
+            fetch(k + 1);
+        }
+        wait_copies();                                                 // in front of y's stores, which take longer
         // y: a lane has token 32 t + col, columns 8 a + 4 half + 0..3 of the slice.  The factors of columns come from the lanes
         // that made them, through LDS (within the wave: the hardware keeps LDS accesses of a wave in order).
         if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su) * invP;
         __builtin_amdgcn_wave_barrier();
+        const __amdgpu_buffer_rsrc_t ry = rows_buffer(y + (first + (int64_t)k * kBlock) * ldy + hv * d.Dv, n, ldy, d.Dv);
+        const auto write = [&](auto aligned) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int row = 32 * t + col;
-            const float eq = fac[64 * kRowEQ + row];
-            T *p = y + (first + (int64_t)k * kBlock + row) * ldy + hv * d.Dv + slice * 32;
+            for (int t = 0; t < 2; ++t) {
+                const int row = 32 * t + col, c0 = slice * 32 + 4 * half;
+                const uint32_t off = row * ld_y + c0 * (uint32_t)sizeof(T);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const f4_t fs = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
-                const f4_t fu = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
-                const int c0 = 8 * a + 4 * half, left = d.Dv - slice * 32 - c0;
-                float o[4];
+                for (int a = 0; a < 4; ++a) {
+                    const f4_t fs = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
+                    const f4_t fu = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
+                    float o[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = Y[t][4 * a + j] * fs[j] * eq + Z[t][4 * a + j] * fu[j];
-                if (row < n && slice < slices) {
-                    if (left >= 4) {
-                        store_f32(p + c0, o);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float e[1] = {o[j]};
-                            if (j < left) store_f32(p + c0 + j, e);
-                        }
-                    }
+                    for (int j = 0; j < 4; ++j) o[j] = fmaf(Y[t][4 * a + j], fs[j] * eq[t], Z[t][4 * a + j] * fu[j]);
+                    store4<decltype(aligned)::value>(ry, off + 8 * a * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, o, y);
                 }
             }
-        }
+        };
+        if (wide) write(std::true_type());
+        else write(std::false_type());
         __builtin_amdgcn_wave_barrier();
     }
-    if (sT && on) {
-#pragma unroll
-        for (int i = 0; i < DKB; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = 32 * i + acc_row(r, half);
-                if (row < d.Dk) sT[state_at + (int64_t)row * d.Dv + c] = S[i][r];
-            }
-    }
+    if (sT) store_state<DKB>(make_rsrc(sT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
 }
 
 // Rows of y that no sequence holds.
@@ -272,7 +270,7 @@ hipError_t fwd(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &i
     const hipError_t e = hipFuncSetAttribute((const void *)delta_fwd_kernel<T, DKB>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     delta_fwd_kernel<T, DKB><<<(unsigned)(heads * ((slices + waves - 1) / waves)), 64 * waves, bytes, st>>>(
-        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, sT, states);
+        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, wide_rows<T>(y.p, y.ld, d.Dv), sT, states);
     return hipGetLastError();
 }
 

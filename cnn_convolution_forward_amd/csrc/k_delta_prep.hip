@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
             const float E = (float)exp(v), F = (float)exp(__shfl(v, 63) - v);
             G[lane] = v;
             bt[lane] = b;
-            rows[64 * kRowBEK + lane] = b * E * kap[0][lane];
+            rows[64 * kRowEK + lane] = E * kap[0][lane];
             rows[64 * kRowBeta + lane] = b;
             rows[64 * kRowFK + lane] = F * kap[0][lane];
             rows[64 * kRowEQ + lane] = d.scale * E * kap[1][lane];
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int i = tid >> 2, j = (tid & 3) * 16 + e;
-            if (j <= i) tm = fmaxf(tm, fabsf(Ti[i][j]));
+            if (j <= i) tm = fmaxf(tm, fabsf(BWD ? Ti[i][j] : Ti[i][j] * bt[j]));
         }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) tm = fmaxf(tm, __shfl_xor(tm, m));
@@ -268,27 +268,28 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
         };
         for (int f = wave; f < kTriPages; f += 4) {
             const int ib = f < 2 ? 0 : 1, m = ib ? f - 2 : f, i = 32 * ib + col;
-            put(0, f, split8([&](int e) {
+            // forward: times beta of the column, so that the kernel behind it has R = V - E K S
+            put(0, f, split8(BWD ? st : 1.f, [&](int e) {
                     const int j = page_at(m, half, e);
-                    return j <= i ? Ti[i][j] * st : 0.f;
+                    return j > i ? 0.f : BWD ? Ti[i][j] : Ti[i][j] * bt[j] * st;
                 }));
         }
         if constexpr (!BWD) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (u && wave > 1) break;
-                put(1, low_page(1 - u, wave), split8([&](int e) { return pv[u][e] * sp; }));
+                put(1, low_page(1 - u, wave), split8(sp, [&](int e) { return pv[u][e]; }));
             }
         } else {
             for (int f = wave; f < kTriPages; f += 4) {
                 const int jb = f < 4 ? 0 : 1, m = jb ? f - 2 : f, j = 32 * jb + col;
-                put(1, f, split8([&](int e) {
+                put(1, f, split8(st, [&](int e) {
                         const int i = page_at(m, half, e);
-                        return j <= i ? Ti[i][j] * st : 0.f;
+                        return j <= i ? Ti[i][j] : 0.f;
                     }));
-                put(2, f, split8([&](int e) {
+                put(2, f, split8(sp, [&](int e) {
                         const int i = page_at(m, half, e);
-                        return j <= i ? d.scale * qk[i][j] * decay(i, j) * sp : 0.f;
+                        return j <= i ? d.scale * qk[i][j] * decay(i, j) : 0.f;
                     }));
             }
         }

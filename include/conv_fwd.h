@@ -561,7 +561,8 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * 1 <= dim_k, dim_v <= 128, heads, heads_v >= 1.  CONV_ERR_PARAM otherwise, and where
  * heads does not divide heads_v, seq->C is not heads_v*dim_v, scale is not finite, or
  * eps is negative or not finite; CONV_ERR_OVERFLOW where B*heads_v*dim_k*dim_v is 2^31 or
- * more, or the sequences' 64-token blocks (rows/64 + B of them) times heads_v 2^21 or more.
+ * more, the sequences' 64-token blocks (rows/64 + B of them) times heads_v 2^21 or more, or a
+ * row stride 2^22 elements or more.
  *
  * Whole sequences are computed in blocks of 64 tokens by matrix products whose
  * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
