@@ -36,7 +36,8 @@ EXPORTS = ("conv_out_dim", "conv_status_str", "conv_version",
            "conv_fwd_ex_workspace_bytes", "conv_fwd_ex_bf16", "conv_fwd_ex_f32",
            "conv_causal_fwd", "conv_causal_bwd_workspace_bytes", "conv_causal_bwd", "conv_causal_step",
            "conv_scan_fwd_workspace_bytes", "conv_scan_fwd", "conv_scan_bwd_workspace_bytes", "conv_scan_bwd",
-           "conv_scan_step", "conv_delta_fwd_workspace_bytes", "conv_delta_fwd", "conv_delta_step", "conv_norm_fwd", "conv_norm_bwd_workspace_bytes", "conv_norm_bwd", "conv_adamw_step", "conv_adamw_state_values")
+           "conv_scan_step", "conv_delta_fwd_workspace_bytes", "conv_delta_fwd", "conv_delta_bwd_workspace_bytes",
+           "conv_delta_bwd", "conv_delta_step", "conv_norm_fwd", "conv_norm_bwd_workspace_bytes", "conv_norm_bwd", "conv_adamw_step", "conv_adamw_state_values")
 
 LAYOUT = {"nchw": 0, "nhwc": 1}
 OUT_DTYPE = {"f32": 0, "bf16": 1}
@@ -179,6 +180,10 @@ def lib():
         L.conv_delta_fwd_workspace_bytes.argtypes = [_ps, _pd]
         L.conv_delta_fwd.restype = _i
         L.conv_delta_fwd.argtypes = [_ps, _pd] + row * 5 + [_vp] + row + [_vp] * 3 + [_sz, _vp]
+        L.conv_delta_bwd_workspace_bytes.restype = _sz
+        L.conv_delta_bwd_workspace_bytes.argtypes = [_ps, _pd]
+        L.conv_delta_bwd.restype = _i
+        L.conv_delta_bwd.argtypes = [_ps, _pd] + row * 5 + [_vp] + row + [_vp] + row * 5 + [_vp] * 2 + [_sz, _vp]
         L.conv_delta_step.restype = _i
         L.conv_delta_step.argtypes = [_ps, _pd] + row * 5 + [_vp] + row + [_vp]
         L.conv_norm_fwd.restype = _i
@@ -385,6 +390,16 @@ def conv_delta_fwd_workspace_bytes(seq, par):
 def conv_delta_fwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, s0, y, ldy, sT, states, ws, ws_bytes, stream=None):
     return lib().conv_delta_fwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, s0, y, ldy, sT, states, ws, ws_bytes,
                                 stream)
+
+
+def conv_delta_bwd_workspace_bytes(seq, par):
+    return lib().conv_delta_bwd_workspace_bytes(seq, par)
+
+
+def conv_delta_bwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, states, dy, lddy, dsT, dq, lddq, dk, lddk, dv, lddv,
+                   dgate, lddg, dbeta, lddb, ds0, ws, ws_bytes, stream=None):
+    return lib().conv_delta_bwd(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, states, dy, lddy, dsT, dq, lddq, dk,
+                                lddk, dv, lddv, dgate, lddg, dbeta, lddb, ds0, ws, ws_bytes, stream)
 
 
 def conv_delta_step(seq, par, q, ldq, k, ldk, v, ldv, gate, ldg, beta, ldb, S, y, ldy, stream=None):
@@ -1185,6 +1200,38 @@ def delta_rule(q, k, v, g, beta, scale=None, unit=False, eps=1e-6, s0=None, offs
     _run(conv_delta_fwd(seq, par, *data, _dense(s0, ends, torch.float32, "s0", dev), y.data_ptr(), ldy, sT.data_ptr(),
                         None if states is None else states.data_ptr(), ws, wsb, _stream_of(v)), "conv_delta_fwd")
     return (y, sT, states) if with_states else (y, sT)
+
+
+def delta_rule_backward(q, k, v, g, beta, dy, states, scale=None, unit=False, eps=1e-6, ds=None, offsets=None, max_len=None,
+                        out=None, workspace=None):
+    """(dq, dk, dv, dg, dbeta, ds0) of (y, s) = delta_rule(...) for upstream dy, like v, and ds, float32 (B, value heads,
+    dim_k, dim_v) or None for zeros (conv_delta_bwd).  states: as delta_rule(..., with_states=True) returned them for the same
+    inputs.  dg, dbeta and ds0 are float32; dq and dk are sums over the value heads that share a head.  `out`: (dq, dk, dv, dg,
+    dbeta) to write into, perhaps slices of wider tensors, None for one to be allocated; rows that no sequence holds, and workspace
+    (of conv_delta_bwd_workspace_bytes): as in delta_rule."""
+    torch = _torch()
+    seq, par = make_delta(q, v, offsets, max_len, scale, unit, eps, fill=out is None)
+    data = _delta_inputs(q, k, v, g, beta)
+    dev = v.get_device()
+    lddy = _heads_ld(dy, v.shape, v.dtype, "dy", dev)
+    o = (None,) * 5 if out is None else out
+    # rows that no sequence holds are set by the call only where all outputs are new ones
+    new = torch.zeros if out is not None and offsets is not None else torch.empty
+    grads, where = [], []
+    for t, like, name in zip(o, (q, k, v, g, beta), ("dq", "dk", "dv", "dg", "dbeta")):
+        if t is None:
+            t = new(like.shape, dtype=like.dtype, device=like.device)
+        ld = _gate_ld(t, like.shape, name, dev) if like is g or like is beta else _heads_ld(t, like.shape, like.dtype, name, dev)
+        grads.append(t)
+        where += (t.data_ptr(), ld)
+    ends = (seq.B, par.heads_v, par.dim_k, par.dim_v)
+    ds0 = torch.empty(ends, dtype=torch.float32, device=v.device)
+    ws, wsb, held = _workspace(workspace, conv_delta_bwd_workspace_bytes(seq, par) if workspace is None else 0, v)
+    nb = -(-seq.T // SCAN_BLOCK)
+    _run(conv_delta_bwd(seq, par, *data, _dense(states, (seq.B, nb) + ends[1:], torch.float32, "states", dev), dy.data_ptr(), lddy,
+                        _dense(ds, ends, torch.float32, "ds", dev), *where, ds0.data_ptr(), ws, wsb, _stream_of(v)),
+         "conv_delta_bwd")
+    return (*grads, ds0)
 
 
 def delta_rule_step(q, k, v, g, beta, s, scale=None, unit=False, eps=1e-6, out=None):

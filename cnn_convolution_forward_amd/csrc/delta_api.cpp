@@ -76,6 +76,42 @@ conv_status_t conv_delta_fwd(const conv_seq_t *seq, const conv_delta_t *par, con
     return to_status(launch_delta_fwd(s, d, e == 2, in, s0, RowsOut{y, ldy}, sT, states, workspace, (hipStream_t)stream));
 }
 
+size_t conv_delta_bwd_workspace_bytes(const conv_seq_t *seq, const conv_delta_t *par) {
+    Seq s;
+    Delta d;
+    return make_delta(seq, par, false, s, d) == CONV_OK ? delta_bwd_workspace(s, d, esize(seq) == 2) : 0;
+}
+
+conv_status_t conv_delta_bwd(const conv_seq_t *seq, const conv_delta_t *par, const void *q, int64_t ldq, const void *k,
+                             int64_t ldk, const void *v, int64_t ldv, const float *gate, int64_t ldg, const float *beta,
+                             int64_t ldb, const float *states, const void *dy, int64_t lddy, const float *dsT, void *dq,
+                             int64_t lddq, void *dk, int64_t lddk, void *dv, int64_t lddv, float *dgate, int64_t lddg,
+                             float *dbeta, int64_t lddb, float *ds0, void *workspace, size_t workspace_bytes, void *stream) {
+    Seq s;
+    Delta d;
+    TRY(make_delta(seq, par, false, s, d));
+    if ((s.rows > 0 && (!q || !k || !v || !gate || !beta || !dy || !dq || !dk || !dv || !dgate || !dbeta)) ||
+        (s.rows > 0 && s.T > 0 && !states))                 // no tokens, no states
+        return CONV_ERR_NULL;
+    const int e = esize(seq);
+    const size_t need = delta_bwd_workspace(s, d, e == 2);
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    const DeltaIn in{{q, ldq}, {k, ldk}, {v, ldv}, {gate, ldg}, {beta, ldb}};
+    const Inputs i = inputs(in, d, s.rows, e);
+    const int64_t ends = (int64_t)s.B * d.Hv * d.Dk * d.Dv, nb = (s.T + CONV_SCAN_BLOCK - 1) / CONV_SCAN_BLOCK;
+    const int64_t wide = (int64_t)d.H * d.Dk;
+    const Span sdy{dy, s.rows, s.C, lddy, e}, sdq{dq, s.rows, wide, lddq, e}, sdk{dk, s.rows, wide, lddk, e},
+        sdv{dv, s.rows, s.C, lddv, e}, sdg{dgate, s.rows, d.Hv, lddg, 4}, sdb{dbeta, s.rows, d.Hv, lddb, 4},
+        ss = dense(states, ends * nb, 4), sdT = dense(dsT, ends, 4), sd0 = dense(ds0, ends, 4),
+        sws = dense(need ? workspace : nullptr, (int64_t)workspace_bytes, 1);
+    TRY(check_align({i.q, i.k, i.v, i.g, i.b, ss, sdy, sdT, sdq, sdk, sdv, sdg, sdb, sd0}));
+    TRY(check_steps({i.q, i.k, i.v, i.g, i.b, sdy, sdq, sdk, sdv, sdg, sdb}));
+    TRY(check_alias({sdq, sdk, sdv, sdg, sdb, sd0, sws}, {i.q, i.k, i.v, i.g, i.b, ss, sdy, sdT}));
+    return to_status(launch_delta_bwd(s, d, e == 2, in, states, Rows{dy, lddy}, dsT, RowsOut{dq, lddq}, RowsOut{dk, lddk},
+                                      RowsOut{dv, lddv}, RowsOut{dgate, lddg}, RowsOut{dbeta, lddb}, ds0, workspace,
+                                      (hipStream_t)stream));
+}
+
 conv_status_t conv_delta_step(const conv_seq_t *seq, const conv_delta_t *par, const void *q, int64_t ldq, const void *k,
                               int64_t ldk, const void *v, int64_t ldv, const float *gate, int64_t ldg, const float *beta,
                               int64_t ldb, float *S, void *y, int64_t ldy, void *stream) {

@@ -30,6 +30,9 @@ struct DeltaIn {
 size_t delta_fwd_workspace(const Seq &s, const Delta &d, bool bf16);      // bytes
 hipError_t launch_delta_fwd(const Seq &s, const Delta &d, bool bf16, const DeltaIn &in, const float *s0, RowsOut y, float *sT,
                             float *states, void *ws, hipStream_t st);
+size_t delta_bwd_workspace(const Seq &s, const Delta &d, bool bf16);
+hipError_t launch_delta_bwd(const Seq &s, const Delta &d, bool bf16, const DeltaIn &in, const float *states, Rows dy, const float *dsT,
+                            RowsOut dq, RowsOut dk, RowsOut dv, RowsOut dg, RowsOut dbeta, float *ds0, void *ws, hipStream_t st);
 hipError_t launch_delta_step(const Seq &s, const Delta &d, bool bf16, const DeltaIn &in, float *S, RowsOut y, hipStream_t st);
 
 }  // namespace convfwd

@@ -592,6 +592,24 @@ CONV_API conv_status_t conv_delta_fwd(const conv_seq_t *seq, const conv_delta_t 
                                       int64_t ldg, const float *beta, int64_t ldb, const float *s0, void *y, int64_t ldy,
                                       float *sT, float *states, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Device workspace of conv_delta_bwd; 0 where none is needed, or on invalid
+ * arguments. */
+CONV_API size_t conv_delta_bwd_workspace_bytes(const conv_seq_t *seq, const conv_delta_t *par);
+
+/* Gradients for upstream dy (of y) and dsT (of sT; NULL: zero): dq, dk, dv, dgate,
+ * dbeta, and ds0 (B, heads_v, dim_k, dim_v), or NULL.  states: as conv_delta_fwd saved
+ * them for the same inputs.  dq and dk are sums over the value heads that share a
+ * head, and with unit = 1 lead through the unit length.  With dS the total gradient of S, u = beta e and
+ * S' = exp(g) S[t-1], per token from the last to the first:
+ *     dS[t] += scale q dy^T,  dq = scale S[t] dy,  z = dS[t]^T k,  dbeta = z.e,  dv = beta z,
+ *     dk = dS[t] u - beta S' z,  dS' = dS[t] - beta k z^T,  dgate = <dS', S'>,  dS[t-1] = exp(g) dS' */
+CONV_API conv_status_t conv_delta_bwd(const conv_seq_t *seq, const conv_delta_t *par, const void *q, int64_t ldq,
+                                      const void *k, int64_t ldk, const void *v, int64_t ldv, const float *gate,
+                                      int64_t ldg, const float *beta, int64_t ldb, const float *states, const void *dy,
+                                      int64_t lddy, const float *dsT, void *dq, int64_t lddq, void *dk, int64_t lddk,
+                                      void *dv, int64_t lddv, float *dgate, int64_t lddg, float *dbeta, int64_t lddb,
+                                      float *ds0, void *workspace, size_t workspace_bytes, void *stream);
+
 /* One new token for each of B sequences: q, k, v, gate, beta and y are one row
  * for each; S (B, heads_v, dim_k, dim_v) is updated in place.  seq->T, offsets and
  * tokens are not read. */
