@@ -246,8 +246,9 @@ template <int PARTS> struct GradPages {
 };
 // Floats behind the pages.
 enum { kSizes = 0 /* 3 x 4 x 64: largest values of a token's U, Z, dY by slice */, kDots = 768 /* 5 x 4 x 64 */, kTotals = 2048 /* 2 x 64 */,
-       kScales = 2176 /* 4: of B1, B2, M1, M2 */, kKept = 2180 /* 4 */, kBack = 2184 /* 3 x 64: inverse scales of U, Z, dY */,
-       kSmall = 2376 };
+       kBack = 2176 /* 3 x 64: inverse scales of U, Z, dY */, kScales = 2368 /* 2 x 4: of B1, B2, M1, M2 by block of tokens */,
+       kKept = 2376 /* 4 */, kTop = 2380 /* 2 x 4: largest values of S and dS by slice */, kRec = 2388 /* the rows record */,
+       kSmall = kRec + kRowsFloats };
 
 // A token's dv or dk: four neighbouring values of a row, zeros past `left`.
 template <typename T, bool WIDE> __device__ __forceinline__ f4_t load4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left) {
@@ -283,18 +284,22 @@ struct GradOut {
     bool wide_k, wide_v, wide_s;
 };
 
+// Eight waves: in the first part waves 0..3 make U and waves 4..7 Z, of 32 columns of v each; in the second every wave has one of
+// B and M by i or by j, for one block of tokens; in the third waves 0..3 have dq and what k reads, waves 4..7 what it writes, of 32
+// rows of the state each.
 template <typename T, int DKB>
-__global__ __launch_bounds__(256) void delta_grad_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ v,
+__global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ v,
                                                          int64_t ldv, const T *__restrict__ dy, int64_t lddy,
                                                          const float *__restrict__ states, GradOut out) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2, F = 4 * DKB;
     typedef GradPages<PARTS> P;
     extern __shared__ __align__(1024) char lds[];
-    float *small = reinterpret_cast<float *>(lds + P::kAll * 1024);
+    float *small = reinterpret_cast<float *>(lds + P::kAll * 1024), *rows = small + kRec;
     const int64_t slot = blockIdx.x / d.H;
     const int hk = (int)(blockIdx.x % d.H);
-    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
+    const bool upper = wave >= 4;
     const Block at = find_block(s, ws.per, slot);
     int64_t first;
     int len;
@@ -302,254 +307,244 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(Seq s, Delta d, DeltaWs
     if (at.k < 0 || (int64_t)at.k * kBlock >= len) return;
     const int64_t r0 = first + (int64_t)at.k * kBlock;
     const int n = min(len - at.k * kBlock, kBlock);
-    const uint4 *qk = ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage + lane;
-    const auto global_page = [&](int i) { return __builtin_bit_cast(h8_t, qk[i * kPage]); };      // K, KT, Q, QT, PARTS * F each
+    const uint4 *qk = ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage;
+    const auto global_page = [&](int i) { return __builtin_bit_cast(h8_t, qk[i * kPage + lane]); };      // K, KT, Q, QT, PARTS * F each
     const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(lds + i * 1024 + lane * 16); };
     const auto put = [&](int i, const h8_t &p) { *reinterpret_cast<h8_t *>(lds + i * 1024 + lane * 16) = p; };
-    acc_t dq[2] = {zeros(), zeros()}, dk[2] = {zeros(), zeros()};        // summed over the value heads that share the key head
+    acc_t sum[2] = {zeros(), zeros()};                                  // dq or dk over the value heads that share the key head
     if (threadIdx.x < 128) small[kTotals + threadIdx.x] = 0.f;
 
     for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
         const int64_t rec = slot * d.Hv + hv;
-        const float *rows = ws.rows + rec * kRowsFloats;
-        const double *G = reinterpret_cast<const double *>(rows + 64 * kRowG);
-        const float gamma = rows[kGamma], invT = rows[kInvT], invP = rows[kInvP];
+        // addresses and pages that are the same for every value head: keep the compiler from making all of them in front of
+        // the loop, which takes a thousand registers
+        asm volatile("" : "+s"(qk), "+v"(lane));
+        const int half = lane >> 5, col = lane & 31;
+        for (int i = threadIdx.x; i < kRowsFloats; i += 512) rows[i] = ws.rows[rec * kRowsFloats + i];
         const uint4 *tri = ws.tri + rec * ws.tri_pages * kPage + lane;
         const auto tri_page = [&](int i) { return __builtin_bit_cast(h8_t, tri[i * kPage]); };   // T, TT, PT: hi then lo
         const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(rows + 64 * row + 32 * t + 8 * a + 4 * half); };
         const float *sp = states + (((int64_t)at.b * ((s.T + kBlock - 1) / kBlock) + at.k) * d.Hv + hv) * d.Dk * d.Dv;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(sp, 4 * d.Dk * d.Dv),
-                                     re = make_rsrc(ws.ends + rec * DKB * slices * 1024, DKB * slices * 4096),
-                                     rv = rows_buffer(v + r0 * ldv + hv * d.Dv, n, ldv, d.Dv),
-                                     rdy = rows_buffer(dy + r0 * lddy + hv * d.Dv, n, lddy, d.Dv);
+                                     re = make_rsrc(ws.ends + rec * DKB * slices * 1024, DKB * slices * 4096);
+        __syncthreads();
+        const float gamma = rows[kGamma], invT = rows[kInvT], invP = rows[kInvP];
 
-        // ---- a wave to 32 columns of v: U and Z, transposed (lane = token 32 t + col, registers = columns) ----
-        acc_t U[2] = {zeros(), zeros()}, Z[2] = {zeros(), zeros()};
+        // ---- U or Z, transposed: lane = token 32 t + col, registers = columns ----
+        acc_t U[2] = {zeros(), zeros()};
         f4_t dyr[2][4];
-        float zv[2] = {0.f, 0.f}, kept = 0.f;
-        if (wave < slices) {
-            const int c = 32 * wave + col;
+        float mu[2] = {}, mo[2] = {}, top = 0.f;
+        const auto first_part = [&](auto is_second) {
+            constexpr bool second = decltype(is_second)::value;
+            const int c = 32 * w + col;
             const uint32_t at_v = c < d.Dv ? (uint32_t)sizeof(T) * c : kOob;
-            acc_t S[DKB], E[DKB];
-            load_state<DKB>(rs, c < d.Dv ? 4 * c : kOob, 4 * d.Dv, half, S);
-            load_state<DKB>(re, 4 * c, 128 * slices, half, E);
-            float m = 0.f, me = 0.f;
+            const T *src = second ? dy + r0 * lddy + hv * d.Dv : v + r0 * ldv + hv * d.Dv;
+            const int64_t ld = second ? lddy : ldv;
+            const __amdgpu_buffer_rsrc_t rc = rows_buffer(src, n, ld, d.Dv);
+            acc_t X[2] = {zeros(), zeros()};
+            {   // K S or K dS
+                acc_t S[DKB];
+                if constexpr (second) load_state<DKB>(re, 4 * c, 128 * slices, half, S);
+                else load_state<DKB>(rs, c < d.Dv ? 4 * c : kOob, 4 * d.Dv, half, S);
 #pragma unroll
-            for (int i = 0; i < DKB; ++i) {
-                m = max_abs(S[i], m);
-                me = max_abs(E[i], me);
+                for (int i = 0; i < DKB; ++i) top = max_abs(S[i], top);
+                top = max_halves(top);
+                const float sc = pow2_scale(top), isc = pow2_inv(sc);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) kept = fmaf(S[i][r], E[i][r], kept);
-            }
-            kept *= gamma;
-            const float sc = pow2_scale(max_halves(m)), isc = pow2_inv(sc), se = pow2_scale(max_halves(me)), ise = pow2_inv(se);
-            acc_t X[2] = {zeros(), zeros()}, W[2] = {zeros(), zeros()};
+                for (int i = 0; i < 2 * DKB; ++i) {
+                    const Pair f = split8(sc, [&](int j) { return S[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
-            for (int i = 0; i < 2 * DKB; ++i) {
-                const Pair f = split8(sc, [&](int j) { return S[i >> 1][8 * (i & 1) + j]; });
-                const Pair g = split8(se, [&](int j) { return E[i >> 1][8 * (i & 1) + j]; });
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8_t kp = global_page(t * 2 * DKB + i);
-                    X[t] = mfma(kp, f.hi, X[t]);
-                    W[t] = mfma(kp, g.hi, W[t]);
-                    X[t] = mfma(kp, f.lo, X[t]);
-                    W[t] = mfma(kp, g.lo, W[t]);
-                    if constexpr (PARTS == 2) {
-                        const h8_t kl = global_page(F + t * 2 * DKB + i);
-                        X[t] = mfma(kl, f.hi, X[t]);
-                        W[t] = mfma(kl, g.hi, W[t]);
+                    for (int t = 0; t < 2; ++t) {
+                        const h8_t kp = global_page(t * 2 * DKB + i);
+                        X[t] = mfma(kp, f.hi, X[t]);
+                        X[t] = mfma(kp, f.lo, X[t]);
+                        if constexpr (PARTS == 2) X[t] = mfma(global_page(F + t * 2 * DKB + i), f.hi, X[t]);
                     }
                 }
-            }
-            // U = T R
-            Column<T> V;
-            V.load(rv, at_v, (uint32_t)(ldv * sizeof(T)), half);
-            m = 0.f;
+                if constexpr (!second) {                                          // <S, dS>
+                    float kept = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+                    for (int i = 0; i < DKB; ++i) {
+                        acc_t E[1];
+                        load_state<1>(re, 4 * c + i * 32 * 128 * slices, 128 * slices, half, E);
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const f4_t ek = factors(kRowEK, t, a), bt = factors(kRowBeta, t, a);
+                        for (int r = 0; r < 16; ++r) kept = fmaf(S[i][r], E[0][r], kept);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        X[t][4 * a + j] = bt[j] * fmaf(-(ek[j] * isc), X[t][4 * a + j], V.get(16 * t + 4 * a + j));
+                    for (int i = 1; i < 64; i <<= 1) kept += __shfl_xor(kept, i);
+                    if (lane == 0) small[kKept + w] = gamma * kept;
                 }
-                m = max_abs(X[t], m);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) X[t][r] *= isc;
             }
-            const float sr = pow2_scale(max_halves(m));
+            Column<T> V;
+            V.load(rc, at_v, (uint32_t)(ld * sizeof(T)), half);
+            float m = 0.f;
+            if constexpr (!second) {                                              // R = beta (V - E K S)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const f4_t ek = factors(kRowEK, t, a), bt = factors(kRowBeta, t, a);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            X[t][4 * a + j] = bt[j] * fmaf(-ek[j], X[t][4 * a + j], V.get(16 * t + 4 * a + j));
+                    }
+                    m = max_abs(X[t], m);
+                }
+            } else {                                                    // P^T dY + F K dS
+#pragma unroll
+                for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(V.get(i)));
+                const float so = pow2_scale(max_halves(m)), ip = pow2_inv(so) * invP;
+                acc_t Y[2] = {zeros(), zeros()};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Pair f;
+                    if constexpr (PARTS == 2) f = split8(so, [&](int j) { return V.get(8 * i + j); });
+                    else f.hi = half8(so, [&](int j) { return V.get(8 * i + j); });
+#pragma unroll
+                    for (int t = 0; t <= i >> 1; ++t) {
+                        const h8_t hi = tri_page(4 * kTriPages + high_page(t, i)), lo = tri_page(5 * kTriPages + high_page(t, i));
+                        Y[t] = mfma(hi, f.hi, Y[t]);
+                        Y[t] = mfma(lo, f.hi, Y[t]);
+                        if constexpr (PARTS == 2) Y[t] = mfma(hi, f.lo, Y[t]);
+                    }
+                }
+                m = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const f4_t fk = factors(kRowFK, t, a);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) X[t][4 * a + j] = fmaf(fk[j], X[t][4 * a + j], Y[t][4 * a + j] * ip);
+                    }
+                    m = max_abs(X[t], m);
+                }
+            }
+            // times T or T^T, transposed: the factor of a column differs from lane to lane before, from register to register behind
+            const float sx = pow2_scale(max_halves(m));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const Pair f = split8(sr, [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
+                const Pair f = split8(sx, [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
-                for (int t = i >> 1; t < 2; ++t) {
-                    const h8_t hi = tri_page(low_page(t, i)), lo = tri_page(kTriPages + low_page(t, i));
+                for (int t = 0; t < 2; ++t) {
+                    if (second ? t > i >> 1 : t < i >> 1) continue;
+                    const int p = second ? 2 * kTriPages + high_page(t, i) : low_page(t, i);
+                    const h8_t hi = tri_page(p), lo = tri_page(p + kTriPages);
                     U[t] = mfma(f.hi, hi, U[t]);
                     U[t] = mfma(f.lo, hi, U[t]);
                     U[t] = mfma(f.hi, lo, U[t]);
                 }
             }
-            // the factor of a column differs from lane to lane before, and from register to register now
-            float *table = small + kDots + wave * 64;
-            if (half == 0) table[col] = pow2_inv(sr) * invT;
-            // Z = T^T (P^T dY + F K dS)
-            V.load(rdy, at_v, (uint32_t)(lddy * sizeof(T)), half);
-            m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(V.get(i)));
-            const float so = pow2_scale(max_halves(m)), ip = pow2_inv(so) * invP;
-            acc_t Y[2] = {zeros(), zeros()};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Pair f;
-                if constexpr (PARTS == 2) f = split8(so, [&](int j) { return V.get(8 * i + j); });
-                else f.hi = half8(so, [&](int j) { return V.get(8 * i + j); });
-#pragma unroll
-                for (int t = 0; t <= i >> 1; ++t) {
-                    const h8_t hi = tri_page(4 * kTriPages + high_page(t, i)), lo = tri_page(5 * kTriPages + high_page(t, i));
-                    Y[t] = mfma(hi, f.hi, Y[t]);
-                    Y[t] = mfma(lo, f.hi, Y[t]);
-                    if constexpr (PARTS == 2) Y[t] = mfma(hi, f.lo, Y[t]);
-                }
-            }
-            m = 0.f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const f4_t fk = factors(kRowFK, t, a);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) W[t][4 * a + j] = fmaf(fk[j] * ise, W[t][4 * a + j], Y[t][4 * a + j] * ip);
-                }
-                m = max_abs(W[t], m);
-            }
-            const float sx = pow2_scale(max_halves(m));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Pair f = split8(sx, [&](int j) { return W[i >> 1][8 * (i & 1) + j]; });
-#pragma unroll
-                for (int t = 0; t <= i >> 1; ++t) {
-                    const h8_t hi = tri_page(2 * kTriPages + high_page(t, i)), lo = tri_page(3 * kTriPages + high_page(t, i));
-                    Z[t] = mfma(f.hi, hi, Z[t]);
-                    Z[t] = mfma(f.lo, hi, Z[t]);
-                    Z[t] = mfma(f.hi, lo, Z[t]);
-                }
-            }
-            if (half == 0) table[32 + col] = pow2_inv(sx) * invT;
+            float *table = small + kDots + wave * 32;
+            if (half == 0) table[col] = pow2_inv(sx) * invT;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const f4_t fu = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
-                const f4_t fz = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= fu[j], Z[t][4 * a + j] *= fz[j];
+                    for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= fu[j];
             }
-            // dv = beta Z, Z.v, and dY by token
-            const __amdgpu_buffer_rsrc_t rdv = rows_buffer((T *)out.dv.p + r0 * out.dv.ld + hv * d.Dv, n, out.dv.ld, d.Dv);
-            const auto rest = [&](auto aligned) {
-                constexpr bool W4 = decltype(aligned)::value;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int row = 32 * t + col, c0 = 32 * wave + 4 * half;
-                    const float bt = rows[64 * kRowBeta + row];
+            for (int t = 0; t < 2; ++t) mu[t] = max_halves(max_abs(U[t]));
+            if constexpr (second) {                                               // dv = beta Z, Z.v, and dY by token
+                const __amdgpu_buffer_rsrc_t rv = rows_buffer(v + r0 * ldv + hv * d.Dv, n, ldv, d.Dv),
+                                             rdv = rows_buffer((T *)out.dv.p + r0 * out.dv.ld + hv * d.Dv, n, out.dv.ld, d.Dv);
+                float zv[2] = {0.f, 0.f};
+                const auto rest = [&](auto aligned) {
+                    constexpr bool W4 = decltype(aligned)::value;
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        const int left = d.Dv - c0 - 8 * a;
-                        const uint32_t in_row = (c0 + 8 * a) * (uint32_t)sizeof(T);
-                        const f4_t vr = load4<T, W4>(rv, row * (uint32_t)(ldv * sizeof(T)) + in_row, left);
-                        dyr[t][a] = load4<T, W4>(rdy, row * (uint32_t)(lddy * sizeof(T)) + in_row, left);
-                        float o[4];
+                    for (int t = 0; t < 2; ++t) {
+                        const int row = 32 * t + col, c0 = 32 * w + 4 * half;
+                        const float bt = rows[64 * kRowBeta + row];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            zv[t] = fmaf(Z[t][4 * a + j], vr[j], zv[t]);
-                            o[j] = bt * Z[t][4 * a + j];
+                        for (int a = 0; a < 4; ++a) {
+                            const int left = d.Dv - c0 - 8 * a;
+                            const uint32_t in_row = (c0 + 8 * a) * (uint32_t)sizeof(T);
+                            const f4_t vr = load4<T, W4>(rv, row * (uint32_t)(ldv * sizeof(T)) + in_row, left);
+                            dyr[t][a] = load4<T, W4>(rc, row * (uint32_t)(lddy * sizeof(T)) + in_row, left);
+                            float o[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                zv[t] = fmaf(U[t][4 * a + j], vr[j], zv[t]);
+                                mo[t] = fmaxf(mo[t], fabsf(dyr[t][a][j]));
+                                o[j] = bt * U[t][4 * a + j];
+                            }
+                            store4<W4>(rdv, row * (uint32_t)(out.dv.ld * sizeof(T)) + in_row, left, o, (T *)nullptr);
                         }
-                        store4<W4>(rdv, row * (uint32_t)(out.dv.ld * sizeof(T)) + in_row, left, o, (T *)nullptr);
+                        mo[t] = max_halves(mo[t]);
+                        zv[t] += __shfl_xor(zv[t], 32);
                     }
-                }
-            };
-            if (out.wide_v) rest(std::true_type());
-            else rest(std::false_type());
-        }
-        // a token's largest values over all slices
-        {
-            float mu[2] = {}, mz[2] = {}, mo[2] = {};
-            if (wave < slices) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    mu[t] = max_halves(max_abs(U[t]));
-                    mz[t] = max_halves(max_abs(Z[t]));
-#pragma unroll
-                    for (int a = 0; a < 4; ++a)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mo[t] = fmaxf(mo[t], fabsf(dyr[t][a][j]));
-                    mo[t] = max_halves(mo[t]);
-                    zv[t] += __shfl_xor(zv[t], 32);
-                }
+                };
+                if (out.wide_v) rest(std::true_type());
+                else rest(std::false_type());
+                small[kDots + (4 * 4 + w) * 64 + lane] = half ? zv[1] : zv[0];
             }
-            kept = kept + __shfl_xor(kept, 32);
-#pragma unroll
-            for (int i = 1; i < 32; i <<= 1) kept += __shfl_xor(kept, i);
-            // the other half's lanes hold the same
-            const float m0 = half ? mu[1] : mu[0], m1 = half ? mz[1] : mz[0], m2 = half ? mo[1] : mo[0];
-            small[kSizes + (0 * 4 + wave) * 64 + lane] = m0;
-            small[kSizes + (1 * 4 + wave) * 64 + lane] = m1;
-            small[kSizes + (2 * 4 + wave) * 64 + lane] = m2;
-            __syncthreads();                                            // also: every wave is done with its table
-            small[kDots + (4 * 4 + wave) * 64 + lane] = half ? zv[1] : zv[0];
-            if (lane == 0) small[kKept + wave] = kept;
+        };
+        if (w < slices) {
+            if (upper) first_part(std::true_type());
+            else first_part(std::false_type());
+        } else if (upper) {
+            small[kDots + (4 * 4 + w) * 64 + lane] = 0.f;
         }
-        float back[3][2];                                               // inverse scales of a token's U, Z, dY
+        if (!upper && w >= slices && lane == 0) small[kKept + w] = 0.f;
+        // a token's largest values over all slices, and the states'
+        small[kSizes + ((upper ? 1 : 0) * 4 + w) * 64 + lane] = half ? mu[1] : mu[0];
+        if (upper) small[kSizes + (2 * 4 + w) * 64 + lane] = half ? mo[1] : mo[0];
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+        for (int i = 1; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
+        if (lane == 0) small[kTop + wave] = top;
+        __syncthreads();
+        const auto token_scale = [&](int q, int tok) {
+            const float *p = small + kSizes + q * 256 + tok;
+            return pow2_scale(fmaxf(fmaxf(p[0], p[64]), fmaxf(p[128], p[192])));
+        };
+        if (w < slices) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                float m = 0.f;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) m = fmaxf(m, small[kSizes + (q * 4 + w) * 64 + 32 * t + col]);
-                back[q][t] = pow2_scale(m);
-            }
-        if (wave < slices) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+                const float su = token_scale(upper ? 1 : 0, 32 * t + col), so = upper ? token_scale(2, 32 * t + col) : 0.f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int p = 8 * t + 2 * wave + u;
-                    const Pair a = split8(back[0][t], [&](int j) { return U[t][8 * u + j]; });
-                    const Pair z = split8(back[1][t], [&](int j) { return Z[t][8 * u + j]; });
-                    put(P::kU + p, a.hi), put(P::kU + 16 + p, a.lo);
-                    put(P::kZ + p, z.hi), put(P::kZ + 16 + p, z.lo);
-                    const Pair o = split8(back[2][t], [&](int j) { return dyr[t][2 * u + (j >> 2)][j & 3]; });
-                    put(P::kY + p, o.hi);
-                    if constexpr (PARTS == 2) put(P::kY + 16 + p, o.lo);
+                    const int p = (upper ? P::kZ : P::kU) + 8 * t + 2 * w + u;
+                    const Pair a = split8(su, [&](int j) { return U[t][8 * u + j]; });
+                    put(p, a.hi), put(p + 16, a.lo);
+                    if (upper) {
+                        const Pair o = split8(so, [&](int j) { return dyr[t][2 * u + (j >> 2)][j & 3]; });
+                        put(P::kY + 8 * t + 2 * w + u, o.hi);
+                        if constexpr (PARTS == 2) put(P::kY + 16 + 8 * t + 2 * w + u, o.lo);
+                    }
                 }
+            }
         }
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) back[q][t] = pow2_inv(back[q][t]);
-        if (wave == 0) {
-#pragma unroll
-            for (int q = 0; q < 3; ++q) small[kBack + 64 * q + lane] = half ? back[q][1] : back[q][0];
-        }
+        if (wave < 3) small[kBack + 64 * wave + lane] = pow2_inv(token_scale(wave, lane));
+        const float *tp = small + kTop;
+        const float ss = pow2_scale(fmaxf(fmaxf(tp[0], tp[1]), fmaxf(tp[2], tp[3]))), se = pow2_scale(fmaxf(fmaxf(tp[4], tp[5]), fmaxf(tp[6], tp[7])));
         __syncthreads();
 
-        // ---- B and M: wave 0 and 1 B, 2 and 3 M; the even ones with lane = i ----
-        {
-            const bool is_m = wave >= 2, by_i = !(wave & 1);
+        // ---- B and M ----
+        const auto second_part = [&](auto m_or_b, auto lane_is_i) {
+            // by i: lane = i, a block of i has one or two blocks of j
+            constexpr bool is_m = decltype(m_or_b)::value, by_i = decltype(lane_is_i)::value, two = is_m || PARTS == 2;
             const int pa = is_m ? P::kZ : P::kY;                        // rows i: Z or dY; rows j: U
-            acc_t C[3];
+            const double *G = reinterpret_cast<const double *>(rows + 64 * kRowG);
+            const int blocks = upper ? 1 : 2;                           // waves 0..3: the block of tokens with two partners
+            const int mine_b = by_i == upper ? 0 : 1;
+            acc_t C[2];
             float m = 0.f;
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                const int ib = q ? 1 : 0, jb = q == 2 ? 1 : 0;
+            for (int q = 0; q < 2; ++q) {
+                if (q >= blocks) break;
+                const int other_b = upper ? mine_b : q;
+                const int ib = by_i ? mine_b : other_b, jb = by_i ? other_b : mine_b;
                 acc_t x = zeros();
                 for (int u = 0; u < 2 * slices; ++u) {
                     const h8_t a = page(pa + 8 * ib + u), bh = page(P::kU + 8 * jb + u), bl = page(P::kU + 16 + 8 * jb + u);
                     h8_t al = {};
-                    const bool two = is_m || PARTS == 2;
                     if (two) al = page(pa + 16 + 8 * ib + u);
                     if (by_i) {
                         x = mfma(bh, a, x);
@@ -562,17 +557,18 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     }
                 }
                 // the lane's own token and its factors; the other index runs over the registers
-                const int mine = 32 * (by_i ? ib : jb) + col;
+                const int mine = 32 * mine_b + col;
                 const float inv_mine = small[kBack + 64 * (by_i ? (is_m ? 1 : 2) : 0) + mine];
                 const double g_mine = G[mine];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int other = 32 * (by_i ? jb : ib) + acc_row(r, half);
+                    const int other = 32 * other_b + acc_row(r, half);
                     const int i = by_i ? mine : other, j = by_i ? other : mine;
                     const bool in = is_m ? j < i : j <= i;
                     const float D = expf((float)(by_i ? g_mine - G[other] : G[other] - g_mine));
                     // what the contraction's index brings along: lane = i: keys j; lane = j: queries i, or beta and keys i
-                    float f = by_i ? rows[64 * kRowKK + other] : is_m ? rows[64 * kRowBeta + other] * rows[64 * kRowKK + other] : rows[64 * kRowKQ + other];
+                    float f = rows[64 * (by_i || is_m ? kRowKK : kRowKQ) + other];
+                    if (!by_i && is_m) f *= rows[64 * kRowBeta + other];
                     f *= is_m ? -D : d.scale * D;
                     const float inv_other = small[kBack + 64 * (by_i ? 0 : is_m ? 1 : 2) + other];
                     x[r] = in ? x[r] * (inv_mine * inv_other) * f : 0.f;
@@ -583,143 +579,144 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(Seq s, Delta d, DeltaWs
             const float sc = pow2_scale(max_wave(m));
             const int to = is_m ? (by_i ? P::kM1 : P::kM2) : (by_i ? P::kB1 : P::kB2);
 #pragma unroll
-            for (int q = 0; q < 3; ++q)
+            for (int q = 0; q < 2; ++q) {
+                if (q >= blocks) break;
+                const int other_b = upper ? mine_b : q;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int ib = q ? 1 : 0, jb = q == 2 ? 1 : 0;
-                    const int p = to + (by_i ? low_page(ib, 2 * jb + u) : high_page(jb, 2 * ib + u));
+                    const int p = to + (by_i ? low_page(mine_b, 2 * other_b + u) : high_page(mine_b, 2 * other_b + u));
                     const Pair f = split8(sc, [&](int j) { return C[q][8 * u + j]; });
                     put(p, f.hi);
                     put(kTriPages + p, f.lo);
                 }
-            if (lane == 0) small[kScales + wave] = pow2_inv(sc);
-        }
+            }
+            if (lane == 0) small[kScales + 4 * mine_b + w] = pow2_inv(sc);
+        };
+        if (w == 0) second_part(std::false_type(), std::true_type());
+        else if (w == 1) second_part(std::false_type(), std::false_type());
+        else if (w == 2) second_part(std::true_type(), std::true_type());
+        else second_part(std::true_type(), std::false_type());
         __syncthreads();
 
-        // ---- a wave to 32 rows of the state: dq, read and write, transposed (lane = token, registers = dk) ----
-        float dot[4][2] = {};
-        acc_t q1[2], wr[2], rd[2];
-        if (wave < DKB) {
-            // products with S and dS: rows of the state are the operand's rows, under one power of two
-            const int row = 32 * wave + col;
-            const auto state_pages = [&](__amdgpu_buffer_rsrc_t r, bool padded, f4_t(&f)[16]) {
-                const uint32_t ld = padded ? 128 * slices : 4 * d.Dv;
-                const int width = padded ? 32 * slices : d.Dv;
+        // ---- dq and read, or write, transposed: lane = token, registers = dk; the state's rows are the operand's ----
+        asm volatile("" : "+s"(qk));
+        float dot[2][2] = {};
+        acc_t A[2] = {zeros(), zeros()}, Bb[2] = {zeros(), zeros()};
+        const auto third_part = [&](auto is_second) {
+            constexpr bool second = decltype(is_second)::value;
+            const int row = 32 * w + col;
+            const __amdgpu_buffer_rsrc_t r = second ? re : rs;
+            const uint32_t ld = second ? 128 * slices : 4 * d.Dv;
+            const int width = second ? 32 * slices : d.Dv;
+            const float sc = second ? se : ss;
+            const auto with_state = [&](auto aligned) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {                          // columns 8 u + 4 half + 0..3
-                    if (u >= 4 * slices) {
-                        f[u] = f4_t{0.f, 0.f, 0.f, 0.f};
-                        continue;
+                for (int u = 0; u < 8; ++u) {
+                    if (u >= 2 * slices) break;
+                    const int c0 = 16 * u + 4 * half;
+                    const f4_t f0 = load4<float, decltype(aligned)::value>(r, row * ld + 4 * c0, width - c0);
+                    const f4_t f1 = load4<float, decltype(aligned)::value>(r, row * ld + 4 * c0 + 32, width - c0 - 8);
+                    const Pair a = split8(sc, [&](int j) { return j < 4 ? f0[j & 3] : f1[j & 3]; });
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if constexpr (second) {
+                            const h8_t uh = page(P::kU + 8 * t + u), ul = page(P::kU + 16 + 8 * t + u);
+                            A[t] = mfma(a.hi, uh, A[t]);
+                            A[t] = mfma(a.lo, uh, A[t]);
+                            A[t] = mfma(a.hi, ul, A[t]);
+                        } else {
+                            const h8_t o = page(P::kY + 8 * t + u), zh = page(P::kZ + 8 * t + u), zl = page(P::kZ + 16 + 8 * t + u);
+                            A[t] = mfma(a.hi, o, A[t]);
+                            Bb[t] = mfma(a.hi, zh, Bb[t]);
+                            A[t] = mfma(a.lo, o, A[t]);
+                            Bb[t] = mfma(a.lo, zh, Bb[t]);
+                            if constexpr (PARTS == 2) A[t] = mfma(a.hi, page(P::kY + 16 + 8 * t + u), A[t]);
+                            Bb[t] = mfma(a.hi, zl, Bb[t]);
+                        }
                     }
-                    const int c0 = 8 * u + 4 * half;
-                    if (padded || out.wide_s) f[u] = load4<float, true>(r, row * ld + 4 * c0, width - c0);
-                    else f[u] = load4<float, false>(r, row * ld + 4 * c0, width - c0);
                 }
-                float m = 0.f;
-#pragma unroll
-                for (int u = 0; u < 16; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(f[u][j]));
-                return pow2_scale(max_wave(m));
             };
-            f4_t f[16];
-            acc_t q0[2] = {zeros(), zeros()}, r0[2] = {zeros(), zeros()}, w0[2] = {zeros(), zeros()};
-            const float ss = state_pages(rs, false, f), iss = pow2_inv(ss);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (u >= 2 * slices) break;
-                const Pair a = split8(ss, [&](int j) { return f[2 * u + (j >> 2)][j & 3]; });
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8_t o = page(P::kY + 8 * t + u), zh = page(P::kZ + 8 * t + u), zl = page(P::kZ + 16 + 8 * t + u);
-                    q0[t] = mfma(a.hi, o, q0[t]);
-                    r0[t] = mfma(a.hi, zh, r0[t]);
-                    q0[t] = mfma(a.lo, o, q0[t]);
-                    r0[t] = mfma(a.lo, zh, r0[t]);
-                    if constexpr (PARTS == 2) q0[t] = mfma(a.hi, page(P::kY + 16 + 8 * t + u), q0[t]);
-                    r0[t] = mfma(a.hi, zl, r0[t]);
-                }
-            }
-            const float se = state_pages(re, true, f), ise = pow2_inv(se);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (u >= 2 * slices) break;
-                const Pair a = split8(se, [&](int j) { return f[2 * u + (j >> 2)][j & 3]; });
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8_t uh = page(P::kU + 8 * t + u), ul = page(P::kU + 16 + 8 * t + u);
-                    w0[t] = mfma(a.hi, uh, w0[t]);
-                    w0[t] = mfma(a.lo, uh, w0[t]);
-                    w0[t] = mfma(a.hi, ul, w0[t]);
-                }
-            }
+            if (second || out.wide_s) with_state(std::true_type());
+            else with_state(std::false_type());
             // products of keys and queries with B and M
-            acc_t bq[2] = {zeros(), zeros()}, bw[2] = {zeros(), zeros()}, mr[2] = {zeros(), zeros()}, mw[2] = {zeros(), zeros()};
+            acc_t p1[2] = {zeros(), zeros()}, p2[2] = {zeros(), zeros()};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const h8_t kt = global_page(PARTS * F + 4 * wave + u), qt = global_page(3 * PARTS * F + 4 * wave + u);
+                const h8_t kt = global_page(PARTS * F + 4 * w + u), qt = global_page((second ? 3 : 1) * PARTS * F + 4 * w + u);
                 h8_t kl = {}, ql = {};
-                if constexpr (PARTS == 2) kl = global_page((PARTS + 1) * F + 4 * wave + u), ql = global_page((3 * PARTS + 1) * F + 4 * wave + u);
+                if constexpr (PARTS == 2) kl = global_page((PARTS + 1) * F + 4 * w + u), ql = global_page(((second ? 3 : 1) * PARTS + 1) * F + 4 * w + u);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (t >= u >> 1) {
-                        const int p = low_page(t, u);
-                        const h8_t b = page(P::kB1 + p), c = page(P::kM1 + p);
-                        bq[t] = mfma(kt, b, bq[t]);
-                        mr[t] = mfma(kt, c, mr[t]);
-                        bq[t] = mfma(kt, page(P::kB1 + kTriPages + p), bq[t]);
-                        mr[t] = mfma(kt, page(P::kM1 + kTriPages + p), mr[t]);
-                        if constexpr (PARTS == 2) bq[t] = mfma(kl, b, bq[t]), mr[t] = mfma(kl, c, mr[t]);
-                    }
-                    if (t <= u >> 1) {
-                        const int p = high_page(t, u);
-                        const h8_t b = page(P::kB2 + p), c = page(P::kM2 + p);
-                        bw[t] = mfma(qt, b, bw[t]);
-                        mw[t] = mfma(kt, c, mw[t]);
-                        bw[t] = mfma(qt, page(P::kB2 + kTriPages + p), bw[t]);
-                        mw[t] = mfma(kt, page(P::kM2 + kTriPages + p), mw[t]);
-                        if constexpr (PARTS == 2) bw[t] = mfma(ql, b, bw[t]), mw[t] = mfma(kl, c, mw[t]);
-                    }
+                    if (second ? t > u >> 1 : t < u >> 1) continue;
+                    const int p = second ? high_page(t, u) : low_page(t, u);
+                    const int b0 = (second ? P::kB2 : P::kB1) + p, c0 = (second ? P::kM2 : P::kM1) + p;
+                    const h8_t b = page(b0), c = page(c0);
+                    p1[t] = mfma(qt, b, p1[t]);
+                    p2[t] = mfma(kt, c, p2[t]);
+                    p1[t] = mfma(qt, page(b0 + kTriPages), p1[t]);
+                    p2[t] = mfma(kt, page(c0 + kTriPages), p2[t]);
+                    if constexpr (PARTS == 2) p1[t] = mfma(ql, b, p1[t]), p2[t] = mfma(kl, c, p2[t]);
                 }
             }
-            const float i1 = small[kScales], i2 = small[kScales + 1], i3 = small[kScales + 2], i4 = small[kScales + 3];
+            const float iss = pow2_inv(sc);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 32 * t + col;
-                const float E = rows[64 * kRowE + tok], Fd = rows[64 * kRowF + tok], bt = rows[64 * kRowBeta + tok];
-                const float fq = d.scale * E * iss * small[kBack + 128 + tok], fr = -E * iss * small[kBack + 64 + tok],
-                            fw = Fd * ise * small[kBack + tok], kk = rows[64 * kRowKK + tok], kq = rows[64 * kRowKQ + tok];
+                const float i1 = small[kScales + 4 * t + (second ? 1 : 0)], i2 = small[kScales + 4 * t + (second ? 3 : 2)];
+                const float E = rows[64 * kRowE + tok], kk = rows[64 * kRowKK + tok], kq = rows[64 * kRowKQ + tok];
+                // waves 0..3: of dY S^T and of Z S^T; waves 4..7: of U dS^T
+                const float fa = second ? rows[64 * kRowF + tok] * iss * small[kBack + tok] : d.scale * E * iss * small[kBack + 128 + tok];
+                const float fb = -E * iss * small[kBack + 64 + tok];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     // the token's key and query: pages of this block of dk lie as the registers do
-                    const h8_t kh = global_page(t * 2 * DKB + 2 * wave + u), qh = global_page(2 * PARTS * F + t * 2 * DKB + 2 * wave + u);
+                    const int p = t * 2 * DKB + 2 * w + u;
+                    const h8_t kh = global_page(p), qh = global_page(2 * PARTS * F + p);
                     h8_t kl = {}, ql = {};
-                    if constexpr (PARTS == 2) kl = global_page(F + t * 2 * DKB + 2 * wave + u), ql = global_page((2 * PARTS + 1) * F + t * 2 * DKB + 2 * wave + u);
+                    if constexpr (PARTS == 2) kl = global_page(F + p), ql = global_page((2 * PARTS + 1) * F + p);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int r = 8 * u + j;
-                        const float kx = ((float)kh[j] + (float)kl[j]) * kk, qx = ((float)qh[j] + (float)ql[j]) * kq;
-                        const float w_state = w0[t][r] * fw;
-                        q1[t][r] = fmaf(q0[t][r], fq, bq[t][r] * i1);
-                        rd[t][r] = fmaf(r0[t][r], fr, mr[t][r] * i3);
-                        wr[t][r] = w_state + fmaf(bw[t][r], i2, mw[t][r] * i4);
-                        dot[0][t] = fmaf(qx, q1[t][r], dot[0][t]);
-                        dot[1][t] = fmaf(kx, rd[t][r], dot[1][t]);
-                        dot[2][t] = fmaf(kx, wr[t][r], dot[2][t]);
-                        dot[3][t] = fmaf(kx, w_state, dot[3][t]);
-                        dq[t][r] += q1[t][r];
-                        dk[t][r] += fmaf(bt, rd[t][r], wr[t][r]);
+                        const int q = 8 * u + j;
+                        const float kx = ((float)kh[j] + (float)kl[j]) * kk;
+                        if constexpr (second) {
+                            const float state = A[t][q] * fa;
+                            A[t][q] = state + fmaf(p1[t][q], i1, p2[t][q] * i2);
+                            dot[0][t] = fmaf(kx, A[t][q], dot[0][t]);
+                            dot[1][t] = fmaf(kx, state, dot[1][t]);
+                        } else {
+                            const float qx = ((float)qh[j] + (float)ql[j]) * kq;
+                            A[t][q] = fmaf(A[t][q], fa, p1[t][q] * i1);
+                            Bb[t][q] = fmaf(Bb[t][q], fb, p2[t][q] * i2);
+                            dot[0][t] = fmaf(qx, A[t][q], dot[0][t]);
+                            dot[1][t] = fmaf(kx, Bb[t][q], dot[1][t]);
+                        }
+                        sum[t][q] += A[t][q];
                     }
                 }
             }
+        };
+        if (w < DKB) {
+            if (upper) third_part(std::true_type());
+            else third_part(std::false_type());
         }
+        // dots: q.dq, k.read, k.write, k.(F U dS^T)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) dot[q][t] += __shfl_xor(dot[q][t], 32);
-            small[kDots + (q * 4 + wave) * 64 + lane] = half ? dot[q][1] : dot[q][0];
+            small[kDots + (((upper ? 2 : 0) + q) * 4 + w) * 64 + lane] = half ? dot[q][1] : dot[q][0];
         }
         __syncthreads();
+        // beta read goes to the waves that have write, in the place of the pages
+        float *pass = reinterpret_cast<float *>(lds) + w * 2048;
+        if (!upper && w < DKB) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float bt = rows[64 * kRowBeta + 32 * t + col];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) pass[(16 * t + q) * 64 + lane] = bt * Bb[t][q];
+            }
+        }
         if (wave == 0) {
             const auto total = [&](int q) {
                 const float *p = small + kDots + q * 256 + lane;
@@ -727,54 +724,65 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(Seq s, Delta d, DeltaWs
             };
             const float bt = rows[64 * kRowBeta + lane];
             const float t0 = total(0), t1 = total(1), t2 = total(2);
-            double run = (double)t0 + (double)bt * t1 - (double)t2, w = (double)total(3);
+            double run = (double)t0 + (double)bt * t1 - (double)t2, all = (double)total(3);
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
                 const double o = __shfl_down(run, m);
                 if (lane + m < 64) run += o;
-                w += __shfl_xor(w, m);
+                all += __shfl_xor(all, m);
             }
-            w += (double)((small[kKept] + small[kKept + 1]) + (small[kKept + 2] + small[kKept + 3]));
+            all += (double)((small[kKept] + small[kKept + 1]) + (small[kKept + 2] + small[kKept + 3]));
             if (lane < n) {
-                ((float *)out.dg.p)[(r0 + lane) * out.dg.ld + hv] = (float)(run + w);
+                ((float *)out.dg.p)[(r0 + lane) * out.dg.ld + hv] = (float)(run + all);
                 ((float *)out.db.p)[(r0 + lane) * out.db.ld + hv] = total(4) + t1;
             }
             small[kTotals + lane] += t0;
             small[kTotals + 64 + lane] += fmaf(bt, t1, t2);
         }
+        __syncthreads();
+        if (upper && w < DKB) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) sum[t][q] += pass[(16 * t + q) * 64 + lane];
+        }
         __syncthreads();                                                // the pages and floats are free for the next head
     }
     // through the unit length: x / |x| takes the part along x out of the gradient
-    if (wave < DKB) {
-        const float *rows = ws.rows + (slot * d.Hv + hk * d.group) * kRowsFloats;
-        const auto finish = [&](auto aligned, const RowsOut &o, acc_t(&g)[2], int which) {
-            const __amdgpu_buffer_rsrc_t r = rows_buffer((T *)o.p + r0 * o.ld + hk * d.Dk, n, o.ld, d.Dk);
+    const int half = lane >> 5, col = lane & 31;
+    if (w < DKB) {
+        const float *rec = ws.rows + (slot * d.Hv + hk * d.group) * kRowsFloats;
+        const RowsOut o = upper ? out.dk : out.dq;
+        const int base = upper ? 0 : 2 * PARTS * F;
+        const __amdgpu_buffer_rsrc_t r = rows_buffer((T *)o.p + r0 * o.ld + hk * d.Dk, n, o.ld, d.Dk);
+        const auto finish = [&](auto aligned) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 32 * t + col;
-                const float size = rows[64 * (which ? kRowSizeQ : kRowSizeK) + tok], kap = rows[64 * (which ? kRowKQ : kRowKK) + tok];
-                const float along = d.unit ? small[kTotals + (which ? 0 : 64) + tok] * kap : 0.f;
+                const float size = rec[64 * (upper ? kRowSizeK : kRowSizeQ) + tok], kap = rec[64 * (upper ? kRowKK : kRowKQ) + tok];
+                const float along = d.unit ? small[kTotals + (upper ? 64 : 0) + tok] * kap : 0.f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const h8_t hi = global_page((which ? 2 * PARTS * F : 0) + t * 2 * DKB + 2 * wave + u);
+                    const int p = base + t * 2 * DKB + 2 * w + u;
+                    const h8_t hi = global_page(p);
                     h8_t lo = {};
-                    if constexpr (PARTS == 2) lo = global_page(((which ? 2 * PARTS : 0) + 1) * F + t * 2 * DKB + 2 * wave + u);
+                    if constexpr (PARTS == 2) lo = global_page(p + F);
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         float f[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float x = (float)hi[4 * a + j] + (float)lo[4 * a + j];
-                            f[j] = size * (d.unit ? fmaf(-along, x, g[t][8 * u + 4 * a + j]) : g[t][8 * u + 4 * a + j]);
+                            f[j] = size * (d.unit ? fmaf(-along, x, sum[t][8 * u + 4 * a + j]) : sum[t][8 * u + 4 * a + j]);
                         }
-                        const int c0 = 32 * wave + 16 * u + 8 * a + 4 * half;
+                        const int c0 = 32 * w + 16 * u + 8 * a + 4 * half;
                         store4<decltype(aligned)::value>(r, tok * (uint32_t)(o.ld * sizeof(T)) + c0 * (uint32_t)sizeof(T), d.Dk - c0, f, (T *)nullptr);
                     }
                 }
             }
         };
-        if (out.wide_k) finish(std::true_type(), out.dq, dq, 1), finish(std::true_type(), out.dk, dk, 0);
-        else finish(std::false_type(), out.dq, dq, 1), finish(std::false_type(), out.dk, dk, 0);
+        if (out.wide_k) finish(std::true_type());
+        else finish(std::false_type());
     }
 }
 
@@ -806,7 +814,7 @@ hipError_t bwd(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &i
     bytes = GradPages<PARTS>::kAll * 1024 + kSmall * 4;
     e = hipFuncSetAttribute((const void *)delta_grad_kernel<T, DKB>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    delta_grad_kernel<T, DKB><<<(unsigned)(ws.blocks * d.H), 256, bytes, st>>>(s, d, ws, slices, (const T *)in.v.p, in.v.ld,
+    delta_grad_kernel<T, DKB><<<(unsigned)(ws.blocks * d.H), 512, bytes, st>>>(s, d, ws, slices, (const T *)in.v.p, in.v.ld,
                                                                               (const T *)dy.p, dy.ld, states, out);
     return hipGetLastError();
 }
