@@ -102,6 +102,8 @@ struct DeltaWs {
     uint4 *tri;              // per block and value head, forward: T hi, T lo, P hi, P lo; backward: T, TT, PT, hi and lo
     float *rows;             // per block and value head: kRowsFloats
     float *ends;             // backward: gradients of the states behind the blocks, dk x dv padded to 32s
+    float *sums;             // per sequence, value head and segment: what a segment makes of a state, dk x (dv + dk) padded to 32s
+    int segments, seg_blocks;
     int qk_pages, tri_pages;
     int per;                 // blocks of each of equal sequences
     int64_t blocks;
@@ -110,6 +112,16 @@ struct DeltaWs {
 // The parts in `base`; returns the bytes they take.
 int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *base, DeltaWs &ws);
 void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, hipStream_t st);
+
+// The joining of segments; `back`: of gradients, from the last segment to the first.
+hipError_t launch_delta_join(const Seq &s, const Delta &d, const DeltaWs &ws, bool back, hipStream_t st);
+
+// Waves of a workgroup share the pages in LDS; fewer to a workgroup where that leaves compute units empty.
+inline int waves_of(int64_t chains, int slices) {
+    int waves = slices < 4 ? slices : 4;
+    while (waves > 1 && chains * ((slices + waves - 1) / waves) < 256) waves = (waves + 1) / 2;
+    return waves;
+}
 
 // First block number of sequence b, and block n's place.
 __device__ __forceinline__ int64_t first_block(const Seq &s, int per, int b, int64_t first) {

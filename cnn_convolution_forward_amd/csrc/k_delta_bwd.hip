@@ -35,7 +35,8 @@ template <int DKB, int PARTS> struct ChainPages {
     static constexpr int kBuffers = 2 * kAll <= 156 ? 2 : 1;
 };
 
-template <typename T, int DKB>
+// SUM: what a segment makes of a gradient behind it, as in the forward pass.
+template <typename T, int DKB, bool SUM>
 __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ dy,
                                                           int64_t lddy, const float *__restrict__ dsT, float *__restrict__ ds0) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
@@ -44,7 +45,9 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads);
-    const int slice = (int)(blockIdx.x / heads) * waves + wave;
+    // segments from the last on, which only here ends where its sequence does
+    const int runs = SUM ? ws.segments - 1 : ws.segments, seg = (int)(blockIdx.x / heads) % runs + (SUM ? 1 : 0);
+    const int slice = (int)(blockIdx.x / heads) / runs * waves + wave;
     const int b = bh / d.Hv, hv = bh % d.Hv, hk = hv / d.group;
     const int c = slice * 32 + col;
     const uint32_t at_s = c < d.Dv ? 4 * c : kOob, at_v = c < d.Dv ? (uint32_t)sizeof(T) * c : kOob;
@@ -53,15 +56,28 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
     int64_t first;
     int len;
     seq_range(s, b, first, len);
-    const int blocks = (len + kBlock - 1) / kBlock;
+    const int all = (len + kBlock - 1) / kBlock, begin = seg * ws.seg_blocks, blocks = min(all, begin + ws.seg_blocks);
+    if (seg > 0 && begin >= all) return;
     const int64_t slot0 = first_block(s, ws.per, b, first);
     const int state = d.Dk * d.Dv;
     const uint32_t lds0 = lds_address(lds);
+    const uint32_t ld_m = 128 * (slices + DKB), at_m = 4 * c;
+    const int size = 32 * DKB * 32 * (slices + DKB);
+    float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
 
     acc_t S[DKB];
 #pragma unroll
     for (int i = 0; i < DKB; ++i) S[i] = zeros();
-    if (dsT) load_state<DKB>(make_rsrc(dsT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    if (SUM && slice >= slices) {
+#pragma unroll
+        for (int i = 0; i < DKB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[i][r] = 32 * i + acc_row(r, half) == c - 32 * slices ? 1.f : 0.f;
+    } else if (blocks == all) {
+        if (dsT) load_state<DKB>(make_rsrc(dsT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    } else if (!SUM) {
+        load_state<DKB>(make_rsrc(sums + size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
+    }
 
     const auto fetch = [&](int k) {
         const uint32_t buf = lds0 + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
@@ -72,10 +88,10 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
         copy_pages<P::kTri>(ws.tri + (rec * ws.tri_pages + 2 * kTriPages) * kPage, buf + (P::kK + P::kQT) * 1024, wave, waves, lane);
         if (wave == waves - 1) copy1((const uint4 *)(ws.rows + rec * kRowsFloats), buf + (P::kAll - 1) * 1024, 16 * lane);
     };
-    if (blocks > 0) fetch(blocks - 1);
+    if (begin < blocks) fetch(blocks - 1);
     wait_copies();
 
-    for (int k = blocks - 1; k >= 0; --k) {
+    for (int k = blocks - 1; k >= begin; --k) {
         __syncthreads();
         const char *buf = lds + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
         const int n = min(len - k * kBlock, kBlock);
@@ -87,7 +103,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
         const float *fac = reinterpret_cast<const float *>(buf + (P::kAll - 1) * 1024);
         const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(fac + 64 * row + 32 * t + 8 * a + 4 * half); };
-        store_state<DKB>(make_rsrc(ws.ends + at * DKB * slices * 1024, DKB * slices * 4096), at_e, ld_e, half, S);
+        if constexpr (!SUM) store_state<DKB>(make_rsrc(ws.ends + at * DKB * slices * 1024, DKB * slices * 4096), at_e, ld_e, half, S);
 
         // K dS; as in the forward pass, pages are read a step ahead of their products
         constexpr int kTT = P::kK + P::kQT, kPT = kTT + 2 * kTriPages;
@@ -125,7 +141,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
         for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(dY.get(i)));
         const float so = pow2_scale(max_halves(m));
-        if (P::kBuffers == 2 && k > 0) fetch(k - 1);
+        if (P::kBuffers == 2 && k > begin) fetch(k - 1);
         acc_t W[2] = {zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -227,13 +243,17 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
             for (int r = 0; r < 16; ++r) S[i][r] = fmaf(a[r] + e[r], isw, gamma * S[i][r]);
         }
-        if (P::kBuffers == 1 && k > 0) {
+        if (P::kBuffers == 1 && k > begin) {
             __syncthreads();                                           // every wave is done with the pages
             fetch(k - 1);
         }
         wait_copies();
     }
-    if (ds0) store_state<DKB>(make_rsrc(ds0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    if constexpr (SUM) {
+        store_state<DKB>(make_rsrc(sums, 4 * size), slice < slices + DKB ? at_m : kOob, ld_m, half, S);
+        return;
+    }
+    if (ds0 && seg == 0) store_state<DKB>(make_rsrc(ds0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
 }
 
 // ---- the gradients of a block ----
@@ -796,22 +816,31 @@ void fill(const Seq &s, const RowsOut &o, int cols, int esize, hipStream_t st) {
     delta_fill_kernel<<<f.blocks, 256, 0, st>>>(s, f);
 }
 
+template <typename T, int DKB, bool SUM>
+hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, Rows dy, const float *dsT, float *ds0, hipStream_t st) {
+    typedef ChainPages<DKB, sizeof(T) == 2 ? 1 : 2> P;
+    const int slices = (d.Dv + 31) / 32, columns = slices + (SUM ? DKB : 0);
+    const int64_t chains = (int64_t)s.B * d.Hv * (SUM ? ws.segments - 1 : ws.segments);
+    const int waves = waves_of(chains, columns), bytes = P::kBuffers * P::kAll * 1024;
+    const hipError_t e = hipFuncSetAttribute((const void *)delta_chain_kernel<T, DKB, SUM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    delta_chain_kernel<T, DKB, SUM><<<(unsigned)(chains * ((columns + waves - 1) / waves)), 64 * waves, bytes, st>>>(
+        s, d, ws, slices, (const T *)dy.p, dy.ld, dsT, ds0);
+    return hipGetLastError();
+}
+
 template <typename T, int DKB>
 hipError_t bwd(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, const float *states, Rows dy, const float *dsT,
                const GradOut &out, float *ds0, hipStream_t st) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    typedef ChainPages<DKB, PARTS> P;
     const int slices = (d.Dv + 31) / 32;
-    const int64_t heads = (int64_t)s.B * d.Hv;
-    int waves = slices;
-    while (waves > 1 && heads * ((slices + waves - 1) / waves) < 256) waves = (waves + 1) / 2;
-    int bytes = P::kBuffers * P::kAll * 1024;
-    hipError_t e = hipFuncSetAttribute((const void *)delta_chain_kernel<T, DKB>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    delta_chain_kernel<T, DKB><<<(unsigned)(heads * ((slices + waves - 1) / waves)), 64 * waves, bytes, st>>>(
-        s, d, ws, slices, (const T *)dy.p, dy.ld, dsT, ds0);
-    if ((e = hipGetLastError()) != hipSuccess || ws.blocks == 0) return e;
-    bytes = GradPages<PARTS>::kAll * 1024 + kSmall * 4;
+    hipError_t e;
+    if (ws.segments > 1) {
+        if ((e = chain<T, DKB, true>(s, d, ws, dy, dsT, ds0, st)) != hipSuccess) return e;
+        if ((e = launch_delta_join(s, d, ws, true, st)) != hipSuccess) return e;
+    }
+    if ((e = chain<T, DKB, false>(s, d, ws, dy, dsT, ds0, st)) != hipSuccess || ws.blocks == 0) return e;
+    const int bytes = GradPages<PARTS>::kAll * 1024 + kSmall * 4;
     e = hipFuncSetAttribute((const void *)delta_grad_kernel<T, DKB>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     delta_grad_kernel<T, DKB><<<(unsigned)(ws.blocks * d.H), 512, bytes, st>>>(s, d, ws, slices, (const T *)in.v.p, in.v.ld,

@@ -20,43 +20,61 @@
 namespace convfwd {
 namespace {
 
-template <int DKB, int PARTS> struct FwdPages {
+// SUM: without y, for what a segment makes of a state.
+template <int DKB, int PARTS, bool SUM> struct FwdPages {
     static constexpr int F = 4 * DKB;                   // pages of one part of K, KT or Q
-    static constexpr int kQK = 3 * PARTS * F;
-    static constexpr int kTri = 2 * kTriPages + PARTS * kTriPages;      // T hi and lo; of P, lo only where y has 24 bits
+    static constexpr int kQK = (SUM ? 2 : 3) * PARTS * F;
+    static constexpr int kTri = (2 + (SUM ? 0 : PARTS)) * kTriPages;    // T hi and lo; of P, lo only where y has 24 bits
     static constexpr int kAll = kQK + kTri + 1;         // and a page of the rows' factors
     static constexpr int kBuffers = 2 * kAll <= 156 ? 2 : 1;
 };
 
-template <typename T, int DKB>
+template <typename T, int DKB, bool SUM>
 __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ v,
                                                         int64_t ldv, const float *__restrict__ s0, T *__restrict__ y,
                                                         int64_t ldy, bool wide, float *__restrict__ sT,
                                                         float *__restrict__ states) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    typedef FwdPages<DKB, PARTS> P;
+    typedef FwdPages<DKB, PARTS, SUM> P;
     extern __shared__ __align__(1024) char lds[];
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     float *table = reinterpret_cast<float *>(lds + P::kBuffers * P::kAll * 1024) + wave * 64;      // two factors for each column
     const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads);
-    const int slice = (int)(blockIdx.x / heads) * waves + wave;
+    const int runs = SUM ? ws.segments - 1 : ws.segments, seg = (int)(blockIdx.x / heads) % runs;
+    const int slice = (int)(blockIdx.x / heads) / runs * waves + wave;
     const int b = bh / d.Hv, hv = bh % d.Hv, hk = hv / d.group;
-    const int c = slice * 32 + col;                                    // columns past the last are zeros and not stored
+    // columns past the last are zeros and not stored; SUM: behind v's 32 slices columns those of the matrix, which start as the identity
+    const int c = slice * 32 + col;
     const uint32_t at_s = c < d.Dv ? 4 * c : kOob, at_v = c < d.Dv ? (uint32_t)sizeof(T) * c : kOob;
     const uint32_t ld_s = 4 * d.Dv, ld_v = (uint32_t)(ldv * sizeof(T)), ld_y = (uint32_t)(ldy * sizeof(T));
     int64_t first;
     int len;
     seq_range(s, b, first, len);
-    const int blocks = (len + kBlock - 1) / kBlock;
+    const int all = (len + kBlock - 1) / kBlock, begin = seg * ws.seg_blocks, blocks = min(all, begin + ws.seg_blocks);
+    if (seg > 0 && begin >= all) return;                               // an empty sequence has its first segment
+    if (SUM && blocks == all) return;                                  // nothing follows the last one
     const int64_t slot0 = first_block(s, ws.per, b, first);
     const int state = d.Dk * d.Dv;
     const uint32_t lds0 = lds_address(lds);
+    // in front of a later segment, the state that joining left in the place of the last one's offset
+    const uint32_t ld_m = 128 * (slices + DKB), at_m = 4 * c;
+    const int size = 32 * DKB * 32 * (slices + DKB);
+    float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
 
     acc_t S[DKB];
 #pragma unroll
     for (int i = 0; i < DKB; ++i) S[i] = zeros();
-    if (s0) load_state<DKB>(make_rsrc(s0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    if (SUM && slice >= slices) {
+#pragma unroll
+        for (int i = 0; i < DKB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[i][r] = 32 * i + acc_row(r, half) == c - 32 * slices ? 1.f : 0.f;
+    } else if (seg == 0) {
+        if (s0) load_state<DKB>(make_rsrc(s0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    } else if (!SUM) {
+        load_state<DKB>(make_rsrc(sums - size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
+    }
 
     const auto fetch = [&](int k) {
         const uint32_t buf = lds0 + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
@@ -65,10 +83,10 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         copy_pages<P::kTri>(ws.tri + rec * ws.tri_pages * kPage, buf + P::kQK * 1024, wave, waves, lane);
         if (wave == waves - 1) copy1((const uint4 *)(ws.rows + rec * kRowsFloats), buf + (P::kAll - 1) * 1024, 16 * lane);
     };
-    if (blocks > 0) fetch(0);
+    if (begin < blocks) fetch(begin);
     wait_copies();
 
-    for (int k = 0; k < blocks; ++k) {
+    for (int k = begin; k < blocks; ++k) {
         // Every wave's part of the pages is there; every wave is done with the other buffer.
         __syncthreads();
         const char *buf = lds + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
@@ -80,7 +98,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
         const float *fac = reinterpret_cast<const float *>(buf + (P::kAll - 1) * 1024);
         const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(fac + 64 * row + 32 * t + 8 * a + 4 * half); };
-        if (states)
+        if (!SUM && states)
             store_state<DKB>(make_rsrc(states + (((int64_t)b * ((s.T + kBlock - 1) / kBlock) + k) * d.Hv + hv) * state, 4 * state), at_s,
                              ld_s, half, S);
 
@@ -97,7 +115,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
             for (int u = 0; u < 2 * PARTS; ++u) {
                 kp[i & 1][u] = page((u >> 1) * P::F + (u & 1) * 2 * DKB + i);
-                qp[i & 1][u] = page(kQ + (u >> 1) * P::F + (u & 1) * 2 * DKB + i);
+                if constexpr (!SUM) qp[i & 1][u] = page(kQ + (u >> 1) * P::F + (u & 1) * 2 * DKB + i);
             }
         };
         read_kq(0);
@@ -118,15 +136,17 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 X[t] = mfma(kp[i & 1][t], f.hi, X[t]);
-                Y[t] = mfma(f.hi, qp[i & 1][t], Y[t]);
+                if constexpr (!SUM) Y[t] = mfma(f.hi, qp[i & 1][t], Y[t]);
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 X[t] = mfma(kp[i & 1][t], f.lo, X[t]);
                 if constexpr (PARTS == 2) {
                     X[t] = mfma(kp[i & 1][2 + t], f.hi, X[t]);
-                    Y[t] = mfma(f.lo, qp[i & 1][t], Y[t]);
-                    Y[t] = mfma(f.hi, qp[i & 1][2 + t], Y[t]);
+                    if constexpr (!SUM) {
+                        Y[t] = mfma(f.lo, qp[i & 1][t], Y[t]);
+                        Y[t] = mfma(f.hi, qp[i & 1][2 + t], Y[t]);
+                    }
                 }
             }
         }
@@ -154,7 +174,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
         for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
 #pragma unroll
-        for (int u = 0; u < PARTS * kTriPages; ++u) low[u] = page(kP + u);
+        for (int u = 0; u < (SUM ? 0 : PARTS * kTriPages); ++u) low[u] = page(kP + u);
         read_kt(0, kt);
         __builtin_amdgcn_sched_barrier(0);
         // U = T beta R
@@ -180,7 +200,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= iu, W[t][4 * a + j] = U[t][4 * a + j] * fk[t][a][j];
             }
-            m = max_abs(U[t], m);
+            if constexpr (!SUM) m = max_abs(U[t], m);
             mw = max_abs(W[t], mw);
         }
         const float su = pow2_scale(max_halves(m)), sw = pow2_scale(max_halves(mw)), isw = pow2_inv(sw);
@@ -203,7 +223,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             }
             // every page of U in one of the DKB steps
 #pragma unroll
-            for (int q = i; q < 4; q += DKB) {
+            for (int q = i; q < (SUM ? 0 : 4); q += DKB) {
                 Pair f;
                 if constexpr (PARTS == 2) f = split8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
                 else f.hi = half8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
@@ -225,6 +245,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             fetch(k + 1);
         }
         wait_copies();                                                 // in front of y's stores, which take longer
+        if constexpr (SUM) continue;
         // y: a lane has token 32 t + col, columns 8 a + 4 half + 0..3 of the slice.  The factors of columns come from the lanes
         // that made them, through LDS (within the wave: the hardware keeps LDS accesses of a wave in order).
         if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su) * invP;
@@ -250,28 +271,39 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         else write(std::false_type());
         __builtin_amdgcn_wave_barrier();
     }
-    if (sT) store_state<DKB>(make_rsrc(sT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
+    if constexpr (SUM) {
+        store_state<DKB>(make_rsrc(sums, 4 * size), slice < slices + DKB ? at_m : kOob, ld_m, half, S);
+        return;
+    }
+    if (sT && blocks == all) store_state<DKB>(make_rsrc(sT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
 }
 
 // Rows of y that no sequence holds.
 template <typename T> __global__ __launch_bounds__(256) void delta_fill_kernel(Seq s, Fill f) { fill_rows(s, f, blockIdx.x, gridDim.x); }
 
+template <typename T, int DKB, bool SUM>
+hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, const float *s0, RowsOut y, float *sT,
+                 float *states, hipStream_t st) {
+    typedef FwdPages<DKB, sizeof(T) == 2 ? 1 : 2, SUM> P;
+    const int slices = (d.Dv + 31) / 32, columns = slices + (SUM ? DKB : 0);
+    const int64_t chains = (int64_t)s.B * d.Hv * (SUM ? ws.segments - 1 : ws.segments);
+    const int waves = waves_of(chains, columns);
+    const int bytes = P::kBuffers * P::kAll * 1024 + waves * 256;
+    const hipError_t e = hipFuncSetAttribute((const void *)delta_fwd_kernel<T, DKB, SUM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    delta_fwd_kernel<T, DKB, SUM><<<(unsigned)(chains * ((columns + waves - 1) / waves)), 64 * waves, bytes, st>>>(
+        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, wide_rows<T>(y.p, y.ld, d.Dv), sT, states);
+    return hipGetLastError();
+}
+
 template <typename T, int DKB>
 hipError_t fwd(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, const float *s0, RowsOut y, float *sT,
                float *states, hipStream_t st) {
-    constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    typedef FwdPages<DKB, PARTS> P;
-    const int slices = (d.Dv + 31) / 32;
-    const int64_t heads = (int64_t)s.B * d.Hv;
-    // Waves of a workgroup share the pages in LDS; fewer to a workgroup where that leaves compute units empty.
-    int waves = slices;
-    while (waves > 1 && heads * ((slices + waves - 1) / waves) < 256) waves = (waves + 1) / 2;
-    const int bytes = P::kBuffers * P::kAll * 1024 + waves * 256;
-    const hipError_t e = hipFuncSetAttribute((const void *)delta_fwd_kernel<T, DKB>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    delta_fwd_kernel<T, DKB><<<(unsigned)(heads * ((slices + waves - 1) / waves)), 64 * waves, bytes, st>>>(
-        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, wide_rows<T>(y.p, y.ld, d.Dv), sT, states);
-    return hipGetLastError();
+    if (ws.segments > 1) {
+        hipError_t e = chain<T, DKB, true>(s, d, ws, in, s0, y, sT, states, st);
+        if (e != hipSuccess || (e = launch_delta_join(s, d, ws, false, st)) != hipSuccess) return e;
+    }
+    return chain<T, DKB, false>(s, d, ws, in, s0, y, sT, states, st);
 }
 
 template <typename T>

@@ -316,7 +316,90 @@ void prep(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, hi
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
+// Segments of a sequence: its chain of blocks is cut where there are too few chains to fill the chip's 1024 SIMDs with a wave
+// each.  What a segment makes of any state is a matrix and an offset, found by running it from the identity and from zero
+// (twice the columns); the segments are joined one after another, and run again from their states.  That is
+// three times the work over n times the waves: from four segments on it pays (one sequence of 32768 tokens in 8 heads of 128:
+// NNN us instead of 2638), and a segment has at least four blocks.
+void cut(const Seq &s, const Delta &d, DeltaWs &ws) {
+    const int blocks = (s.T + kBlock - 1) / kBlock, slices = (d.Dv + 31) / 32;
+    const int64_t waves = (int64_t)s.B * d.Hv * slices;
+    const int n = (int)std::min<int64_t>(1024 / waves, blocks / 4);
+    ws.segments = 1, ws.seg_blocks = std::max(blocks, 1);
+    if (n < 4) return;
+    ws.seg_blocks = (blocks + n - 1) / n;
+    ws.segments = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
+}
+
+// S' = M S + N from segment to segment, a wave to 32 columns: S in registers, M the other operand.  N makes way for S'.
+template <int DKB>
+__global__ __launch_bounds__(64) void delta_join_kernel(Seq s, Delta d, DeltaWs ws, int slices, bool back) {
+    const int lane = threadIdx.x, half = lane >> 5, col = lane & 31;
+    const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads), slice = (int)(blockIdx.x / heads);
+    int64_t first;
+    int len;
+    seq_range(s, bh / d.Hv, first, len);
+    const int blocks = (len + kBlock - 1) / kBlock, n = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
+    const int ld = 32 * (slices + DKB), size = 32 * DKB * ld;
+    float *base = ws.sums + (int64_t)bh * ws.segments * size;
+    const uint32_t at = 4 * (32 * slice + col);
+    if (n < 3) return;
+    acc_t S[DKB], N[DKB];
+    load_state<DKB>(make_rsrc(base + (back ? (int64_t)(n - 1) * size : 0), 4 * size), at, 4 * ld, half, S);
+    for (int i = 1; i < n - 1; ++i) {
+        float *seg = base + (int64_t)(back ? n - 1 - i : i) * size;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(seg, 4 * size);
+        load_state<DKB>(r, at, 4 * ld, half, N);
+        float m = 0.f;
+#pragma unroll
+        for (int q = 0; q < DKB; ++q) m = max_abs(S[q], m);
+        const float sc = pow2_scale(max_halves(m)), isc = pow2_inv(sc);
+        Pair f[2 * DKB];
+#pragma unroll
+        for (int u = 0; u < 2 * DKB; ++u) f[u] = split8(sc, [&](int j) { return S[u >> 1][8 * (u & 1) + j]; });
+#pragma unroll
+        for (int q = 0; q < DKB; ++q) {
+            // 32 rows of M, under one power of two
+            f4_t row[4 * DKB];
+            const float *p = seg + (int64_t)(32 * q + col) * ld + 32 * slices + 4 * half;
+            m = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4 * DKB; ++u) {
+                row[u] = *reinterpret_cast<const f4_t *>(p + 8 * u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(row[u][j]));
+            }
+#pragma unroll
+            for (int u = 1; u < 64; u <<= 1) m = fmaxf(m, __shfl_xor(m, u));
+            const float sm = pow2_scale(m), im = pow2_inv(sm);
+            acc_t a = zeros(), b = zeros();
+#pragma unroll
+            for (int u = 0; u < 2 * DKB; ++u) {
+                const Pair w = split8(sm, [&](int j) { return row[2 * u + (j >> 2)][j & 3]; });
+                a = mfma(w.hi, f[u].hi, a);
+                b = mfma(w.hi, f[u].lo, b);
+                b = mfma(w.lo, f[u].hi, b);
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) S[q][x] = fmaf((a[x] + b[x]) * im, isc, N[q][x]);
+        }
+        store_state<DKB>(r, at, 4 * ld, half, S);
+    }
+}
+
 }  // namespace
+
+hipError_t launch_delta_join(const Seq &s, const Delta &d, const DeltaWs &ws, bool back, hipStream_t st) {
+    const int slices = (d.Dv + 31) / 32;
+    const unsigned grid = (unsigned)(s.B * d.Hv * slices);
+    switch ((d.Dk + 31) / 32) {
+    case 1: delta_join_kernel<1><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
+    case 2: delta_join_kernel<2><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
+    case 3: delta_join_kernel<3><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
+    default: delta_join_kernel<4><<<grid, 64, 0, st>>>(s, d, ws, slices, back);
+    }
+    return hipGetLastError();
+}
 
 int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *base, DeltaWs &ws) {
     const int dkb = (d.Dk + 31) / 32, dvb = (d.Dv + 31) / 32;
@@ -335,6 +418,8 @@ int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *ba
     ws.tri = (uint4 *)take(ws.blocks * d.Hv * ws.tri_pages * 1024);
     ws.rows = (float *)take(ws.blocks * d.Hv * kRowsFloats * 4);
     ws.ends = bwd ? (float *)take(ws.blocks * d.Hv * dkb * dvb * 4096) : nullptr;
+    cut(s, d, ws);
+    ws.sums = ws.segments > 1 ? (float *)take((int64_t)s.B * d.Hv * ws.segments * dkb * (dkb + dvb) * 4096) : nullptr;
     return at;
 }
 

@@ -22,7 +22,11 @@ namespace convfwd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 512;        // workgroups of the backward pass, each with a row of partial sums
+// Workgroups that walk through the rows.  Backward, each has a row of partial sums: 256 of them are enough to fill the chip
+// with wide rows (16384 x 2048 bf16: 39.4 us, with 512 43.8), narrow ones have shorter sums and want more waves (131072 x 128:
+// 24.2 us with 512, 31.2 with 256).  Forward: 25.4 us at 768, 27.2 at 1024, 66 with a workgroup for every four rows.
+constexpr int kMaxForward = 768;
+constexpr int max_backward(int G) { return G == 16 ? 512 : 256; }
 
 template <int G> __device__ __forceinline__ float group_sum(float v, float *red, int &phase) {
 #pragma unroll
@@ -40,14 +44,14 @@ template <int G> __device__ __forceinline__ float group_sum(float v, float *red,
 }
 
 // NV packs of VEC channels: pack i of thread li is at channel (i G + li) VEC.  Channels past C are zeros.
-template <typename T, int VEC, int NV, int G> struct RowRegs {
+template <typename T, int VEC, int NV, int G, bool ONCE> struct RowRegs {
     typename Pack<T, VEC>::type v[NV];
     __device__ __forceinline__ void load(const T *p, int li, int C) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * G + li) * VEC;
             if (c + VEC <= C) {
-                v[i] = load_pack<T, VEC>(p + c);
+                v[i] = ONCE ? load_once<T, VEC>(p + c) : load_pack<T, VEC>(p + c);
             } else {
                 T t[VEC];
 #pragma unroll
@@ -82,15 +86,24 @@ __device__ __forceinline__ void store_row(T *p, int li, int C, const float (&f)[
 template <int VEC, int NV, int G>
 __device__ __forceinline__ void load_param(const float *p, float other, int li, int C, float (&f)[NV][VEC]) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * G + li) * VEC;
+        if (p && c + VEC <= C) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (i * G + li) * VEC + j;
-            f[i][j] = p && c < C ? p[c] : other;
+            for (int j = 0; j < VEC; j += 4) {
+                float t[4];
+                load_f32<float, 4>(p + c + j, t);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) f[i][j + q] = t[q];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[i][j] = p && c + j < C ? p[c + j] : other;
         }
+    }
 }
 
-template <typename T, int VEC, int NV, int G>
+template <typename T, int VEC, int NV, int G, bool ONCE>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(int64_t rows, int C, float eps, const T *__restrict__ x,
                                                             int64_t ldx, const float *__restrict__ w,
                                                             const float *__restrict__ b, T *__restrict__ y, int64_t ldy,
@@ -102,13 +115,13 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(int64_t rows, int C,
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
     float wf[NV][VEC], bf[NV][VEC];
-    RowRegs<T, VEC, NV, G> next;
+    RowRegs<T, VEC, NV, G, ONCE> next;
     if (r < rows) next.load(x + r * ldx, li, C);
     load_param<VEC, NV, G>(w, 1.f, li, C, wf);
     load_param<VEC, NV, G>(b, 0.f, li, C, bf);
     const float inv = 1.f / (float)C;
     for (; r < rows; r += step) {
-        const RowRegs<T, VEC, NV, G> now = next;
+        const RowRegs<T, VEC, NV, G, ONCE> now = next;
         if (r + step < rows) next.load(x + (r + step) * ldx, li, C);
         float f[NV][VEC];
         now.get(f);
@@ -170,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_wide_kernel(int64_t rows, i
 }
 
 // part: per workgroup C sums of dy xh, then C sums of dy; NULL: not wanted.
-template <typename T, int VEC, int NV, int G>
+template <typename T, int VEC, int NV, int G, bool ONCE>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C, const T *__restrict__ x, int64_t ldx,
                                                             const float *__restrict__ w, const float *__restrict__ mean,
                                                             const float *__restrict__ rstd, const T *__restrict__ dy,
@@ -184,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + gi;
     float wf[NV][VEC], dw[NV][VEC], db[NV][VEC];
-    RowRegs<T, VEC, NV, G> nx, ny;
+    RowRegs<T, VEC, NV, G, ONCE> nx, ny;
     float nm = 0.f, nk = 0.f;
     if (r < rows) {
         nx.load(x + r * ldx, li, C);
@@ -198,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
         for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.f;
     const float inv = 1.f / (float)C;
     for (; r < rows; r += step) {
-        const RowRegs<T, VEC, NV, G> cx = nx, cy = ny;
+        const RowRegs<T, VEC, NV, G, ONCE> cx = nx, cy = ny;
         const float m = nm, k = nk;
         if (r + step < rows) {
             nx.load(x + (r + step) * ldx, li, C);
@@ -295,19 +308,21 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(int64_t rows, i
     }
 }
 
-// dw and db from the workgroups' sums: 32 columns to a workgroup, eight threads to a column.
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float *__restrict__ part, int blocks, int C,
-                                                       float *__restrict__ dw, float *__restrict__ db) {
-    __shared__ float sums[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+// dw and db from the workgroups' sums: 32 columns to a workgroup, 32 threads to a column.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict__ part, int blocks, int C,
+                                                        float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float sums[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float s = 0.f;
-    if (c < 2 * C)
-        for (int i = y; i < blocks; i += 8) s += part[(int64_t)i * 2 * C + c];
-    sums[y][threadIdx.x & 31] = s;
+    if (c < 2 * C) {
+#pragma unroll 4
+        for (int i = y; i < blocks; i += 32) s += part[(int64_t)i * 2 * C + c];
+    }
+    sums[y][x] = s;
     __syncthreads();
     if (y || c >= 2 * C) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sums[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += sums[i][x];
     float *out = c < C ? dw : db;
     if (out) out[c < C ? c : c - C] = s;
 }
@@ -359,21 +374,22 @@ hipError_t launch_norm_fwd(int64_t rows, int C, bool bf16, float eps, const void
     return pick(C, bf16, [&](auto *t, auto g, auto n) {
         typedef std::remove_pointer_t<decltype(t)> T;
         constexpr int G = decltype(g)::value, NV = decltype(n)::value, VEC = sizeof(T) == 2 ? 8 : 4;
-        const int blocks = blocks_of(rows, C, bf16, 2048);
+        const int blocks = blocks_of(rows, C, bf16, kMaxForward);
         if constexpr (G)
-            norm_fwd_kernel<T, VEC, NV, G><<<blocks, kThreads, 0, st>>>(rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
+            (read_once(x, ldx, sizeof(T)) ? norm_fwd_kernel<T, VEC, NV, G, true> : norm_fwd_kernel<T, VEC, NV, G, false>)<<<blocks, kThreads, 0, st>>>(
+                rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
         else
             norm_fwd_wide_kernel<T><<<blocks, kThreads, 0, st>>>(rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
         return hipGetLastError();
     });
 }
 
-int64_t norm_bwd_workspace_floats(int64_t rows, int C, bool bf16) { return 2 * (int64_t)C * blocks_of(rows, C, bf16, kMaxBlocks); }
+int64_t norm_bwd_workspace_floats(int64_t rows, int C, bool bf16) { return 2 * (int64_t)C * blocks_of(rows, C, bf16, max_backward(split_of(C, bf16).G)); }
 
 hipError_t launch_norm_bwd(int64_t rows, int C, bool bf16, const void *x, int64_t ldx, const float *w, const float *mean,
                            const float *rstd, const void *dy, int64_t lddy, void *dx, int64_t lddx, float *dw, float *db,
                            float *part, hipStream_t st) {
-    const int blocks = blocks_of(rows, C, bf16, kMaxBlocks);
+    const int blocks = blocks_of(rows, C, bf16, max_backward(split_of(C, bf16).G));
     if (!dw && !db) part = nullptr;
     hipError_t e = hipSuccess;
     if (rows > 0)
@@ -381,15 +397,16 @@ hipError_t launch_norm_bwd(int64_t rows, int C, bool bf16, const void *x, int64_
             typedef std::remove_pointer_t<decltype(t)> T;
             constexpr int G = decltype(g)::value, NV = decltype(n)::value, VEC = sizeof(T) == 2 ? 8 : 4;
             if constexpr (G)
-                norm_bwd_kernel<T, VEC, NV, G><<<blocks, kThreads, 0, st>>>(rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy,
-                                                                            lddy, (T *)dx, lddx, part);
+                (read_once(x, ldx, sizeof(T)) && read_once(dy, lddy, sizeof(T)) ? norm_bwd_kernel<T, VEC, NV, G, true>
+                                                                          : norm_bwd_kernel<T, VEC, NV, G, false>)<<<blocks, kThreads, 0, st>>>(
+                rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy, lddy, (T *)dx, lddx, part);
             else
                 norm_bwd_wide_kernel<T><<<blocks, kThreads, 0, st>>>(rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy, lddy,
                                                                      (T *)dx, lddx, part);
             return hipGetLastError();
         });
     if (e != hipSuccess || (!dw && !db)) return e;
-    norm_sum_kernel<<<(2 * C + 31) / 32, 256, 0, st>>>(part, blocks, C, dw, db);
+    norm_sum_kernel<<<(2 * C + 31) / 32, 1024, 0, st>>>(part, blocks, C, dw, db);
     return hipGetLastError();
 }
 

@@ -131,7 +131,7 @@ def _cols(e):
     return np.sqrt((e * e).sum(0))
 
 
-def forward_bounds(q, k, v, g, beta, hist, scale, ku, half):
+def forward_bounds(q, k, v, g, beta, hist, scale, ku, half, grow=1.0):
     """Bounds of y (L, dv), and of S in front of every block and after the last token (blocks + 1, dv): the 2-norm of the
     error of a column.  q and k as used, ku their relative error; half: products for y take one fp16 number."""
     L = len(q)
@@ -148,11 +148,11 @@ def forward_bounds(q, k, v, g, beta, hist, scale, ku, half):
         end = p.last * S + (p.F * p.k).T @ U
         # y takes S after each token, whose columns are off by no more than those in front of the block
         ey[r] = y.e + abs(scale) * np.sqrt((q[r] ** 2).sum(1))[:, None] * es[-1]
-        es.append(es[-1] + _cols(end.e))
+        es.append(es[-1] + grow * _cols(end.e))
     return ey, np.array(es)
 
 
-def backward_bounds(q, k, v, g, beta, hist, behind, scale, dy, dsT, ku, f, on):
+def backward_bounds(q, k, v, g, beta, hist, behind, scale, dy, dsT, ku, f, on, grow=1.0):
     """Bounds of (dq, dk, dv, dg, dbeta) and of the columns of ds0 (2-norm); dq and dk as through_unit leaves them."""
     L, dk_, dv_ = len(q), q.shape[1], v.shape[1]
     eq, ek, ev, eg, eb = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v), np.zeros(L), np.zeros(L)
@@ -189,7 +189,7 @@ def backward_bounds(q, k, v, g, beta, hist, behind, scale, dy, dsT, ku, f, on):
         ev[r] = (p.beta * Z).e + np.abs(beta[r])[:, None] * kn[:, None] * ec
         eb[r] = db.e[:, 0] + kn * (np.abs(e) @ ec)
         eg[r] = dg.e[:, 0] + np.sqrt((before ** 2).sum(1)) @ ec
-        ec = ec + _cols(d0.e)
+        ec = ec + grow * _cols(d0.e)
 
     def back(e, x, d, f):
         if not on:

@@ -99,6 +99,7 @@ class Case:
 def _whole(c, s0=True):
     """Forward and backward against the reference; returns what the calls returned."""
     n = c.off[-1]
+    grow = 2 * c.dk ** 0.5 if max(c.lens) > 1000 else 1.0        # sequences that may be run in segments
     s0 = c.s0 if s0 else None
     y = c.like(c.v)
     out = tuple(c.like(t) for t in c.data())
@@ -113,7 +114,7 @@ def _whole(c, s0=True):
     for i, h, hk, r, q, k, v, g, b, fq, fk in c.sequences():
         at = "sequence %d head %d" % (i, h)
         ref, hist = R.forward(q, k, v, g, b, s0v[i, h], c.scale)
-        ey, es = R.forward_bounds(q, k, v, g, b, hist, c.scale, c.ku(), c.half)
+        ey, es = R.forward_bounds(q, k, v, g, b, hist, c.scale, c.ku(), c.half, grow)
         _check(yv[r, h], ref, ey, c.half, "y of " + at)
         for t in range(0, len(q), 64):
             assert np.all(np.abs(stv[i, t // 64, h] - hist[t]) <= es[t // 64] + 2.0 ** -23 * np.abs(hist[t])), "state %d of %s" % (t, at)
@@ -122,7 +123,7 @@ def _whole(c, s0=True):
         _, hist = R.forward(q, k, v, g, b, stv[i, 0, h] if len(q) else s0v[i, h], c.scale)
         (dq, dk, dv, dg, db, d0), behind = R.backward(q, k, v, g, b, hist, c.scale, dyv[r, h], dsv[i, h])
         if len(q):
-            eq, ek, ev, eg, eb, ec, back = R.backward_bounds(q, k, v, g, b, hist, behind, c.scale, dyv[r, h], dsv[i, h], c.ku(), None, c.unit)
+            eq, ek, ev, eg, eb, ec, back = R.backward_bounds(q, k, v, g, b, hist, behind, c.scale, dyv[r, h], dsv[i, h], c.ku(), None, c.unit, grow)
             # a saved state is off by its own bound, and what is made of it in its block by as much as a gradient of it says
             more = np.repeat(es[:-1], 64, 0)[:len(q)]
             kn, on = np.sqrt((k * k).sum(1)), np.sqrt((q * q).sum(1))
@@ -170,6 +171,17 @@ CASES = [
 @pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
 def test_delta_rule(case):
     _whole(Case(*case))
+
+
+@pytest.mark.parametrize("case", [("bf16", [1100], 1, 1, 32, 32, False, True, 0), ("bf16", [64 * 40, 0, 700, 1, 64 * 16, 1300], 1, 2, 33, 40, True, True, 3),
+                                  ("f32", [64 * 16] * 2, 1, 2, 24, 72, False, True, 0), ("f32", [1500, 64 * 5, 64 * 6 + 1], 2, 2, 96, 20, True, False, 0)],
+                         ids=["0", "1", "2", "3"])
+def test_sequences_in_segments(case):
+    """Long sequences of few heads are cut into segments that run at once."""
+    c = Case(*case, g=lambda r, s: -np.exp(r.uniform(-9, -2, s)))
+    got = _whole(c)
+    again = B.delta_rule(*c.data(), s0=c.s0, with_states=True, **c.opts())
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
 def test_no_first_state():
