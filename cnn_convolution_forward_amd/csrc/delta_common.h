@@ -29,6 +29,10 @@ typedef float acc_t __attribute__((ext_vector_type(16)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = 64;                    // tokens
+constexpr double kLog2eD = 1.4426950408889634074;
+
+// exp of a difference of cumulative log decays, both times log2(e).
+__device__ __forceinline__ float decay_of(double gi, double gj) { return __builtin_amdgcn_exp2f((float)(gi - gj)); }
 constexpr int kPage = 64;                     // uint4s of a page
 
 __host__ __device__ constexpr int page_at(int m, int h, int s) { return 16 * m + (s < 4 ? 4 * h + s : 4 + 4 * h + s); }
@@ -86,7 +90,7 @@ __device__ __forceinline__ float max_abs(const acc_t &v, float m = 0.f) {
 __device__ __forceinline__ float max_halves(float m) { return fmaxf(m, __shfl_xor(m, 32)); }
 
 // Rows record of a block and value head: 64 floats each, then scalars.  The first four fill a page.
-enum { kRowEK, kRowBeta, kRowFK, kRowEQ, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ, kRowG /* doubles */, kRowG2, kRowCount };
+enum { kRowEK, kRowBeta, kRowFK, kRowEQ, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ, kRowG /* doubles, times log2(e) */, kRowG2, kRowCount };
 enum { kGamma = 64 * kRowCount, kInvT, kInvP };
 constexpr int kRowsFloats = 64 * kRowCount + 64;
 
@@ -205,29 +209,55 @@ template <int DKB> __device__ __forceinline__ void store_state(__amdgpu_buffer_r
     for (int i = 0; i < 16 * DKB; ++i) store_at(r, base + (32 * (i >> 4) + acc_row(i & 15, 0)) * ld, S[i >> 4][i & 15]);
 }
 
-// Four neighbouring columns of a row, of which `left` are the head's.  WIDE: rows and columns are aligned to four.
-template <bool WIDE> __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left, const float (&f)[4], uint16_t *) {
-    if constexpr (WIDE) {
+// Four neighbouring columns of a row where all four are the head's, of which `left` are; else zeros.  The address need only
+// be aligned to an element.
+template <typename T> __device__ __forceinline__ f4_t load4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left) {
+    f4_t f;
+    const int o = left >= 4 ? (int)off : (int)kOob;
+    if constexpr (sizeof(T) == 2) {
         typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
-        const u2_t v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
-        __builtin_amdgcn_raw_buffer_store_b64(v, r, left > 0 ? (int)off : (int)kOob, 0, 0);
+        const u2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0);
+        f[0] = __uint_as_float(v[0] << 16), f[1] = __uint_as_float(v[0] & 0xffff0000u);
+        f[2] = __uint_as_float(v[1] << 16), f[3] = __uint_as_float(v[1] & 0xffff0000u);
     } else {
+        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(f[j]), r, left > j ? (int)off + 2 * j : (int)kOob, 0, 0);
+        for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[j]);
     }
+    return f;
 }
-template <bool WIDE> __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left, const float (&f)[4], float *) {
-    if constexpr (WIDE) {
-        const u32x4_t v = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, left > 0 ? (int)off : (int)kOob, 0, 0);
-    } else {
+// The last columns of a head whose width is no multiple of four, one by one (a wide load that passes the buffer's end is dropped
+// whole); zeros where `left` is 4 or more, or none.
+template <typename T> __device__ __forceinline__ f4_t load_rest(__amdgpu_buffer_rsrc_t r, uint32_t off, int left) {
+    f4_t f = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) store_at(r, left > j ? off + 4 * j : kOob, f[j]);
+    for (int j = 0; j < 3; ++j) {
+        const int e = left < 4 && left > j ? (int)off + j * (int)sizeof(T) : (int)kOob;
+        if constexpr (sizeof(T) == 2) f[j] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, e, 0, 0) << 16);
+        else f[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, e, 0, 0));
     }
+    return f;
 }
-// Rows of heads of `dim` whose groups of four columns are aligned.
-template <typename T> bool wide_rows(const void *p, int64_t ld, int dim) {
-    return dim % 4 == 0 && ld % 4 == 0 && (uintptr_t)p % (4 * sizeof(T)) == 0;
+__device__ __forceinline__ void store_wide(__amdgpu_buffer_rsrc_t r, int off, const float (&f)[4], uint16_t *) {
+    typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+    const u2_t v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0);
+}
+__device__ __forceinline__ void store_wide(__amdgpu_buffer_rsrc_t r, int off, const float (&f)[4], float *) {
+    const u32x4_t v = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
+// The same for storing.  ragged: the width of heads is no multiple of four.
+template <typename T> __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left, bool ragged, const float (&f)[4], T *kind) {
+    store_wide(r, left >= 4 ? (int)off : (int)kOob, f, kind);
+    if (ragged) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int o = left < 4 && left > j ? (int)off + j * (int)sizeof(T) : (int)kOob;
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(f[j]), r, o, 0, 0);
+            else store_at(r, o, f[j]);
+        }
+    }
 }
 
 }  // namespace convfwd

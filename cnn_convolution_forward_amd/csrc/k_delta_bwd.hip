@@ -258,40 +258,19 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 
 // ---- the gradients of a block ----
 
-// Pages in LDS: U and Z (lane = token, places = columns of v, hi and lo), dY (the same), and the 64x64 matrices B and M,
+// Pages in LDS.  First, in the place of dY, B and M: K (lane = token), T, TT and PT.  Then U and Z (lane = token, places = columns of v, hi and lo), dY (the same), and the 64x64 matrices B and M,
 // each as lane = i, places = j and as lane = j, places = i.
 template <int PARTS> struct GradPages {
     static constexpr int kU = 0, kZ = 32, kY = 64, kB1 = kY + 16 * PARTS, kB2 = kB1 + 2 * kTriPages, kM1 = kB2 + 2 * kTriPages,
                          kM2 = kM1 + 2 * kTriPages, kAll = kM2 + 2 * kTriPages;
+    static constexpr int kK = kY, kTri = kK + 16 * PARTS, kTT = kTri + 2 * kTriPages, kPT = kTT + 2 * kTriPages;
+    static_assert(kPT + 2 * kTriPages <= kAll, "fits");
 };
 // Floats behind the pages.
 enum { kSizes = 0 /* 3 x 4 x 64: largest values of a token's U, Z, dY by slice */, kDots = 768 /* 5 x 4 x 64 */, kTotals = 2048 /* 2 x 64 */,
        kBack = 2176 /* 3 x 64: inverse scales of U, Z, dY */, kScales = 2368 /* 2 x 4: of B1, B2, M1, M2 by block of tokens */,
        kKept = 2376 /* 4 */, kTop = 2380 /* 2 x 4: largest values of S and dS by slice */, kRec = 2388 /* the rows record */,
        kSmall = kRec + kRowsFloats };
-
-// A token's dv or dk: four neighbouring values of a row, zeros past `left`.
-template <typename T, bool WIDE> __device__ __forceinline__ f4_t load4(__amdgpu_buffer_rsrc_t r, uint32_t off, int left) {
-    f4_t f;
-    if constexpr (WIDE && sizeof(T) == 2) {
-        typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
-        const u2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, left > 0 ? (int)off : (int)kOob, 0, 0);
-        f[0] = __uint_as_float(v[0] << 16), f[1] = __uint_as_float(v[0] & 0xffff0000u);
-        f[2] = __uint_as_float(v[1] << 16), f[3] = __uint_as_float(v[1] & 0xffff0000u);
-    } else if constexpr (WIDE) {
-        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, left > 0 ? (int)off : (int)kOob, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int o = left > j ? (int)off + j * (int)sizeof(T) : (int)kOob;
-            if constexpr (sizeof(T) == 2) f[j] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0) << 16);
-            else f[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
-        }
-    }
-    return f;
-}
 
 __device__ __forceinline__ float max_wave(float m) {
 #pragma unroll
@@ -301,7 +280,6 @@ __device__ __forceinline__ float max_wave(float m) {
 
 struct GradOut {
     RowsOut dq, dk, dv, dg, db;
-    bool wide_k, wide_v, wide_s;
 };
 
 // Eight waves: in the first part waves 0..3 make U and waves 4..7 Z, of 32 columns of v each; in the second every wave has one of
@@ -340,13 +318,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
         // the loop, which takes a thousand registers
         asm volatile("" : "+s"(qk), "+v"(lane));
         const int half = lane >> 5, col = lane & 31;
+        copy_pages<PARTS * F>(qk, lds_address(lds) + P::kK * 1024, wave, 8, lane);
+        copy_pages<6 * kTriPages>(ws.tri + rec * ws.tri_pages * kPage, lds_address(lds) + P::kTri * 1024, wave, 8, lane);
         for (int i = threadIdx.x; i < kRowsFloats; i += 512) rows[i] = ws.rows[rec * kRowsFloats + i];
-        const uint4 *tri = ws.tri + rec * ws.tri_pages * kPage + lane;
-        const auto tri_page = [&](int i) { return __builtin_bit_cast(h8_t, tri[i * kPage]); };   // T, TT, PT: hi then lo
         const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(rows + 64 * row + 32 * t + 8 * a + 4 * half); };
         const float *sp = states + (((int64_t)at.b * ((s.T + kBlock - 1) / kBlock) + at.k) * d.Hv + hv) * d.Dk * d.Dv;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(sp, 4 * d.Dk * d.Dv),
                                      re = make_rsrc(ws.ends + rec * DKB * slices * 1024, DKB * slices * 4096);
+        wait_copies();
         __syncthreads();
         const float gamma = rows[kGamma], invT = rows[kInvT], invP = rows[kInvP];
 
@@ -375,10 +354,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     const Pair f = split8(sc, [&](int j) { return S[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const h8_t kp = global_page(t * 2 * DKB + i);
+                        const h8_t kp = page(P::kK + t * 2 * DKB + i);
                         X[t] = mfma(kp, f.hi, X[t]);
                         X[t] = mfma(kp, f.lo, X[t]);
-                        if constexpr (PARTS == 2) X[t] = mfma(global_page(F + t * 2 * DKB + i), f.hi, X[t]);
+                        if constexpr (PARTS == 2) X[t] = mfma(page(P::kK + F + t * 2 * DKB + i), f.hi, X[t]);
                     }
                 }
                 if constexpr (!second) {                                          // <S, dS>
@@ -426,7 +405,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     else f.hi = half8(so, [&](int j) { return V.get(8 * i + j); });
 #pragma unroll
                     for (int t = 0; t <= i >> 1; ++t) {
-                        const h8_t hi = tri_page(4 * kTriPages + high_page(t, i)), lo = tri_page(5 * kTriPages + high_page(t, i));
+                        const h8_t hi = page(P::kPT + high_page(t, i)), lo = page(P::kPT + kTriPages + high_page(t, i));
                         Y[t] = mfma(hi, f.hi, Y[t]);
                         Y[t] = mfma(lo, f.hi, Y[t]);
                         if constexpr (PARTS == 2) Y[t] = mfma(hi, f.lo, Y[t]);
@@ -452,8 +431,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (second ? t > i >> 1 : t < i >> 1) continue;
-                    const int p = second ? 2 * kTriPages + high_page(t, i) : low_page(t, i);
-                    const h8_t hi = tri_page(p), lo = tri_page(p + kTriPages);
+                    const int p = second ? P::kTT + high_page(t, i) : P::kTri + low_page(t, i);
+                    const h8_t hi = page(p), lo = page(p + kTriPages);
                     U[t] = mfma(f.hi, hi, U[t]);
                     U[t] = mfma(f.lo, hi, U[t]);
                     U[t] = mfma(f.hi, lo, U[t]);
@@ -476,33 +455,45 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 const __amdgpu_buffer_rsrc_t rv = rows_buffer(v + r0 * ldv + hv * d.Dv, n, ldv, d.Dv),
                                              rdv = rows_buffer((T *)out.dv.p + r0 * out.dv.ld + hv * d.Dv, n, out.dv.ld, d.Dv);
                 float zv[2] = {0.f, 0.f};
-                const auto rest = [&](auto aligned) {
-                    constexpr bool W4 = decltype(aligned)::value;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int row = 32 * t + col, c0 = 32 * w + 4 * half;
-                        const float bt = rows[64 * kRowBeta + row];
+                for (int t = 0; t < 2; ++t) {
+                    const int row = 32 * t + col, c0 = 32 * w + 4 * half;
+                    const float bt = rows[64 * kRowBeta + row];
+                    const uint32_t at_row = row * (uint32_t)(ldv * sizeof(T)), at_dy = row * (uint32_t)(lddy * sizeof(T));
+                    f4_t vr[4];
 #pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            const int left = d.Dv - c0 - 8 * a;
-                            const uint32_t in_row = (c0 + 8 * a) * (uint32_t)sizeof(T);
-                            const f4_t vr = load4<T, W4>(rv, row * (uint32_t)(ldv * sizeof(T)) + in_row, left);
-                            dyr[t][a] = load4<T, W4>(rc, row * (uint32_t)(lddy * sizeof(T)) + in_row, left);
-                            float o[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                zv[t] = fmaf(U[t][4 * a + j], vr[j], zv[t]);
-                                mo[t] = fmaxf(mo[t], fabsf(dyr[t][a][j]));
-                                o[j] = bt * U[t][4 * a + j];
-                            }
-                            store4<W4>(rdv, row * (uint32_t)(out.dv.ld * sizeof(T)) + in_row, left, o, (T *)nullptr);
-                        }
-                        mo[t] = max_halves(mo[t]);
-                        zv[t] += __shfl_xor(zv[t], 32);
+                    for (int a = 0; a < 4; ++a) {
+                        const uint32_t in_row = (c0 + 8 * a) * (uint32_t)sizeof(T);
+                        vr[a] = load4<T>(rv, at_row + in_row, d.Dv - c0 - 8 * a);
+                        dyr[t][a] = load4<T>(rc, at_dy + in_row, d.Dv - c0 - 8 * a);
                     }
-                };
-                if (out.wide_v) rest(std::true_type());
-                else rest(std::false_type());
+                    if ((d.Dv & 3) && (d.Dv >> 5) == w) {               // the wave has the last columns
+                        const int last = (d.Dv & ~3) - 4 * half - 32 * w;          // of the half in which they lie, a multiple of 8
+                        const int left = last & 7 ? 0 : d.Dv & 3;
+                        const uint32_t in_row = (d.Dv & ~3) * (uint32_t)sizeof(T);
+                        const f4_t v1 = load_rest<T>(rv, at_row + in_row, left), o1 = load_rest<T>(rc, at_dy + in_row, left);
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+#pragma unroll
+                            for (int j = 0; j < 3; ++j) {
+                                vr[a][j] = last == 8 * a ? v1[j] : vr[a][j];
+                                dyr[t][a][j] = last == 8 * a ? o1[j] : dyr[t][a][j];
+                            }
+                    }
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        float o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            zv[t] = fmaf(U[t][4 * a + j], vr[a][j], zv[t]);
+                            mo[t] = fmaxf(mo[t], fabsf(dyr[t][a][j]));
+                            o[j] = bt * U[t][4 * a + j];
+                        }
+                        store4(rdv, row * (uint32_t)(out.dv.ld * sizeof(T)) + (c0 + 8 * a) * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, d.Dv & 3, o, (T *)nullptr);
+                    }
+                    mo[t] = max_halves(mo[t]);
+                    zv[t] += __shfl_xor(zv[t], 32);
+                }
                 small[kDots + (4 * 4 + w) * 64 + lane] = half ? zv[1] : zv[0];
             }
         };
@@ -585,13 +576,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     const int other = 32 * other_b + acc_row(r, half);
                     const int i = by_i ? mine : other, j = by_i ? other : mine;
                     const bool in = is_m ? j < i : j <= i;
-                    const float D = expf((float)(by_i ? g_mine - G[other] : G[other] - g_mine));
+                    const float D = by_i ? decay_of(g_mine, G[other]) : decay_of(G[other], g_mine);
                     // what the contraction's index brings along: lane = i: keys j; lane = j: queries i, or beta and keys i
                     float f = rows[64 * (by_i || is_m ? kRowKK : kRowKQ) + other];
                     if (!by_i && is_m) f *= rows[64 * kRowBeta + other];
                     f *= is_m ? -D : d.scale * D;
                     const float inv_other = small[kBack + 64 * (by_i ? 0 : is_m ? 1 : 2) + other];
-                    x[r] = in ? x[r] * (inv_mine * inv_other) * f : 0.f;
+                    float value = x[r] * (inv_mine * inv_other) * f;
+                    asm("" : "+v"(value));                              // all of it, then a selection: no branch for each
+                    x[r] = in ? value : 0.f;
                 }
                 C[q] = x;
                 m = max_abs(x, m);
@@ -625,57 +618,70 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
         const auto third_part = [&](auto is_second) {
             constexpr bool second = decltype(is_second)::value;
             const int row = 32 * w + col;
-            const __amdgpu_buffer_rsrc_t r = second ? re : rs;
             const uint32_t ld = second ? 128 * slices : 4 * d.Dv;
             const int width = second ? 32 * slices : d.Dv;
             const float sc = second ? se : ss;
-            const auto with_state = [&](auto aligned) {
+            f4_t quads[16];                                             // columns 8 u + 4 half + 0..3; zeros past the state's
+            h8_t kt[4 * PARTS], qt[4 * PARTS];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (u >= 2 * slices) break;
-                    const int c0 = 16 * u + 4 * half;
-                    const f4_t f0 = load4<float, decltype(aligned)::value>(r, row * ld + 4 * c0, width - c0);
-                    const f4_t f1 = load4<float, decltype(aligned)::value>(r, row * ld + 4 * c0 + 32, width - c0 - 8);
-                    const Pair a = split8(sc, [&](int j) { return j < 4 ? f0[j & 3] : f1[j & 3]; });
+            for (int u = 0; u < 16; ++u) {
+                const int c0 = 8 * u + 4 * half;
+                quads[u] = load4<float>(second ? re : rs, row * ld + 4 * c0, u < 4 * slices ? width - c0 : 0);
+            }
+            if (!second && (d.Dv & 3)) {                                // the last columns of S
+                const int last = (d.Dv & ~3) - 4 * half;
+                const f4_t f = load_rest<float>(rs, row * ld + 4 * (d.Dv & ~3), last & 7 ? 0 : d.Dv & 3);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if constexpr (second) {
-                            const h8_t uh = page(P::kU + 8 * t + u), ul = page(P::kU + 16 + 8 * t + u);
-                            A[t] = mfma(a.hi, uh, A[t]);
-                            A[t] = mfma(a.lo, uh, A[t]);
-                            A[t] = mfma(a.hi, ul, A[t]);
-                        } else {
-                            const h8_t o = page(P::kY + 8 * t + u), zh = page(P::kZ + 8 * t + u), zl = page(P::kZ + 16 + 8 * t + u);
-                            A[t] = mfma(a.hi, o, A[t]);
-                            Bb[t] = mfma(a.hi, zh, Bb[t]);
-                            A[t] = mfma(a.lo, o, A[t]);
-                            Bb[t] = mfma(a.lo, zh, Bb[t]);
-                            if constexpr (PARTS == 2) A[t] = mfma(a.hi, page(P::kY + 16 + 8 * t + u), A[t]);
-                            Bb[t] = mfma(a.hi, zl, Bb[t]);
-                        }
-                    }
+                for (int u = 0; u < 16; ++u)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) quads[u][j] = last == 8 * u ? f[j] : quads[u][j];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const auto read_t = [&] {
+#pragma unroll
+                for (int u = 0; u < 4 * PARTS; ++u) {
+                    kt[u] = global_page((PARTS + (u >> 2)) * F + 4 * w + (u & 3));
+                    qt[u] = global_page(((second ? 3 : 1) * PARTS + (u >> 2)) * F + 4 * w + (u & 3));
                 }
             };
-            if (second || out.wide_s) with_state(std::true_type());
-            else with_state(std::false_type());
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (u == 4) read_t();                                   // some of the state's registers are free by then
+                if (u >= 2 * slices) continue;
+                const Pair a = split8(sc, [&](int j) { return quads[2 * u + (j >> 2)][j & 3]; });
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if constexpr (second) {
+                        const h8_t uh = page(P::kU + 8 * t + u), ul = page(P::kU + 16 + 8 * t + u);
+                        A[t] = mfma(a.hi, uh, A[t]);
+                        A[t] = mfma(a.lo, uh, A[t]);
+                        A[t] = mfma(a.hi, ul, A[t]);
+                    } else {
+                        const h8_t o = page(P::kY + 8 * t + u), zh = page(P::kZ + 8 * t + u), zl = page(P::kZ + 16 + 8 * t + u);
+                        A[t] = mfma(a.hi, o, A[t]);
+                        Bb[t] = mfma(a.hi, zh, Bb[t]);
+                        A[t] = mfma(a.lo, o, A[t]);
+                        Bb[t] = mfma(a.lo, zh, Bb[t]);
+                        if constexpr (PARTS == 2) A[t] = mfma(a.hi, page(P::kY + 16 + 8 * t + u), A[t]);
+                        Bb[t] = mfma(a.hi, zl, Bb[t]);
+                    }
+                }
+            }
             // products of keys and queries with B and M
             acc_t p1[2] = {zeros(), zeros()}, p2[2] = {zeros(), zeros()};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const h8_t kt = global_page(PARTS * F + 4 * w + u), qt = global_page((second ? 3 : 1) * PARTS * F + 4 * w + u);
-                h8_t kl = {}, ql = {};
-                if constexpr (PARTS == 2) kl = global_page((PARTS + 1) * F + 4 * w + u), ql = global_page(((second ? 3 : 1) * PARTS + 1) * F + 4 * w + u);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (second ? t > u >> 1 : t < u >> 1) continue;
                     const int p = second ? high_page(t, u) : low_page(t, u);
                     const int b0 = (second ? P::kB2 : P::kB1) + p, c0 = (second ? P::kM2 : P::kM1) + p;
                     const h8_t b = page(b0), c = page(c0);
-                    p1[t] = mfma(qt, b, p1[t]);
-                    p2[t] = mfma(kt, c, p2[t]);
-                    p1[t] = mfma(qt, page(b0 + kTriPages), p1[t]);
-                    p2[t] = mfma(kt, page(c0 + kTriPages), p2[t]);
-                    if constexpr (PARTS == 2) p1[t] = mfma(ql, b, p1[t]), p2[t] = mfma(kl, c, p2[t]);
+                    p1[t] = mfma(qt[u], b, p1[t]);
+                    p2[t] = mfma(kt[u], c, p2[t]);
+                    p1[t] = mfma(qt[u], page(b0 + kTriPages), p1[t]);
+                    p2[t] = mfma(kt[u], page(c0 + kTriPages), p2[t]);
+                    if constexpr (PARTS == 2) p1[t] = mfma(qt[4 + u], b, p1[t]), p2[t] = mfma(kt[4 + u], c, p2[t]);
                 }
             }
             const float iss = pow2_inv(sc);
@@ -775,34 +781,30 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
         const RowsOut o = upper ? out.dk : out.dq;
         const int base = upper ? 0 : 2 * PARTS * F;
         const __amdgpu_buffer_rsrc_t r = rows_buffer((T *)o.p + r0 * o.ld + hk * d.Dk, n, o.ld, d.Dk);
-        const auto finish = [&](auto aligned) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int tok = 32 * t + col;
-                const float size = rec[64 * (upper ? kRowSizeK : kRowSizeQ) + tok], kap = rec[64 * (upper ? kRowKK : kRowKQ) + tok];
-                const float along = d.unit ? small[kTotals + (upper ? 64 : 0) + tok] * kap : 0.f;
+        for (int t = 0; t < 2; ++t) {
+            const int tok = 32 * t + col;
+            const float size = rec[64 * (upper ? kRowSizeK : kRowSizeQ) + tok], kap = rec[64 * (upper ? kRowKK : kRowKQ) + tok];
+            const float along = d.unit ? small[kTotals + (upper ? 64 : 0) + tok] * kap : 0.f;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int p = base + t * 2 * DKB + 2 * w + u;
-                    const h8_t hi = global_page(p);
-                    h8_t lo = {};
-                    if constexpr (PARTS == 2) lo = global_page(p + F);
+            for (int u = 0; u < 2; ++u) {
+                const int p = base + t * 2 * DKB + 2 * w + u;
+                const h8_t hi = global_page(p);
+                h8_t lo = {};
+                if constexpr (PARTS == 2) lo = global_page(p + F);
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        float f[4];
+                for (int a = 0; a < 2; ++a) {
+                    float f[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = (float)hi[4 * a + j] + (float)lo[4 * a + j];
-                            f[j] = size * (d.unit ? fmaf(-along, x, sum[t][8 * u + 4 * a + j]) : sum[t][8 * u + 4 * a + j]);
-                        }
-                        const int c0 = 32 * w + 16 * u + 8 * a + 4 * half;
-                        store4<decltype(aligned)::value>(r, tok * (uint32_t)(o.ld * sizeof(T)) + c0 * (uint32_t)sizeof(T), d.Dk - c0, f, (T *)nullptr);
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = (float)hi[4 * a + j] + (float)lo[4 * a + j];
+                        f[j] = size * (d.unit ? fmaf(-along, x, sum[t][8 * u + 4 * a + j]) : sum[t][8 * u + 4 * a + j]);
                     }
+                    const int c0 = 32 * w + 16 * u + 8 * a + 4 * half;
+                    store4(r, tok * (uint32_t)(o.ld * sizeof(T)) + c0 * (uint32_t)sizeof(T), d.Dk - c0, d.Dk & 3, f, (T *)nullptr);
                 }
             }
-        };
-        if (out.wide_k) finish(std::true_type());
-        else finish(std::false_type());
+        }
     }
 }
 
@@ -868,11 +870,7 @@ hipError_t launch_delta_bwd(const Seq &s, const Delta &d, bool bf16, const Delta
     if (ws.blocks > 0) launch_delta_prep(s, d, bf16, true, ws, in, st);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    GradOut out{dq, dk, dv, dg, dbeta, false, false, false};
-    const auto wide = [&](const void *p, int64_t ld, int dim) { return bf16 ? wide_rows<uint16_t>(p, ld, dim) : wide_rows<float>(p, ld, dim); };
-    out.wide_k = wide(dq.p, dq.ld, d.Dk) && wide(dk.p, dk.ld, d.Dk);
-    out.wide_v = wide(in.v.p, in.v.ld, d.Dv) && wide(dy.p, dy.ld, d.Dv) && wide(dv.p, dv.ld, d.Dv);
-    out.wide_s = d.Dv % 4 == 0 && (uintptr_t)states % 16 == 0;
+    const GradOut out{dq, dk, dv, dg, dbeta};
 #define CASE(n) \
     case n: return bf16 ? bwd<uint16_t, n>(s, d, ws, in, states, dy, dsT, out, ds0, st) : bwd<float, n>(s, d, ws, in, states, dy, dsT, out, ds0, st)
     switch ((d.Dk + 31) / 32) {

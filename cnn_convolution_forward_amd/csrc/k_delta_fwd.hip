@@ -13,8 +13,6 @@
 // The pages of K, K^T, Q, T and P (66 KB for bf16 heads of 128) are brought to LDS
 // asynchronously, a block ahead where two buffers fit.  Values are
 // loaded a block ahead into registers.
-#include <type_traits>
-
 #include "delta_common.h"
 
 namespace convfwd {
@@ -32,7 +30,7 @@ template <int DKB, int PARTS, bool SUM> struct FwdPages {
 template <typename T, int DKB, bool SUM>
 __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs ws, int slices, const T *__restrict__ v,
                                                         int64_t ldv, const float *__restrict__ s0, T *__restrict__ y,
-                                                        int64_t ldy, bool wide, float *__restrict__ sT,
+                                                        int64_t ldy, float *__restrict__ sT,
                                                         float *__restrict__ states) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
     typedef FwdPages<DKB, PARTS, SUM> P;
@@ -251,24 +249,20 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su) * invP;
         __builtin_amdgcn_wave_barrier();
         const __amdgpu_buffer_rsrc_t ry = rows_buffer(y + (first + (int64_t)k * kBlock) * ldy + hv * d.Dv, n, ldy, d.Dv);
-        const auto write = [&](auto aligned) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int row = 32 * t + col, c0 = slice * 32 + 4 * half;
-                const uint32_t off = row * ld_y + c0 * (uint32_t)sizeof(T);
+        for (int t = 0; t < 2; ++t) {
+            const int row = 32 * t + col, c0 = slice * 32 + 4 * half;
+            const uint32_t off = row * ld_y + c0 * (uint32_t)sizeof(T);
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const f4_t fs = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
-                    const f4_t fu = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
-                    float o[4];
+            for (int a = 0; a < 4; ++a) {
+                const f4_t fs = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
+                const f4_t fu = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
+                float o[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = fmaf(Y[t][4 * a + j], fs[j] * eq[t], Z[t][4 * a + j] * fu[j]);
-                    store4<decltype(aligned)::value>(ry, off + 8 * a * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, o, y);
-                }
+                for (int j = 0; j < 4; ++j) o[j] = fmaf(Y[t][4 * a + j], fs[j] * eq[t], Z[t][4 * a + j] * fu[j]);
+                store4(ry, off + 8 * a * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, d.Dv & 3, o, y);
             }
-        };
-        if (wide) write(std::true_type());
-        else write(std::false_type());
+        }
         __builtin_amdgcn_wave_barrier();
     }
     if constexpr (SUM) {
@@ -292,7 +286,7 @@ hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn 
     const hipError_t e = hipFuncSetAttribute((const void *)delta_fwd_kernel<T, DKB, SUM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     delta_fwd_kernel<T, DKB, SUM><<<(unsigned)(chains * ((columns + waves - 1) / waves)), 64 * waves, bytes, st>>>(
-        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, wide_rows<T>(y.p, y.ld, d.Dv), sT, states);
+        s, d, ws, slices, (const T *)in.v.p, in.v.ld, s0, (T *)y.p, y.ld, sT, states);
     return hipGetLastError();
 }
 

@@ -168,7 +168,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
                 const double t = __shfl_up(v, m);
                 if (lane >= m) v += t;
             }
-            const float E = (float)exp(v), F = (float)exp(__shfl(v, 63) - v);
+            v *= kLog2eD;
+            const float E = decay_of(v, 0.0), F = decay_of(__shfl(v, 63), v);
             G[lane] = v;
             bt[lane] = b;
             rows[64 * kRowEK + lane] = E * kap[0][lane];
@@ -187,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
             if (lane == 63) rows[kGamma] = E;
         }
         __syncthreads();
-        const auto decay = [&](int i, int j) { return expf((float)(G[i] - G[j])); };
+        const auto decay = [&](int i, int j) { return decay_of(G[i], G[j]); };
         // P where it is wanted, and A into LDS
         Pair pp[2];
         float pv[2][8], pm = 0.f;
@@ -331,10 +332,15 @@ void cut(const Seq &s, const Delta &d, DeltaWs &ws) {
     ws.segments = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
 }
 
-// S' = M S + N from segment to segment, a wave to 32 columns: S in registers, M the other operand.  N makes way for S'.
+// S' = M S + N from segment to segment: a workgroup to 32 columns, a wave to 32 rows of them.  M is loaded and split a
+// segment ahead; S goes through LDS as pages, each wave's under its own powers of two, so that one barrier is all that a
+// segment waits for.  N makes way for S'.
 template <int DKB>
-__global__ __launch_bounds__(64) void delta_join_kernel(Seq s, Delta d, DeltaWs ws, int slices, bool back) {
-    const int lane = threadIdx.x, half = lane >> 5, col = lane & 31;
+__global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, DeltaWs ws, int slices, bool back) {
+    __shared__ __align__(16) h8_t pages[2][DKB][4][64];                 // by turns: of each wave, page 0 hi and lo, page 1 hi and lo
+    __shared__ float inverse[2][DKB][32];
+    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads), slice = (int)(blockIdx.x / heads);
     int64_t first;
     int len;
@@ -342,48 +348,58 @@ __global__ __launch_bounds__(64) void delta_join_kernel(Seq s, Delta d, DeltaWs 
     const int blocks = (len + kBlock - 1) / kBlock, n = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
     const int ld = 32 * (slices + DKB), size = 32 * DKB * ld;
     float *base = ws.sums + (int64_t)bh * ws.segments * size;
-    const uint32_t at = 4 * (32 * slice + col);
+    const uint32_t at = 4 * (32 * slice + col) + 32 * wave * 4 * ld;    // the wave's rows
     if (n < 3) return;
-    acc_t S[DKB], N[DKB];
-    load_state<DKB>(make_rsrc(base + (back ? (int64_t)(n - 1) * size : 0), 4 * size), at, 4 * ld, half, S);
+    const auto segment = [&](int i) { return base + (int64_t)(back ? n - 1 - i : i) * size; };
+    f4_t row[4 * DKB];
+    acc_t S[1], N[1], next[1];
+    const auto fetch = [&](int i) {
+        const float *p = segment(i) + (int64_t)(32 * wave + col) * ld + 32 * slices + 4 * half;
+#pragma unroll
+        for (int u = 0; u < 4 * DKB; ++u) row[u] = *reinterpret_cast<const f4_t *>(p + 8 * u);
+        load_state<1>(make_rsrc(segment(i), 4 * size), at, 4 * ld, half, next);
+    };
+    load_state<1>(make_rsrc(segment(0), 4 * size), at, 4 * ld, half, S);
+    fetch(1);
     for (int i = 1; i < n - 1; ++i) {
-        float *seg = base + (int64_t)(back ? n - 1 - i : i) * size;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(seg, 4 * size);
-        load_state<DKB>(r, at, 4 * ld, half, N);
         float m = 0.f;
 #pragma unroll
-        for (int q = 0; q < DKB; ++q) m = max_abs(S[q], m);
-        const float sc = pow2_scale(max_halves(m)), isc = pow2_inv(sc);
-        Pair f[2 * DKB];
+        for (int u = 0; u < 4 * DKB; ++u)
 #pragma unroll
-        for (int u = 0; u < 2 * DKB; ++u) f[u] = split8(sc, [&](int j) { return S[u >> 1][8 * (u & 1) + j]; });
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(row[u][j]));
+#pragma unroll
+        for (int u = 1; u < 64; u <<= 1) m = fmaxf(m, __shfl_xor(m, u));
+        const float sm = pow2_scale(m), im = pow2_inv(sm);
+        Pair w[2 * DKB];
+#pragma unroll
+        for (int u = 0; u < 2 * DKB; ++u) w[u] = split8(sm, [&](int j) { return row[2 * u + (j >> 2)][j & 3]; });
+        N[0] = next[0];
+        if (i + 1 < n - 1) fetch(i + 1);
+        const float sc = pow2_scale(max_halves(max_abs(S[0])));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const Pair f = split8(sc, [&](int j) { return S[0][8 * u + j]; });
+            pages[i & 1][wave][2 * u][lane] = f.hi;
+            pages[i & 1][wave][2 * u + 1][lane] = f.lo;
+        }
+        if (half == 0) inverse[i & 1][wave][col] = pow2_inv(sc);
+        __syncthreads();
 #pragma unroll
         for (int q = 0; q < DKB; ++q) {
-            // 32 rows of M, under one power of two
-            f4_t row[4 * DKB];
-            const float *p = seg + (int64_t)(32 * q + col) * ld + 32 * slices + 4 * half;
-            m = 0.f;
+            acc_t a = zeros();
 #pragma unroll
-            for (int u = 0; u < 4 * DKB; ++u) {
-                row[u] = *reinterpret_cast<const f4_t *>(p + 8 * u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(row[u][j]));
+            for (int u = 0; u < 2; ++u) {
+                const h8_t hi = pages[i & 1][q][2 * u][lane], lo = pages[i & 1][q][2 * u + 1][lane];
+                a = mfma(w[2 * q + u].hi, hi, a);
+                a = mfma(w[2 * q + u].hi, lo, a);
+                a = mfma(w[2 * q + u].lo, hi, a);
             }
+            const float f = inverse[i & 1][q][col];
 #pragma unroll
-            for (int u = 1; u < 64; u <<= 1) m = fmaxf(m, __shfl_xor(m, u));
-            const float sm = pow2_scale(m), im = pow2_inv(sm);
-            acc_t a = zeros(), b = zeros();
-#pragma unroll
-            for (int u = 0; u < 2 * DKB; ++u) {
-                const Pair w = split8(sm, [&](int j) { return row[2 * u + (j >> 2)][j & 3]; });
-                a = mfma(w.hi, f[u].hi, a);
-                b = mfma(w.hi, f[u].lo, b);
-                b = mfma(w.lo, f[u].hi, b);
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) S[q][x] = fmaf((a[x] + b[x]) * im, isc, N[q][x]);
+            for (int x = 0; x < 16; ++x) N[0][x] = fmaf(a[x] * im, f, N[0][x]);
         }
-        store_state<DKB>(r, at, 4 * ld, half, S);
+        S[0] = N[0];
+        store_state<1>(make_rsrc(segment(i), 4 * size), at, 4 * ld, half, S);
     }
 }
 
@@ -394,9 +410,9 @@ hipError_t launch_delta_join(const Seq &s, const Delta &d, const DeltaWs &ws, bo
     const unsigned grid = (unsigned)(s.B * d.Hv * slices);
     switch ((d.Dk + 31) / 32) {
     case 1: delta_join_kernel<1><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
-    case 2: delta_join_kernel<2><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
-    case 3: delta_join_kernel<3><<<grid, 64, 0, st>>>(s, d, ws, slices, back); break;
-    default: delta_join_kernel<4><<<grid, 64, 0, st>>>(s, d, ws, slices, back);
+    case 2: delta_join_kernel<2><<<grid, 128, 0, st>>>(s, d, ws, slices, back); break;
+    case 3: delta_join_kernel<3><<<grid, 192, 0, st>>>(s, d, ws, slices, back); break;
+    default: delta_join_kernel<4><<<grid, 256, 0, st>>>(s, d, ws, slices, back);
     }
     return hipGetLastError();
 }
