@@ -81,6 +81,14 @@ template <typename F> __device__ __forceinline__ Pair split8(float scale, F valu
     return p;
 }
 
+// Four values of one column of LDS, from four rows.  Of 16 lanes, p is row lane/4 % 4, columns 4 (lane % 4) .. + 3, and lane i gets
+// column i: a transposed page from an upright one.
+__device__ __forceinline__ h4_t read_columns(const _Float16 *p) {
+    typedef short s4_t __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4_t lds_s4_t;
+    return __builtin_bit_cast(h4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t *)p));
+}
+
 __device__ __forceinline__ float max_abs(const acc_t &v, float m = 0.f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
@@ -102,7 +110,7 @@ constexpr int kTriPages = 6;
 
 // Where the parts of the workspace lie.  Counts are pages.
 struct DeltaWs {
-    uint4 *qk;               // per block and key head: K, KT, Q, QT (backward only), each `parts` times
+    uint4 *qk;               // per block and key head: K, Q, or backward K, KT, Q, QT, each `parts` times
     uint4 *tri;              // per block and value head, forward: T hi, T lo, P hi, P lo; backward: T, TT, PT, hi and lo
     float *rows;             // per block and value head: kRowsFloats
     float *ends;             // backward: gradients of the states behind the blocks, dk x dv padded to 32s

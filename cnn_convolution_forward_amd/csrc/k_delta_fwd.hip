@@ -10,7 +10,7 @@
 // With the operands swapped, products with S and U give Y transposed: a lane then
 // has four neighbouring values of a token and stores them together.
 //
-// The pages of K, K^T, Q, T and P (66 KB for bf16 heads of 128) are brought to LDS
+// The pages of K, Q, T and P (50 KB for bf16 heads of 128) are brought to LDS
 // asynchronously, a block ahead where two buffers fit.  Values are
 // loaded a block ahead into registers.
 #include "delta_common.h"
@@ -20,8 +20,8 @@ namespace {
 
 // SUM: without y, for what a segment makes of a state.
 template <int DKB, int PARTS, bool SUM> struct FwdPages {
-    static constexpr int F = 4 * DKB;                   // pages of one part of K, KT or Q
-    static constexpr int kQK = (SUM ? 2 : 3) * PARTS * F;
+    static constexpr int F = 4 * DKB;                   // pages of one part of K or Q
+    static constexpr int kQK = (SUM ? 1 : 2) * PARTS * F;
     static constexpr int kTri = (2 + (SUM ? 0 : PARTS)) * kTriPages;    // T hi and lo; of P, lo only where y has 24 bits
     static constexpr int kAll = kQK + kTri + 1;         // and a page of the rows' factors
     static constexpr int kBuffers = 2 * kAll <= 156 ? 2 : 1;
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         for (int i = 0; i < DKB; ++i) m = max_abs(S[i], m);
         const float sc = pow2_scale(max_halves(m)), isc = pow2_inv(sc);
         acc_t X[2] = {zeros(), zeros()}, Y[2] = {zeros(), zeros()};
-        constexpr int kT = P::kQK, kP = kT + 2 * kTriPages, kQ = 2 * PARTS * P::F;
+        constexpr int kT = P::kQK, kP = kT + 2 * kTriPages, kQ = PARTS * P::F;
         h8_t kp[2][2 * PARTS], qp[2][2 * PARTS];
         const auto read_kq = [&](int i) {
 #pragma unroll
@@ -164,9 +164,16 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         const float sr = pow2_scale(max_halves(m));
         if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);           // behind V's loads, which would wait for it
         h8_t kt[4 * PARTS], kt2[4 * PARTS], low[PARTS * kTriPages];
+        // rows 32 i .. + 31 of K^T, from the pages of K: 16 rows are a page's columns, four lanes of 8 bytes to a token
         const auto read_kt = [&](int i, h8_t(&to)[4 * PARTS]) {
+            const char *p = buf + ((lane >> 4) & 1) * 1024 + ((lane & 1) * 32 + 4 * half + ((lane >> 2) & 3)) * 16 + ((lane >> 1) & 1) * 8;
 #pragma unroll
-            for (int u = 0; u < 4 * PARTS; ++u) to[u] = page((PARTS + (u >> 2)) * P::F + 4 * i + (u & 3));
+            for (int u = 0; u < 4 * PARTS; ++u) {
+                const char *q = p + ((u >> 2) * P::F + ((u >> 1) & 1) * 2 * DKB + 2 * i) * 1024 + (u & 1) * 256;
+                const h4_t a = read_columns((const _Float16 *)q), b = read_columns((const _Float16 *)(q + 128));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[u][j] = a[j], to[u][4 + j] = b[j];
+            }
         };
         f4_t fk[2][4];
 #pragma unroll

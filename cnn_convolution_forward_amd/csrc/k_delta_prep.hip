@@ -43,7 +43,7 @@ template <typename T, int N> __device__ __forceinline__ void load_part(const T *
 }
 
 template <typename T, int DKB, bool BWD>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
+__global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
                                                               const T *__restrict__ k, int64_t ldk,
                                                               const float *__restrict__ g, int64_t ldg,
                                                               const float *__restrict__ beta, int64_t ldb) {
@@ -55,12 +55,12 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
     __shared__ __align__(16) char shared[kTiles];
     Tiles *xs = reinterpret_cast<Tiles *>(shared);
     Square &A = *reinterpret_cast<Square *>(shared), &Ti = *reinterpret_cast<Square *>(shared + sizeof(Square));
-    __shared__ Square kk, qk;
     __shared__ double G[kBlock];
     __shared__ float kap[2][kBlock], size[2][kBlock], bt[kBlock], red[8];
     const int64_t slot = blockIdx.x / d.H;
     const int hk = (int)(blockIdx.x % d.H);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Block at = find_block(s, ws.per, slot);
     int64_t first;
     int len;
@@ -70,43 +70,48 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
     const int n = min(len - at.k * kBlock, kBlock);
 
     // rows as fp16 under their own power of two, and the factor that makes the row of it
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    {
         const int row = tid >> 2, c = (tid & 3) * N;
-        float f[N];
-        if (row < n) {
-            load_part<T, N>((which ? q + (r0 + row) * ldq : k + (r0 + row) * ldk) + hk * d.Dk, c, d.Dk, f);
-        } else {
+        float f[2][N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = 0.f;
-        }
-        float m = 0.f;
+        for (int which = 0; which < 2; ++which) {
+            if (row < n) {
+                load_part<T, N>((which ? q + (r0 + row) * ldq : k + (r0 + row) * ldk) + hk * d.Dk, c, d.Dk, f[which]);
+            } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[i]));
-        m = fmaxf(m, __shfl_xor(m, 1));
-        m = fmaxf(m, __shfl_xor(m, 2));
-        const float sc = pow2_scale(m, 60);
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            h4_t hi, lo;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = f[i + j] * sc;
-                ss = fmaf(x, x, ss);
-                hi[j] = (_Float16)x;
-                lo[j] = (_Float16)(x - (float)hi[j]);
+                for (int i = 0; i < N; ++i) f[which][i] = 0.f;
             }
-            *reinterpret_cast<h4_t *>(&xs[which][0][row][c + i]) = hi;
-            if constexpr (PARTS == 2) *reinterpret_cast<h4_t *>(&xs[which][PARTS - 1][row][c + i]) = lo;
         }
-        ss += __shfl_xor(ss, 1);
-        ss += __shfl_xor(ss, 2);
-        if ((tid & 3) == 0) {
-            // unit length: x / sqrt(sum x^2 + eps) with sum x^2 = ss / sc^2; a row of zeros stays
-            const float f0 = !d.unit ? pow2_inv(sc) : ss == 0.f ? 0.f : 1.f / sqrtf(ss + d.eps * sc * sc);
-            kap[which][row] = f0;
-            size[which][row] = f0 * sc;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[which][i]));
+            m = fmaxf(m, __shfl_xor(m, 1));
+            m = fmaxf(m, __shfl_xor(m, 2));
+            const float sc = pow2_scale(m, 60);
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                h4_t hi, lo;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = f[which][i + j] * sc;
+                    ss = fmaf(x, x, ss);
+                    hi[j] = (_Float16)x;
+                    lo[j] = (_Float16)(x - (float)hi[j]);
+                }
+                *reinterpret_cast<h4_t *>(&xs[which][0][row][c + i]) = hi;
+                if constexpr (PARTS == 2) *reinterpret_cast<h4_t *>(&xs[which][PARTS - 1][row][c + i]) = lo;
+            }
+            ss += __shfl_xor(ss, 1);
+            ss += __shfl_xor(ss, 2);
+            if ((tid & 3) == 0) {
+                // unit length: x / sqrt(sum x^2 + eps) with sum x^2 = ss / sc^2; a row of zeros stays
+                const float f0 = !d.unit ? pow2_inv(sc) : ss == 0.f ? 0.f : 1.f / sqrtf(ss + d.eps * sc * sc);
+                kap[which][row] = f0;
+                size[which][row] = f0 * sc;
+            }
         }
     }
     __syncthreads();
@@ -119,45 +124,48 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
         for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
         return v;
     };
+    // k.k and q.k of the three blocks of 32x32 on and below the diagonal: wave 0 k.k of the one below, wave 1 those on it, waves 2
+    // and 3 the same of q.k.  They stay in registers, rows j for P (lane = i, as its pages have it) and rows i for the others.
+    const int which = wave >> 1, count = wave & 1 ? 2 : 1;
+    constexpr bool kByI = !BWD;                                           // of q.k
+    acc_t prod[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        prod[u] = zeros();
+        if (u >= count) break;
+        const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
+#pragma unroll
+        for (int m = 0; m < 2 * DKB; ++m) {
+            const h8_t a = row_page(which, 0, ib, m), b = row_page(0, 0, jb, m);
+            const bool swap = which && kByI;
+            prod[u] = swap ? mfma(b, a, prod[u]) : mfma(a, b, prod[u]);
+            if constexpr (PARTS == 2) {
+                const h8_t al = row_page(which, 1, ib, m), bl = row_page(0, 1, jb, m);
+                prod[u] = swap ? mfma(bl, a, prod[u]) : mfma(a, bl, prod[u]);
+                prod[u] = swap ? mfma(b, al, prod[u]) : mfma(al, b, prod[u]);
+            }
+        }
+    }
     {   // pages of keys and queries
         uint4 *out = ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage + lane;
         constexpr int F = 4 * DKB;
-        for (int i = wave; i < (BWD ? 4 : 3) * PARTS * F; i += 4) {
-            const int kind = i / (PARTS * F), part = i / F % PARTS, f = i % F;      // K, KT, Q, QT
-            const int which = kind >> 1;
+        for (int i = wave; i < (BWD ? 4 : 2) * PARTS * F; i += 4) {
+            const int kind = BWD ? i / (PARTS * F) : 2 * (i / (PARTS * F)), part = i / F % PARTS, f = i % F;      // K, KT, Q, QT
             h8_t v;
             if (!(kind & 1)) {
-                v = row_page(which, part, f / (2 * DKB), f % (2 * DKB));
-            } else {
+                v = row_page(kind >> 1, part, f / (2 * DKB), f % (2 * DKB));
+            } else {                                                    // lane = dk; places 0..3 tokens 16 m + 4 half on, 4..7 those 8 on
+                const _Float16 *p = &xs[kind >> 1][part][16 * (f % 4) + 4 * half][32 * (f / 4) + (lane & 16)];
+                p += (lane & 15) / 4 * LD + 4 * (lane & 3);
+                const h4_t a = read_columns(p), b = read_columns(p + 8 * LD);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = xs[which][part][page_at(f % 4, half, j)][32 * (f / 4) + col];
+                for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
             }
             out[i * kPage] = __builtin_bit_cast(uint4, v);
         }
     }
-    // k.k and q.k, the three blocks of 32x32 on and below the diagonal
-    for (int i = wave; i < 6; i += 4) {
-        const int which = i / 3, ib = i % 3 ? 1 : 0, jb = i % 3 == 2 ? 1 : 0;
-        acc_t c = zeros();
-#pragma unroll
-        for (int m = 0; m < 2 * DKB; ++m) {
-            const h8_t a = row_page(which, 0, ib, m), b = row_page(0, 0, jb, m);
-            c = mfma(a, b, c);
-            if constexpr (PARTS == 2) {
-                c = mfma(a, row_page(0, 1, jb, m), c);
-                c = mfma(row_page(which, 1, ib, m), b, c);
-            }
-        }
-        float(*out)[65] = which ? qk : kk;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = 32 * ib + acc_row(r, half), cl = 32 * jb + col;
-            out[row][cl] = c[r] * kap[which][row] * kap[0][cl];
-        }
-    }
 
     for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
-        __syncthreads();                                                // the last head's arrays are free
         const int64_t rec = slot * d.Hv + hv;
         float *rows = ws.rows + rec * kRowsFloats;
         if (wave == 0) {
@@ -187,30 +195,50 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
             }
             if (lane == 63) rows[kGamma] = E;
         }
-        __syncthreads();
-        const auto decay = [&](int i, int j) { return decay_of(G[i], G[j]); };
-        // P where it is wanted, and A into LDS
-        Pair pp[2];
-        float pv[2][8], pm = 0.f;
+        __syncthreads();                                                // also: keys and queries, or the last head's arrays, are free
+        acc_t val[2];
+        float pm = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int m = wave, ib = 1 - u;                             // block 1 has pages 0..3, block 0 pages 0 and 1
-            if (u && wave > 1) break;
-            const int i = 32 * ib + col;
+            if (u >= count) break;
+            const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
+            const bool by_i = which && kByI;
+            const int mine = 32 * (by_i ? ib : jb) + col;
+            const double g_mine = G[mine];
+            const float k_mine = kap[by_i ? 1 : 0][mine];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int j = page_at(m, half, e);
-                const float D = j <= i ? decay(i, j) : 0.f;
-                pv[u][e] = j <= i ? d.scale * qk[i][j] * D : 0.f;
-                pm = fmaxf(pm, fabsf(pv[u][e]));
-                A[i][j] = j < i ? bt[i] * kk[i][j] * D : 0.f;
+            for (int r = 0; r < 16; ++r) {
+                const int other = 32 * (by_i ? jb : ib) + acc_row(r, half);
+                const int i = by_i ? mine : other, j = by_i ? other : mine;
+                const float D = by_i ? decay_of(g_mine, G[other]) : decay_of(G[other], g_mine);
+                float x = prod[u][r] * (k_mine * kap[by_i ? 0 : which][other]) * D * (which ? d.scale : bt[i]);
+                asm("" : "+v"(x));                                      // all of it, then a selection: no branch for each
+                x = j < i || (which && j == i) ? x : 0.f;
+                val[u][r] = x;
+                pm = fmaxf(pm, fabsf(x));
+                if (!which) A[i][j] = x;
             }
         }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) pm = fmaxf(pm, __shfl_xor(pm, m));
         if (lane == 0) red[wave] = pm;
         __syncthreads();
-        const float sp = pow2_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+        const float sp = pow2_scale(fmaxf(red[2], red[3]));
+        uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
+        const auto put = [&](int kind, int page, const Pair &p) {
+            out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
+            out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
+        };
+        if (which) {                                                    // P or P^T: registers 8 m .. 8 m + 7 are pages
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u >= count) break;
+                const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    put(BWD ? 2 : 1, BWD ? high_page(jb, 2 * ib + m) : low_page(ib, 2 * jb + m), split8(sp, [&](int e) { return val[u][8 * m + e]; }));
+            }
+        }
 
         // T: the blocks on the diagonal
         {
@@ -235,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
         for (int lev = 1; lev < 4; ++lev) {
             if (wave < 4 - lev) {
                 const int bi = wave + lev, bj = wave, c = lane & 15, o = 4 * (lane >> 4);
-                f4_t sum = {0.f, 0.f, 0.f, 0.f}, out = {0.f, 0.f, 0.f, 0.f};
+                f4_t sum = {0.f, 0.f, 0.f, 0.f}, res = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int kb = 0; kb < lev; ++kb)
 #pragma unroll
@@ -244,9 +272,9 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
                                                                    Ti[16 * (bj + kb) + o + u][16 * bj + c], sum, 0, 0, 0);
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    out = __builtin_amdgcn_mfma_f32_16x16x4f32(Ti[16 * bi + c][16 * bi + o + u], sum[u], out, 0, 0, 0);
+                    res = __builtin_amdgcn_mfma_f32_16x16x4f32(Ti[16 * bi + c][16 * bi + o + u], sum[u], res, 0, 0, 0);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) Ti[16 * bi + o + u][16 * bj + c] = -out[u];
+                for (int u = 0; u < 4; ++u) Ti[16 * bi + o + u][16 * bj + c] = -res[u];
             }
             __syncthreads();
         }
@@ -262,35 +290,20 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Seq s, Delta d, De
         __syncthreads();
         const float st = pow2_scale(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
         if (tid == 0) rows[kInvT] = pow2_inv(st), rows[kInvP] = pow2_inv(sp);
-        uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
-        const auto put = [&](int kind, int page, const Pair &p) {
-            out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
-            out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
-        };
         for (int f = wave; f < kTriPages; f += 4) {
             const int ib = f < 2 ? 0 : 1, m = ib ? f - 2 : f, i = 32 * ib + col;
             // forward: times beta of the column, so that the kernel behind it has R = V - E K S
-            put(0, f, split8(BWD ? st : 1.f, [&](int e) {
+            put(0, f, split8(st, [&](int e) {
                     const int j = page_at(m, half, e);
-                    return j > i ? 0.f : BWD ? Ti[i][j] : Ti[i][j] * bt[j] * st;
+                    return j > i ? 0.f : BWD ? Ti[i][j] : Ti[i][j] * bt[j];
                 }));
         }
-        if constexpr (!BWD) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u && wave > 1) break;
-                put(1, low_page(1 - u, wave), split8(sp, [&](int e) { return pv[u][e]; }));
-            }
-        } else {
+        if constexpr (BWD) {
             for (int f = wave; f < kTriPages; f += 4) {
                 const int jb = f < 4 ? 0 : 1, m = jb ? f - 2 : f, j = 32 * jb + col;
                 put(1, f, split8(st, [&](int e) {
                         const int i = page_at(m, half, e);
                         return j <= i ? Ti[i][j] : 0.f;
-                    }));
-                put(2, f, split8(sp, [&](int e) {
-                        const int i = page_at(m, half, e);
-                        return j <= i ? d.scale * qk[i][j] * decay(i, j) : 0.f;
                     }));
             }
         }
@@ -421,7 +434,7 @@ int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *ba
     const int dkb = (d.Dk + 31) / 32, dvb = (d.Dv + 31) / 32;
     ws.per = (s.T + kBlock - 1) / kBlock;
     ws.blocks = s.off ? s.rows / kBlock + s.B : (int64_t)s.B * ws.per;
-    ws.qk_pages = (bwd ? 4 : 3) * (bf16 ? 1 : 2) * 4 * dkb;
+    ws.qk_pages = (bwd ? 4 : 2) * (bf16 ? 1 : 2) * 4 * dkb;
     ws.tri_pages = (bwd ? 6 : 4) * kTriPages;
     char *p = (char *)base;
     int64_t at = 0;
