@@ -114,7 +114,8 @@ struct DeltaWs {
     uint4 *tri;              // per block and value head, forward: T hi, T lo, P hi, P lo; backward: T, TT, PT, hi and lo
     float *rows;             // per block and value head: kRowsFloats
     float *ends;             // backward: gradients of the states behind the blocks, dk x dv padded to 32s
-    float *sums;             // per sequence, value head and segment: what a segment makes of a state, dk x (dv + dk) padded to 32s
+    float *sums;             // per sequence, value head and segment: what it makes of a state, an offset dk x dv and a matrix dk x dk,
+                             // transposed, both padded to 32s
     int segments, seg_blocks;
     int qk_pages, tri_pages;
     int per;                 // blocks of each of equal sequences
@@ -123,7 +124,22 @@ struct DeltaWs {
 
 // The parts in `base`; returns the bytes they take.
 int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *base, DeltaWs &ws);
-void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, hipStream_t st);
+// fill: rows of the outputs that no sequence holds.
+void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, const Fill &fill, hipStream_t st);
+struct FillRows {
+    RowsOut o;
+    int cols, esize;
+};
+inline Fill delta_fill(const Seq &s, std::initializer_list<FillRows> outs) {
+    Fill f = {};
+    if (!s.fill || s.rows == 0) return f;
+    for (const FillRows &r : outs) {
+        f.p[f.n] = (uint16_t *)r.o.p, f.ld[f.n] = r.o.ld * (r.esize / 2), f.units[f.n] = r.cols * (r.esize / 2);
+        ++f.n;
+    }
+    f.blocks = (int)std::min<int64_t>((s.rows + 255) / 256, 1024);
+    return f;
+}
 
 // The joining of segments; `back`: of gradients, from the last segment to the first.
 hipError_t launch_delta_join(const Seq &s, const Delta &d, const DeltaWs &ws, bool back, hipStream_t st);
@@ -215,6 +231,21 @@ template <int DKB> __device__ __forceinline__ void store_state(__amdgpu_buffer_r
     const uint32_t base = at + 4 * half * ld;
 #pragma unroll
     for (int i = 0; i < 16 * DKB; ++i) store_at(r, base + (32 * (i >> 4) + acc_row(i & 15, 0)) * ld, S[i >> 4][i & 15]);
+}
+
+// What a segment makes of a state: 32 columns of the offset, or (from slice `slices` on) of the matrix, as rows of its transpose.
+template <int DKB> __device__ __forceinline__ void store_sum(float *sums, int slices, int slice, int lane, const acc_t (&S)[DKB]) {
+    const int half = lane >> 5, col = lane & 31, offset = 32 * DKB * 32 * slices;
+    if (slice < slices) {
+        store_state<DKB>(make_rsrc(sums, 4 * offset), 4 * (32 * slice + col), 128 * slices, half, S);
+    } else if (slice < slices + DKB) {
+        float *p = sums + offset + (32 * (slice - slices) + col) * 32 * DKB + 4 * half;
+#pragma unroll
+        for (int i = 0; i < 4 * DKB; ++i) {
+            const float f[4] = {S[i >> 2][4 * (i & 3)], S[i >> 2][4 * (i & 3) + 1], S[i >> 2][4 * (i & 3) + 2], S[i >> 2][4 * (i & 3) + 3]};
+            store_f32(p + 8 * i, f);
+        }
+    }
 }
 
 // Four neighbouring columns of a row where all four are the head's, of which `left` are; else zeros.  The address need only

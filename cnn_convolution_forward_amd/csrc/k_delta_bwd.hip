@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
     const int64_t slot0 = first_block(s, ws.per, b, first);
     const int state = d.Dk * d.Dv;
     const uint32_t lds0 = lds_address(lds);
-    const uint32_t ld_m = 128 * (slices + DKB), at_m = 4 * c;
+    const uint32_t ld_m = 128 * slices, at_m = 4 * c;
     const int size = 32 * DKB * 32 * (slices + DKB);
     float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
 
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
         wait_copies();
     }
     if constexpr (SUM) {
-        store_state<DKB>(make_rsrc(sums, 4 * size), slice < slices + DKB ? at_m : kOob, ld_m, half, S);
+        store_sum<DKB>(sums, slices, slice, lane, S);
         return;
     }
     if (ds0 && seg == 0) store_state<DKB>(make_rsrc(ds0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
@@ -808,16 +808,6 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
     }
 }
 
-// Rows of one output that no sequence holds; `units` of two bytes to a row.
-__global__ __launch_bounds__(256) void delta_fill_kernel(Seq s, Fill f) { fill_rows(s, f, blockIdx.x, gridDim.x); }
-void fill(const Seq &s, const RowsOut &o, int cols, int esize, hipStream_t st) {
-    if (!s.fill || s.rows == 0) return;
-    Fill f = {};
-    f.p[0] = (uint16_t *)o.p, f.ld[0] = o.ld * (esize / 2), f.n = 1, f.units = cols * (esize / 2);
-    f.blocks = (int)std::min<int64_t>((s.rows + 255) / 256, 1024);
-    delta_fill_kernel<<<f.blocks, 256, 0, st>>>(s, f);
-}
-
 template <typename T, int DKB, bool SUM>
 hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, Rows dy, const float *dsT, float *ds0, hipStream_t st) {
     typedef ChainPages<DKB, sizeof(T) == 2 ? 1 : 2> P;
@@ -862,12 +852,8 @@ hipError_t launch_delta_bwd(const Seq &s, const Delta &d, bool bf16, const Delta
     DeltaWs ws;
     delta_layout(s, d, bf16, true, base, ws);
     const int e = bf16 ? 2 : 4;
-    fill(s, dq, d.H * d.Dk, e, st);
-    fill(s, dk, d.H * d.Dk, e, st);
-    fill(s, dv, d.Hv * d.Dv, e, st);
-    fill(s, dg, d.Hv, 4, st);
-    fill(s, dbeta, d.Hv, 4, st);
-    if (ws.blocks > 0) launch_delta_prep(s, d, bf16, true, ws, in, st);
+    const Fill fill = delta_fill(s, {{dq, d.H * d.Dk, e}, {dk, d.H * d.Dk, e}, {dv, d.Hv * d.Dv, e}, {dg, d.Hv, 4}, {dbeta, d.Hv, 4}});
+    if (ws.blocks > 0) launch_delta_prep(s, d, bf16, true, ws, in, fill, st);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const GradOut out{dq, dk, dv, dg, dbeta};

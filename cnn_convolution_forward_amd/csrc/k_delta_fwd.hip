@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
     const int state = d.Dk * d.Dv;
     const uint32_t lds0 = lds_address(lds);
     // in front of a later segment, the state that joining left in the place of the last one's offset
-    const uint32_t ld_m = 128 * (slices + DKB), at_m = 4 * c;
+    const uint32_t ld_m = 128 * slices, at_m = 4 * c;
     const int size = 32 * DKB * 32 * (slices + DKB);
     float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
 
@@ -273,14 +273,11 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         __builtin_amdgcn_wave_barrier();
     }
     if constexpr (SUM) {
-        store_state<DKB>(make_rsrc(sums, 4 * size), slice < slices + DKB ? at_m : kOob, ld_m, half, S);
+        store_sum<DKB>(sums, slices, slice, lane, S);
         return;
     }
     if (sT && blocks == all) store_state<DKB>(make_rsrc(sT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
 }
-
-// Rows of y that no sequence holds.
-template <typename T> __global__ __launch_bounds__(256) void delta_fill_kernel(Seq s, Fill f) { fill_rows(s, f, blockIdx.x, gridDim.x); }
 
 template <typename T, int DKB, bool SUM>
 hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, const float *s0, RowsOut y, float *sT,
@@ -310,8 +307,6 @@ hipError_t fwd(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &i
 template <typename T>
 hipError_t run(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, const float *s0, RowsOut y, float *sT,
                float *states, hipStream_t st) {
-    const Fill f = fill_of<T>(s, 4, {(T *)y.p}, {y.ld});
-    if (f.blocks) delta_fill_kernel<T><<<f.blocks, 256, 0, st>>>(s, f);
     switch ((d.Dk + 31) / 32) {
     case 1: return fwd<T, 1>(s, d, ws, in, s0, y, sT, states, st);
     case 2: return fwd<T, 2>(s, d, ws, in, s0, y, sT, states, st);
@@ -331,7 +326,7 @@ hipError_t launch_delta_fwd(const Seq &s, const Delta &d, bool bf16, const Delta
                             float *states, void *base, hipStream_t st) {
     DeltaWs ws;
     delta_layout(s, d, bf16, false, base, ws);
-    if (ws.blocks > 0) launch_delta_prep(s, d, bf16, false, ws, in, st);
+    if (ws.blocks > 0) launch_delta_prep(s, d, bf16, false, ws, in, delta_fill(s, {{y, d.Hv * d.Dv, bf16 ? 2 : 4}}), st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return bf16 ? run<uint16_t>(s, d, ws, in, s0, y, sT, states, st) : run<float>(s, d, ws, in, s0, y, sT, states, st);

@@ -310,6 +310,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d,
     }
 }
 
+__global__ __launch_bounds__(kThreads) void delta_fill_kernel(Seq s, Fill f) { fill_rows(s, f, blockIdx.x, gridDim.x); }
+
 template <typename T, bool BWD>
 void prep(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn &in, hipStream_t st) {
     const dim3 grid((unsigned)(ws.blocks * d.H));
@@ -359,33 +361,31 @@ __global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, De
     int len;
     seq_range(s, bh / d.Hv, first, len);
     const int blocks = (len + kBlock - 1) / kBlock, n = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
-    const int ld = 32 * (slices + DKB), size = 32 * DKB * ld;
+    const int ld = 32 * slices, offset = 32 * DKB * ld, size = offset + 1024 * DKB * DKB;
     float *base = ws.sums + (int64_t)bh * ws.segments * size;
     const uint32_t at = 4 * (32 * slice + col) + 32 * wave * 4 * ld;    // the wave's rows
     if (n < 3) return;
     const auto segment = [&](int i) { return base + (int64_t)(back ? n - 1 - i : i) * size; };
-    f4_t row[4 * DKB];
+    float row[16 * DKB];                                                // the lane's row of M, in the order of a page's places
     acc_t S[1], N[1], next[1];
     const auto fetch = [&](int i) {
-        const float *p = segment(i) + (int64_t)(32 * wave + col) * ld + 32 * slices + 4 * half;
+        const float *p = segment(i) + offset + 32 * wave + col + 4 * half * 32 * DKB;
 #pragma unroll
-        for (int u = 0; u < 4 * DKB; ++u) row[u] = *reinterpret_cast<const f4_t *>(p + 8 * u);
-        load_state<1>(make_rsrc(segment(i), 4 * size), at, 4 * ld, half, next);
+        for (int u = 0; u < 16 * DKB; ++u) row[u] = p[page_at(u >> 3, 0, u & 7) * 32 * DKB];
+        load_state<1>(make_rsrc(segment(i), 4 * offset), at, 4 * ld, half, next);
     };
-    load_state<1>(make_rsrc(segment(0), 4 * size), at, 4 * ld, half, S);
+    load_state<1>(make_rsrc(segment(0), 4 * offset), at, 4 * ld, half, S);
     fetch(1);
     for (int i = 1; i < n - 1; ++i) {
         float m = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4 * DKB; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(row[u][j]));
+        for (int u = 0; u < 16 * DKB; ++u) m = fmaxf(m, fabsf(row[u]));
 #pragma unroll
         for (int u = 1; u < 64; u <<= 1) m = fmaxf(m, __shfl_xor(m, u));
         const float sm = pow2_scale(m), im = pow2_inv(sm);
         Pair w[2 * DKB];
 #pragma unroll
-        for (int u = 0; u < 2 * DKB; ++u) w[u] = split8(sm, [&](int j) { return row[2 * u + (j >> 2)][j & 3]; });
+        for (int u = 0; u < 2 * DKB; ++u) w[u] = split8(sm, [&](int j) { return row[8 * u + j]; });
         N[0] = next[0];
         if (i + 1 < n - 1) fetch(i + 1);
         const float sc = pow2_scale(max_halves(max_abs(S[0])));
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, De
             for (int x = 0; x < 16; ++x) N[0][x] = fmaf(a[x] * im, f, N[0][x]);
         }
         S[0] = N[0];
-        store_state<1>(make_rsrc(segment(i), 4 * size), at, 4 * ld, half, S);
+        store_state<1>(make_rsrc(segment(i), 4 * offset), at, 4 * ld, half, S);
     }
 }
 
@@ -452,7 +452,9 @@ int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *ba
     return at;
 }
 
-void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, hipStream_t st) {
+void launch_delta_prep(const Seq &s, const Delta &d, bool bf16, bool bwd, const DeltaWs &ws, const DeltaIn &in, const Fill &fill, hipStream_t st) {
+    // a launch of its own (4.5 us): workgroups of the kernel below in its place made that one slower for everybody (122 to 154 us)
+    if (fill.blocks) delta_fill_kernel<<<fill.blocks, kThreads, 0, st>>>(s, fill);
     if (bf16) bwd ? prep<uint16_t, true>(s, d, ws, in, st) : prep<uint16_t, false>(s, d, ws, in, st);
     else bwd ? prep<float, true>(s, d, ws, in, st) : prep<float, false>(s, d, ws, in, st);
 }

@@ -157,12 +157,13 @@ __device__ __forceinline__ Block packed_block(const Seq &s, int tokens, int64_t 
     return t;
 }
 
-// Rows of up to three outputs that no sequence holds, to be set to zero: 64 rows to a wave, `blocks`
+// Rows of up to five outputs that no sequence holds, to be set to zero: 64 rows to a wave, `blocks`
 // workgroups for all of them (0: nothing is filled).  Rows are counted in units of two bytes.
 struct Fill {
-    uint16_t *p[3];
-    int64_t ld[3];
-    int n, units, blocks;
+    uint16_t *p[5];
+    int64_t ld[5];
+    int units[5];
+    int n, blocks;
 };
 template <typename T> Fill fill_of(const Seq &s, int waves, std::initializer_list<T *> out, std::initializer_list<int64_t> ld) {
     constexpr int e = sizeof(T) / 2;
@@ -170,8 +171,7 @@ template <typename T> Fill fill_of(const Seq &s, int waves, std::initializer_lis
     if (!s.fill || s.rows == 0) return f;
     for (T *o : out) f.p[f.n++] = (uint16_t *)o;
     int i = 0;
-    for (int64_t l : ld) f.ld[i++] = l * e;
-    f.units = s.C * e;
+    for (int64_t l : ld) f.units[i] = s.C * e, f.ld[i++] = l * e;
     f.blocks = (int)std::min<int64_t>((s.rows + 64 * waves - 1) / (64 * waves), 1024);
     return f;
 }
@@ -197,11 +197,12 @@ __device__ __forceinline__ void fill_rows(const Seq &s, const Fill &f, int64_t k
             const int64_t row = r0 + __builtin_ctzll(open);
             for (int o = 0; o < f.n; ++o) {
                 uint16_t *p = f.p[o] + row * f.ld[o];
-                for (int c = 8 * lane; c < f.units; c += 8 * 64) {
-                    if (c + 8 <= f.units) {
+                const int units = f.units[o];
+                for (int c = 8 * lane; c < units; c += 8 * 64) {
+                    if (c + 8 <= units) {
                         store_pack(p + c, make_uint4(0, 0, 0, 0));
                     } else {
-                        for (int q = c; q < f.units; ++q) p[q] = 0;
+                        for (int q = c; q < units; ++q) p[q] = 0;
                     }
                 }
             }
