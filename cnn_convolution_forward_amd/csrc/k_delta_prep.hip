@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d,
     Tiles *xs = reinterpret_cast<Tiles *>(shared);
     Square &A = *reinterpret_cast<Square *>(shared), &Ti = *reinterpret_cast<Square *>(shared + sizeof(Square));
     __shared__ double G[kBlock];
-    __shared__ float kap[2][kBlock], size[2][kBlock], bt[kBlock], red[8];
+    __shared__ float kap[2][kBlock], size[2][kBlock], betas[2][kBlock], red[8];
     const int64_t slot = blockIdx.x / d.H;
     const int hk = (int)(blockIdx.x % d.H);
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
@@ -168,6 +168,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d,
     for (int hv = hk * d.group; hv < (hk + 1) * d.group; ++hv) {
         const int64_t rec = slot * d.Hv + hv;
         float *rows = ws.rows + rec * kRowsFloats;
+        float *bt = betas[hv & 1];                                      // by turns: the last head's pages of T may still be on their way
         if (wave == 0) {
             const float gv = lane < n ? g[(r0 + lane) * ldg + hv] : 0.f, b = lane < n ? beta[(r0 + lane) * ldb + hv] : 0.f;
             double v = gv < -1e4f ? -1e4 : (double)gv;                  // a NaN stays
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d,
             }
             if (lane == 63) rows[kGamma] = E;
         }
-        __syncthreads();                                                // also: keys and queries, or the last head's arrays, are free
+        __syncthreads();                                                // also: keys and queries, or the last head's A and T, are free
         acc_t val[2];
         float pm = 0.f;
 #pragma unroll

@@ -319,6 +319,23 @@ def test_same_bits_in_any_batch_and_at_any_time():
         assert torch.equal(g1[5][0], grads[5][i])
 
 
+@pytest.mark.parametrize("dt,lens,dk,dv", [("bf16", [64 * 200], 64, 96), ("f32", [64 * 120], 64, 96), ("bf16", [1000] * 8, 128, 128), ("bf16", [70] * 64, 32, 32)],
+                         ids=["segments", "segments-f32", "equal", "short"])
+def test_shared_heads_are_the_same_as_repeated_ones(dt, lens, dk, dv):
+    """Queries and keys of a group of value heads, once for all of them and once for each: the same bits, however many workgroups run at once."""
+    c = Case(dt, lens, 4, 16, dk, dv, g=lambda r, s: -np.exp(r.uniform(-9, -2, s)))
+    q, k, *rest = c.data()
+    o = dict(scale=c.scale, unit=True, eps=c.eps)
+    want = B.delta_rule(q.repeat_interleave(4, -2), k.repeat_interleave(4, -2), *rest, s0=c.s0, with_states=True, **o)
+    back = B.delta_rule_backward(q.repeat_interleave(4, -2), k.repeat_interleave(4, -2), *rest, c.dy, want[2], ds=c.ds, **o)
+    for _ in range(4):
+        got = [B.delta_rule(q, k, *rest, s0=c.s0, with_states=True, **o) for _ in range(2)]
+        grads = [B.delta_rule_backward(q, k, *rest, c.dy, want[2], ds=c.ds, **o) for _ in range(2)]
+        assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+        assert all(torch.equal(a, b) for g in grads for a, b in zip(g[2:], back[2:]))
+        assert all(torch.equal(a, b) for a, b in zip(grads[0][:2], grads[1][:2]))
+
+
 # ---- what does not belong to a sequence ------------------------------------------------
 
 @pytest.mark.parametrize("off,rows,max_len", [([7, 40, 40, 140], 171, 100), ([0, 300, 300, 400], 500, 130), ([0, 0, 0], 70, 1), ([0, 0], 90, 0),
