@@ -166,18 +166,19 @@ __device__ __forceinline__ Block find_block(const Seq &s, int per, int64_t n) {
 // ---- memory ----
 
 // Pages from global memory to LDS, asynchronously: four to a workgroup's wave in turn.  The instruction takes the
-// LDS address from M0 (one wait state after it is written) and adds its offset on both sides.  In assembly because the
+// LDS address from M0 (one wait state after it is written) and adds its offset on both sides; five states cover a base
+// that a vector instruction wrote just before, which the compiler does not look for here.  In assembly because the
 // compiler, which cannot tell one buffer from the other, waits for all such loads before any
 // read of LDS.  They have no output registers; wait_copies is their wait.  Nothing else here uses M0.
 __device__ __forceinline__ void copy4(const uint4 *src, uint32_t dst, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:2048\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072"
                  :
                  : "s"(dst), "v"(at), "s"(src)
                  : "memory");
 }
 __device__ __forceinline__ void copy1(const uint4 *src, uint32_t dst, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(at), "s"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(at), "s"(src) : "memory");
 }
 template <int PAGES> __device__ __forceinline__ void copy_pages(const void *from, uint32_t dst, int wave, int waves, int lane) {
     const uint4 *src = (const uint4 *)from;
