@@ -42,8 +42,12 @@ template <typename T, int N> __device__ __forceinline__ void load_part(const T *
     }
 }
 
+// Three workgroups to a compute unit (168 registers: one more makes it two, and 8 x 2048 x 16 heads of 128 take 30 us longer), where
+// LDS has room for three.
+constexpr int resident(int parts, int dkb) { return parts * dkb > 4 ? 2 : 3; }
+
 template <typename T, int DKB, bool BWD>
-__global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
+__global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
                                                               const T *__restrict__ k, int64_t ldk,
                                                               const float *__restrict__ g, int64_t ldg,
                                                               const float *__restrict__ beta, int64_t ldb) {
