@@ -93,7 +93,8 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[which][i]));
             m = fmaxf(m, __shfl_xor(m, 1));
             m = fmaxf(m, __shfl_xor(m, 2));
-            const float sc = pow2_scale(m, 60);
+            // with unit = 0 the factor stays far from the smallest numbers, as states may be small too
+            const float sc = pow2_scale(m, d.unit ? 113 : 60);
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
@@ -111,8 +112,10 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             ss += __shfl_xor(ss, 1);
             ss += __shfl_xor(ss, 2);
             if ((tid & 3) == 0) {
-                // unit length: x / sqrt(sum x^2 + eps) with sum x^2 = ss / sc^2; a row of zeros stays
-                const float f0 = !d.unit ? pow2_inv(sc) : ss == 0.f ? 0.f : 1.f / sqrtf(ss + d.eps * sc * sc);
+                // unit length: x / sqrt(sum x^2 + eps) with sum x^2 = ss / sc^2.  A row of zeros stays, and its gradient has the
+                // factor 1 / sqrt(eps) (none without eps); past fp32, eps is all of the sum.
+                const float e2 = d.eps * sc * sc;
+                const float f0 = !d.unit ? pow2_inv(sc) : isinf(e2) ? 1.f / (sqrtf(d.eps) * sc) : ss + e2 == 0.f ? 0.f : 1.f / sqrtf(ss + e2);
                 kap[which][row] = f0;
                 size[which][row] = f0 * sc;
             }

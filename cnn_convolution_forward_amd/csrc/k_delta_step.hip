@@ -40,7 +40,8 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(Delta d, int slice
                                                               int64_t ldv, const float *__restrict__ g, int64_t ldg,
                                                               const float *__restrict__ beta, int64_t ldb,
                                                               float *__restrict__ S, T *__restrict__ y, int64_t ldy) {
-    __shared__ float qk[2][kMaxDim], part[4][2 * kCols + 1], size[4];
+    __shared__ float qk[2][kMaxDim], part[4][2 * kCols + 1];
+    __shared__ double size[4];
     const int slice = blockIdx.x % slices;
     const int64_t bh = blockIdx.x / slices;
     const int b = (int)(bh / d.Hv), h = (int)(bh % d.Hv), hk = h / d.group;
@@ -60,12 +61,13 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(Delta d, int slice
         float f[1] = {0.f};
         if (i < d.Dk) load_f32<T, 1>(p + hk * d.Dk + i, f);
         if (d.unit) {
-            float n = f[0] * f[0];
+            double n = (double)f[0] * f[0];                             // every square is in fp64's range
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
             if ((threadIdx.x & 63) == 0) size[wave] = n;
             __syncthreads();
-            f[0] *= 1.f / sqrtf(size[2 * which] + size[2 * which + 1] + d.eps);
+            n = size[2 * which] + size[2 * which + 1] + (double)d.eps;
+            f[0] = n == 0.0 ? 0.f : (float)(f[0] / sqrt(n));            // a row of zeros stays
         }
         qk[which][i] = f[0];
         __syncthreads();

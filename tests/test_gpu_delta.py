@@ -255,6 +255,37 @@ def test_rows_of_zeros():
         assert bool((y[:, 1::4] == 0).all()) and all(bool(torch.isfinite(t).all()) for t in (y, sT) + grads)
 
 
+@pytest.mark.parametrize("dt,eps,packed", [("bf16", 1e-6, False), ("f32", 1e-2, True), ("f32", 1e4, False)])
+def test_gradients_of_rows_of_zeros(dt, eps, packed):
+    """x / sqrt(sum x^2 + eps) has the slope 1 / sqrt(eps) at zero (a padded batch's keys and queries)."""
+    c = Case(dt, [40, 70] if packed else [70] * 2, 2, 4, 32, 48, packed=packed, eps=eps)
+    c.k[..., ::3, :, :] = 0
+    c.q[..., 1::4, :, :] = 0
+    got = _whole(c)
+    assert bool((got[3][1][..., ::3, :, :] != 0).any())
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -60, 2.0 ** 60, 2.0 ** 100])
+def test_unit_length_of_tiny_and_huge_rows(size):
+    """Without eps the unit length does not depend on the size, down to squares far below fp32 and up to those beyond it: the same bits,
+    whole and by steps; and a step leaves rows of zeros, as whole sequences do."""
+    c = Case("f32", [70], 1, 2, 40, 32, eps=0.0)
+    y, sT, st = B.delta_rule(*c.data(), s0=c.s0, with_states=True, **c.opts())
+    q, k, *rest = c.data()
+    y2, sT2 = B.delta_rule(q * size, k * size, *rest, s0=c.s0, **c.opts())
+    assert torch.equal(y, y2) and torch.equal(sT, sT2)
+    grads = [B.delta_rule_backward(q * f, k * f, *rest, c.dy, st, ds=c.ds, **c.opts()) for f in (1.0, size)]
+    assert torch.equal(grads[0][2], grads[1][2]) and torch.equal(grads[0][5], grads[1][5])
+    assert torch.equal(grads[0][0], grads[1][0] * size) and torch.equal(grads[0][1], grads[1][1] * size)
+    o = dict(scale=c.scale, unit=True, eps=0.0)
+    out = []
+    for f in (1.0, size, 0.0):
+        s = c.s0.clone()
+        out.append((B.delta_rule_step(q[:, 0] * f, k[:, 0] * f, *(t[:, 0] for t in rest), s, **o), s))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert bool((out[2][0] == 0).all()) and float((out[2][1] - c.s0 * torch.exp(c.g[:, 0])[..., None, None]).abs().max()) <= 1e-6
+
+
 # ---- token by token, and in parts --------------------------------------------------
 
 @pytest.mark.parametrize("dt,H,Hv,dk,dv,unit", [("bf16", 2, 4, 128, 128, True), ("f32", 1, 3, 37, 99, False), ("bf16", 1, 1, 1, 1, False),
