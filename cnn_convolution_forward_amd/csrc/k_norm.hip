@@ -7,11 +7,15 @@
 //
 // A dozen operations for four to six bytes: HBM is the bound, so each row is
 // read once and held in registers between its sums and its result.  G threads
-// share a row: 16 (four rows to a wave, no barrier), 64, or the whole
-// workgroup with its sums joined in LDS; the fewest with which a thread holds at
-// most 32 channels.  A thread keeps its channels, their weights, bias and sums
+// share a row: 16 (four rows to a wave, no barrier), 64, or a whole workgroup of
+// 256 to 1024 with its sums joined in LDS; the fewest with which a thread holds at
+// most 32 channels (16 where it has 128 registers).  A thread keeps its channels, their weights, bias and sums
 // of gradients in registers while its group walks through rows; the next row is
-// loaded before the present one's sums.  Rows too wide for that are read again.
+// loaded before the present one's sums.  Rows too wide for that, of more than 16384 channels, are read again.
+//
+// bf16, forward and backward: 16384 x 2048 25 us (5.4 TB/s) and 39 us (5.1), 4096 x 8192 26 (5.2) and
+// 50 (4.0; with 256 threads to a row 59), 2048 x 16384 32 (4.2) and 71 (2.9: one workgroup to a compute unit, whose
+// barriers nothing hides).  Rows that are read again: 2048 x 20480 81 and 324 us.
 //
 // The variance is a second sum over the registers, of squared distances from the
 // mean: no cancellation.  Sums over rows: each workgroup adds its own rows, and a
@@ -21,7 +25,9 @@
 namespace convfwd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                          // of a workgroup, but for rows that take more
+constexpr int kWide = 1024;                             // for rows that no workgroup holds
+constexpr int threads_of(int G) { return G > kThreads ? G : kThreads; }
 // Workgroups that walk through the rows.  Backward, each has a row of partial sums: 256 of them are enough to fill the chip
 // with wide rows (16384 x 2048 bf16: 39.4 us, with 512 43.8), narrow ones have shorter sums and want more waves (131072 x 128:
 // 24.2 us with 512, 31.2 with 256).  Forward: 25.4 us at 768, 27.2 at 1024, 66 with a workgroup for every four rows.
@@ -104,11 +110,11 @@ __device__ __forceinline__ void load_param(const float *p, float other, int li, 
 }
 
 template <typename T, int VEC, int NV, int G, bool ONCE>
-__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(int64_t rows, int C, float eps, const T *__restrict__ x,
+__global__ __launch_bounds__(threads_of(G)) void norm_fwd_kernel(int64_t rows, int C, float eps, const T *__restrict__ x,
                                                             int64_t ldx, const float *__restrict__ w,
                                                             const float *__restrict__ b, T *__restrict__ y, int64_t ldy,
                                                             float *__restrict__ mean, float *__restrict__ rstd) {
-    constexpr int kRows = kThreads / G;
+    constexpr int kRows = threads_of(G) / G;
     __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
     int phase = 0;
     const int li = threadIdx.x % G;
@@ -155,22 +161,22 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(int64_t rows, int C,
 
 // Rows wider than the registers: one workgroup to a row, which is read three times, mostly from the cache.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void norm_fwd_wide_kernel(int64_t rows, int C, float eps, const T *__restrict__ x,
+__global__ __launch_bounds__(kWide) void norm_fwd_wide_kernel(int64_t rows, int C, float eps, const T *__restrict__ x,
                                                                  int64_t ldx, const float *__restrict__ w,
                                                                  const float *__restrict__ b, T *__restrict__ y,
                                                                  int64_t ldy, float *__restrict__ mean,
                                                                  float *__restrict__ rstd) {
-    __shared__ float red[2 * kThreads / 64];
+    __shared__ float red[2 * kWide / 64];
     int phase = 0;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const T *p = x + r * ldx;
         float f[1], s = 0.f;
-        for (int c = threadIdx.x; c < C; c += kThreads) load_f32<T, 1>(p + c, f), s += f[0];
-        const float m = group_sum<kThreads>(s, red, phase) / (float)C;
+        for (int c = threadIdx.x; c < C; c += kWide) load_f32<T, 1>(p + c, f), s += f[0];
+        const float m = group_sum<kWide>(s, red, phase) / (float)C;
         s = 0.f;
-        for (int c = threadIdx.x; c < C; c += kThreads) load_f32<T, 1>(p + c, f), s = fmaf(f[0] - m, f[0] - m, s);
-        const float k = 1.f / sqrtf(group_sum<kThreads>(s, red, phase) / (float)C + eps);
-        for (int c = threadIdx.x; c < C; c += kThreads) {
+        for (int c = threadIdx.x; c < C; c += kWide) load_f32<T, 1>(p + c, f), s = fmaf(f[0] - m, f[0] - m, s);
+        const float k = 1.f / sqrtf(group_sum<kWide>(s, red, phase) / (float)C + eps);
+        for (int c = threadIdx.x; c < C; c += kWide) {
             load_f32<T, 1>(p + c, f);
             const float o[1] = {fmaf((f[0] - m) * k, w ? w[c] : 1.f, b ? b[c] : 0.f)};
             store_f32(y + r * ldy + c, o);
@@ -184,12 +190,12 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_wide_kernel(int64_t rows, i
 
 // part: per workgroup C sums of dy xh, then C sums of dy; NULL: not wanted.
 template <typename T, int VEC, int NV, int G, bool ONCE>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C, const T *__restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(threads_of(G)) void norm_bwd_kernel(int64_t rows, int C, const T *__restrict__ x, int64_t ldx,
                                                             const float *__restrict__ w, const float *__restrict__ mean,
                                                             const float *__restrict__ rstd, const T *__restrict__ dy,
                                                             int64_t lddy, T *__restrict__ dx, int64_t lddx,
                                                             float *__restrict__ part) {
-    constexpr int kRows = kThreads / G, kWidth = G * VEC * NV;
+    constexpr int kRows = threads_of(G) / G, kWidth = G * VEC * NV;
     __shared__ float red[2 * (G > 64 ? G / 64 : 1)];
     __shared__ float sums[kRows > 1 ? kRows * kWidth : 1];
     int phase = 0;
@@ -204,7 +210,9 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
         ny.load(dy + r * lddy, li, C);
         nm = mean[r], nk = rstd[r];
     }
-    load_param<VEC, NV, G>(w, 1.f, li, C, wf);
+    // 1024 threads have 128 registers each: weights are read again for each row, from the cache
+    constexpr bool kHold = G < 1024;
+    if constexpr (kHold) load_param<VEC, NV, G>(w, 1.f, li, C, wf);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -221,6 +229,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
         float f[NV][VEC], g[NV][VEC], s0 = 0.f, s1 = 0.f;
         cx.get(f);
         cy.get(g);
+        if constexpr (!kHold) {
+            asm volatile("" : "+s"(w));                                  // in the loop
+            load_param<VEC, NV, G>(w, 1.f, li, C, wf);
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -252,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) sums[gi * kWidth + (i * G + li) * VEC + j] = q ? db[i][j] : dw[i][j];
             __syncthreads();
-            for (int c = threadIdx.x; c < C; c += kThreads) {
+            for (int c = threadIdx.x; c < C; c += kThreads) {       // kRows > 1: kThreads of them
                 float s = sums[c];
 #pragma unroll
                 for (int i = 1; i < kRows; ++i) s += sums[i * kWidth + c];
@@ -272,19 +284,19 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(int64_t rows, int C,
 
 // One workgroup to a block of rows: a channel's sums are kept in memory, by the thread that owns it.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(int64_t rows, int C, const T *__restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(kWide) void norm_bwd_wide_kernel(int64_t rows, int C, const T *__restrict__ x, int64_t ldx,
                                                                  const float *__restrict__ w, const float *__restrict__ mean,
                                                                  const float *__restrict__ rstd, const T *__restrict__ dy,
                                                                  int64_t lddy, T *__restrict__ dx, int64_t lddx,
                                                                  float *__restrict__ part) {
-    __shared__ float red[2 * kThreads / 64];
+    __shared__ float red[2 * kWide / 64];
     int phase = 0;
     float *out = part ? part + (int64_t)blockIdx.x * 2 * C : nullptr;
     bool first = true;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, first = false) {
         const float m = mean[r], k = rstd[r];
         float f[1], g[1], s0 = 0.f, s1 = 0.f;
-        for (int c = threadIdx.x; c < C; c += kThreads) {
+        for (int c = threadIdx.x; c < C; c += kWide) {
             load_f32<T, 1>(x + r * ldx + c, f);
             load_f32<T, 1>(dy + r * lddy + c, g);
             const float h = (f[0] - m) * k;
@@ -296,9 +308,9 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(int64_t rows, i
             s0 += g[0];
             s1 = fmaf(g[0], h, s1);
         }
-        s0 = group_sum<kThreads>(s0, red, phase) / (float)C;
-        s1 = group_sum<kThreads>(s1, red, phase) / (float)C;
-        for (int c = threadIdx.x; c < C; c += kThreads) {
+        s0 = group_sum<kWide>(s0, red, phase) / (float)C;
+        s1 = group_sum<kWide>(s1, red, phase) / (float)C;
+        for (int c = threadIdx.x; c < C; c += kWide) {
             load_f32<T, 1>(x + r * ldx + c, f);
             load_f32<T, 1>(dy + r * lddy + c, g);
             const float h = (f[0] - m) * k;
@@ -327,11 +339,12 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict_
     if (out) out[c < C ? c : c - C] = s;
 }
 
-// Threads to a row, and packs to a thread; G = 0: a row does not fit.
+// Threads to a row, and packs to a thread; G = 0: a row does not fit.  From 513 packs on the two directions differ: forward
+// 4096 x 8192 bf16 takes 26 us with 256 threads and 32 with 512, backward, with four times the registers, 59 and 50.
 struct Split {
     int G, NV;
 };
-Split split_of(int C, bool bf16) {
+Split split_of(int C, bool bf16, bool bwd) {
     const int n = (C + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);       // packs
     if (n <= 16) return {16, 1};
     if (n <= 32) return {16, 2};
@@ -339,31 +352,47 @@ Split split_of(int C, bool bf16) {
     if (n <= 128) return {64, 2};
     if (n <= 256) return {64, 4};
     if (n <= 512) return {256, 2};
-    if (n <= 1024) return {256, 4};
+    if (n <= 1024) return bwd ? Split{512, 2} : Split{256, 4};
+    if (n <= 2048) return bwd && !bf16 ? Split{512, 4} : Split{1024, 2};
+    if (n <= 4096 && !bf16) return {1024, 4};
     return {0, 0};
 }
 
-template <typename F> hipError_t pick(int C, bool bf16, F f) {
-    const Split s = split_of(C, bf16);
+template <bool BWD, typename F> hipError_t pick(int C, bool bf16, F f) {
+    const Split s = split_of(C, bf16, BWD);
+#define F32(g, n) \
+    if (s.G == g && s.NV == n && !bf16) return f((float *)0, std::integral_constant<int, g>(), std::integral_constant<int, n>())
 #define CASE(g, n) \
-    if (s.G == g && s.NV == n) return bf16 ? f((uint16_t *)0, std::integral_constant<int, g>(), std::integral_constant<int, n>()) \
-                                           : f((float *)0, std::integral_constant<int, g>(), std::integral_constant<int, n>())
+    F32(g, n);     \
+    if (s.G == g && s.NV == n) return f((uint16_t *)0, std::integral_constant<int, g>(), std::integral_constant<int, n>())
     CASE(16, 1);
     CASE(16, 2);
     CASE(64, 1);
     CASE(64, 2);
     CASE(64, 4);
     CASE(256, 2);
-    CASE(256, 4);
+    if constexpr (BWD) {
+        CASE(512, 2);
+        F32(512, 4);
+    } else {
+        CASE(256, 4);
+        F32(1024, 2);
+    }
+    if (s.G == 1024 && s.NV == 2) return f((uint16_t *)0, std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+    F32(1024, 4);
     CASE(0, 0);
 #undef CASE
+#undef F32
     return hipErrorInvalidValue;
 }
 
-int blocks_of(int64_t rows, int C, bool bf16, int most) {
-    const int G = split_of(C, bf16).G;
-    const int64_t per = G ? kThreads / G : 1;
+int blocks_of(int64_t rows, int G, int most) {
+    const int64_t per = G ? threads_of(G) / G : 1;
     return (int)std::min<int64_t>((rows + per - 1) / per, most);
+}
+int blocks_bwd(int64_t rows, int C, bool bf16) {
+    const int G = split_of(C, bf16, true).G;
+    return blocks_of(rows, G, max_backward(G));
 }
 
 }  // namespace
@@ -371,37 +400,37 @@ int blocks_of(int64_t rows, int C, bool bf16, int most) {
 hipError_t launch_norm_fwd(int64_t rows, int C, bool bf16, float eps, const void *x, int64_t ldx, const float *w, const float *b,
                            void *y, int64_t ldy, float *mean, float *rstd, hipStream_t st) {
     if (rows == 0) return hipSuccess;
-    return pick(C, bf16, [&](auto *t, auto g, auto n) {
+    return pick<false>(C, bf16, [&](auto *t, auto g, auto n) {
         typedef std::remove_pointer_t<decltype(t)> T;
         constexpr int G = decltype(g)::value, NV = decltype(n)::value, VEC = sizeof(T) == 2 ? 8 : 4;
-        const int blocks = blocks_of(rows, C, bf16, kMaxForward);
+        const int blocks = blocks_of(rows, G, kMaxForward);
         if constexpr (G)
-            (read_once(x, ldx, sizeof(T)) ? norm_fwd_kernel<T, VEC, NV, G, true> : norm_fwd_kernel<T, VEC, NV, G, false>)<<<blocks, kThreads, 0, st>>>(
+            (read_once(x, ldx, sizeof(T)) ? norm_fwd_kernel<T, VEC, NV, G, true> : norm_fwd_kernel<T, VEC, NV, G, false>)<<<blocks, threads_of(G), 0, st>>>(
                 rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
         else
-            norm_fwd_wide_kernel<T><<<blocks, kThreads, 0, st>>>(rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
+            norm_fwd_wide_kernel<T><<<blocks, kWide, 0, st>>>(rows, C, eps, (const T *)x, ldx, w, b, (T *)y, ldy, mean, rstd);
         return hipGetLastError();
     });
 }
 
-int64_t norm_bwd_workspace_floats(int64_t rows, int C, bool bf16) { return 2 * (int64_t)C * blocks_of(rows, C, bf16, max_backward(split_of(C, bf16).G)); }
+int64_t norm_bwd_workspace_floats(int64_t rows, int C, bool bf16) { return 2 * (int64_t)C * blocks_bwd(rows, C, bf16); }
 
 hipError_t launch_norm_bwd(int64_t rows, int C, bool bf16, const void *x, int64_t ldx, const float *w, const float *mean,
                            const float *rstd, const void *dy, int64_t lddy, void *dx, int64_t lddx, float *dw, float *db,
                            float *part, hipStream_t st) {
-    const int blocks = blocks_of(rows, C, bf16, max_backward(split_of(C, bf16).G));
+    const int blocks = blocks_bwd(rows, C, bf16);
     if (!dw && !db) part = nullptr;
     hipError_t e = hipSuccess;
     if (rows > 0)
-        e = pick(C, bf16, [&](auto *t, auto g, auto n) {
+        e = pick<true>(C, bf16, [&](auto *t, auto g, auto n) {
             typedef std::remove_pointer_t<decltype(t)> T;
             constexpr int G = decltype(g)::value, NV = decltype(n)::value, VEC = sizeof(T) == 2 ? 8 : 4;
             if constexpr (G)
                 (read_once(x, ldx, sizeof(T)) && read_once(dy, lddy, sizeof(T)) ? norm_bwd_kernel<T, VEC, NV, G, true>
-                                                                          : norm_bwd_kernel<T, VEC, NV, G, false>)<<<blocks, kThreads, 0, st>>>(
+                                                                          : norm_bwd_kernel<T, VEC, NV, G, false>)<<<blocks, threads_of(G), 0, st>>>(
                 rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy, lddy, (T *)dx, lddx, part);
             else
-                norm_bwd_wide_kernel<T><<<blocks, kThreads, 0, st>>>(rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy, lddy,
+                norm_bwd_wide_kernel<T><<<blocks, kWide, 0, st>>>(rows, C, (const T *)x, ldx, w, mean, rstd, (const T *)dy, lddy,
                                                                      (T *)dx, lddx, part);
             return hipGetLastError();
         });

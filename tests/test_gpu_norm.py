@@ -58,6 +58,13 @@ def test_widths(C, dt):
         _both(*_make(C * 10 + n, n, C, dt), 1e-5, dt, (C, n))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,C", [(1, 8194), (700, 8200), (530, 12288), (300, 16379), (530, 16384), (300, 16385), (3, 40000)])
+def test_wide_rows(n, C, dt):
+    """Rows that take a workgroup of 1024 threads, and wider ones; more of them than workgroups too."""
+    _both(*_make(n + C, n, C, dt), 1e-5, dt, (n, C))
+
+
 @pytest.mark.parametrize("dt,n,C", [("bf16", 40000, 128), ("f32", 70001, 33), ("bf16", 9001, 520), ("f32", 2500, 2048), ("bf16", 1300, 9000)])
 def test_many_rows(dt, n, C):
     """More rows than the workgroups take in one turn."""
