@@ -114,7 +114,7 @@ struct DeltaWs {
     uint4 *tri;              // per block and value head, forward: T hi, T lo, P hi, P lo; backward: T, TT, PT, hi and lo
     float *rows;             // per block and value head: kRowsFloats
     float *ends;             // backward: gradients of the states behind the blocks, dk x dv padded to 32s
-    float *sums;             // per sequence, value head and segment: what it makes of a state, an offset dk x dv and a matrix dk x dk,
+    float *sums;             // per segment and value head: what it makes of a state, an offset dk x dv and a matrix dk x dk,
                              // transposed, both padded to 32s
     int segments, seg_blocks;
     int qk_pages, tri_pages;
@@ -154,6 +154,10 @@ inline int waves_of(int64_t chains, int slices) {
 // First block number of sequence b, and block n's place.
 __device__ __forceinline__ int64_t first_block(const Seq &s, int per, int b, int64_t first) {
     return s.off ? first / kBlock + b : (int64_t)b * per;
+}
+// First segment number of sequence b; numbers are unique, as those of blocks are.
+__device__ __forceinline__ int64_t first_segment(const Seq &s, const DeltaWs &ws, int b, int64_t first) {
+    return s.off ? first / ((int64_t)kBlock * ws.seg_blocks) + b : (int64_t)b * ws.segments;
 }
 __device__ __forceinline__ Block find_block(const Seq &s, int per, int64_t n) {
     if (s.off) return packed_block(s, kBlock, n);

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
     const uint32_t lds0 = lds_address(lds);
     const uint32_t ld_m = 128 * slices, at_m = 4 * c;
     const int size = 32 * DKB * 32 * (slices + DKB);
-    float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
+    float *sums = ws.sums + ((first_segment(s, ws, b, first) + seg) * d.Hv + hv) * size;
 
     acc_t S[DKB];
 #pragma unroll
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
     } else if (blocks == all) {
         if (dsT) load_state<DKB>(make_rsrc(dsT + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
     } else if (!SUM) {
-        load_state<DKB>(make_rsrc(sums + size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
+        load_state<DKB>(make_rsrc(sums + (int64_t)d.Hv * size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
     }
 
     const auto fetch = [&](int k) {

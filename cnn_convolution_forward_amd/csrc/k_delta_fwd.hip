@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
     // in front of a later segment, the state that joining left in the place of the last one's offset
     const uint32_t ld_m = 128 * slices, at_m = 4 * c;
     const int size = 32 * DKB * 32 * (slices + DKB);
-    float *sums = ws.sums + ((int64_t)bh * ws.segments + seg) * size;
+    float *sums = ws.sums + ((first_segment(s, ws, b, first) + seg) * d.Hv + hv) * size;
 
     acc_t S[DKB];
 #pragma unroll
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
     } else if (seg == 0) {
         if (s0) load_state<DKB>(make_rsrc(s0 + (int64_t)bh * state, 4 * state), at_s, ld_s, half, S);
     } else if (!SUM) {
-        load_state<DKB>(make_rsrc(sums - size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
+        load_state<DKB>(make_rsrc(sums - (int64_t)d.Hv * size, 4 * size), slice < slices ? at_m : kOob, ld_m, half, S);
     }
 
     const auto fetch = [&](int k) {

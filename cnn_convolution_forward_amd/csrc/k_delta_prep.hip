@@ -14,6 +14,8 @@
 // before.  T: the four 16x16 blocks on the diagonal by substitution, a lane to a
 // column, then the blocks below from the products T_ii A_ij T_jj on the fp32 matrix
 // instructions: three levels instead of 64 steps.
+#include <math.h>
+
 #include "delta_common.h"
 
 namespace convfwd {
@@ -343,14 +345,21 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 // Segments of a sequence: its chain of blocks is cut where there are too few chains to fill the chip's 1024 SIMDs with a wave
 // each.  What a segment makes of any state is a matrix and an offset, found by running it from the identity and from zero
 // (twice the columns); the segments are joined one after another, and run again from their states.  That is
-// three times the work over n times the waves: from four segments on it pays (one sequence of 32768 tokens in 8 heads of 128:
-// NNN us instead of 2638), and a segment has at least four blocks.
+// three times the work over n times the waves (one sequence of 32768 tokens in 8 heads of 128: 410 us instead of 2638).
+// - Waves: packed sequences count as as many of the longest as hold their tokens (9 sequences of 5003 tokens, the longest of 2605,
+//   fp32 in 6 heads of 72 and 99: 121 us, cut for nine of the longest 145).
+// - A block takes 11 us in both passes and the joining of a segment 3: 2 sqrt(blocks) segments are the best number
+//   (backward, 11981 tokens in 16 heads of 64 and 10: 478 us, with 47 segments instead of 27 505).
+// - Fewer than three segments, or than eight blocks, do not pay (8 x 2048 tokens in 16 heads of 128 in two: forward 318 us
+//   instead of 322, backward 950 instead of 914).
+// - Every sequence's workgroups for every segment are launched, and end at once where it has none: at most 16384 waves.
 void cut(const Seq &s, const Delta &d, DeltaWs &ws) {
-    const int blocks = (s.T + kBlock - 1) / kBlock, slices = (d.Dv + 31) / 32;
-    const int64_t waves = (int64_t)s.B * d.Hv * slices;
-    const int n = (int)std::min<int64_t>(1024 / waves, blocks / 4);
-    ws.segments = 1, ws.seg_blocks = std::max(blocks, 1);
-    if (n < 4) return;
+    const int longest = (int)std::min<int64_t>(s.T, s.rows), blocks = (longest + kBlock - 1) / kBlock, slices = (d.Dv + 31) / 32;
+    ws.segments = 1, ws.seg_blocks = std::max((s.T + kBlock - 1) / kBlock, 1);
+    if (blocks < 8) return;
+    const int64_t one = d.Hv * slices, waves = std::min<int64_t>(s.B, (s.rows + longest - 1) / longest) * one;
+    const int n = (int)std::min({1024 / waves, (int64_t)blocks / 2, (int64_t)(2 * sqrt((double)blocks)), 16384 / (s.B * one)});
+    if (n < 3) return;
     ws.seg_blocks = (blocks + n - 1) / n;
     ws.segments = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
 }
@@ -367,13 +376,14 @@ __global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, De
     const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads), slice = (int)(blockIdx.x / heads);
     int64_t first;
     int len;
-    seq_range(s, bh / d.Hv, first, len);
+    const int b = bh / d.Hv, hv = bh % d.Hv;
+    seq_range(s, b, first, len);
     const int blocks = (len + kBlock - 1) / kBlock, n = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
     const int ld = 32 * slices, offset = 32 * DKB * ld, size = offset + 1024 * DKB * DKB;
-    float *base = ws.sums + (int64_t)bh * ws.segments * size;
+    float *base = ws.sums + (first_segment(s, ws, b, first) * d.Hv + hv) * size;
     const uint32_t at = 4 * (32 * slice + col) + 32 * wave * 4 * ld;    // the wave's rows
     if (n < 3) return;
-    const auto segment = [&](int i) { return base + (int64_t)(back ? n - 1 - i : i) * size; };
+    const auto segment = [&](int i) { return base + (int64_t)(back ? n - 1 - i : i) * d.Hv * size; };
     float row[16 * DKB];                                                // the lane's row of M, in the order of a page's places
     acc_t S[1], N[1], next[1];
     const auto fetch = [&](int i) {
@@ -456,7 +466,8 @@ int64_t delta_layout(const Seq &s, const Delta &d, bool bf16, bool bwd, void *ba
     ws.rows = (float *)take(ws.blocks * d.Hv * kRowsFloats * 4);
     ws.ends = bwd ? (float *)take(ws.blocks * d.Hv * dkb * dvb * 4096) : nullptr;
     cut(s, d, ws);
-    ws.sums = ws.segments > 1 ? (float *)take((int64_t)s.B * d.Hv * ws.segments * dkb * (dkb + dvb) * 4096) : nullptr;
+    const int64_t segments = s.off ? s.rows / ((int64_t)kBlock * ws.seg_blocks) + s.B : (int64_t)s.B * ws.segments;
+    ws.sums = ws.segments > 1 ? (float *)take(segments * d.Hv * dkb * (dkb + dvb) * 4096) : nullptr;
     return at;
 }
 

@@ -184,6 +184,14 @@ def test_sequences_in_segments(case):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("dt,max_len", [("bf16", 900), ("f32", 5000)])
+def test_segments_among_many_short_sequences(dt, max_len):
+    """One long sequence among short and empty ones, with the longest given exactly and far too long."""
+    c = Case(dt, [3] * 20 + [900, 0, 0, 640] + [70] * 6, 1, 2, 32, 40, packed=True, g=lambda r, s: -np.exp(r.uniform(-9, -2, s)))
+    c.kw["max_len"] = max_len
+    _whole(c)
+
+
 def test_no_first_state():
     _whole(Case("bf16", [100], 1, 2, 48, 40), s0=False)
 
