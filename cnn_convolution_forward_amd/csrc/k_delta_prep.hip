@@ -16,6 +16,8 @@
 // instructions: three levels instead of 64 steps.
 #include <math.h>
 
+#include <type_traits>
+
 #include "delta_common.h"
 
 namespace convfwd {
@@ -237,6 +239,7 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
         const auto put = [&](int kind, int page, const Pair &p) {
             out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
+            if (!BWD && PARTS == 1 && kind == 1) return;                // P's lo: y of bf16 does without
             out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
         };
         if (which) {                                                    // P or P^T: registers 8 m .. 8 m + 7 are pages
@@ -364,8 +367,8 @@ void cut(const Seq &s, const Delta &d, DeltaWs &ws) {
     ws.segments = (blocks + ws.seg_blocks - 1) / ws.seg_blocks;
 }
 
-// S' = M S + N from segment to segment: a workgroup to 32 columns, a wave to 32 rows of them.  M is loaded and split a
-// segment ahead; S goes through LDS as pages, each wave's under its own powers of two, so that one barrier is all that a
+// S' = M S + N from segment to segment: a workgroup to 32 columns, a wave to 32 rows of them.  M is loaded two
+// segments ahead; S goes through LDS as pages, each wave's under its own powers of two, so that one barrier is all that a
 // segment waits for.  N makes way for S'.
 template <int DKB>
 __global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, DeltaWs ws, int slices, bool back) {
@@ -384,53 +387,60 @@ __global__ __launch_bounds__(64 * DKB) void delta_join_kernel(Seq s, Delta d, De
     const uint32_t at = 4 * (32 * slice + col) + 32 * wave * 4 * ld;    // the wave's rows
     if (n < 3) return;
     const auto segment = [&](int i) { return base + (int64_t)(back ? n - 1 - i : i) * d.Hv * size; };
-    float row[16 * DKB];                                                // the lane's row of M, in the order of a page's places
-    acc_t S[1], N[1], next[1];
-    const auto fetch = [&](int i) {
+    // by turns, two segments ahead: the lane's row of M, in the order of a page's places, and N
+    float row[2][16 * DKB];
+    acc_t S[1], N[1], next[2][1];
+    const auto fetch = [&](int i, float(&r)[16 * DKB], acc_t(&to)[1]) {
         const float *p = segment(i) + offset + 32 * wave + col + 4 * half * 32 * DKB;
 #pragma unroll
-        for (int u = 0; u < 16 * DKB; ++u) row[u] = p[page_at(u >> 3, 0, u & 7) * 32 * DKB];
-        load_state<1>(make_rsrc(segment(i), 4 * offset), at, 4 * ld, half, next);
+        for (int u = 0; u < 16 * DKB; ++u) r[u] = p[page_at(u >> 3, 0, u & 7) * 32 * DKB];
+        load_state<1>(make_rsrc(segment(i), 4 * offset), at, 4 * ld, half, to);
     };
     load_state<1>(make_rsrc(segment(0), 4 * offset), at, 4 * ld, half, S);
-    fetch(1);
-    for (int i = 1; i < n - 1; ++i) {
+    fetch(1, row[1], next[1]);
+    if (n > 3) fetch(2, row[0], next[0]);
+    const auto step = [&](int i, auto turn) {
+        constexpr int x = decltype(turn)::value;
         float m = 0.f;
 #pragma unroll
-        for (int u = 0; u < 16 * DKB; ++u) m = fmaxf(m, fabsf(row[u]));
+        for (int u = 0; u < 16 * DKB; ++u) m = fmaxf(m, fabsf(row[x][u]));
 #pragma unroll
         for (int u = 1; u < 64; u <<= 1) m = fmaxf(m, __shfl_xor(m, u));
         const float sm = pow2_scale(m), im = pow2_inv(sm);
         Pair w[2 * DKB];
 #pragma unroll
-        for (int u = 0; u < 2 * DKB; ++u) w[u] = split8(sm, [&](int j) { return row[8 * u + j]; });
-        N[0] = next[0];
-        if (i + 1 < n - 1) fetch(i + 1);
+        for (int u = 0; u < 2 * DKB; ++u) w[u] = split8(sm, [&](int j) { return row[x][8 * u + j]; });
+        N[0] = next[x][0];
+        if (i + 2 < n - 1) fetch(i + 2, row[x], next[x]);
         const float sc = pow2_scale(max_halves(max_abs(S[0])));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const Pair f = split8(sc, [&](int j) { return S[0][8 * u + j]; });
-            pages[i & 1][wave][2 * u][lane] = f.hi;
-            pages[i & 1][wave][2 * u + 1][lane] = f.lo;
+            pages[x][wave][2 * u][lane] = f.hi;
+            pages[x][wave][2 * u + 1][lane] = f.lo;
         }
-        if (half == 0) inverse[i & 1][wave][col] = pow2_inv(sc);
+        if (half == 0) inverse[x][wave][col] = pow2_inv(sc);
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < DKB; ++q) {
             acc_t a = zeros();
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const h8_t hi = pages[i & 1][q][2 * u][lane], lo = pages[i & 1][q][2 * u + 1][lane];
+                const h8_t hi = pages[x][q][2 * u][lane], lo = pages[x][q][2 * u + 1][lane];
                 a = mfma(w[2 * q + u].hi, hi, a);
                 a = mfma(w[2 * q + u].hi, lo, a);
                 a = mfma(w[2 * q + u].lo, hi, a);
             }
-            const float f = inverse[i & 1][q][col];
+            const float f = inverse[x][q][col];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) N[0][x] = fmaf(a[x] * im, f, N[0][x]);
+            for (int j = 0; j < 16; ++j) N[0][j] = fmaf(a[j] * im, f, N[0][j]);
         }
         S[0] = N[0];
         store_state<1>(make_rsrc(segment(i), 4 * offset), at, 4 * ld, half, S);
+    };
+    for (int i = 1; i < n - 1; i += 2) {
+        step(i, std::integral_constant<int, 1>());
+        if (i + 1 < n - 1) step(i + 1, std::integral_constant<int, 0>());
     }
 }
 
