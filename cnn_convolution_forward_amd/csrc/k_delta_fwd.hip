@@ -10,9 +10,14 @@
 // With the operands swapped, products with S and U give Y transposed: a lane then
 // has four neighbouring values of a token and stores them together.
 //
-// The pages of K, Q, T and P (50 KB for bf16 heads of 128) are brought to LDS
-// asynchronously, a block ahead where two buffers fit.  Values are
-// loaded a block ahead into registers.
+// The pages of K, Q, T and P (51 KB for bf16 heads of 128) are brought to LDS
+// asynchronously, a block ahead where two buffers fit; values are loaded at their block's start.
+//
+// What bounds it: the chain itself.  A block's products depend on each other, and there is one wave to a SIMD
+// (8 x 2048 tokens in 16 heads of 128: 512 waves for 1024 SIMDs, 210 us for 32 blocks of which the matrix instructions
+// take 45): 2500 cycles K S and Q S, 2200 R with the wait for V, 1900 U, 2000 the new S, 1500 y; saving the states
+// adds 2500.  Tried and slower, as their registers are moved to and fro: V a block ahead (323 to 337 us for the whole
+// call), the states' accesses four columns wide and transposed between lanes (323 to 329).
 #include "delta_common.h"
 
 namespace convfwd {
@@ -100,7 +105,8 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             store_state<DKB>(make_rsrc(states + (((int64_t)b * ((s.T + kBlock - 1) / kBlock) + k) * d.Hv + hv) * state, 4 * state), at_s,
                              ld_s, half, S);
 
-        // products with S: K S for U, and (Q S)^T for y.  Pages are read a step ahead, or in front of the phase that needs them:
+        // products with S: K S for U, and (Q S)^T for y, for bf16 with S in one fp16 number: at most 2^-12 of each product, where y's
+        // own rounding is 2^-9.  Pages are read a step ahead, or in front of the phase that needs them:
         // there is one wave to a SIMD, so nothing else would hide LDS's latency
         float m = 0.f;
 #pragma unroll
@@ -226,7 +232,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
                 a = mfma(now[u], wf[u].lo, a);
                 if constexpr (PARTS == 2) a = mfma(now[4 + u], wf[u].hi, a);
             }
-            // every page of U in one of the DKB steps
+            // every page of U in one of the DKB steps; for bf16 in one fp16 number, as S for y
 #pragma unroll
             for (int q = i; q < (SUM ? 0 : 4); q += DKB) {
                 Pair f;
