@@ -659,7 +659,7 @@ CONV_API conv_status_t conv_norm_bwd(int dtype, int64_t rows, int C, const void 
 /* ---- the optimiser step --------------------------------------------------
  *
  * AdamW over `count` tensors at once, from the fp32 (or bf16) gradients that
- * conv_bwd_weight_bf16, conv_causal_bwd and conv_scan_bwd write to the bf16
+ * conv_bwd_weight_bf16, conv_causal_bwd, conv_scan_bwd and conv_norm_bwd write to the bf16
  * weights that the next forward pass reads.  With c1 = 1 - beta1^step and
  * c2 = 1 - beta2^step (step: this one's number, from 1):
  *
