@@ -15,9 +15,9 @@
 // column, then the blocks below from the products T_ii A_ij T_jj on the fp32 matrix
 // instructions: three levels instead of 64 steps.
 //
-// 8 x 2048 tokens in 16 heads of 128, bf16: 125 us forward, 145 backward, for 134 MB read and 223 (433) MB written; the
-// floor of these bytes is 69 (109) us.  The rest is the substitution's and the levels' latency, with three workgroups to a compute
-// unit to cover it.
+// 8 x 2048 tokens in 16 heads of 128, bf16: 109 us forward, 134 backward, for 134 MB read and 223 (433) MB written; the
+// floor of these bytes is 69 (109) us.  The rest is latency, of the loads (9500 of a workgroup's 44000
+// cycles), the scan of the gates (5900), the substitution and the levels (5600), with four workgroups to a compute unit to cover it.
 #include <math.h>
 
 #include <type_traits>
@@ -50,9 +50,9 @@ template <typename T, int N> __device__ __forceinline__ void load_part(const T *
     }
 }
 
-// Three workgroups to a compute unit (168 registers: one more makes it two, and 8 x 2048 x 16 heads of 128 take 30 us longer), where
-// LDS has room for three.
-constexpr int resident(int parts, int dkb) { return parts * dkb > 4 ? 2 : 3; }
+// Four workgroups to a compute unit where LDS has room for them, which takes 128 registers (and a few spilled): 8 x 2048 tokens in 16
+// heads of 128 bf16 in 109 us instead of 126 with three.
+constexpr int resident(int parts, int dkb) { return parts * dkb > 4 ? 2 : 4; }
 
 template <typename T, int DKB, bool BWD>
 __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_prep_kernel(Seq s, Delta d, DeltaWs ws, const T *__restrict__ q, int64_t ldq,
@@ -80,6 +80,13 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
     if (at.k < 0 || (int64_t)at.k * kBlock >= len) return;
     const int64_t r0 = first + (int64_t)at.k * kBlock;
     const int n = min(len - at.k * kBlock, kBlock);
+
+    // gates of the first value head; those of the others are loaded a head ahead
+    float gv = 0.f, b = 0.f;
+    const auto load_gates = [&](int hv) {
+        if (wave == 0 && lane < n) gv = g[(r0 + lane) * ldg + hv], b = beta[(r0 + lane) * ldb + hv];
+    };
+    load_gates(hk * d.group);
 
     // rows as fp16 under their own power of two, and the factor that makes the row of it
     {
@@ -139,27 +146,34 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
         return v;
     };
-    // k.k and q.k of the three blocks of 32x32 on and below the diagonal: wave 0 k.k of the one below, wave 1 those on it, waves 2
-    // and 3 the same of q.k.  They stay in registers, rows j for P (lane = i, as its pages have it) and rows i for the others.
-    const int which = wave >> 1, count = wave & 1 ? 2 : 1;
+    // k.k (waves 0, 1) and q.k of the three blocks of 32x32 on and below the diagonal: each wave has one of those with i in 32..63, and
+    // half of the registers of the first on the diagonal, whose product both waves take.  They stay in registers, rows j for P
+    // (lane = i, as its pages have it) and rows i for the others.
+    const int which = wave >> 1, part = wave & 1;
     constexpr bool kByI = !BWD;                                           // of q.k
-    acc_t prod[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        prod[u] = zeros();
-        if (u >= count) break;
-        const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
+    const bool by_i = which && kByI;
+    const auto product = [&](int ib, int jb) {
+        acc_t x = zeros();
 #pragma unroll
         for (int m = 0; m < 2 * DKB; ++m) {
             const h8_t a = row_page(which, 0, ib, m), b = row_page(0, 0, jb, m);
-            const bool swap = which && kByI;
-            prod[u] = swap ? mfma(b, a, prod[u]) : mfma(a, b, prod[u]);
+            x = by_i ? mfma(b, a, x) : mfma(a, b, x);
             if constexpr (PARTS == 2) {
                 const h8_t al = row_page(which, 1, ib, m), bl = row_page(0, 1, jb, m);
-                prod[u] = swap ? mfma(bl, a, prod[u]) : mfma(a, bl, prod[u]);
-                prod[u] = swap ? mfma(b, al, prod[u]) : mfma(al, b, prod[u]);
+                x = by_i ? mfma(bl, a, x) : mfma(a, bl, x);
+                x = by_i ? mfma(b, al, x) : mfma(al, b, x);
             }
         }
+        return x;
+    };
+    float prod[24];
+    {
+        const acc_t x = product(1, part);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) prod[r] = x[r];
+        const acc_t y = product(0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) prod[16 + r] = part ? y[8 + r] : y[r];
     }
     {   // pages of keys and queries
         uint4 *out = ws.qk + (slot * d.H + hk) * ws.qk_pages * kPage + lane;
@@ -185,7 +199,6 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         float *rows = ws.rows + rec * kRowsFloats;
         float *bt = betas[hv & 1];                                      // by turns: the last head's pages of T may still be on their way
         if (wave == 0) {
-            const float gv = lane < n ? g[(r0 + lane) * ldg + hv] : 0.f, b = lane < n ? beta[(r0 + lane) * ldb + hv] : 0.f;
             double v = gv < -1e4f ? -1e4 : (double)gv;                  // a NaN stays
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
@@ -210,27 +223,25 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
                 reinterpret_cast<double *>(rows + 64 * kRowG)[lane] = v;
             }
             if (lane == 63) rows[kGamma] = E;
+            if (hv + 1 < (hk + 1) * d.group) load_gates(hv + 1);
         }
         __syncthreads();                                                // also: keys and queries, or the last head's A and T, are free
-        acc_t val[2];
-        float pm = 0.f;
+        float val[24], pm = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            if (u >= count) break;
-            const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
-            const bool by_i = which && kByI;
+            const int ib = u ? 0 : 1, jb = u ? 0 : part;
             const int mine = 32 * (by_i ? ib : jb) + col;
             const double g_mine = G[mine];
             const float k_mine = kap[by_i ? 1 : 0][mine];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int other = 32 * (by_i ? jb : ib) + acc_row(r, half);
+            for (int r = 0; r < (u ? 8 : 16); ++r) {
+                const int other = 32 * (by_i ? jb : ib) + (u ? 16 * part : 0) + acc_row(r, half);
                 const int i = by_i ? mine : other, j = by_i ? other : mine;
                 const float D = by_i ? decay_of(g_mine, G[other]) : decay_of(G[other], g_mine);
-                float x = prod[u][r] * (k_mine * kap[by_i ? 0 : which][other]) * D * (which ? d.scale : bt[i]);
+                float x = prod[16 * u + r] * (k_mine * kap[by_i ? 0 : which][other]) * D * (which ? d.scale : bt[i]);
                 asm("" : "+v"(x));                                      // all of it, then a selection: no branch for each
                 x = j < i || (which && j == i) ? x : 0.f;
-                val[u][r] = x;
+                val[16 * u + r] = x;
                 pm = fmaxf(pm, fabsf(x));
                 if (!which) A[i][j] = x;
             }
@@ -247,14 +258,10 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
         };
         if (which) {                                                    // P or P^T: registers 8 m .. 8 m + 7 are pages
+            const auto page = [&](int ib, int jb, int m) { return BWD ? high_page(jb, 2 * ib + m) : low_page(ib, 2 * jb + m); };
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u >= count) break;
-                const int ib = count == 1 ? 1 : u, jb = count == 1 ? 0 : u;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    put(BWD ? 2 : 1, BWD ? high_page(jb, 2 * ib + m) : low_page(ib, 2 * jb + m), split8(sp, [&](int e) { return val[u][8 * m + e]; }));
-            }
+            for (int u = 0; u < 3; ++u)
+                put(BWD ? 2 : 1, u < 2 ? page(1, part, u) : page(0, 0, part), split8(sp, [&](int e) { return val[8 * u + e]; }));
         }
 
         // T: the blocks on the diagonal
