@@ -480,6 +480,51 @@ def test_captured_graph():
         assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(after, s), i
 
 
+def test_segments_on_two_streams_and_in_a_graph():
+    """Sequences that are cut: calls on two streams at once and a replayed graph give the bits of a call alone."""
+    long = lambda r, s: -np.exp(r.uniform(-9, -2, s))
+    cs = [Case("bf16", [900, 0, 3, 1400], 1, 2, 64, 96, packed=True, g=long), Case("f32", [1100] * 2, 2, 2, 40, 33, g=long, seed=3)]
+
+    def run(c):
+        y, sT, st = B.delta_rule(*c.data(), s0=c.s0, with_states=True, **c.opts())
+        return (y, sT) + B.delta_rule_backward(*c.data(), c.dy, st, ds=c.ds, **c.opts())
+
+    want = [run(c) for c in cs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cs], [None, None]
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                got[i] = run(c)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for a, b in zip(want, got) for p, q in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [run(c) for c in cs]
+    for i in range(3):
+        for c in cs:
+            c.v.copy_(torch.randn_like(c.v.float()))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = [run(c) for c in cs]
+        assert all(torch.equal(p, q) for a, b in zip(want, out) for p, q in zip(a, b)), i
+
+
+def test_descending_offsets_of_long_sequences_stay_inside():
+    """As below, with sequences that are cut into segments, and a workspace between guards."""
+    c = Case("bf16", [1500], 1, 2, 32, 32)
+    data, dy = [t[0].contiguous() for t in c.data()], c.dy[0].contiguous()
+    for off in ([0, 1500, 0, 1500], [1500, 700, 0, 1 << 30], [0, 1500, 700, 1500]):
+        kw = dict(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_len=1500, unit=True)
+        seq, par = B.make_delta(data[0], data[2], fill=True, **kw)
+        held = torch.full((B.conv_delta_bwd_workspace_bytes(seq, par) + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+        n = B.conv_delta_fwd_workspace_bytes(seq, par)
+        y, sT, st = B.delta_rule(*data, with_states=True, workspace=held[4096:4096 + n], **kw)
+        assert bool((held[:4096] == 0x5a).all()) and bool((held[4096 + n:] == 0x5a).all())
+        B.delta_rule_backward(*data, dy, torch.zeros_like(st), workspace=held[4096:-4096], **kw)
+        assert bool((held[:4096] == 0x5a).all()) and bool((held[-4096:] == 0x5a).all())
+
+
 def test_given_workspaces():
     c = Case("bf16", [100], 1, 2, 48, 40)
     par = B.make_delta(c.q, c.v, scale=c.scale, unit=True)
