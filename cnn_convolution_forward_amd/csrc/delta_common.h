@@ -176,7 +176,7 @@ __device__ __forceinline__ Block find_block(const Seq &s, int per, int64_t n) {
 // read of LDS.  They have no output registers; wait_copies is their wait.  Nothing else here uses M0.
 __device__ __forceinline__ void copy4(const uint4 *src, uint32_t dst, uint32_t at) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:2048\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072"
+                 "global_load_lds_dwordx4 %1, %2 offset:2*1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:3*1024"
                  :
                  : "s"(dst), "v"(at), "s"(src)
                  : "memory");

@@ -359,13 +359,13 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 // Segments of a sequence: its chain of blocks is cut where there are too few chains to fill the chip's 1024 SIMDs with a wave
 // each.  What a segment makes of any state is a matrix and an offset, found by running it from the identity and from zero
 // (twice the columns); the segments are joined one after another, and run again from their states.  That is
-// three times the work over n times the waves (one sequence of 32768 tokens in 8 heads of 128: 410 us instead of 2638).
+// three times the work over n times the waves (one sequence of 32768 tokens in 8 heads of 128: 395 us instead of 2638).
 // - Waves: packed sequences count as as many of the longest as hold their tokens (9 sequences of 5003 tokens, the longest of 2605,
 //   fp32 in 6 heads of 72 and 99: 121 us, cut for nine of the longest 145).
 // - A block takes 11 us in both passes and the joining of a segment 3: 2 sqrt(blocks) segments are the best number
 //   (backward, 11981 tokens in 16 heads of 64 and 10: 478 us, with 47 segments instead of 27 505).
 // - Fewer than three segments, or than eight blocks, do not pay (8 x 2048 tokens in 16 heads of 128 in two: forward 318 us
-//   instead of 322, backward 950 instead of 914).
+//   instead of 322, backward 950 instead of 914, at that step).
 // - Every sequence's workgroups for every segment are launched, and end at once where it has none: at most 16384 waves.
 void cut(const Seq &s, const Delta &d, DeltaWs &ws) {
     const int longest = (int)std::min<int64_t>(s.T, s.rows), blocks = (longest + kBlock - 1) / kBlock, slices = (d.Dv + 31) / 32;
