@@ -10,7 +10,7 @@
 // With the operands swapped, products with S and U give Y transposed: a lane then
 // has four neighbouring values of a token and stores them together.
 //
-// The pages of K, Q, T and P (51 KB for bf16 heads of 128) are brought to LDS
+// The pages of K, Q, T and P (57 KB for bf16 heads of 128) are brought to LDS
 // asynchronously, a block ahead where two buffers fit; values are loaded at their block's start.
 //
 // What bounds it: the chain itself.  A block's products depend on each other, and there is one wave to a SIMD
@@ -27,7 +27,7 @@ namespace {
 template <int DKB, int PARTS, bool SUM> struct FwdPages {
     static constexpr int F = 4 * DKB;                   // pages of one part of K or Q
     static constexpr int kQK = (SUM ? 1 : 2) * PARTS * F;
-    static constexpr int kTri = (2 + (SUM ? 0 : PARTS)) * kTriPages;    // T hi and lo; of P, lo only where y has 24 bits
+    static constexpr int kTri = (SUM ? 2 : 4) * kTriPages;              // T and P, hi and lo
     static constexpr int kAll = kQK + kTri + 1;         // and a page of the rows' factors
     static constexpr int kBuffers = 2 * kAll <= 156 ? 2 : 1;
 };
@@ -105,8 +105,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             store_state<DKB>(make_rsrc(states + (((int64_t)b * ((s.T + kBlock - 1) / kBlock) + k) * d.Hv + hv) * state, 4 * state), at_s,
                              ld_s, half, S);
 
-        // products with S: K S for U, and (Q S)^T for y, for bf16 with S in one fp16 number: at most 2^-12 of each product, where y's
-        // own rounding is 2^-9.  Pages are read a step ahead, or in front of the phase that needs them:
+        // products with S: K S for U, and (Q S)^T for y.  Pages are read a step ahead, or in front of the phase that needs them:
         // there is one wave to a SIMD, so nothing else would hide LDS's latency
         float m = 0.f;
 #pragma unroll
@@ -145,12 +144,10 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 X[t] = mfma(kp[i & 1][t], f.lo, X[t]);
+                if constexpr (!SUM) Y[t] = mfma(f.lo, qp[i & 1][t], Y[t]);
                 if constexpr (PARTS == 2) {
                     X[t] = mfma(kp[i & 1][2 + t], f.hi, X[t]);
-                    if constexpr (!SUM) {
-                        Y[t] = mfma(f.lo, qp[i & 1][t], Y[t]);
-                        Y[t] = mfma(f.hi, qp[i & 1][2 + t], Y[t]);
-                    }
+                    if constexpr (!SUM) Y[t] = mfma(f.hi, qp[i & 1][2 + t], Y[t]);
                 }
             }
         }
@@ -169,7 +166,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         }
         const float sr = pow2_scale(max_halves(m));
         if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);           // behind V's loads, which would wait for it
-        h8_t kt[4 * PARTS], kt2[4 * PARTS], low[PARTS * kTriPages];
+        h8_t kt[4 * PARTS], kt2[4 * PARTS], low[2 * kTriPages];
         // rows 32 i .. + 31 of K^T, from the pages of K: 16 rows are a page's columns, four lanes of 8 bytes to a token
         const auto read_kt = [&](int i, h8_t(&to)[4 * PARTS]) {
             const char *p = buf + ((lane >> 4) & 1) * 1024 + ((lane & 1) * 32 + 4 * half + ((lane >> 2) & 3)) * 16 + ((lane >> 1) & 1) * 8;
@@ -185,7 +182,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
         for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
 #pragma unroll
-        for (int u = 0; u < (SUM ? 0 : PARTS * kTriPages); ++u) low[u] = page(kP + u);
+        for (int u = 0; u < (SUM ? 0 : 2 * kTriPages); ++u) low[u] = page(kP + u);
         read_kt(0, kt);
         __builtin_amdgcn_sched_barrier(0);
         // U = T beta R
@@ -232,19 +229,15 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
                 a = mfma(now[u], wf[u].lo, a);
                 if constexpr (PARTS == 2) a = mfma(now[4 + u], wf[u].hi, a);
             }
-            // every page of U in one of the DKB steps; for bf16 in one fp16 number, as S for y
+            // every page of U in one of the DKB steps
 #pragma unroll
             for (int q = i; q < (SUM ? 0 : 4); q += DKB) {
-                Pair f;
-                if constexpr (PARTS == 2) f = split8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
-                else f.hi = half8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
+                const Pair f = split8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
 #pragma unroll
                 for (int t = q >> 1; t < 2; ++t) {
                     Z[t] = mfma(f.hi, low[low_page(t, q)], Z[t]);
-                    if constexpr (PARTS == 2) {
-                        Z[t] = mfma(f.lo, low[low_page(t, q)], Z[t]);
-                        Z[t] = mfma(f.hi, low[kTriPages + low_page(t, q)], Z[t]);
-                    }
+                    Z[t] = mfma(f.lo, low[low_page(t, q)], Z[t]);
+                    Z[t] = mfma(f.hi, low[kTriPages + low_page(t, q)], Z[t]);
                 }
             }
 #pragma unroll

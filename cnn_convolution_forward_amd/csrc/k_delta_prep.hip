@@ -254,7 +254,6 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
         const auto put = [&](int kind, int page, const Pair &p) {
             out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
-            if (!BWD && PARTS == 1 && kind == 1) return;                // P's lo: y of bf16 does without
             out[((2 * kind + 1) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.lo);
         };
         if (which) {                                                    // P or P^T: registers 8 m .. 8 m + 7 are pages

@@ -566,8 +566,7 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  *
  * Whole sequences are computed in blocks of 64 tokens by matrix products whose
  * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
- * fp32; decays are added up in fp64.  For bf16, where y is rounded to 8 bits, its two products have one
- * operand of 11 bits (S, and beta e).  A log decay below -10000 counts
+ * fp32; decays are added up in fp64.  A log decay below -10000 counts
  * as -10000: nothing of the state is left.  Infinities and NaN: a state, or a token's values, that are not finite
  * make results of their head non-finite from the start of their 64-token
  * block on (gradients: before it too), in their own sequence only.
