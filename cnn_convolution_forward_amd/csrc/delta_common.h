@@ -224,6 +224,14 @@ template <typename T> struct Column {
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(sizeof(T) == 2 ? v[i] << 16 : v[i]); }
 };
 
+// Of tokens 32 t .. 32 t + 31.
+template <typename T> __device__ __forceinline__ float max_column(const Column<T> &c, int t) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(c.get(16 * t + i)));
+    return m;
+}
+
 // A state's columns (dim_k x dim_v, dim_v apart) to and from a result's registers.
 template <int DKB> __device__ __forceinline__ void load_state(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t ld, int half, acc_t (&S)[DKB]) {
     const uint32_t base = at + 4 * half * ld;

@@ -143,24 +143,25 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
                 if constexpr (PARTS == 2) X[t] = mfma(kp[i & 1][2 + t], f.hi, X[t]);
             }
         }
-        // P^T dY
-        m = 0.f;
+        // P^T dY: of tokens 0..31 from dY of 0..31, of 32.., and of 0..31 from dY of 32.., whose columns have a power of two for
+        // each half of the tokens, as in the forward pass
+        float so[2];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(dY.get(i)));
-        const float so = pow2_scale(max_halves(m));
+        for (int t = 0; t < 2; ++t) so[t] = pow2_scale(max_halves(max_column(dY, t)));
         if (P::kBuffers == 2 && k > begin) fetch(k - 1);
-        acc_t W[2] = {zeros(), zeros()};
+        acc_t W[3] = {zeros(), zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             Pair f;
-            if constexpr (PARTS == 2) f = split8(so, [&](int j) { return dY.get(8 * i + j); });
-            else f.hi = half8(so, [&](int j) { return dY.get(8 * i + j); });        // exact
+            if constexpr (PARTS == 2) f = split8(so[i >> 1], [&](int j) { return dY.get(8 * i + j); });
+            else f.hi = half8(so[i >> 1], [&](int j) { return dY.get(8 * i + j); });        // exact
 #pragma unroll
             for (int t = 0; t <= i >> 1; ++t) {
                 const int u = high_page(t, i);
-                W[t] = mfma(pt[u], f.hi, W[t]);
-                W[t] = mfma(pt[kTriPages + u], f.hi, W[t]);
-                if constexpr (PARTS == 2) W[t] = mfma(pt[u], f.lo, W[t]);
+                acc_t &to = W[t < i >> 1 ? 2 : t];
+                to = mfma(pt[u], f.hi, to);
+                to = mfma(pt[kTriPages + u], f.hi, to);
+                if constexpr (PARTS == 2) to = mfma(pt[u], f.lo, to);
             }
         }
         f4_t fk[2][4];
@@ -170,27 +171,30 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
         for (int u = 0; u < 2 * kTriPages; ++u) tt[u] = page(kTT + u);
         // gradient of U
-        const float ip = pow2_inv(so) * invP;
-        m = 0.f;
+        const float ip[2] = {pow2_inv(so[0]) * invP, pow2_inv(so[1]) * invP};
+        float sx[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) X[t][4 * a + j] = fmaf(fk[t][a][j] * isc, X[t][4 * a + j], W[t][4 * a + j] * ip);
-            m = max_abs(X[t], m);
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * a + j;
+                    X[t][r] = fmaf(fk[t][a][j] * isc, X[t][r], t ? W[1][r] * ip[1] : fmaf(W[2][r], ip[1], W[0][r] * ip[0]));
+                }
+            sx[t] = pow2_scale(max_halves(max_abs(X[t])));
         }
-        const float sx = pow2_scale(max_halves(m));
-        acc_t Z[2] = {zeros(), zeros()};
+        acc_t Z[3] = {zeros(), zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Pair f = split8(sx, [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
+            const Pair f = split8(sx[i >> 1], [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
+            const auto to = [&](int t) -> acc_t & { return Z[t < i >> 1 ? 2 : t]; };
 #pragma unroll
-            for (int t = 0; t <= i >> 1; ++t) Z[t] = mfma(tt[high_page(t, i)], f.hi, Z[t]);
+            for (int t = 0; t <= i >> 1; ++t) to(t) = mfma(tt[high_page(t, i)], f.hi, to(t));
 #pragma unroll
-            for (int t = 0; t <= i >> 1; ++t) Z[t] = mfma(tt[high_page(t, i)], f.lo, Z[t]);
+            for (int t = 0; t <= i >> 1; ++t) to(t) = mfma(tt[high_page(t, i)], f.lo, to(t));
 #pragma unroll
-            for (int t = 0; t <= i >> 1; ++t) Z[t] = mfma(tt[kTriPages + high_page(t, i)], f.hi, Z[t]);
+            for (int t = 0; t <= i >> 1; ++t) to(t) = mfma(tt[kTriPages + high_page(t, i)], f.hi, to(t));
         }
         f4_t eq[2][4], ek[2][4], bt[2][4];
 #pragma unroll
@@ -200,7 +204,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
             bt[u >> 2][u & 3] = factors(kRowBeta, u >> 2, u & 3);
         }
         // dS
-        const float iz = pow2_inv(sx) * invT;
+        const float iz[2] = {pow2_inv(sx[0]) * invT, pow2_inv(sx[1]) * invT};
         m = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -209,7 +213,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    Z[t][r] = -(Z[t][r] * iz) * (ek[t][a][j] * bt[t][a][j]);
+                    Z[t][r] = -(t ? Z[1][r] * iz[1] : fmaf(Z[2][r], iz[1], Z[0][r] * iz[0])) * (ek[t][a][j] * bt[t][a][j]);
                     W[t][r] = eq[t][a][j] * dY.get(16 * t + r);
                 }
             m = max_abs(W[t], max_abs(Z[t], m));
@@ -388,7 +392,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
             }
             Column<T> V;
             V.load(rc, at_v, (uint32_t)(ld * sizeof(T)), half);
-            float m = 0.f;
+            float sx[2];                                                // of X, a power of two for each half of the tokens
             if constexpr (!second) {                                              // R = beta (V - E K S)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -399,63 +403,69 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                         for (int j = 0; j < 4; ++j)
                             X[t][4 * a + j] = bt[j] * fmaf(-ek[j], X[t][4 * a + j], V.get(16 * t + 4 * a + j));
                     }
-                    m = max_abs(X[t], m);
+                    sx[t] = pow2_scale(max_halves(max_abs(X[t])));
                 }
             } else {                                                    // P^T dY + F K dS
+                float so[2], ip[2];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(V.get(i)));
-                const float so = pow2_scale(max_halves(m)), ip = pow2_inv(so) * invP;
-                acc_t Y[2] = {zeros(), zeros()};
+                for (int t = 0; t < 2; ++t) so[t] = pow2_scale(max_halves(max_column(V, t))), ip[t] = pow2_inv(so[t]) * invP;
+                acc_t Y[3] = {zeros(), zeros(), zeros()};               // the last: of tokens 0..31 from those of 32..
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     Pair f;
-                    if constexpr (PARTS == 2) f = split8(so, [&](int j) { return V.get(8 * i + j); });
-                    else f.hi = half8(so, [&](int j) { return V.get(8 * i + j); });
+                    if constexpr (PARTS == 2) f = split8(so[i >> 1], [&](int j) { return V.get(8 * i + j); });
+                    else f.hi = half8(so[i >> 1], [&](int j) { return V.get(8 * i + j); });
 #pragma unroll
                     for (int t = 0; t <= i >> 1; ++t) {
                         const h8_t hi = page(P::kPT + high_page(t, i)), lo = page(P::kPT + kTriPages + high_page(t, i));
-                        Y[t] = mfma(hi, f.hi, Y[t]);
-                        Y[t] = mfma(lo, f.hi, Y[t]);
-                        if constexpr (PARTS == 2) Y[t] = mfma(hi, f.lo, Y[t]);
+                        acc_t &to = Y[t < i >> 1 ? 2 : t];
+                        to = mfma(hi, f.hi, to);
+                        to = mfma(lo, f.hi, to);
+                        if constexpr (PARTS == 2) to = mfma(hi, f.lo, to);
                     }
                 }
-                m = 0.f;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
                         const f4_t fk = factors(kRowFK, t, a);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) X[t][4 * a + j] = fmaf(fk[j], X[t][4 * a + j], Y[t][4 * a + j] * ip);
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 4 * a + j;
+                            X[t][r] = fmaf(fk[j], X[t][r], t ? Y[1][r] * ip[1] : fmaf(Y[2][r], ip[1], Y[0][r] * ip[0]));
+                        }
                     }
-                    m = max_abs(X[t], m);
+                    sx[t] = pow2_scale(max_halves(max_abs(X[t])));
                 }
             }
             // times T or T^T, transposed: the factor of a column differs from lane to lane before, from register to register behind
-            const float sx = pow2_scale(max_halves(m));
+            acc_t cross = zeros();                                      // what one half of the tokens has from the other
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const Pair f = split8(sx, [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
+                const Pair f = split8(sx[i >> 1], [&](int j) { return X[i >> 1][8 * (i & 1) + j]; });
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (second ? t > i >> 1 : t < i >> 1) continue;
                     const int p = second ? P::kTT + high_page(t, i) : P::kTri + low_page(t, i);
                     const h8_t hi = page(p), lo = page(p + kTriPages);
-                    U[t] = mfma(f.hi, hi, U[t]);
-                    U[t] = mfma(f.lo, hi, U[t]);
-                    U[t] = mfma(f.hi, lo, U[t]);
+                    acc_t &to = t == i >> 1 ? U[t] : cross;
+                    to = mfma(f.hi, hi, to);
+                    to = mfma(f.lo, hi, to);
+                    to = mfma(f.hi, lo, to);
                 }
             }
-            float *table = small + kDots + wave * 32;
-            if (half == 0) table[col] = pow2_inv(sx) * invT;
+            float *table = small + kDots + wave * 64;
+            if (half == 0) table[col] = pow2_inv(sx[0]) * invT, table[32 + col] = pow2_inv(sx[1]) * invT;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                const f4_t fu = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
+                const f4_t f0 = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half), f1 = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= fu[j];
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * a + j;
+                    U[0][r] = second ? fmaf(cross[r], f1[j], U[0][r] * f0[j]) : U[0][r] * f0[j];
+                    U[1][r] = second ? U[1][r] * f1[j] : fmaf(cross[r], f0[j], U[1][r] * f1[j]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) mu[t] = max_halves(max_abs(U[t]));

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
     extern __shared__ __align__(1024) char lds[];
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    float *table = reinterpret_cast<float *>(lds + P::kBuffers * P::kAll * 1024) + wave * 64;      // two factors for each column
+    float *table = reinterpret_cast<float *>(lds + P::kBuffers * P::kAll * 1024) + wave * 96;      // three factors for each column
     const int heads = s.B * d.Hv, bh = (int)(blockIdx.x % heads);
     const int runs = SUM ? ws.segments - 1 : ws.segments, seg = (int)(blockIdx.x / heads) % runs;
     const int slice = (int)(blockIdx.x / heads) / runs * waves + wave;
@@ -151,9 +151,10 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
                 }
             }
         }
-        // R = V - E K S
+        // R = V - E K S.  A column of it, as of U, has a power of two for each half of the tokens: tokens 32.. then cost 0..31,
+        // which do not depend on them, no bits, however large they are
         acc_t Rr[2];
-        m = 0.f;
+        float sr[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -162,9 +163,8 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
                 for (int j = 0; j < 4; ++j)
                     Rr[t][4 * a + j] = fmaf(-(ek[t][a][j] * isc), X[t][4 * a + j], V.get(16 * t + 4 * a + j));
             }
-            m = max_abs(Rr[t], m);
+            sr[t] = pow2_scale(max_halves(max_abs(Rr[t])));
         }
-        const float sr = pow2_scale(max_halves(m));
         if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);           // behind V's loads, which would wait for it
         h8_t kt[4 * PARTS], kt2[4 * PARTS], low[2 * kTriPages];
         // rows 32 i .. + 31 of K^T, from the pages of K: 16 rows are a page's columns, four lanes of 8 bytes to a token
@@ -181,42 +181,47 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         f4_t fk[2][4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
-#pragma unroll
-        for (int u = 0; u < (SUM ? 0 : 2 * kTriPages); ++u) low[u] = page(kP + u);
         read_kt(0, kt);
         __builtin_amdgcn_sched_barrier(0);
-        // U = T beta R
-        acc_t U[2] = {zeros(), zeros()};
+        // U = T beta R: of tokens 0..31, of 32.. from R of 32.., and from R of 0..31
+        acc_t part[3] = {zeros(), zeros(), zeros()};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Pair f = split8(sr, [&](int j) { return Rr[i >> 1][8 * (i & 1) + j]; });
+            const Pair f = split8(sr[i >> 1], [&](int j) { return Rr[i >> 1][8 * (i & 1) + j]; });
+            const auto to = [&](int t) -> acc_t & { return part[t + (t > i >> 1)]; };
 #pragma unroll
-            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[low_page(t, i)], f.hi, U[t]);
+            for (int t = i >> 1; t < 2; ++t) to(t) = mfma(tri[low_page(t, i)], f.hi, to(t));
 #pragma unroll
-            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[low_page(t, i)], f.lo, U[t]);
+            for (int t = i >> 1; t < 2; ++t) to(t) = mfma(tri[low_page(t, i)], f.lo, to(t));
 #pragma unroll
-            for (int t = i >> 1; t < 2; ++t) U[t] = mfma(tri[kTriPages + low_page(t, i)], f.hi, U[t]);
+            for (int t = i >> 1; t < 2; ++t) to(t) = mfma(tri[kTriPages + low_page(t, i)], f.hi, to(t));
         }
-        const float iu = pow2_inv(sr) * invT;
-        acc_t W[2];
-        m = 0.f;
-        float mw = 0.f;
+#pragma unroll
+        for (int u = 0; u < (SUM ? 0 : 2 * kTriPages); ++u) low[u] = page(kP + u);      // in T's registers
+        __builtin_amdgcn_sched_barrier(0);
+        const float iu[2] = {pow2_inv(sr[0]) * invT, pow2_inv(sr[1]) * invT};
+        acc_t U[2], W[2];
+        float su[2] = {1.f, 1.f}, mw = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) U[t][4 * a + j] *= iu, W[t][4 * a + j] = U[t][4 * a + j] * fk[t][a][j];
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * a + j;
+                    U[t][r] = t ? fmaf(part[2][r], iu[0], part[1][r] * iu[1]) : part[0][r] * iu[0];
+                    W[t][r] = U[t][r] * fk[t][a][j];
+                }
             }
-            if constexpr (!SUM) m = max_abs(U[t], m);
+            if constexpr (!SUM) su[t] = pow2_scale(max_halves(max_abs(U[t])));
             mw = max_abs(W[t], mw);
         }
-        const float su = pow2_scale(max_halves(m)), sw = pow2_scale(max_halves(mw)), isw = pow2_inv(sw);
+        const float sw = pow2_scale(max_halves(mw)), isw = pow2_inv(sw);
         // S = E_last S + (F K)^T U, and between its products (P U)^T for y
         Pair wf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) wf[i] = split8(sw, [&](int j) { return W[i >> 1][8 * (i & 1) + j]; });
-        acc_t Z[2] = {zeros(), zeros()};
+        acc_t Z[3] = {zeros(), zeros(), zeros()};                       // as the parts of U
 #pragma unroll
         for (int i = 0; i < DKB; ++i) {
             h8_t(&now)[4 * PARTS] = i & 1 ? kt2 : kt;
@@ -232,12 +237,13 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             // every page of U in one of the DKB steps
 #pragma unroll
             for (int q = i; q < (SUM ? 0 : 4); q += DKB) {
-                const Pair f = split8(su, [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
+                const Pair f = split8(su[q >> 1], [&](int j) { return U[q >> 1][8 * (q & 1) + j]; });
 #pragma unroll
                 for (int t = q >> 1; t < 2; ++t) {
-                    Z[t] = mfma(f.hi, low[low_page(t, q)], Z[t]);
-                    Z[t] = mfma(f.lo, low[low_page(t, q)], Z[t]);
-                    Z[t] = mfma(f.hi, low[kTriPages + low_page(t, q)], Z[t]);
+                    acc_t &to = Z[t + (t > q >> 1)];
+                    to = mfma(f.hi, low[low_page(t, q)], to);
+                    to = mfma(f.lo, low[low_page(t, q)], to);
+                    to = mfma(f.hi, low[kTriPages + low_page(t, q)], to);
                 }
             }
 #pragma unroll
@@ -252,7 +258,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         if constexpr (SUM) continue;
         // y: a lane has token 32 t + col, columns 8 a + 4 half + 0..3 of the slice.  The factors of columns come from the lanes
         // that made them, through LDS (within the wave: the hardware keeps LDS accesses of a wave in order).
-        if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su) * invP;
+        if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su[0]) * invP, table[64 + col] = pow2_inv(su[1]) * invP;
         __builtin_amdgcn_wave_barrier();
         const __amdgpu_buffer_rsrc_t ry = rows_buffer(y + (first + (int64_t)k * kBlock) * ldy + hv * d.Dv, n, ldy, d.Dv);
 #pragma unroll
@@ -262,10 +268,14 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const f4_t fs = *reinterpret_cast<const f4_t *>(table + 8 * a + 4 * half);
-                const f4_t fu = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
+                const f4_t f0 = *reinterpret_cast<const f4_t *>(table + 32 + 8 * a + 4 * half);
+                const f4_t f1 = *reinterpret_cast<const f4_t *>(table + 64 + 8 * a + 4 * half);
                 float o[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = fmaf(Y[t][4 * a + j], fs[j] * eq[t], Z[t][4 * a + j] * fu[j]);
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * a + j;
+                    o[j] = fmaf(Y[t][r], fs[j] * eq[t], t ? fmaf(Z[2][r], f0[j], Z[1][r] * f1[j]) : Z[0][r] * f0[j]);
+                }
                 store4(ry, off + 8 * a * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, d.Dv & 3, o, y);
             }
         }
@@ -285,7 +295,7 @@ hipError_t chain(const Seq &s, const Delta &d, const DeltaWs &ws, const DeltaIn 
     const int slices = (d.Dv + 31) / 32, columns = slices + (SUM ? DKB : 0);
     const int64_t chains = (int64_t)s.B * d.Hv * (SUM ? ws.segments - 1 : ws.segments);
     const int waves = waves_of(chains, columns);
-    const int bytes = P::kBuffers * P::kAll * 1024 + waves * 256;
+    const int bytes = P::kBuffers * P::kAll * 1024 + waves * 384;
     const hipError_t e = hipFuncSetAttribute((const void *)delta_fwd_kernel<T, DKB, SUM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     delta_fwd_kernel<T, DKB, SUM><<<(unsigned)(chains * ((columns + waves - 1) / waves)), 64 * waves, bytes, st>>>(

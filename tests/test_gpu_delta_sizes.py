@@ -1,0 +1,125 @@
+"""Values far apart in size, and ones that are not finite, in the gated delta rule: what a token's results do not depend on
+costs them no bits.  Powers of two are exact, so most tests ask for equal bits; the rest go against the definition in
+float64, token by token, with the infinities and NaN that it has."""
+import numpy as np
+import pytest
+import torch
+
+import delta_reference as R
+from cnn_convolution_forward_amd import binding as B
+from test_gpu_delta import NAN, Case, _np
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def _forward(c, **other):
+    d = dict(zip("qkvgb", c.data()))
+    return B.delta_rule(*{**d, **other}.values(), s0=c.s0, with_states=True, **c.opts())
+
+
+def _backward(c, states, dy=None, **other):
+    d = dict(zip("qkvgb", c.data()))
+    return B.delta_rule_backward(*{**d, **other}.values(), c.dy if dy is None else dy, states, ds=c.ds, **c.opts())
+
+
+# ---- columns of values and of upstream gradients -----------------------------------------
+
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("f32", True), ("f32", False)])
+@pytest.mark.parametrize("token,clean", [(40, 32), (63, 32), (70, 64), (100, 96), (127, 96)])
+def test_large_values_leave_earlier_tokens_alone(dt, unit, token, clean):
+    """A value 2**60 times the others', which no token before it depends on: up to the 32 tokens of its own, the same bits."""
+    c = Case(dt, [130], 2, 4, 40, 48, unit=unit, seed=30)
+    y0, _, st0 = _forward(c)
+    v = c.v.clone()
+    v[:, token] *= 2.0 ** 60
+    y, _, st = _forward(c, v=v)
+    assert torch.equal(y[:, :clean], y0[:, :clean]) and torch.equal(st[:, :token // 64 + 1], st0[:, :token // 64 + 1])
+    assert not torch.equal(y[:, clean:], y0[:, clean:])
+
+
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("f32", True), ("f32", False)])
+@pytest.mark.parametrize("token,clean", [(0, 32), (10, 32), (31, 32), (50, 64), (64, 96), (90, 96)])
+def test_large_upstream_gradients_leave_later_tokens_alone(dt, unit, token, clean):
+    c = Case(dt, [130], 2, 4, 40, 48, unit=unit, seed=31)
+    st = _forward(c)[2]
+    want = _backward(c, st)
+    dy = c.dy.clone()
+    dy[:, token] *= 2.0 ** 60
+    got = _backward(c, st, dy)
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+        assert torch.equal(a[:, clean:], b[:, clean:]), name
+        assert not torch.equal(a[:, :clean], b[:, :clean]), name
+
+
+def _definition(q, k, v, g, b, S, scale):
+    """The recurrence with the infinities and NaN that it makes."""
+    y = np.zeros_like(v)
+    with np.errstate(all="ignore"):
+        for t in range(len(q)):
+            S = np.exp(g[t]) * S
+            S = S + np.outer(k[t], b[t] * (v[t] - k[t] @ S))
+            y[t] = scale * (q[t] @ S)
+    return y, S
+
+
+def _held(c, clean, name, token, head, bad, first):
+    """One bad value in an input: outputs that are finite have to be the definition's, those of tokens from `first` on may be NaN."""
+    data = dict(zip("qkvgb", (t.clone() for t in c.data())))
+    x = data[name]
+    x[(0, token, head) + ((3,) if x.dim() == 4 else ())] = bad
+    y, sT, _ = _forward(c, **data)
+    c2 = Case.__new__(Case)
+    c2.__dict__.update(c.__dict__)
+    c2.q, c2.k, c2.v, c2.g, c2.beta = data.values()
+    y, sT, yc = _np(y).reshape(-1, c.Hv, c.dv), _np(sT), _np(clean[0]).reshape(-1, c.Hv, c.dv)
+    with np.errstate(all="ignore"):
+        todo = list(c2.sequences())
+    for (i, h, hk, r, q, k, v, g, b, _, _), (*_, q0, k0, v0, g0, b0, _, _) in zip(todo, c.sequences()):
+        at = "%s token %d head %d unit %d" % (name, token, h, c.unit)
+        mine = head == (hk if name in "qk" else h)
+        ref, S = _definition(q, k, v, g, b, _np(c.s0)[i, h], c.scale)
+        fin, got = np.isfinite(ref), np.isfinite(y[r, h])
+        assert mine or fin.all()
+        assert not (got & ~fin).any(), at                            # nothing finite where the definition is not
+        assert got[:first].all() if mine else got.all(), at
+        _, hist = R.forward(q0, k0, v0, g0, b0, _np(c.s0)[i, h], c.scale)
+        ey, es = R.forward_bounds(q0, k0, v0, g0, b0, hist, c.scale, c.ku(), False)
+        tol = ey + (2.0 ** -8 * (np.abs(ref) + ey) if c.half else 2.0 ** -23 * np.abs(ref))
+        with np.errstate(invalid="ignore"):
+            assert not (got & ~(np.abs(y[r, h] - ref) <= tol)).any(), at
+            sg, sf = np.isfinite(sT[i, h]), np.isfinite(S)
+            assert not (sg & ~sf).any() and not (sg & ~(np.abs(sT[i, h] - S) <= es[-1] + 2.0 ** -23 * np.abs(S))).any(), at
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("bf16", False), ("f32", True), ("f32", False)])
+def test_values_that_are_not_finite(dt, unit, bad):
+    """In every quarter of a block.  Earlier tokens may be lost, back to the 32 that a tile holds; what stays finite is right."""
+    c = Case(dt, [130], 1, 2, 32, 40, unit=unit, seed=32)
+    clean = _forward(c)
+    for token in (0, 20, 31, 32, 50, 63, 64, 97, 129):
+        _held(c, clean, "v", token, 1, bad, token // 32 * 32)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("f32", False)])
+def test_upstream_gradients_that_are_not_finite(dt, unit, bad):
+    """A column of one token: later tokens, other heads, and dv's and ds0's other columns keep their bits."""
+    c = Case(dt, [130], 1, 2, 32, 40, unit=unit, seed=33)
+    st = _forward(c)[2]
+    want = _backward(c, st)
+    for token in (0, 20, 31, 32, 50, 63, 64, 97, 129):
+        dy = c.dy.clone()
+        dy[0, token, 1, 3] = bad
+        got = _backward(c, st, dy)
+        later = (token // 32 + 1) * 32
+        for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+            assert torch.equal(a[:, later:], b[:, later:]), (name, token)
+            if name not in ("dq", "dk"):
+                assert torch.equal(a[:, :, 0], b[:, :, 0]), (name, token)
+        other = torch.arange(40, device="cuda") != 3
+        assert torch.equal(got[2][:, :, 1][..., other], want[2][:, :, 1][..., other]), token
+        assert torch.equal(got[5][:, :, :, other], want[5][:, :, :, other]), token
+        assert not bool(torch.isfinite(got[2][0, :token + 1, 1, 3]).any()), token
