@@ -97,10 +97,15 @@ __device__ __forceinline__ float max_abs(const acc_t &v, float m = 0.f) {
 // Over the two halves of a wave: the whole of a column of a result.
 __device__ __forceinline__ float max_halves(float m) { return fmaxf(m, __shfl_xor(m, 32)); }
 
-// Rows record of a block and value head: 64 floats each, then scalars.  The first four fill a page.
-enum { kRowEK, kRowBeta, kRowFK, kRowEQ, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ, kRowG /* doubles, times log2(e) */, kRowG2, kRowCount };
-enum { kGamma = 64 * kRowCount, kInvT, kInvP };
+// Rows record of a block and value head: 64 floats each, then a scalar.  The first four fill a page.  kRowInv*: what the power of
+// two of each row of T, P and, backward, T^T and P^T has to be made good with.  Rows have their own, as they belong to tokens:
+// queries and keys far larger than another token's, or infinite, cost that one nothing.
+enum { kRowEK, kRowInvT, kRowFK, kRowEQ, kRowInvP, kForwardRows,
+       kRowEZ = 0 /* E K beta InvTT, of Z in dS */, kRowInvPT = 1, kRowBeta = 4, kRowEKBack, kRowE, kRowF, kRowKK, kRowKQ, kRowSizeK, kRowSizeQ,
+       kRowInvTBack, kRowInvTT, kRowG /* doubles, times log2(e) */, kRowG2, kRowCount };
+enum { kGamma = 64 * kRowCount };
 constexpr int kRowsFloats = 64 * kRowCount + 64;
+static_assert(kRowG % 2 == 0 && (int)kForwardRows <= (int)kRowCount, "doubles are aligned");
 
 // Pages of T, TT, P, PT (64x64, lower triangular): 6 of 8, hi and lo.  T and P: lane = row i, places = columns j; page of
 // block ib, m: ib 0 has m = 0, 1.  TT and PT: lane = column j, places = rows i; block 1 has m = 2, 3.

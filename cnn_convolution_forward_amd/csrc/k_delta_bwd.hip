@@ -104,7 +104,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
         const int n = min(len - k * kBlock, kBlock);
         const int64_t at = (slot0 + k) * d.Hv + hv;
         const float *rec = ws.rows + at * kRowsFloats;
-        const float gamma = rec[kGamma], invT = rec[kInvT], invP = rec[kInvP];
+        const float gamma = rec[kGamma];
         Column<T> dY;
         dY.load(rows_buffer(dy + (first + (int64_t)k * kBlock) * lddy + hv * d.Dv, n, lddy, d.Dv), at_v, ld_v, half);
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
@@ -164,14 +164,14 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
                 if constexpr (PARTS == 2) to = mfma(pt[u], f.lo, to);
             }
         }
-        f4_t fk[2][4];
+        f4_t fk[2][4], jp[2][4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
+        for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3), jp[u >> 2][u & 3] = factors(kRowInvPT, u >> 2, u & 3);
         h8_t tt[2 * kTriPages];
 #pragma unroll
         for (int u = 0; u < 2 * kTriPages; ++u) tt[u] = page(kTT + u);
         // gradient of U
-        const float ip[2] = {pow2_inv(so[0]) * invP, pow2_inv(so[1]) * invP};
+        const float ip[2] = {pow2_inv(so[0]), pow2_inv(so[1])};
         float sx[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    X[t][r] = fmaf(fk[t][a][j] * isc, X[t][r], t ? W[1][r] * ip[1] : fmaf(W[2][r], ip[1], W[0][r] * ip[0]));
+                    X[t][r] = fmaf(fk[t][a][j] * isc, X[t][r], (t ? W[1][r] * ip[1] : fmaf(W[2][r], ip[1], W[0][r] * ip[0])) * jp[t][a][j]);
                 }
             sx[t] = pow2_scale(max_halves(max_abs(X[t])));
         }
@@ -196,15 +196,11 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
             for (int t = 0; t <= i >> 1; ++t) to(t) = mfma(tt[kTriPages + high_page(t, i)], f.hi, to(t));
         }
-        f4_t eq[2][4], ek[2][4], bt[2][4];
+        f4_t eq[2][4], ez[2][4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            eq[u >> 2][u & 3] = factors(kRowEQ, u >> 2, u & 3);
-            ek[u >> 2][u & 3] = factors(kRowEK, u >> 2, u & 3);
-            bt[u >> 2][u & 3] = factors(kRowBeta, u >> 2, u & 3);
-        }
+        for (int u = 0; u < 8; ++u) eq[u >> 2][u & 3] = factors(kRowEQ, u >> 2, u & 3), ez[u >> 2][u & 3] = factors(kRowEZ, u >> 2, u & 3);
         // dS
-        const float iz[2] = {pow2_inv(sx[0]) * invT, pow2_inv(sx[1]) * invT};
+        const float iz[2] = {pow2_inv(sx[0]), pow2_inv(sx[1])};
         m = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -213,7 +209,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    Z[t][r] = -(t ? Z[1][r] * iz[1] : fmaf(Z[2][r], iz[1], Z[0][r] * iz[0])) * (ek[t][a][j] * bt[t][a][j]);
+                    Z[t][r] = -(t ? Z[1][r] * iz[1] : fmaf(Z[2][r], iz[1], Z[0][r] * iz[0])) * ez[t][a][j];
                     W[t][r] = eq[t][a][j] * dY.get(16 * t + r);
                 }
             m = max_abs(W[t], max_abs(Z[t], m));
@@ -339,7 +335,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                                      re = make_rsrc(ws.ends + rec * DKB * slices * 1024, DKB * slices * 4096);
         wait_copies();
         __syncthreads();
-        const float gamma = rows[kGamma], invT = rows[kInvT], invP = rows[kInvP];
+        const float gamma = rows[kGamma];
 
         // ---- U or Z, transposed: lane = token 32 t + col, registers = columns ----
         acc_t U[2] = {zeros(), zeros()};
@@ -398,7 +394,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        const f4_t ek = factors(kRowEK, t, a), bt = factors(kRowBeta, t, a);
+                        const f4_t ek = factors(kRowEKBack, t, a), bt = factors(kRowBeta, t, a);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             X[t][4 * a + j] = bt[j] * fmaf(-ek[j], X[t][4 * a + j], V.get(16 * t + 4 * a + j));
@@ -408,7 +404,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
             } else {                                                    // P^T dY + F K dS
                 float so[2], ip[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) so[t] = pow2_scale(max_halves(max_column(V, t))), ip[t] = pow2_inv(so[t]) * invP;
+                for (int t = 0; t < 2; ++t) so[t] = pow2_scale(max_halves(max_column(V, t))), ip[t] = pow2_inv(so[t]);
                 acc_t Y[3] = {zeros(), zeros(), zeros()};               // the last: of tokens 0..31 from those of 32..
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -428,11 +424,11 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        const f4_t fk = factors(kRowFK, t, a);
+                        const f4_t fk = factors(kRowFK, t, a), jp = factors(kRowInvPT, t, a);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int r = 4 * a + j;
-                            X[t][r] = fmaf(fk[j], X[t][r], t ? Y[1][r] * ip[1] : fmaf(Y[2][r], ip[1], Y[0][r] * ip[0]));
+                            X[t][r] = fmaf(fk[j], X[t][r], (t ? Y[1][r] * ip[1] : fmaf(Y[2][r], ip[1], Y[0][r] * ip[0])) * jp[j]);
                         }
                     }
                     sx[t] = pow2_scale(max_halves(max_abs(X[t])));
@@ -455,7 +451,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 }
             }
             float *table = small + kDots + wave * 64;
-            if (half == 0) table[col] = pow2_inv(sx[0]) * invT, table[32 + col] = pow2_inv(sx[1]) * invT;
+            if (half == 0) table[col] = pow2_inv(sx[0]), table[32 + col] = pow2_inv(sx[1]);
+            const float *it = rows + 64 * (second ? kRowInvTT : kRowInvTBack) + col;        // of the lane's tokens
+            const float it0 = it[0], it1 = it[32];
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -463,8 +461,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    U[0][r] = second ? fmaf(cross[r], f1[j], U[0][r] * f0[j]) : U[0][r] * f0[j];
-                    U[1][r] = second ? U[1][r] * f1[j] : fmaf(cross[r], f0[j], U[1][r] * f1[j]);
+                    U[0][r] = (second ? fmaf(cross[r], f1[j], U[0][r] * f0[j]) : U[0][r] * f0[j]) * it0;
+                    U[1][r] = (second ? U[1][r] * f1[j] : fmaf(cross[r], f0[j], U[1][r] * f1[j])) * it1;
                 }
             }
 #pragma unroll

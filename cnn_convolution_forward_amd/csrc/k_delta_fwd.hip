@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         const char *buf = lds + (P::kBuffers == 2 ? (k & 1) * P::kAll * 1024 : 0);
         const int n = min(len - k * kBlock, kBlock);
         const float *rec = ws.rows + ((slot0 + k) * d.Hv + hv) * kRowsFloats;
-        const float gamma = rec[kGamma], invT = rec[kInvT], invP = rec[kInvP];
+        const float gamma = rec[kGamma], invP[2] = {rec[64 * kRowInvP + col], rec[64 * kRowInvP + 32 + col]};
         Column<T> V;
         V.load(rows_buffer(v + (first + (int64_t)k * kBlock) * ldv + hv * d.Dv, n, ldv, d.Dv), at_v, ld_v, half);
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
@@ -178,9 +178,6 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
                 for (int j = 0; j < 4; ++j) to[u][j] = a[j], to[u][4 + j] = b[j];
             }
         };
-        f4_t fk[2][4];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
         read_kt(0, kt);
         __builtin_amdgcn_sched_barrier(0);
         // U = T beta R: of tokens 0..31, of 32.. from R of 32.., and from R of 0..31
@@ -198,8 +195,11 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         }
 #pragma unroll
         for (int u = 0; u < (SUM ? 0 : 2 * kTriPages); ++u) low[u] = page(kP + u);      // in T's registers
+        f4_t it[2][4], fk[2][4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) it[u >> 2][u & 3] = factors(kRowInvT, u >> 2, u & 3), fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
         __builtin_amdgcn_sched_barrier(0);
-        const float iu[2] = {pow2_inv(sr[0]) * invT, pow2_inv(sr[1]) * invT};
+        const float iu[2] = {pow2_inv(sr[0]), pow2_inv(sr[1])};
         acc_t U[2], W[2];
         float su[2] = {1.f, 1.f}, mw = 0.f;
 #pragma unroll
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    U[t][r] = t ? fmaf(part[2][r], iu[0], part[1][r] * iu[1]) : part[0][r] * iu[0];
+                    U[t][r] = (t ? fmaf(part[2][r], iu[0], part[1][r] * iu[1]) : part[0][r] * iu[0]) * it[t][a][j];
                     W[t][r] = U[t][r] * fk[t][a][j];
                 }
             }
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         if constexpr (SUM) continue;
         // y: a lane has token 32 t + col, columns 8 a + 4 half + 0..3 of the slice.  The factors of columns come from the lanes
         // that made them, through LDS (within the wave: the hardware keeps LDS accesses of a wave in order).
-        if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su[0]) * invP, table[64 + col] = pow2_inv(su[1]) * invP;
+        if (half == 0) table[col] = isc, table[32 + col] = pow2_inv(su[0]), table[64 + col] = pow2_inv(su[1]);
         __builtin_amdgcn_wave_barrier();
         const __amdgpu_buffer_rsrc_t ry = rows_buffer(y + (first + (int64_t)k * kBlock) * ldy + hv * d.Dv, n, ldy, d.Dv);
 #pragma unroll
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    o[j] = fmaf(Y[t][r], fs[j] * eq[t], t ? fmaf(Z[2][r], f0[j], Z[1][r] * f1[j]) : Z[0][r] * f0[j]);
+                    o[j] = fmaf(Y[t][r] * fs[j], eq[t], (t ? fmaf(Z[2][r], f0[j], Z[1][r] * f1[j]) : Z[0][r] * f0[j]) * invP[t]);
                 }
                 store4(ry, off + 8 * a * (uint32_t)sizeof(T), d.Dv - c0 - 8 * a, d.Dv & 3, o, y);
             }

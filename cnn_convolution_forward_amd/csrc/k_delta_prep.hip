@@ -68,7 +68,8 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
     Tiles *xs = reinterpret_cast<Tiles *>(shared);
     Square &A = *reinterpret_cast<Square *>(shared), &Ti = *reinterpret_cast<Square *>(shared + sizeof(Square));
     __shared__ double G[kBlock];
-    __shared__ float kap[2][kBlock], size[2][kBlock], betas[2][kBlock], red[8];
+    __shared__ float kap[2][kBlock], size[2][kBlock], betas[2][kBlock];
+    __shared__ float top_p[2][2][32], top_t[kBlock], top_tt[BWD ? 4 : 1][kBlock];       // largest values: of rows of P by wave and tile, of T and T^T
     const int64_t slot = blockIdx.x / d.H;
     const int hk = (int)(blockIdx.x % d.H);
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
@@ -198,6 +199,7 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         const int64_t rec = slot * d.Hv + hv;
         float *rows = ws.rows + rec * kRowsFloats;
         float *bt = betas[hv & 1];                                      // by turns: the last head's pages of T may still be on their way
+        float ekb = 0.f;
         if (wave == 0) {
             double v = gv < -1e4f ? -1e4 : (double)gv;                  // a NaN stays
 #pragma unroll
@@ -209,11 +211,13 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             const float E = decay_of(v, 0.0), F = decay_of(__shfl(v, 63), v);
             G[lane] = v;
             bt[lane] = b;
-            rows[64 * kRowEK + lane] = E * kap[0][lane];
-            rows[64 * kRowBeta + lane] = b;
+            const float ek = E * kap[0][lane];
+            ekb = ek * b;
+            rows[64 * (BWD ? kRowEKBack : kRowEK) + lane] = ek;
             rows[64 * kRowFK + lane] = F * kap[0][lane];
             rows[64 * kRowEQ + lane] = d.scale * E * kap[1][lane];
             if constexpr (BWD) {
+                rows[64 * kRowBeta + lane] = b;
                 rows[64 * kRowE + lane] = E;
                 rows[64 * kRowF + lane] = F;
                 rows[64 * kRowKK + lane] = kap[0][lane];
@@ -226,13 +230,14 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             if (hv + 1 < (hk + 1) * d.group) load_gates(hv + 1);
         }
         __syncthreads();                                                // also: keys and queries, or the last head's A and T, are free
-        float val[24], pm = 0.f;
+        float val[24];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int ib = u ? 0 : 1, jb = u ? 0 : part;
             const int mine = 32 * (by_i ? ib : jb) + col;
             const double g_mine = G[mine];
             const float k_mine = kap[by_i ? 1 : 0][mine];
+            float top = 0.f;
 #pragma unroll
             for (int r = 0; r < (u ? 8 : 16); ++r) {
                 const int other = 32 * (by_i ? jb : ib) + (u ? 16 * part : 0) + acc_row(r, half);
@@ -242,15 +247,13 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
                 asm("" : "+v"(x));                                      // all of it, then a selection: no branch for each
                 x = j < i || (which && j == i) ? x : 0.f;
                 val[16 * u + r] = x;
-                pm = fmaxf(pm, fabsf(x));
+                top = fmaxf(top, fabsf(x));
                 if (!which) A[i][j] = x;
             }
+            top = max_halves(top);
+            if (which && half == 0) top_p[part][u][col] = top;
         }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) pm = fmaxf(pm, __shfl_xor(pm, m));
-        if (lane == 0) red[wave] = pm;
         __syncthreads();
-        const float sp = pow2_scale(fmaxf(red[2], red[3]));
         uint4 *out = ws.tri + rec * ws.tri_pages * kPage + lane;
         const auto put = [&](int kind, int page, const Pair &p) {
             out[((2 * kind) * kTriPages + page) * kPage] = __builtin_bit_cast(uint4, p.hi);
@@ -258,9 +261,14 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         };
         if (which) {                                                    // P or P^T: registers 8 m .. 8 m + 7 are pages
             const auto page = [&](int ib, int jb, int m) { return BWD ? high_page(jb, 2 * ib + m) : low_page(ib, 2 * jb + m); };
+            // the lane's row, which is in two tiles of P (rows 32.. and 0..31, the latter cut in two) or three or one of P^T
+            const float first = fmaxf(top_p[0][1][col], top_p[1][1][col]);
+            const float low = BWD ? fmaxf(first, top_p[0][0][col]) : first, high = BWD ? top_p[1][0][col] : fmaxf(top_p[0][0][col], top_p[1][0][col]);
+            const float s_low = pow2_scale(low), s_high = pow2_scale(high), sp[2] = {BWD && !part ? s_low : s_high, s_low};
 #pragma unroll
             for (int u = 0; u < 3; ++u)
-                put(BWD ? 2 : 1, u < 2 ? page(1, part, u) : page(0, 0, part), split8(sp, [&](int e) { return val[8 * u + e]; }));
+                put(BWD ? 2 : 1, u < 2 ? page(1, part, u) : page(0, 0, part), split8(sp[u >> 1], [&](int e) { return val[8 * u + e]; }));
+            if (part == 0) rows[64 * (BWD ? kRowInvPT : kRowInvP) + lane] = pow2_inv(half ? s_high : s_low);
         }
 
         // T: the blocks on the diagonal
@@ -301,20 +309,43 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             }
             __syncthreads();
         }
-        float tm = 0.f;
+        {
+            float tm = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int i = tid >> 2, j = (tid & 3) * 16 + e;
-            if (j <= i) tm = fmaxf(tm, fabsf(BWD ? Ti[i][j] : Ti[i][j] * bt[j]));
+            for (int e = 0; e < 16; ++e) {
+                const int i = tid >> 2, j = (tid & 3) * 16 + e;
+                if (j <= i) tm = fmaxf(tm, fabsf(BWD ? Ti[i][j] : Ti[i][j] * bt[j]));
+            }
+            tm = fmaxf(tm, __shfl_xor(tm, 1));
+            tm = fmaxf(tm, __shfl_xor(tm, 2));
+            if ((tid & 3) == 0) top_t[tid >> 2] = tm;
+            if constexpr (BWD) {
+                tm = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = 16 * wave + e;
+                    if (lane <= i) tm = fmaxf(tm, fabsf(Ti[i][lane]));
+                }
+                top_tt[wave][lane] = tm;
+            }
         }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) tm = fmaxf(tm, __shfl_xor(tm, m));
-        if (lane == 0) red[4 + wave] = tm;
         __syncthreads();
-        const float st = pow2_scale(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
-        if (tid == 0) rows[kInvT] = pow2_inv(st), rows[kInvP] = pow2_inv(sp);
+        const auto scale_t = [&](int i) { return pow2_scale(top_t[i]); };
+        const auto scale_tt = [&](int j) {
+            constexpr int w = BWD ? 1 : 0;
+            return pow2_scale(fmaxf(fmaxf(top_tt[0][j], top_tt[w][j]), fmaxf(top_tt[2 * w][j], top_tt[3 * w][j])));
+        };
+        if (wave == 0) {
+            rows[64 * (BWD ? kRowInvTBack : kRowInvT) + lane] = pow2_inv(scale_t(lane));
+            if constexpr (BWD) {
+                const float inv = pow2_inv(scale_tt(lane));
+                rows[64 * kRowInvTT + lane] = inv;
+                rows[64 * kRowEZ + lane] = ekb * inv;
+            }
+        }
         for (int f = wave; f < kTriPages; f += 4) {
             const int ib = f < 2 ? 0 : 1, m = ib ? f - 2 : f, i = 32 * ib + col;
+            const float st = scale_t(i);
             // forward: times beta of the column, so that the kernel behind it has R = V - E K S
             put(0, f, split8(st, [&](int e) {
                     const int j = page_at(m, half, e);
@@ -324,6 +355,7 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
         if constexpr (BWD) {
             for (int f = wave; f < kTriPages; f += 4) {
                 const int jb = f < 4 ? 0 : 1, m = jb ? f - 2 : f, j = 32 * jb + col;
+                const float st = scale_tt(j);
                 put(1, f, split8(st, [&](int e) {
                         const int i = page_at(m, half, e);
                         return j <= i ? Ti[i][j] : 0.f;

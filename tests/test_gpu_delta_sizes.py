@@ -123,3 +123,76 @@ def test_upstream_gradients_that_are_not_finite(dt, unit, bad):
         assert torch.equal(got[2][:, :, 1][..., other], want[2][:, :, 1][..., other]), token
         assert torch.equal(got[5][:, :, :, other], want[5][:, :, :, other]), token
         assert not bool(torch.isfinite(got[2][0, :token + 1, 1, 3]).any()), token
+
+
+# ---- rows of queries and keys, gates ------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_queries_of_any_size(dt):
+    """y is linear in a token's query: with rows many powers of two apart, each has the bits that it has alone."""
+    c = Case(dt, [130], 2, 4, 40, 48, unit=False, seed=34)
+    y0, s0, _ = _forward(c)
+    f = torch.from_numpy(np.ldexp(1.0, np.random.default_rng(1).integers(-40, 40, (1, 130, 2, 1)))).float().cuda()
+    y, s, _ = _forward(c, q=(c.q * f).to(c.dt))
+    assert torch.equal(y, (y0 * f.repeat_interleave(2, 2)).to(c.dt)) and torch.equal(s, s0)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("bf16", False), ("f32", True), ("f32", False)])
+def test_one_token_that_is_not_finite(dt, unit, bad):
+    """A query spoils its own output only; a key or a gate the tokens from its 32 on."""
+    c = Case(dt, [130], 1, 2, 32, 40, unit=unit, seed=35)
+    clean = _forward(c)
+    for token in (0, 20, 31, 32, 50, 63, 64, 97, 129):
+        for name, head in (("q", 0), ("k", 0), ("g", 1), ("b", 1)):
+            if name == "g" and bad == -INF:
+                continue                                             # a decay to nothing
+            _held(c, clean, name, token, head, bad, token // 32 * 32)
+        data = c.q.clone()
+        data[0, token, 0, 3] = bad
+        y = _forward(c, q=data)[0]
+        other = torch.arange(130, device="cuda") != token
+        assert torch.equal(y[:, other], clean[0][:, other]) and not bool(torch.isfinite(y[:, token]).any()), token
+
+
+def _gradients(c, q, k, v, g, b, fq, fk, S, dy, ds):
+    """The definition's, with the infinities and NaN that they have."""
+    hist = np.zeros((len(q) + 1,) + S.shape)
+    hist[0] = S
+    with np.errstate(all="ignore"):
+        for t in range(len(q)):
+            D = np.exp(g[t]) * hist[t]
+            hist[t + 1] = D + np.outer(k[t], b[t] * (v[t] - k[t] @ D))
+        (dq, dk, dv, dg, db, d0), _ = R.backward(q, k, v, g, b, hist, c.scale, dy, ds)
+        return R.through_unit(dq, q, fq, c.unit), R.through_unit(dk, k, fk, c.unit), dv, dg, db, d0
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("bf16", False), ("f32", True), ("f32", False)])
+def test_gradients_beside_one_that_is_not_finite(dt, unit, bad):
+    """What stays finite is what the definition leaves finite, and keeps its bits; outside the value's block all of that does."""
+    c = Case(dt, [130], 1, 1, 32, 40, unit=unit, seed=36)
+    st = _forward(c)[2]
+    want = _backward(c, st)
+    for token in (0, 20, 31, 32, 50, 63, 64, 97, 129):
+        for name in "qkvgb":
+            data = dict(zip("qkvgb", (t.clone() for t in c.data())))
+            x = data[name]
+            x[(0, token, 0) + ((3,) if x.dim() == 4 else ())] = bad
+            st2 = _forward(c, **data)[2]
+            got = _backward(c, st2, **data)
+            c2 = Case.__new__(Case)
+            c2.__dict__.update(c.__dict__)
+            c2.q, c2.k, c2.v, c2.g, c2.beta = data.values()
+            with np.errstate(all="ignore"):
+                (_, _, _, _, q, k, v, g, b, fq, fk), = c2.sequences()
+            ref = _gradients(c, q, k, v, g, b, fq, fk, _np(c.s0)[0, 0], _np(c.dy)[0, :, 0], _np(c.ds)[0, 0])
+            outside = np.arange(130) // 64 != token // 64
+            for what, a, w, r in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), got, want, ref):
+                at = (name, token, what)
+                a, w = _np(a).reshape(r.shape), _np(w).reshape(r.shape)
+                fin, held = np.isfinite(r), np.isfinite(a)
+                assert not (held & ~fin).any(), at
+                assert np.array_equal(a[held], w[held]), at
+                if what != "ds0":
+                    assert np.array_equal(held[outside], fin[outside]), at
