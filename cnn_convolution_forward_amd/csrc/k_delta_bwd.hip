@@ -276,15 +276,9 @@ template <int PARTS> struct GradPages {
 };
 // Floats behind the pages.
 enum { kSizes = 0 /* 3 x 4 x 64: largest values of a token's U, Z, dY by slice */, kDots = 768 /* 5 x 4 x 64 */, kTotals = 2048 /* 2 x 64 */,
-       kBack = 2176 /* 3 x 64: inverse scales of U, Z, dY */, kScales = 2368 /* 2 x 4: of B1, B2, M1, M2 by block of tokens */,
-       kKept = 2376 /* 4 */, kTop = 2380 /* 2 x 4: largest values of S and dS by slice */, kRec = 2388 /* the rows record */,
+       kBack = 2176 /* 3 x 64: inverse scales of U, Z, dY */, kScales = 2368 /* 4 x 64: of B1, B2, M1, M2 by token */,
+       kKept = 2624 /* 4 */, kTop = 2628 /* 2 x 4: largest values of S and dS by slice */, kRec = 2636 /* the rows record */,
        kSmall = kRec + kRowsFloats };
-
-__device__ __forceinline__ float max_wave(float m) {
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
-    return m;
-}
 
 struct GradOut {
     RowsOut dq, dk, dv, dg, db;
@@ -605,7 +599,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 C[q] = x;
                 m = max_abs(x, m);
             }
-            const float sc = pow2_scale(max_wave(m));
+            const float sc = pow2_scale(max_halves(m));                 // of the lane's row: a token's gradients cost others no bits
             const int to = is_m ? (by_i ? P::kM1 : P::kM2) : (by_i ? P::kB1 : P::kB2);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -619,7 +613,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     put(kTriPages + p, f.lo);
                 }
             }
-            if (lane == 0) small[kScales + 4 * mine_b + w] = pow2_inv(sc);
+            if (half == 0) small[kScales + 64 * w + 32 * mine_b + col] = pow2_inv(sc);
         };
         if (w == 0) second_part(std::false_type(), std::true_type());
         else if (w == 1) second_part(std::false_type(), std::false_type());
@@ -704,7 +698,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 32 * t + col;
-                const float i1 = small[kScales + 4 * t + (second ? 1 : 0)], i2 = small[kScales + 4 * t + (second ? 3 : 2)];
+                const float i1 = small[kScales + 64 * (second ? 1 : 0) + tok], i2 = small[kScales + 64 * (second ? 3 : 2) + tok];
                 const float E = rows[64 * kRowE + tok], kk = rows[64 * kRowKK + tok], kq = rows[64 * kRowKQ + tok];
                 // waves 0..3: of dY S^T and of Z S^T; waves 4..7: of U dS^T
                 const float fa = second ? rows[64 * kRowF + tok] * iss * small[kBack + tok] : d.scale * E * iss * small[kBack + 128 + tok];

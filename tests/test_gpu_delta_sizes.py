@@ -53,6 +53,16 @@ def test_large_upstream_gradients_leave_later_tokens_alone(dt, unit, token, clea
         assert not torch.equal(a[:, :clean], b[:, :clean]), name
 
 
+@pytest.mark.parametrize("dt,unit", [("bf16", True), ("f32", True), ("f32", False)])
+def test_upstream_gradients_of_any_size(dt, unit):
+    """A query's gradient is linear in the upstream gradient of its token, and depends on no other's."""
+    c = Case(dt, [130], 2, 4, 40, 48, unit=unit, seed=37)
+    st = _forward(c)[2]
+    f = torch.from_numpy(np.ldexp(1.0, np.random.default_rng(2).integers(-40, 40, (1, 130, 1, 1)))).float().cuda()
+    same = torch.equal(_backward(c, st, (c.dy * f).to(c.dt))[0], (_backward(c, st)[0] * f).to(c.dt))
+    assert same
+
+
 def _definition(q, k, v, g, b, S, scale):
     """The recurrence with the infinities and NaN that it makes."""
     y = np.zeros_like(v)
