@@ -48,10 +48,11 @@ __device__ __forceinline__ acc_t zeros() {
     return z;
 }
 
-// The power of two that brings a (>= 0) to [2^13, 2^14), at most 2^most; infinities get the smallest.
-__device__ __forceinline__ float pow2_scale(float a, int most = 113) {
+// The power of two that brings a (>= 0) to [2^13, 2^14), at most 2^113, so that its inverse is a normal number; infinities get the
+// smallest.  What such an inverse is multiplied with may be small too: it meets the sum first, then the next factor.
+__device__ __forceinline__ float pow2_scale(float a) {
     const int e = (int)(__float_as_uint(a) >> 23) & 255;
-    return __uint_as_float((uint32_t)min(267 - e, 127 + most) << 23);
+    return __uint_as_float((uint32_t)min(267 - e, 240) << 23);
 }
 // 1/s of a power of two.
 __device__ __forceinline__ float pow2_inv(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }

@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(Seq s, Delta d, DeltaW
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * a + j;
-                    X[t][r] = fmaf(fk[t][a][j] * isc, X[t][r], (t ? W[1][r] * ip[1] : fmaf(W[2][r], ip[1], W[0][r] * ip[0])) * jp[t][a][j]);
+                    X[t][r] = fmaf(fk[t][a][j], X[t][r] * isc, (t ? W[1][r] * ip[1] : fmaf(W[2][r], ip[1], W[0][r] * ip[0])) * jp[t][a][j]);
                 }
             sx[t] = pow2_scale(max_halves(max_abs(X[t])));
         }
@@ -592,7 +592,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     if (!by_i && is_m) f *= rows[64 * kRowBeta + other];
                     f *= is_m ? -D : d.scale * D;
                     const float inv_other = small[kBack + 64 * (by_i ? 0 : is_m ? 1 : 2) + other];
-                    float value = x[r] * (inv_mine * inv_other) * f;
+                    float value = x[r] * inv_mine * inv_other * f;
                     asm("" : "+v"(value));                              // all of it, then a selection: no branch for each
                     x[r] = in ? value : 0.f;
                 }
@@ -701,8 +701,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 const float i1 = small[kScales + 64 * (second ? 1 : 0) + tok], i2 = small[kScales + 64 * (second ? 3 : 2) + tok];
                 const float E = rows[64 * kRowE + tok], kk = rows[64 * kRowKK + tok], kq = rows[64 * kRowKQ + tok];
                 // waves 0..3: of dY S^T and of Z S^T; waves 4..7: of U dS^T
-                const float fa = second ? rows[64 * kRowF + tok] * iss * small[kBack + tok] : d.scale * E * iss * small[kBack + 128 + tok];
-                const float fb = -E * iss * small[kBack + 64 + tok];
+                const float fa = second ? rows[64 * kRowF + tok] * small[kBack + tok] : d.scale * E * small[kBack + 128 + tok];
+                const float fb = -E * small[kBack + 64 + tok];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     // the token's key and query: pages of this block of dk lie as the registers do
@@ -715,14 +715,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                         const int q = 8 * u + j;
                         const float kx = ((float)kh[j] + (float)kl[j]) * kk;
                         if constexpr (second) {
-                            const float state = A[t][q] * fa;
+                            const float state = A[t][q] * iss * fa;
                             A[t][q] = state + fmaf(p1[t][q], i1, p2[t][q] * i2);
                             dot[0][t] = fmaf(kx, A[t][q], dot[0][t]);
                             dot[1][t] = fmaf(kx, state, dot[1][t]);
                         } else {
                             const float qx = ((float)qh[j] + (float)ql[j]) * kq;
-                            A[t][q] = fmaf(A[t][q], fa, p1[t][q] * i1);
-                            Bb[t][q] = fmaf(Bb[t][q], fb, p2[t][q] * i2);
+                            A[t][q] = fmaf(A[t][q] * iss, fa, p1[t][q] * i1);
+                            Bb[t][q] = fmaf(Bb[t][q] * iss, fb, p2[t][q] * i2);
                             dot[0][t] = fmaf(qx, A[t][q], dot[0][t]);
                             dot[1][t] = fmaf(kx, Bb[t][q], dot[1][t]);
                         }

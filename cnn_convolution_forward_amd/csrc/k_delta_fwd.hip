@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             for (int a = 0; a < 4; ++a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    Rr[t][4 * a + j] = fmaf(-(ek[t][a][j] * isc), X[t][4 * a + j], V.get(16 * t + 4 * a + j));
+                    Rr[t][4 * a + j] = fmaf(-ek[t][a][j], X[t][4 * a + j] * isc, V.get(16 * t + 4 * a + j));
             }
             sr[t] = pow2_scale(max_halves(max_abs(Rr[t])));
         }

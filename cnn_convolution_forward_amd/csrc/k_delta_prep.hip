@@ -109,8 +109,7 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[which][i]));
             m = fmaxf(m, __shfl_xor(m, 1));
             m = fmaxf(m, __shfl_xor(m, 2));
-            // with unit = 0 the factor stays far from the smallest numbers, as states may be small too
-            const float sc = pow2_scale(m, d.unit ? 113 : 60);
+            const float sc = pow2_scale(m);
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
@@ -243,7 +242,7 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
                 const int other = 32 * (by_i ? jb : ib) + (u ? 16 * part : 0) + acc_row(r, half);
                 const int i = by_i ? mine : other, j = by_i ? other : mine;
                 const float D = by_i ? decay_of(g_mine, G[other]) : decay_of(G[other], g_mine);
-                float x = prod[16 * u + r] * (k_mine * kap[by_i ? 0 : which][other]) * D * (which ? d.scale : bt[i]);
+                float x = prod[16 * u + r] * k_mine * kap[by_i ? 0 : which][other] * D * (which ? d.scale : bt[i]);     // two small factors: not their product
                 asm("" : "+v"(x));                                      // all of it, then a selection: no branch for each
                 x = j < i || (which && j == i) ? x : 0.f;
                 val[16 * u + r] = x;

@@ -568,6 +568,7 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
  * fp32; decays are added up in fp64.  The power of two is that of the largest value in a row or column; in a column of values
  * or of upstream gradients, of the largest of tokens 0..31, or 32..63, of a block: values far smaller than that have fewer bits.
+ * So have, with unit = 0, rows of q and k whose largest value is below 2^-90.
  * A log decay below -10000 counts as -10000: nothing of the state is left.  Infinities and NaN: a state, or a token's values, that are not
  * finite make results of their head non-finite, perhaps from the start of their 64-token
  * block on (v and dy: of their 32 tokens; gradients: before it too), in their own sequence only.

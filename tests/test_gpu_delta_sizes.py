@@ -165,6 +165,33 @@ def test_one_token_that_is_not_finite(dt, unit, bad):
         assert torch.equal(y[:, other], clean[0][:, other]) and not bool(torch.isfinite(y[:, token]).any()), token
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k"])
+def test_tiny_queries_and_keys(dt, name):
+    """With unit = 0: 2**-90 times the queries, and 2**-90 beside 2**-60 times the keys, whose products with each other
+    are nothing beside 1 either way.  Outputs and gradients follow by powers of two, up to roundings.
+
+    Powers of two end at 2**113.  A row of q or k and what is made of it with values of size 1 stays below that.  In the backward pass
+    one operand (products of dy and corrections, times what makes a row of q from numbers of size 2**13) is near 2**-103
+    and ends up with an error of 2**-25 2**-113 = 2**-138, less than 2**-30 of its row's largest, where it had 22 bits.  Other fp32 values
+    then round the other way, by 2**-24 of a partial sum; no sum has more than 192 terms, 192 2**-24 < 2**-16."""
+    c = Case(dt, [130], 2, 4, 40, 48, unit=False, seed=38, g=lambda r, s: -r.uniform(0, 0.05, s))
+    c.ds.zero_()
+    if name == "k":
+        c.s0.zero_()
+    got = []
+    for e in (0, -90) if name == "q" else (-60, -90):
+        x = {name: getattr(c, name) * 2.0 ** e}
+        y, s, st = _forward(c, **x)
+        got.append((y, s) + _backward(c, st, **x))
+    f = 2.0 ** -90 if name == "q" else 2.0 ** -30
+    power = (1, 0, 0, 1, 1, 1, 1, 1) if name == "q" else (1, 1, 1, 0, 1, 1, 1, 0)
+    for what, a, b, n in zip(("y", "sT", "dq", "dk", "dv", "dg", "dbeta", "ds0"), *got, power):
+        w = a.double() * f ** n
+        assert float((b.double() - w).abs().max()) <= (2.0 ** -8 if a.dtype == torch.bfloat16 else 2.0 ** -16) * float(w.abs().max()), what
+        assert bool((a != 0).any()), what
+
+
 def _gradients(c, q, k, v, g, b, fq, fk, S, dy, ds):
     """The definition's, with the infinities and NaN that they have."""
     hist = np.zeros((len(q) + 1,) + S.shape)
