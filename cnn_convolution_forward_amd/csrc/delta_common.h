@@ -179,16 +179,17 @@ __device__ __forceinline__ Block find_block(const Seq &s, int per, int64_t n) {
 // LDS address from M0 (one wait state after it is written) and adds its offset on both sides; five states cover a base
 // that a vector instruction wrote just before, which the compiler does not look for here.  In assembly because the
 // compiler, which cannot tell one buffer from the other, waits for all such loads before any
-// read of LDS.  They have no output registers; wait_copies is their wait.  Nothing else here uses M0.
+// read of LDS.  They have no output registers; wait_copies is their wait.  M0 is named as written, which the compiler
+// warns about, as it never keeps a value there.
 __device__ __forceinline__ void copy4(const uint4 *src, uint32_t dst, uint32_t at) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:2*1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:3*1024"
                  :
                  : "s"(dst), "v"(at), "s"(src)
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void copy1(const uint4 *src, uint32_t dst, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(at), "s"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(at), "s"(src) : "memory", "m0");
 }
 template <int PAGES> __device__ __forceinline__ void copy_pages(const void *from, uint32_t dst, int wave, int waves, int lane) {
     const uint4 *src = (const uint4 *)from;

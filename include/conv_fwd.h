@@ -569,9 +569,9 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * fp32; decays are added up in fp64.  The power of two is that of the largest value in a row or column; in a column of values
  * or of upstream gradients, of the largest of tokens 0..31, or 32..63, of a block: values far smaller than that have fewer bits.
  * So have, with unit = 0, rows of q and k whose largest value is below 2^-90.
- * A log decay below -10000 counts as -10000: nothing of the state is left.  Infinities and NaN: a state, or a token's values, that are not
- * finite make results of their head non-finite, perhaps from the start of their 64-token
- * block on (v and dy: of their 32 tokens; gradients: before it too), in their own sequence only.
+ * A log decay below -10000 counts as -10000: nothing of the state is left.  Infinities and NaN: results that depend on one
+ * are not finite, in its own sequence and head only.  Nor need those be of tokens in front of it among the same 32, or
+ * gradients of its 64-token block; what is finite is right.
  *
  * Long sequences are cut into segments that run at once and are joined where a batch has few of them: results then
  * differ by roundings from those of the same sequence in another batch.  They have the same bits in any batch with T of at
