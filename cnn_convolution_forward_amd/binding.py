@@ -1138,6 +1138,8 @@ def make_delta(q, v, offsets=None, max_len=None, scale=None, unit=False, eps=1e-
     if q.dim() != v.dim() or v.dim() != (3 if step or offsets is not None else 4):
         raise ValueError("q and v must be (sequences, %sheads, dim)%s" % ("" if step else "tokens, ",
                                                                       "" if step else ", or (tokens, heads, dim) packed with offsets"))
+    if not all(q.shape[-2:] + v.shape[-2:]):
+        raise ValueError("q and v must have heads, and heads channels")
     rows = v.shape[:-2]
     heads, dim = v.shape[-2:]
     par = DeltaParams(q.shape[-2], heads, q.shape[-1], dim, int(bool(unit)), q.shape[-1] ** -0.5 if scale is None else scale, eps)
