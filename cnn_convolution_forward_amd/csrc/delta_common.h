@@ -49,7 +49,7 @@ __device__ __forceinline__ acc_t zeros() {
 }
 
 // The power of two that brings a (>= 0) to [2^13, 2^14), at most 2^113, so that its inverse is a normal number; infinities get the
-// smallest.  What such an inverse is multiplied with may be small too: it meets the sum first, then the next factor.
+// smallest.  What such an inverse is multiplied with may be small, or large, too: the sum meets it first where it is below 1.
 __device__ __forceinline__ float pow2_scale(float a) {
     const int e = (int)(__float_as_uint(a) >> 23) & 255;
     return __uint_as_float((uint32_t)min(267 - e, 240) << 23);

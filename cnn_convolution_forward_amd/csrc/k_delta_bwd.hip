@@ -579,7 +579,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                 }
                 // the lane's own token and its factors; the other index runs over the registers
                 const int mine = 32 * mine_b + col;
-                const float inv_mine = small[kBack + 64 * (by_i ? (is_m ? 1 : 2) : 0) + mine];
+                const float inv_mine = small[kBack + 64 * (by_i ? (is_m ? 1 : 2) : 0) + mine], i0 = fminf(inv_mine, 1.f), i1 = fmaxf(inv_mine, 1.f);
                 const double g_mine = G[mine];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -592,7 +592,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     if (!by_i && is_m) f *= rows[64 * kRowBeta + other];
                     f *= is_m ? -D : d.scale * D;
                     const float inv_other = small[kBack + 64 * (by_i ? 0 : is_m ? 1 : 2) + other];
-                    float value = x[r] * inv_mine * inv_other * f;
+                    float value = x[r] * i0 * (inv_other * i1) * f;
                     asm("" : "+v"(value));                              // all of it, then a selection: no branch for each
                     x[r] = in ? value : 0.f;
                 }
@@ -694,15 +694,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(Seq s, Delta d, DeltaWs
                     if constexpr (PARTS == 2) p1[t] = mfma(qt[4 + u], b, p1[t]), p2[t] = mfma(kt[4 + u], c, p2[t]);
                 }
             }
-            const float iss = pow2_inv(sc);
+            const float iss = fminf(pow2_inv(sc), 1.f), ist = fmaxf(pow2_inv(sc), 1.f);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 32 * t + col;
                 const float i1 = small[kScales + 64 * (second ? 1 : 0) + tok], i2 = small[kScales + 64 * (second ? 3 : 2) + tok];
                 const float E = rows[64 * kRowE + tok], kk = rows[64 * kRowKK + tok], kq = rows[64 * kRowKQ + tok];
                 // waves 0..3: of dY S^T and of Z S^T; waves 4..7: of U dS^T
-                const float fa = second ? rows[64 * kRowF + tok] * small[kBack + tok] : d.scale * E * small[kBack + 128 + tok];
-                const float fb = -E * small[kBack + 64 + tok];
+                const float fa = ist * (second ? rows[64 * kRowF + tok] * small[kBack + tok] : d.scale * E * small[kBack + 128 + tok]);
+                const float fb = -ist * (E * small[kBack + 64 + tok]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     // the token's key and query: pages of this block of dk lie as the registers do

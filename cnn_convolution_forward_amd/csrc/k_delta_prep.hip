@@ -235,14 +235,14 @@ __global__ __launch_bounds__(kThreads, resident(sizeof(T) / 2, DKB)) void delta_
             const int ib = u ? 0 : 1, jb = u ? 0 : part;
             const int mine = 32 * (by_i ? ib : jb) + col;
             const double g_mine = G[mine];
-            const float k_mine = kap[by_i ? 1 : 0][mine];
+            const float k_mine = kap[by_i ? 1 : 0][mine], k0 = fminf(k_mine, 1.f), k1 = fmaxf(k_mine, 1.f);
             float top = 0.f;
 #pragma unroll
             for (int r = 0; r < (u ? 8 : 16); ++r) {
                 const int other = 32 * (by_i ? jb : ib) + (u ? 16 * part : 0) + acc_row(r, half);
                 const int i = by_i ? mine : other, j = by_i ? other : mine;
                 const float D = by_i ? decay_of(g_mine, G[other]) : decay_of(G[other], g_mine);
-                float x = prod[16 * u + r] * k_mine * kap[by_i ? 0 : which][other] * D * (which ? d.scale : bt[i]);     // two small factors: not their product
+                float x = prod[16 * u + r] * k0 * (kap[by_i ? 0 : which][other] * k1) * D * (which ? d.scale : bt[i]);
                 asm("" : "+v"(x));                                      // all of it, then a selection: no branch for each
                 x = j < i || (which && j == i) ? x : 0.f;
                 val[16 * u + r] = x;

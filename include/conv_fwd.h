@@ -568,7 +568,8 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
  * fp32; decays are added up in fp64.  The power of two is that of the largest value in a row or column; in a column of values
  * or of upstream gradients, of the largest of tokens 0..31, or 32..63, of a block: values far smaller than that have fewer bits.
- * So have, with unit = 0, rows of q and k whose largest value is below 2^-90.
+ * So have rows and columns whose largest value is below 2^-90 (of q and k with unit = 0); values and states
+ * beyond 2^100 may end as infinities.
  * A log decay below -10000 counts as -10000: nothing of the state is left.  Infinities and NaN: results that depend on one
  * are not finite, in its own sequence and head only.  Nor need those be of tokens in front of it among the same 32, or
  * gradients of its 64-token block; what is finite is right.

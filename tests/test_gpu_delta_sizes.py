@@ -166,6 +166,38 @@ def test_one_token_that_is_not_finite(dt, unit, bad):
         assert torch.equal(y[:, other], clean[0][:, other]) and not bool(torch.isfinite(y[:, token]).any()), token
 
 
+@pytest.mark.parametrize("e", [-80, 95])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_tiny_and_huge_values(dt, e):
+    """Results follow the size of values and states, and, for themselves, of upstream gradients: the same bits but for the power of two."""
+    c = Case(dt, [130], 2, 4, 40, 48, seed=40, g=lambda r, s: -r.uniform(0, 0.05, s))
+    f = 2.0 ** e
+    y, s, st = _forward(c)
+    want = _backward(c, st)
+    s0, ds = c.s0, c.ds
+    c.s0 = s0 * f
+    y2, s2, st2 = _forward(c, v=c.v * f)
+    same = torch.equal(y2, y * f), torch.equal(s2, s * f), torch.equal(st2, st * f)
+    assert all(same), same
+    for got, power in ((_backward(c, st2, v=c.v * f), (1, 1, 0, 1, 1, 0)), (None, (1, 1, 1, 1, 1, 1))):
+        if got is None:
+            c.ds = ds * f
+            got = _backward(c, st, c.dy * f)
+        for what, a, w, n in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), got, want, power):
+            same = torch.equal(a, w * f ** n)
+            assert same, (what, power)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_huge_queries_beside_tiny_keys(dt):
+    """With unit = 0: a factor of 2**120 in the queries and of 2**-80 in the keys, whose products are of an ordinary size."""
+    c = Case(dt, [130], 2, 4, 40, 48, unit=False, seed=41, g=lambda r, s: -r.uniform(0, 0.05, s))
+    c.s0.zero_()
+    (y, s, _), (y2, s2, _) = (_forward(c, q=c.q * 2.0 ** a, k=c.k * 2.0 ** b) for a, b in ((0, -60), (120, -80)))
+    same = torch.equal(y2, y * 2.0 ** 100), torch.equal(s2, s * 2.0 ** -20)
+    assert all(same), same
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("name", ["q", "k"])
 def test_tiny_queries_and_keys(dt, name):
