@@ -2,9 +2,12 @@
 // (k_delta_prep.hip, k_delta_fwd.hip, k_delta_bwd.hip).
 //
 // Products run on v_mfma_f32_32x32x16_f16 with operands that are sums of two fp16
-// numbers, hi + lo, under a power of two that brings the largest magnitude of
-// the operand's row, column or tile to [2^13, 2^14): 22 bits of every value, and an
-// absolute error of 2^-28 of the largest for small ones.  hi hi + hi lo + lo hi then
+// numbers, hi + lo, under a power of two that brings the largest magnitude of the
+// operand's row or column to [2^13, 2^14): 22 bits of a value down to 2^-16 of that largest,
+// and an absolute error of 2^-38 of it below (half of fp16's smallest step; measured).  What shares a power of two is what one
+// result is summed from, so that nothing takes the bits of results that do not depend on it: rows of q, k, T, P, and of the products
+// in the gradients; columns of a state, and of values by 32 tokens.  (The gradients of q and k take one for all of a state.)
+// An infinity has hi = inf and lo = NaN, and the rest of its row or column nothing.  hi hi + hi lo + lo hi then
 // has the accuracy of an fp32 product (what is left out is 2^-22 of it) at three
 // times the cost of an fp16 one and a fifth of the fp32 matrix rate's.  bf16
 // queries, keys, values and upstream gradients fit one fp16 number exactly (8 bits).

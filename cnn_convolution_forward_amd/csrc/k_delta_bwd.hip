@@ -19,11 +19,11 @@
 // behind every block in the workspace; the second takes all blocks at once, with
 // the saved S in front and dS behind each.
 //
-// 8 x 2048 tokens in 16 heads of 128, bf16, 895 to 930 us on different cards: the operands 135, the chain 235, the gradients
-// 590.  The chain is bound as the forward one is.  The second kernel has one workgroup to a compute unit (its pages take
-// 141 KB of LDS) and reads 1.3 GB of states and their gradients, each by columns and by rows, mostly from the caches; a block
-// takes 66000 cycles, of which 18000 wait for states, 11000 make B and M (the decays' exp2 of differences in fp64, four for each
-// pair of tokens) and 19000 the products of the third part.  Tried and slower: the third part's loads in front of the
+// 8 x 2048 tokens in 16 heads of 128, bf16, 955 to 990 us on different cards: the operands 148, the chain 245, the gradients
+// 625.  The chain is bound as the forward one is.  The second kernel has one workgroup to a compute unit (its pages take
+// 143 KB of LDS) and reads 1.3 GB of states and their gradients, each by columns and by rows, mostly from the caches; a block
+// takes 69000 cycles, of which 4000 to 6000 wait for the states' columns, 11000 make B and M (the decays' exp2 of differences in fp64,
+// four for each pair of tokens) and 12000 to 14000 are the products with the states' rows and the wait for these.  Tried and slower: the third part's loads in front of the
 // second (more registers than there are: 1360 us and more), the states' columns loaded four wide and transposed (946 to 965).
 #include <type_traits>
 

@@ -14,9 +14,10 @@
 // asynchronously, a block ahead where two buffers fit; values are loaded at their block's start.
 //
 // What bounds it: the chain itself.  A block's products depend on each other, and there is one wave to a SIMD
-// (8 x 2048 tokens in 16 heads of 128: 512 waves for 1024 SIMDs, 210 us for 32 blocks of which the matrix instructions
-// take 45): 2500 cycles K S and Q S, 2200 R with the wait for V, 1900 U, 2000 the new S, 1500 y; saving the states
-// adds 2500.  Tried and slower, as their registers are moved to and fro: V a block ahead (323 to 337 us for the whole
+// (8 x 2048 tokens in 16 heads of 128: 512 waves for 1024 SIMDs, 240 us for 32 blocks of which the matrix instructions
+// take 57).  Of a block's 13800 cycles K S and Q S take 3000, R with the wait for V and the operands of U 2500, U 2100, the new S
+// and P U 2200, y 1800; saving the states adds 2700.  y's products in 22 bits, and powers of two for rows and for 32 tokens,
+// are 30 of the 240 us.  Tried and slower, as their registers are moved to and fro: V a block ahead (323 to 337 us for the whole
 // call), the states' accesses four columns wide and transposed between lanes (323 to 329).
 #include "delta_common.h"
 

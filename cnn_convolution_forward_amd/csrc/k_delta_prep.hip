@@ -15,9 +15,10 @@
 // column, then the blocks below from the products T_ii A_ij T_jj on the fp32 matrix
 // instructions: three levels instead of 64 steps.
 //
-// 8 x 2048 tokens in 16 heads of 128, bf16: 109 us forward, 134 backward, for 134 MB read and 223 (433) MB written; the
-// floor of these bytes is 69 (109) us.  The rest is latency, of the loads (9500 of a workgroup's 44000
-// cycles), the scan of the gates (5900), the substitution and the levels (5600), with four workgroups to a compute unit to cover it.
+// 8 x 2048 tokens in 16 heads of 128, bf16: 115 us forward, 148 backward, for 134 MB read and 240 (436) MB written; the
+// floor of these bytes is 72 (110) us.  The rest is latency, of the loads (11200 of a workgroup's 46200
+// cycles, backward 17100 of 62500), the scan of the gates (5200), the substitution and the levels (6400), with four workgroups to a
+// compute unit to cover it.
 #include <math.h>
 
 #include <type_traits>
@@ -51,7 +52,7 @@ template <typename T, int N> __device__ __forceinline__ void load_part(const T *
 }
 
 // Four workgroups to a compute unit where LDS has room for them, which takes 128 registers (and a few spilled): 8 x 2048 tokens in 16
-// heads of 128 bf16 in 109 us instead of 126 with three.
+// heads of 128 bf16 in 109 us instead of 126 with three, when that was tried.
 constexpr int resident(int parts, int dkb) { return parts * dkb > 4 ? 2 : 4; }
 
 template <typename T, int DKB, bool BWD>
@@ -389,10 +390,10 @@ int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 // Segments of a sequence: its chain of blocks is cut where there are too few chains to fill the chip's 1024 SIMDs with a wave
 // each.  What a segment makes of any state is a matrix and an offset, found by running it from the identity and from zero
 // (twice the columns); the segments are joined one after another, and run again from their states.  That is
-// three times the work over n times the waves (one sequence of 32768 tokens in 8 heads of 128: 395 us instead of 2638).
+// three times the work over n times the waves (one sequence of 32768 tokens in 8 heads of 128: 414 us; 2638 before there were segments).
 // - Waves: packed sequences count as as many of the longest as hold their tokens (9 sequences of 5003 tokens, the longest of 2605,
 //   fp32 in 6 heads of 72 and 99: 121 us, cut for nine of the longest 145).
-// - A block takes 11 us in both passes and the joining of a segment 3: 2 sqrt(blocks) segments are the best number
+// - A block takes 11 to 15 us in both passes and the joining of a segment 3: 2 sqrt(blocks) segments are the best number
 //   (backward, 11981 tokens in 16 heads of 64 and 10: 478 us, with 47 segments instead of 27 505).
 // - Fewer than three segments, or than eight blocks, do not pay (8 x 2048 tokens in 16 heads of 128 in two: forward 318 us
 //   instead of 322, backward 950 instead of 914, at that step).

@@ -15,7 +15,7 @@
 //
 // bf16, forward and backward: 16384 x 2048 25 us (5.4 TB/s) and 39 us (5.1), 4096 x 8192 26 (5.2) and
 // 50 (4.0; with 256 threads to a row 59), 2048 x 16384 32 (4.2) and 71 (2.9: one workgroup to a compute unit, whose
-// barriers nothing hides).  Rows that are read again: 2048 x 20480 81 and 324 us.
+// barriers nothing hides).  Rows that are read again, by single elements and with sums in memory: 2048 x 20480 81 and 324 us.
 //
 // The variance is a second sum over the registers, of squared distances from the
 // mean: no cancellation.  Sums over rows: each workgroup adds its own rows, and a
@@ -28,7 +28,7 @@ namespace {
 constexpr int kThreads = 256;                          // of a workgroup, but for rows that take more
 constexpr int kWide = 1024;                             // for rows that no workgroup holds
 constexpr int threads_of(int G) { return G > kThreads ? G : kThreads; }
-// Workgroups that walk through the rows.  Backward, each has a row of partial sums: 256 of them are enough to fill the chip
+// Workgroups that walk through the rows; the numbers are the best of those tried at the sizes given.  Backward, each has a row of partial sums: 256 of them are enough to fill the chip
 // with wide rows (16384 x 2048 bf16: 39.4 us, with 512 43.8), narrow ones have shorter sums and want more waves (131072 x 128:
 // 24.2 us with 512, 31.2 with 256).  Forward: 25.4 us at 768, 27.2 at 1024, 66 with a workgroup for every four rows.
 constexpr int kMaxForward = 768;
