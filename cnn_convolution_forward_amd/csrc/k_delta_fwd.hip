@@ -28,7 +28,10 @@ namespace {
 template <int DKB, int PARTS, bool SUM> struct FwdPages {
     static constexpr int F = 4 * DKB;                   // pages of one part of K or Q
     static constexpr int kQK = (SUM ? 1 : 2) * PARTS * F;
-    static constexpr int kTri = (SUM ? 2 : 4) * kTriPages;              // T and P, hi and lo
+    // P's lo from memory, not by way of LDS, where that lets a compute unit hold two workgroups (8 x 2048 tokens in 16 heads of 64:
+    // 211 us with one, 190 with two)
+    static constexpr bool kLowDirect = !SUM && DKB == 2 && PARTS == 1;
+    static constexpr int kTri = (SUM ? 2 : kLowDirect ? 3 : 4) * kTriPages;                 // T and P, hi and lo
     static constexpr int kAll = kQK + kTri + 1;         // and a page of the rows' factors
     static constexpr int kBuffers = 2 * kAll <= 156 ? 2 : 1;
 };
@@ -99,6 +102,12 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
         const float gamma = rec[kGamma], invP[2] = {rec[64 * kRowInvP + col], rec[64 * kRowInvP + 32 + col]};
         Column<T> V;
         V.load(rows_buffer(v + (first + (int64_t)k * kBlock) * ldv + hv * d.Dv, n, ldv, d.Dv), at_v, ld_v, half);
+        h8_t low[2 * kTriPages];
+        if constexpr (P::kLowDirect) {
+            const uint4 *src = ws.tri + (((slot0 + k) * d.Hv + hv) * ws.tri_pages + 3 * kTriPages) * kPage + lane;
+#pragma unroll
+            for (int u = 0; u < kTriPages; ++u) low[kTriPages + u] = __builtin_bit_cast(h8_t, src[u * kPage]);
+        }
         const auto page = [&](int i) { return *reinterpret_cast<const h8_t *>(buf + i * 1024 + lane * 16); };
         const float *fac = reinterpret_cast<const float *>(buf + (P::kAll - 1) * 1024);
         const auto factors = [&](int row, int t, int a) { return *reinterpret_cast<const f4_t *>(fac + 64 * row + 32 * t + 8 * a + 4 * half); };
@@ -167,7 +176,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             sr[t] = pow2_scale(max_halves(max_abs(Rr[t])));
         }
         if (P::kBuffers == 2 && k + 1 < blocks) fetch(k + 1);           // behind V's loads, which would wait for it
-        h8_t kt[4 * PARTS], kt2[4 * PARTS], low[2 * kTriPages];
+        h8_t kt[4 * PARTS], kt2[4 * PARTS];
         // rows 32 i .. + 31 of K^T, from the pages of K: 16 rows are a page's columns, four lanes of 8 bytes to a token
         const auto read_kt = [&](int i, h8_t(&to)[4 * PARTS]) {
             const char *p = buf + ((lane >> 4) & 1) * 1024 + ((lane & 1) * 32 + 4 * half + ((lane >> 2) & 3)) * 16 + ((lane >> 1) & 1) * 8;
@@ -195,7 +204,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(Seq s, Delta d, DeltaWs 
             for (int t = i >> 1; t < 2; ++t) to(t) = mfma(tri[kTriPages + low_page(t, i)], f.hi, to(t));
         }
 #pragma unroll
-        for (int u = 0; u < (SUM ? 0 : 2 * kTriPages); ++u) low[u] = page(kP + u);      // in T's registers
+        for (int u = 0; u < (SUM ? 0 : P::kLowDirect ? kTriPages : 2 * kTriPages); ++u) low[u] = page(kP + u);      // in T's registers
         f4_t it[2][4], fk[2][4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) it[u >> 2][u & 3] = factors(kRowInvT, u >> 2, u & 3), fk[u >> 2][u & 3] = factors(kRowFK, u >> 2, u & 3);
