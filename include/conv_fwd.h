@@ -565,14 +565,17 @@ CONV_API conv_status_t conv_scan_step(const conv_seq_t *seq, float scale, const 
  * row stride 2^22 elements or more.
  *
  * Whole sequences are computed in blocks of 64 tokens by matrix products whose
- * operands are sums of two fp16 numbers under a power of two (22 bits), accumulated in
- * fp32; decays are added up in fp64.  The power of two is that of the largest value in a row or column; in a column of values
- * or of upstream gradients, of the largest of tokens 0..31, or 32..63, of a block: values far smaller than that have fewer bits.
- * So have rows and columns whose largest value is below 2^-90 (of q and k with unit = 0); values and states
- * beyond 2^100 may end as infinities.
- * A log decay below -10000 counts as -10000: nothing of the state is left.  Infinities and NaN: results that depend on one
- * are not finite, in its own sequence and head only.  Nor need those be of tokens in front of it among the same 32, or
- * gradients of its 64-token block; what is finite is right.
+ * operands are sums of two fp16 numbers under a power of two, accumulated in fp32; decays
+ * are added up in fp64.  The power of two is that of the largest value in a row or column: in a
+ * column of values or of upstream gradients, of the largest of tokens 0..31, or 32..63, of a block;
+ * in the gradients of q and k, of the largest in a head's state.  A value has 22 bits down to 2^-16
+ * of that largest, and an error of up to 2^-38 of it below.  Rows and columns whose largest value is below
+ * 2^-90 (of q and k with unit = 0) have fewer bits; values and states beyond 2^100 may end as infinities.
+ * A log decay below -10000 counts as -10000: nothing of the state is left.
+ *
+ * Infinities and NaN: results that depend on one are not finite, in its own sequence and head
+ * only.  Nor need those be of tokens in front of it among the same 32, or gradients of its
+ * 64-token block; what is finite is right.
  *
  * Long sequences are cut into segments that run at once and are joined where a batch has few of them: results then
  * differ by roundings from those of the same sequence in another batch.  They have the same bits in any batch with T of at
@@ -635,7 +638,7 @@ CONV_API conv_status_t conv_delta_step(const conv_seq_t *seq, const conv_delta_t
  *
  *     mean = sum x / C,   rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),   y = (x - mean) rstd weight + bias
  *
- * Arithmetic is fp32, y is rounded once.  mean and rstd, where not NULL, receive
+ * Arithmetic is fp32 (squares beyond its range, of values beyond 10^19, make rstd 0), y is rounded once.  mean and rstd, where not NULL, receive
  * what conv_norm_bwd starts from.  eps: finite, >= 0.  A row's results have the
  * same bits among any other rows (dweight and dbias are sums over all).  Errors
  * are those of the operators over sequences: rows < 0, C < 1, ld < C and
